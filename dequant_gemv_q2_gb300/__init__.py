@@ -15,8 +15,9 @@ import numpy as np
 
 from . import build as _build
 
-FP16, BPDQ, TRELLIS, LEECH, NOWEIGHTS = 0, 1, 2, 3, 4
-FMT_NAMES = {FP16: "fp16", BPDQ: "bpdq", TRELLIS: "trellis", LEECH: "leech", NOWEIGHTS: "noweights"}
+FP16, BPDQ, TRELLIS, LEECH, NOWEIGHTS, INT4 = 0, 1, 2, 3, 4, 5
+FMT_NAMES = {FP16: "fp16", BPDQ: "bpdq", TRELLIS: "trellis", LEECH: "leech", NOWEIGHTS: "noweights", INT4: "int4"}
+EINVAL, ESHAPE, EALIGN = -1, -2, -3
 MAX_NTOK = 64
 INV_SQRT8_F32 = float(np.float32(1.0 / np.sqrt(8.0)))
 
@@ -50,6 +51,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "q2_pack_bpdq": [vp, vp, vp, i32, i32, vp, psz],
         "q2_pack_trellis": [vp, vp, vp, i32, i32, vp, psz],
         "q2_pack_leech": [vp, vp, vp, i32, i32, ctypes.c_float, i32, vp, psz],
+        "q2_pack_int4": [vp, vp, vp, i32, i32, i32, vp, psz],
         "q2_pack_noweights": [i32, i32, vp, psz],
         "q2_bind": [vp, vp, ctypes.POINTER(vp)],
         "q2_workspace_bytes": [vp, i32, psz],
@@ -57,6 +59,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "q2_info": [vp, ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "q2_bytes": [vp, i32, psz],
         "q2_gemv": [i32, vp, vp, vp, i32, vp],
+        "q2_gemv_x8": [vp, vp, vp, vp, i32, vp],
+        "q2_rmsnorm": [vp, ctypes.c_longlong, i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, ctypes.c_longlong, vp, vp, vp],
         "q2_decode_bytes": [vp, psz],
         "q2_decode": [vp, vp, vp],
         "q2_gemv_chain": [i32, vp, vp, vp, vp, i32, i32, vp],
@@ -78,9 +82,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     return L
 
 
-EXPORTS = ["q2_pack_fp16", "q2_pack_bpdq", "q2_pack_trellis", "q2_pack_leech", "q2_pack_noweights",
+EXPORTS = ["q2_pack_fp16", "q2_pack_bpdq", "q2_pack_trellis", "q2_pack_leech", "q2_pack_int4", "q2_pack_noweights",
            "q2_bind", "q2_unbind", "q2_workspace_bytes", "q2_set_workspace", "q2_info", "q2_bytes",
-           "q2_gemv", "q2_gemv_chain", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
+           "q2_gemv", "q2_gemv_chain", "q2_gemv_x8", "q2_rmsnorm", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
            "q2_device_errors", "q2_debug_wait_limit", "q2_rotate", "q2_rotate_split"]
 
 
@@ -145,6 +149,19 @@ def q2_pack_leech(v: np.ndarray, tail: np.ndarray, scale: np.ndarray, C: int, la
                                    ctypes.c_float(INV_SQRT8_F32), int(layout)], "q2_pack_leech")
 
 
+def q2_pack_int4(code: np.ndarray, scale: np.ndarray, zero=None, group: int = 128) -> np.ndarray:
+    """code: uint8 [R][C/2] (low four bits: even column); scale: fp16 [R][C/group]; zero: uint8 of that shape or None (8)."""
+    cd = np.ascontiguousarray(code, dtype=np.uint8)
+    sc = np.ascontiguousarray(scale, dtype=np.float16)
+    zr = None if zero is None else np.ascontiguousarray(zero, dtype=np.uint8)
+    R, C = cd.shape[0], cd.shape[1] * 2
+    if group in (32, 64, 128) and C % group == 0:
+        for a, what in ((sc, "scale"), (zr, "zero")):
+            if a is not None and a.shape != (R, C // group):
+                raise Q2Error(ESHAPE, f"q2_pack_int4: {what} is {a.shape}, not {(R, C // group)}")
+    return _pack("q2_pack_int4", [_ptr(cd), _ptr(sc.view(np.uint16)), _ptr(zr), R, C, int(group)], "q2_pack_int4")
+
+
 def q2_pack_noweights(R: int, C: int) -> np.ndarray:
     return _pack("q2_pack_noweights", [R, C], "q2_pack_noweights")
 
@@ -153,6 +170,16 @@ def _stream_ptr(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _check_tensor(where: str, name: str, t, dtype, shape, strides=None) -> None:
+    """Refuse a tensor that the C call would misread: another type, shape or (row-major unless `strides`) layout, or not on a GPU."""
+    if t.dtype is not dtype or not t.is_cuda:
+        raise Q2Error(EINVAL, f"{where}: {name} is {t.dtype} on {t.device}, not {dtype} on a GPU")
+    if t.shape != shape:
+        raise Q2Error(ESHAPE, f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous() and (strides is None or any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides))):
+        raise Q2Error(ESHAPE, f"{where}: {name} has strides {t.stride()}")
 
 
 def device_errors() -> int:
@@ -219,6 +246,22 @@ class Packed:
         st = load().q2_gemv(self.fmt if fmt is None else int(fmt), self.h, ctypes.c_void_p(x.data_ptr()),
                             ctypes.c_void_p(y.data_ptr()), ntok, _stream_ptr(stream))
         _check(st, "q2_gemv")
+        return y
+
+    def gemv_x8(self, x8, xscale, y=None, stream=None):
+        """y[ntok][R] = xscale[ntok] * (x8[ntok][C] @ W^T) through q2_gemv_x8 (INT4 weights; asynchronous)."""
+        import torch
+        if x8.dim() == 1:
+            x8 = x8.view(1, -1)
+        ntok = x8.shape[0]
+        _check_tensor("q2_gemv_x8", "x8", x8, torch.int8, (ntok, self.C))
+        _check_tensor("q2_gemv_x8", "xscale", xscale, torch.float32, (ntok,))
+        if y is None:
+            y = torch.empty((ntok, self.R), dtype=torch.float16, device=x8.device)
+        else:
+            _check_tensor("q2_gemv_x8", "y", y, torch.float16, (ntok, self.R))
+        _check(load().q2_gemv_x8(self.h, x8.data_ptr(), xscale.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream)),
+               "q2_gemv_x8")
         return y
 
     def decode(self, stream=None):
@@ -306,4 +349,59 @@ class Rotation:
         if out is None:
             out = torch.empty_like(x)
         _check(q2_rotate(x, out, x.shape[0], self.C, self.nh, self.signs, self.q, stream), "q2_rotate")
+        return out
+
+
+class RmsNorm:
+    """Root-mean-square norm of rows with the residual's addition in front and
+    an fp16 and/or an 8-bit output behind it (``q2_rmsnorm``).
+
+    ``weight``: fp16 [C] (numpy, or a torch tensor kept on its device).
+    """
+
+    def __init__(self, weight, eps: float = 1e-6, device="cuda"):
+        import torch
+        w = weight if isinstance(weight, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(weight)).to(device)
+        _check_tensor("RmsNorm", "weight", w, torch.float16, (w.numel(),))
+        self.weight, self.eps, self.C = w, float(eps), w.numel()
+
+    def apply(self, x, residual=None, residual_out=None, out=None, out8=None, scale8=None, stream=None):
+        """Norm of the rows x [ntok][C] or [ntok][heads][C] (fp16; a token's rows contiguous, any token stride).
+
+        ``residual`` (fp16, of x's shape, contiguous) is added first; the sum goes to ``residual_out`` (default:
+        back to ``residual``).  ``out``: fp16 of x's shape, laid out as x may be (x itself included); made here when
+        neither ``out`` nor ``out8`` is given.  ``out8`` (int8, x's shape) and ``scale8`` (fp32, a scale per row)
+        take the 8-bit output.  Returns ``out`` (asynchronous).
+        """
+        import torch
+        shape = x.shape
+        if x.dim() not in (2, 3) or shape[-1] != self.C:
+            raise Q2Error(ESHAPE, f"q2_rmsnorm: x has shape {tuple(shape)}, not [ntok][{self.C}] or [ntok][heads][{self.C}]")
+        ntok, heads = shape[0], shape[1] if len(shape) == 3 else 1
+        tail = (1,) if len(shape) == 2 else (self.C, 1)
+        if out is None and out8 is None:
+            out = torch.empty(shape, dtype=torch.float16, device=x.device)
+        ld = []
+        for name, t in (("x", x), ("out", out)):
+            if t is None:
+                ld.append(0)
+                continue
+            ld.append(t.stride(0) if ntok > 1 else heads * self.C)
+            _check_tensor("q2_rmsnorm", name, t, torch.float16, shape, (t.stride(0),) + tail)
+        if residual is not None:
+            residual_out = residual if residual_out is None else residual_out
+            _check_tensor("q2_rmsnorm", "residual", residual, torch.float16, shape)
+        if residual_out is not None:
+            _check_tensor("q2_rmsnorm", "residual_out", residual_out, torch.float16, shape)
+        if out8 is not None:
+            _check_tensor("q2_rmsnorm", "out8", out8, torch.int8, shape)
+            if scale8 is None:
+                raise Q2Error(EINVAL, "q2_rmsnorm: out8 needs scale8")
+            _check_tensor("q2_rmsnorm", "scale8", scale8, torch.float32, shape[:-1])
+        _check(load().q2_rmsnorm(x.data_ptr(), ld[0], ntok, heads, self.C,
+                                 None if residual is None else residual.data_ptr(),
+                                 None if residual_out is None else residual_out.data_ptr(), self.weight.data_ptr(),
+                                 self.eps, None if out is None else out.data_ptr(), ld[1],
+                                 None if out8 is None else out8.data_ptr(),
+                                 None if out8 is None else scale8.data_ptr(), _stream_ptr(stream)), "q2_rmsnorm")
         return out

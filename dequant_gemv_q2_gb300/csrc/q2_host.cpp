@@ -340,6 +340,64 @@ int q2_pack_leech(const int8_t* v, const uint16_t* tail, const uint16_t* scale,
   return Q2_OK;
 }
 
+// The step's four columns of one row, spread to every eighth bit: column 0 to
+// bit 0, 2 to bit 8, 1 to bit 16, 3 to bit 24 (two code bytes in).
+static inline uint32_t int4_spread(const uint8_t* c) {
+  return (uint32_t)(c[0] & 15) | (uint32_t)(c[1] & 15) << 8 | (uint32_t)(c[0] >> 4) << 16 | (uint32_t)(c[1] >> 4) << 24;
+}
+
+int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero,
+                 int R, int C, int group, void* out, size_t* out_bytes) {
+  if (!out_bytes || (out && (!code || !scale))) return Q2_EINVAL;
+  if (group != 32 && group != 64 && group != 128) return Q2_EINVAL;
+  if (R < 1 || C < group || C % group) return Q2_ESHAPE;
+  Builder b(Q2_INT4, R, C);
+  const int nblk = (C + Q2_INT4_COLS - 1) / Q2_INT4_COLS, ntile = b.hdr.Rpad / 16, gpb = Q2_INT4_COLS / group, G = C / group;
+  const size_t nit = (size_t)ntile * nblk;
+  b.hdr.nslice = (C + Q2_SLICE - 1) / Q2_SLICE;
+  b.hdr.nblock = nblk;
+  b.hdr.reserved = group;
+  b.section(SEC_INT4_W, nit * Q2_INT4_BLOCK_BYTES);
+  b.section(SEC_INT4_SCALE, nit * 16 * gpb * 2);
+  b.section(SEC_INT4_ZERO, zero ? nit * 16 * gpb : 0);
+  if (out && zero)
+    for (size_t i = 0; i < (size_t)R * G; ++i)
+      if (zero[i] > 15) return Q2_EINVAL;
+  bool fill;
+  int st = finish(b, out, out_bytes, &fill);
+  if (st || !fill) return st;
+  unsigned char* w = sec(out, b.hdr, SEC_INT4_W);
+  uint16_t* sc = reinterpret_cast<uint16_t*>(sec(out, b.hdr, SEC_INT4_SCALE));
+  unsigned char* zr = zero ? sec(out, b.hdr, SEC_INT4_ZERO) : nullptr;
+  const uint8_t none[2] = {0x88, 0x88};          // q = 8 outside the matrix
+  for (int rt = 0; rt < ntile; ++rt)
+    for (int g = 0; g < 8; ++g) {                // rows rt*16 + g and + 8
+      const int r0 = rt * 16 + g, r1 = r0 + 8;
+      const uint8_t* c0 = r0 < R ? code + (size_t)r0 * (C / 2) : nullptr;
+      const uint8_t* c1 = r1 < R ? code + (size_t)r1 * (C / 2) : nullptr;
+      for (int blk = 0; blk < nblk; ++blk) {
+        const size_t it = (size_t)rt * nblk + blk;
+        for (int k = 0; k < 32; ++k) {           // runs of 4 columns: lane part j, step t
+          const int j = (k >> 1) & 3, t = (k >> 3) * 2 + (k & 1), c = blk * Q2_INT4_COLS + 4 * k;
+          const uint32_t lo = int4_spread(c0 && c < C ? c0 + c / 2 : none), hi = int4_spread(c1 && c < C ? c1 + c / 2 : none);
+          const uint32_t v = lo | hi << 4;
+          std::memcpy(w + it * Q2_INT4_BLOCK_BYTES + (t >> 2) * 512 + (g * 4 + j) * 16 + (t & 3) * 4, &v, 4);
+        }
+        for (int q = 0; q < gpb; ++q) {
+          const int gi = blk * gpb + q;
+          for (int p = 0; p < 2; ++p) {
+            const int r = p ? r1 : r0;
+            const size_t at = ((it * 8 + g) * gpb + q) * 2 + p;
+            const bool in = r < R && gi < G;
+            sc[at] = in ? scale[(size_t)r * G + gi] : (uint16_t)0;
+            if (zr) zr[at] = in ? zero[(size_t)r * G + gi] : (uint8_t)8;
+          }
+        }
+      }
+    }
+  return Q2_OK;
+}
+
 int q2_pack_noweights(int R, int C, void* out, size_t* out_bytes) {
   if (!out_bytes) return Q2_EINVAL;
   if (R < 1 || C < Q2_SLICE || C % Q2_SLICE) return Q2_ESHAPE;
@@ -372,6 +430,7 @@ static double partial_bound(const unsigned char* blob, const q2_blob_header& d) 
       break;
     }
     case Q2_LEECH: k = 8.0; break;          // |v| <= 8 per coordinate
+    case Q2_INT4: break;                    // no fixed-point sums
     case Q2_NOWEIGHTS: k = 0.04; break;     // the control's synthetic coefficients
     default: k = 0.0;
   }
@@ -385,12 +444,22 @@ int q2_bind(const void* blob_host, const void* blob_dev, q2_handle** h) {
   q2_blob_header hdr;
   std::memcpy(&hdr, blob_host, sizeof(hdr));
   if (hdr.magic != Q2_MAGIC || hdr.version != Q2_VERSION) return Q2_EBLOB;
-  if (hdr.fmt < Q2_FP16 || hdr.fmt > Q2_NOWEIGHTS || hdr.R < 1 || hdr.C < 1 ||
+  if (hdr.fmt < Q2_FP16 || hdr.fmt > Q2_INT4 || hdr.R < 1 || hdr.C < 1 ||
       hdr.Rpad != (hdr.R + 31) / 32 * 32)
     return Q2_EBLOB;
   for (int i = 0; i < Q2_MAX_SECTIONS; ++i)
     if (hdr.len[i] && (hdr.off[i] % kAlign || hdr.off[i] + hdr.len[i] > hdr.total_bytes)) return Q2_EBLOB;
   if (hdr.layout != 0 && !(hdr.fmt == Q2_LEECH && hdr.layout == Q2_LEECH_OFFSET4)) return Q2_EBLOB;
+  if (hdr.fmt == Q2_INT4) {
+    const int group = hdr.reserved;
+    if ((group != 32 && group != 64 && group != 128) || hdr.C % group ||
+        hdr.nblock != (hdr.C + Q2_INT4_COLS - 1) / Q2_INT4_COLS || hdr.nslice != (hdr.C + Q2_SLICE - 1) / Q2_SLICE)
+      return Q2_EBLOB;
+    const uint64_t units = (uint64_t)(hdr.Rpad / 16) * hdr.nblock, sides = units * 16 * (Q2_INT4_COLS / group);
+    if (hdr.len[SEC_INT4_W] != units * Q2_INT4_BLOCK_BYTES || hdr.len[SEC_INT4_SCALE] != sides * 2 ||
+        (hdr.len[SEC_INT4_ZERO] && hdr.len[SEC_INT4_ZERO] != sides))
+      return Q2_EBLOB;
+  }
   q2_handle* p = new (std::nothrow) q2_handle;
   if (!p) return Q2_ENOMEM;
   p->hdr = hdr;
@@ -412,6 +481,10 @@ int q2_workspace_bytes(const q2_handle* h, int ntok, size_t* bytes) {
   const int fmt = h->hdr.fmt;
   if (fmt == Q2_FP16) {                                        // one token: none; more: the tensor-core plan
     *bytes = ntok == 1 ? 0 : q2_tc_workspace_bytes(h, ntok);
+    return Q2_OK;
+  }
+  if (fmt == Q2_INT4) {                                        // sums meet in shared memory
+    *bytes = 0;
     return Q2_OK;
   }
   const bool cuda_core = ntok == 1 || (fmt == Q2_BPDQ && ntok <= Q2_MAX_ACC_TOK) ||
@@ -445,6 +518,7 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* bytes) {
   const q2_blob_header& d = h->hdr;
   switch (d.fmt) {
     case Q2_FP16: *bytes = d.len[SEC_FP16_W]; break;
+    case Q2_INT4: *bytes = d.len[SEC_INT4_W] + d.len[SEC_INT4_SCALE] + d.len[SEC_INT4_ZERO]; break;
     case Q2_BPDQ:
       // batch 1 reads (c0, c1, off); the multi-token path reads the value table
       *bytes = d.len[SEC_BPDQ_BITS] + (ntok == 1 ? d.len[SEC_BPDQ_C01] + d.len[SEC_BPDQ_OFF]
@@ -468,7 +542,8 @@ int q2_decode_bytes(const q2_handle* h, size_t* bytes) {
   switch (d.fmt) {
     case Q2_FP16:
     case Q2_BPDQ: *bytes = (size_t)d.R * d.C * 2; break;
-    case Q2_TRELLIS: *bytes = (size_t)d.R * d.C * 4; break;
+    case Q2_TRELLIS:
+    case Q2_INT4: *bytes = (size_t)d.R * d.C * 4; break;
     case Q2_LEECH: {
       size_t body = (size_t)d.R * d.nblock * 24;
       body = (body + 15) / 16 * 16;
@@ -497,6 +572,7 @@ static int gemv_impl(q2_fmt fmt, const q2_handle* h, const void* x, void* y, int
     case Q2_BPDQ: return q2_launch_bpdq(h, x, y, ntok, s, pf);
     case Q2_TRELLIS: return q2_launch_trellis(h, x, y, ntok, s, pf);
     case Q2_LEECH: return q2_launch_leech(h, x, y, ntok, s, pf);
+    case Q2_INT4: return q2_launch_int4(h, x, y, ntok, s, pf);
     case Q2_NOWEIGHTS: return q2_launch_noweights(h, x, y, ntok, s, pf);
     default: return Q2_EFMT;
   }
@@ -504,6 +580,16 @@ static int gemv_impl(q2_fmt fmt, const q2_handle* h, const void* x, void* y, int
 
 int q2_gemv(q2_fmt fmt, const q2_handle* h, const void* x, void* y, int ntok, q2_stream stream) {
   return gemv_impl(fmt, h, x, y, ntok, stream, nullptr);
+}
+
+int q2_gemv_x8(const q2_handle* h, const void* x8, const float* xscale, void* y, int ntok, q2_stream stream) {
+  if (!h || !x8 || !xscale || !y) return Q2_EINVAL;
+  if (h->hdr.fmt != Q2_INT4) return Q2_EFMT;
+  if (ntok < 1 || ntok > Q2_MAX_NTOK) return Q2_ENTOK;
+  if (reinterpret_cast<uintptr_t>(x8) % 16 || reinterpret_cast<uintptr_t>(y) % 16 || reinterpret_cast<uintptr_t>(xscale) % 4)
+    return Q2_EALIGN;
+  if (h->hdr.Rpad > Q2_MAX_ROWS || h->hdr.nslice > Q2_MAX_SPLIT) return Q2_ESHAPE;
+  return q2_launch_int4_x8(h, x8, xscale, y, ntok, static_cast<void*>(stream));
 }
 
 // The device bytes a GEMV of h reads at ntok tokens on the CUDA-core path,

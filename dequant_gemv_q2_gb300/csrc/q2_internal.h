@@ -33,6 +33,8 @@ int q2_launch_bpdq(const q2_handle* h, const void* x, void* y, int ntok, void* s
 int q2_launch_trellis(const q2_handle* h, const void* x, void* y, int ntok, void* stream, const q2_pf* pf);
 int q2_launch_leech(const q2_handle* h, const void* x, void* y, int ntok, void* stream, const q2_pf* pf);
 int q2_launch_noweights(const q2_handle* h, const void* x, void* y, int ntok, void* stream, const q2_pf* pf);
+int q2_launch_int4(const q2_handle* h, const void* x, void* y, int ntok, void* stream, const q2_pf* pf);
+int q2_launch_int4_x8(const q2_handle* h, const void* x8, const float* xscale, void* y, int ntok, void* stream);
 int q2_launch_decode(const q2_handle* h, void* out, void* stream);
 #ifdef __cplusplus
 }

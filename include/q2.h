@@ -21,6 +21,10 @@
  *   Q2_LEECH     Leech-lattice blocks of 24 weights, w = scale_r * v / sqrt(8),
  *                fp16 tail for the last C % 24 columns ("Unfolding the Leech
  *                Lattice", introduction and section 2; "Tetra", section 5.1).
+ *   Q2_INT4      4-bit weights with group scales, w = s_(r,g) * (q - z_(r,g)),
+ *                groups of 32, 64 or 128 columns (no counterpart on the
+ *                source pages: for the layers of a model that do not stand 2
+ *                bits).
  *   Q2_NOWEIGHTS launch-geometry control: same grid, table build and
  *                reduction as the BPDQ kernel, reads no weight bytes
  *                ("Unfolding the Leech Lattice", contribution C4).
@@ -48,7 +52,8 @@ typedef enum {
   Q2_BPDQ = 1,
   Q2_TRELLIS = 2,
   Q2_LEECH = 3,
-  Q2_NOWEIGHTS = 4
+  Q2_NOWEIGHTS = 4,
+  Q2_INT4 = 5
 } q2_fmt;
 
 enum {
@@ -117,6 +122,15 @@ int q2_pack_trellis(const uint8_t* stream, const uint16_t* table, const uint16_t
 #define Q2_LEECH_OFFSET4 1
 int q2_pack_leech(const int8_t* v, const uint16_t* tail, const uint16_t* scale,
                   int R, int C, float inv_sqrt8, int layout, void* out, size_t* out_bytes);
+
+/* 4-bit weights with group scales, w[r][c] = s[r][g] * (q[r][c] - z[r][g])
+ * with g = c / group, exact (no rounding of w).  code: [R][C/2] bytes, the
+ * low four bits of byte j hold q of column 2j, the high four that of column
+ * 2j + 1.  scale: fp16 bits [R][C/group].  zero: [R][C/group] bytes 0..15
+ * (Q2_EINVAL above), or NULL for z = 8 everywhere.  group is 32, 64 or 128;
+ * C % group == 0, R >= 1. */
+int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero,
+                 int R, int C, int group, void* out, size_t* out_bytes);
 
 /* No-weights control: a header only. */
 int q2_pack_noweights(int R, int C, void* out, size_t* out_bytes);
@@ -234,10 +248,19 @@ int q2_gemv_chain(int n, const q2_fmt* fmt, q2_handle* const* h, const void* con
 #define Q2_NOALLOC_SCRATCH_BYTES (1024 * 1024)
 int q2_gemv_bpdq_noalloc(const q2_handle* h, const void* x, void* y, q2_stream stream);
 
+/* y = W x of a Q2_INT4 handle for activations in 8 bits:
+ *   y[t][r] = fp16( xscale[t] * sum_c w[r][c] * x8[t][c] ),
+ * x8: device int8 [ntok][C], 16-byte aligned; xscale: device fp32 [ntok]
+ * (what q2_rmsnorm writes); y: device fp16 [ntok][R], 16-byte aligned;
+ * 1 <= ntok <= 64.  Each group's sum of q * x8 is exact.  Otherwise as
+ * q2_gemv; needs no workspace.  A handle of another format: Q2_EFMT. */
+int q2_gemv_x8(const q2_handle* h, const void* x8, const float* xscale, void* y, int ntok, q2_stream stream);
+
 /* Debug decode to the canonical form (all formats but Q2_NOWEIGHTS):
  *   fp16:    fp16 [R][C]
  *   BPDQ:    fp16 [R][C], one round-to-nearest-even of c0*b0 + c1*b1 + off
  *   trellis: fp32 [R][C], float(scale_r) * float(sign * table value)
+ *   INT4:    fp32 [R][C], s * (q - z), exact
  *   Leech:   int8 [R][24*(C/24)] lattice coordinates, then fp16 [R][C%24]
  *            tail at byte offset R*24*(C/24) rounded up to 16.
  * out: device buffer of q2_decode_bytes() bytes. */
@@ -270,6 +293,35 @@ int q2_decode(const q2_handle* h, void* out_dev, q2_stream stream);
 int q2_rotate(const void* x, void* x_rot, int ntok, int C, int nh, const void* signs, const float* q,
               q2_stream stream);
 int q2_rotate_split(int C, int* nh, int* nq);
+
+/* ---------------------------------------------------------------------- norm
+ * Root-mean-square norm of rows with the residual's addition in front, as it
+ * runs ahead of a projection (no counterpart on the source pages).  Rows are
+ * (token t, head k), 0 <= t < ntok, 0 <= k < heads, of C columns each:
+ *     h = x + residual                       (fp32; residual may be NULL)
+ *     y = h * weight / sqrt(mean(h^2) + eps) (fp32)
+ *     residual_out = fp16(h); y = fp16(y);
+ *     scale8 = max|y| / 127 over the row, y8 = rint(y / scale8).
+ * heads = 1 is the norm of a hidden state; heads > 1 that of each head of a
+ * projection's output, read where it lies.
+ *   - x: device fp16, row (t, k) at x + t * ldx + k * C elements; y: the same
+ *     with ldy, or NULL; ldx, ldy >= heads * C when ntok > 1.
+ *   - residual, residual_out: device fp16 [ntok * heads][C], both or neither.
+ *   - y8: device int8 [ntok * heads][C] or NULL; scale8: device fp32
+ *     [ntok * heads], needed with y8.  At least one of y and y8.
+ *   - weight: device fp16 [C].  1 <= C <= Q2_NORM_MAX_C; eps >= 0.
+ *   - y may be x, and residual_out may be residual or x, when their rows lie
+ *     at the same places; no other overlap.
+ *   - Pointers need their element's alignment only (Q2_EALIGN); C, ldx and
+ *     ldy multiples of 8 and pointers on 16-byte (y8: 8-byte) boundaries run
+ *     on 16-byte loads and stores.
+ *   - An all-zero row has scale8 = 0.  A row with an inf or NaN has a
+ *     scale8 that is not finite, so y8 * scale8 is not finite either.
+ *   - ntok == 0 does nothing.  Asynchronous on `stream`, launched like
+ *     q2_gemv (all inputs are read after the previous kernel has finished). */
+#define Q2_NORM_MAX_C 32768
+int q2_rmsnorm(const void* x, long long ldx, int ntok, int heads, int C, const void* residual, void* residual_out,
+               const void* weight, float eps, void* y, long long ldy, void* y8, float* scale8, q2_stream stream);
 
 /* Device-side error word of the tensor-core (multi-token) kernels, then
  * cleared: 0 in normal operation; nonzero means a bounded wait on the

@@ -20,6 +20,8 @@ Modules:
   leech    -- Leech-lattice blocks of 24 weights, Golay construction
               ("Unfolding the Leech Lattice", introduction and section 7)
   fp16     -- the dense fp16 control
+  int4     -- 4-bit weights with group scales
+  norm     -- root-mean-square norm with the residual's addition
   matvec   -- f64 reference product and the pass criterion
   rotate   -- the activation rotation x_rot = (H (x) Q)(S x) applied ahead
               of the GEMV ("Qwen3.8-27B on a 12 GB card", section "What

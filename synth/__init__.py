@@ -20,6 +20,9 @@ Canonical layouts (the arrays the packers take):
   coordinates, ``shell``: int ``[R][C//24]``, ``tail``: fp16 ``[R][C%24]``,
   ``scale``: fp16 ``[R]``.
 * fp16 dense -- ``w``: fp16 ``[R][C]``.
+* int4   -- ``code``: uint8 ``[R][C/2]``, the low four bits of byte ``j`` hold
+  column ``2j``; ``scale``: fp16 ``[R][C/group]``; ``zero``: uint8 of that
+  shape (0..15) or None.
 * activations -- ``x``: fp16 ``[N][C]``.
 * rotation -- ``signs``: uint8 ``[ceil(C/8)]`` column sign bits, ``q``: fp32
   ``[nq][nq]`` orthogonal, C = nh * nq.
@@ -294,3 +297,26 @@ def rotation(C: int, nh: int, seed: int) -> dict:
     qm, rm = np.linalg.qr(g)
     qm = qm * np.sign(np.diag(rm))[None, :]
     return {"C": C, "nh": nh, "nq": nq, "signs": signs, "q": qm.astype(np.float32)}
+
+
+def int4(R: int, C: int, group: int, seed: int, zeros: bool = True) -> dict:
+    """4-bit group-scaled canonical weights.
+
+    Draw order: code bytes (uniform) [R][C/2], scale ~ U(0.002, 0.01)
+    [R][C/group], zero ~ uniform 0..15 of that shape (None without zeros).
+    """
+    if C % group:
+        raise ValueError("int4 needs C % group == 0")
+    rng = _rng(seed, 0)
+    code = rng.integers(0, 256, size=(R, C // 2), dtype=np.uint8)
+    scale = rng.uniform(0.002, 0.01, size=(R, C // group)).astype(np.float16)
+    zero = rng.integers(0, 16, size=(R, C // group), dtype=np.uint8) if zeros else None
+    return {"R": R, "C": C, "group": group, "code": code, "scale": scale, "zero": zero}
+
+
+def activations8(N: int, C: int, seed: int) -> tuple:
+    """8-bit activations: int8 [N][C] uniform over -127..127 and fp32 scales
+    ~ U(0.005, 0.05) [N] (stream 1 of ``seed``)."""
+    rng = _rng(seed, 1)
+    x8 = rng.integers(-127, 128, size=(N, C), dtype=np.int8)
+    return x8, rng.uniform(0.005, 0.05, size=N).astype(np.float32)
