@@ -17,7 +17,8 @@ from . import build as _build
 
 FP16, BPDQ, TRELLIS, LEECH, NOWEIGHTS, INT4 = 0, 1, 2, 3, 4, 5
 FMT_NAMES = {FP16: "fp16", BPDQ: "bpdq", TRELLIS: "trellis", LEECH: "leech", NOWEIGHTS: "noweights", INT4: "int4"}
-EINVAL, ESHAPE, EALIGN = -1, -2, -3
+EINVAL, ESHAPE, EALIGN, EWORKSPACE = -1, -2, -3, -7
+ERR_LENGTH, ERR_PAGE = 0x100, 0x200     # bits of device_errors()
 MAX_NTOK = 64
 INV_SQRT8_F32 = float(np.float32(1.0 / np.sqrt(8.0)))
 
@@ -61,6 +62,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "q2_gemv": [i32, vp, vp, vp, i32, vp],
         "q2_gemv_x8": [vp, vp, vp, vp, i32, vp],
         "q2_rmsnorm": [vp, ctypes.c_longlong, i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, ctypes.c_longlong, vp, vp, vp],
+        "q2_attend_workspace_bytes": [i32, i32, i32, i32, psz],
+        "q2_attend": [vp, vp, ctypes.c_longlong, vp, vp, ctypes.c_longlong, vp, i32, i32, ctypes.c_float, vp,
+                      ctypes.c_longlong, vp, sz, vp],
         "q2_decode_bytes": [vp, psz],
         "q2_decode": [vp, vp, vp],
         "q2_gemv_chain": [i32, vp, vp, vp, vp, i32, i32, vp],
@@ -84,7 +88,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
 
 EXPORTS = ["q2_pack_fp16", "q2_pack_bpdq", "q2_pack_trellis", "q2_pack_leech", "q2_pack_int4", "q2_pack_noweights",
            "q2_bind", "q2_unbind", "q2_workspace_bytes", "q2_set_workspace", "q2_info", "q2_bytes",
-           "q2_gemv", "q2_gemv_chain", "q2_gemv_x8", "q2_rmsnorm", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
+           "q2_gemv", "q2_gemv_chain", "q2_gemv_x8", "q2_rmsnorm",
+           "q2_attend", "q2_attend_workspace_bytes", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
            "q2_device_errors", "q2_debug_wait_limit", "q2_rotate", "q2_rotate_split"]
 
 
@@ -183,7 +188,7 @@ def _check_tensor(where: str, name: str, t, dtype, shape, strides=None) -> None:
 
 
 def device_errors() -> int:
-    """The tensor-core kernels' device error word (then cleared); 0 is normal."""
+    """The tensor-core and attention kernels' device error word (then cleared); 0 is normal."""
     v = ctypes.c_uint(0)
     _check(load().q2_device_errors(ctypes.byref(v)), "q2_device_errors")
     return v.value
@@ -404,4 +409,81 @@ class RmsNorm:
                                  self.eps, None if out is None else out.data_ptr(), ld[1],
                                  None if out8 is None else out8.data_ptr(),
                                  None if out8 is None else scale8.data_ptr(), _stream_ptr(stream)), "q2_rmsnorm")
+        return out
+
+
+class _KV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("npages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int)]
+
+
+def _rows(where: str, name: str, t, shape) -> int:
+    """The leading dimension of fp16 rows [batch][heads][dim], each batch row contiguous."""
+    import torch
+    _check_tensor(where, name, t, torch.float16, shape, (t.stride(0), shape[2], 1))
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+class PagedKV:
+    """A paged key-value cache and attention of one new token per sequence over it (``q2_attend``).
+
+    ``k``, ``v``: fp16 pools seen as [pages][page_size][kv_heads][dim], in any order of storage (dim contiguous; both
+    alike).  ``table``: int32 [batch][max_pages] page numbers on the same GPU.  The tensors stay the caller's: pages,
+    table and lengths may be changed between calls.  ``workspace``: uint8, zero when first used (made here if None).
+    """
+
+    def __init__(self, k, v, table, q_heads: int, workspace=None):
+        import torch
+        if k.dim() != 4 or table.dim() != 2:
+            raise Q2Error(ESHAPE, "PagedKV: k is not [pages][page_size][kv_heads][dim], or table not [batch][max_pages]")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            raise Q2Error(ESHAPE, f"PagedKV: k has strides {k.stride()}")
+        for name, t in (("k", k), ("v", v)):
+            _check_tensor("PagedKV", name, t, torch.float16, k.shape, k.stride())
+        if v.stride() != k.stride():
+            raise Q2Error(ESHAPE, f"PagedKV: k has strides {k.stride()}, v {v.stride()}")
+        _check_tensor("PagedKV", "table", table, torch.int32, table.shape, (table.stride(0), 1))
+        self.k, self.v, self.table, self.q_heads = k, v, table, int(q_heads)
+        pages, page, self.kv_heads, self.dim = k.shape
+        self.batch = table.shape[0]
+        self.scale = self.dim ** -0.5
+        self._kv = _KV(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), pages, page, self.kv_heads,
+                       self.dim, table.data_ptr(), table.stride(0) if self.batch > 1 else table.shape[1], table.shape[1])
+        self._ref = ctypes.byref(self._kv)
+        n = ctypes.c_size_t(0)
+        _check(load().q2_attend_workspace_bytes(self.batch, self.q_heads, self.kv_heads, self.dim, ctypes.byref(n)),
+               "q2_attend_workspace_bytes")
+        if workspace is None:
+            workspace = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
+        elif workspace.numel() < n.value:
+            raise Q2Error(EWORKSPACE, f"PagedKV: workspace of {workspace.numel()} bytes, {n.value} needed")
+        self.ws = workspace
+
+    def attend(self, q, lens, new_k=None, new_v=None, scale=None, out=None, stream=None):
+        """Attention of q [batch][q_heads][dim] over the first lens[b] (int32) tokens of each sequence.
+
+        ``new_k``, ``new_v`` [batch][kv_heads][dim]: the new token's, counted by ``lens``; they are stored as token
+        lens[b] - 1.  q, new_k, new_v and ``out`` may have any batch stride (slices of a projection's output).
+        ``scale``: dim ** -0.5 if None.  Returns ``out`` (asynchronous).
+        """
+        import torch
+        shape = (self.batch, self.q_heads, self.dim)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float16, device=q.device)
+        ldq, ldo, ldn = _rows("q2_attend", "q", q, shape), _rows("q2_attend", "out", out, shape), 0
+        _check_tensor("q2_attend", "lens", lens, torch.int32, (self.batch,))
+        nk = nv = None
+        if new_k is not None and new_v is not None:
+            each = (self.batch, self.kv_heads, self.dim)
+            ldn = _rows("q2_attend", "new_k", new_k, each)
+            if _rows("q2_attend", "new_v", new_v, each) != ldn:
+                raise Q2Error(ESHAPE, "q2_attend: new_k and new_v have different batch strides")
+            nk, nv = new_k.data_ptr(), new_v.data_ptr()
+        elif new_k is not None or new_v is not None:
+            raise Q2Error(EINVAL, "q2_attend: new_k and new_v go together")
+        _check(load().q2_attend(self._ref, q.data_ptr(), ldq, nk, nv, ldn, lens.data_ptr(), self.batch, self.q_heads,
+                                self.scale if scale is None else scale, out.data_ptr(), ldo, self.ws.data_ptr(),
+                                self.ws.numel(), _stream_ptr(stream)), "q2_attend")
         return out

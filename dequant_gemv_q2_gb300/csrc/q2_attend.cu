@@ -1,0 +1,535 @@
+// Attention of one new token per sequence over a paged key-value cache,
+//
+//   o[b][h] = sum_l p_l v_l / sum_l p_l,   p_l = exp(scale * q[b][h] . k_l),
+//
+// l over the sequence's lens[b] tokens, k and v of head h / (q_heads /
+// kv_heads) (grouped heads).  Each token's key and value are read once for
+// all query heads of the group and take part in 4 D operations per head, so
+// the cache's bytes bound it.
+//
+// Work is cut into units of 64 tokens of one (sequence, key-value head), in
+// the order (sequence, head, token), and every CTA takes an equal contiguous
+// share of them, worked out on the device from lens: sequences of any mix of
+// lengths load the SMs alike, and one long sequence spreads over all of them.
+// Where a (sequence, head)'s units lie in several CTAs each leaves its sums
+// (maximum, denominator, fp32 numerators) in the workspace, and the CTA that
+// finishes last, by a counter, joins them in CTA order: one launch, and a
+// result that does not depend on which was last.
+//
+// Inside a CTA the four warps take 16 tokens of a unit each, on their own:
+// every warp has a ring of shared-memory stages that it fills with
+// asynchronous 16-byte copies STAGES - 1 units ahead (across the ends of
+// sequences and heads), its own running maximum, denominator and numerators,
+// and meets the others only at the end of a (sequence, head).  Rows past a
+// sequence's end are filled with zeros by the copy and masked, so what an
+// unused part of a page holds (infinities, NaN) has no effect.  The 16-byte
+// pieces of a row are exchanged by the row's low three bits, so that eight
+// rows of one piece (what one matrix load takes) lie in different banks.
+//
+// Both products run on the tensor cores (16 x 8 x 16, fp32 accumulators) with
+// the group's query heads as rows 0..7.  The probabilities are split into two
+// fp16 numbers, p = hi + lo, and lo takes rows 8..15 of the same
+// instructions: the numerators are as exact as with fp32 probabilities (an
+// error of 2^-22 instead of 2^-11 per term) at no cost.
+#include <cuda_fp16.h>
+
+#include "q2_common.cuh"
+
+namespace q2 {
+namespace {
+
+__device__ unsigned int q2_attend_error;
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTile = 16, kUnit = kTile * kWarps;   // tokens of a warp's tile, of a unit
+constexpr int kHeads = 8;                           // query heads of a unit (rows of the products)
+
+struct AttendArgs {
+  __half* k;
+  __half* v;
+  long long page_stride, token_stride, head_stride;
+  const int* table;
+  long long table_stride;
+  const int* lens;
+  const __half* q;
+  const __half* nk;           // new keys and values, or null
+  const __half* nv;
+  __half* o;
+  long long ldq, ldn, ldo;
+  unsigned int* count;        // [batch][units' heads] arrivals, zero between calls
+  float* part;                // [2 * CTAs][kHeads][D] numerators
+  float2* ml;                 // [2 * CTAs][kHeads] maximum, denominator
+  int batch, npages, page, cap;   // cap: tokens that a table row can hold
+  int hu, nht, group;         // heads of units = kv_heads * nht; query heads of a key-value head
+  float sc2;                  // scale * log2(e)
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// p0, p1 as pairs of fp16 numbers whose sums they are (to 2^-22).
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(p0, p1);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(p0 - f.x, p1 - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// A place in the order of units.
+struct Walk {
+  int b, h, chunk, nch, len;
+};
+
+template <int D>
+struct Shape {
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int kTileBytes = kTile * D * 2;                     // keys or values of a tile
+  static constexpr int kRing = kWarps * STAGES * 2 * kTileBytes;
+  static constexpr int kMerge = (kWarps - 1) * kHeads * D * 4;
+  static constexpr int kMl = kWarps * kHeads * 8;
+  static constexpr int fixed = kRing + kMerge + kMl + 16;
+  static int smem(int batch) { return fixed + 4 * (batch + 1); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __grid_constant__ AttendArgs a) {
+  using S = Shape<D>;
+  constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
+  extern __shared__ __align__(16) unsigned char q2_att_smem[];
+  float* merge = reinterpret_cast<float*>(q2_att_smem + S::kRing);     // [kWarps - 1][kHeads][D]
+  float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing + S::kMerge);   // [kWarps][kHeads]
+  int* last = reinterpret_cast<int*>(q2_att_smem + S::kRing + S::kMerge + S::kMl);
+  int* pre = last + 4;                                                 // [batch + 1] units before each sequence
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
+
+  pdl_wait();                                       // everything may come from the previous kernel
+  pdl_trigger();
+  if (warp == 0) {                                  // the units before each sequence
+    int carry = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int len = b < a.batch ? a.lens[b] : 0;
+      if (len < 0 || len > a.cap) len = 0;
+      int v = (len + kUnit - 1) / kUnit * a.hu;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (b < a.batch) pre[b + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+  // sequences without a token give zeros, lengths that the table cannot hold NaN
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const int len = a.lens[b];
+    if (len > 0 && len <= a.cap) continue;
+    if (len != 0 && threadIdx.x == 0) atomicOr(&q2_attend_error, Q2_ERR_LENGTH);
+    const int n = a.hu / a.nht * a.group * D;
+    for (int e = threadIdx.x; e < n; e += kThreads)
+      a.o[b * a.ldo + e] = len ? __ushort_as_half(0x7e00) : __ushort_as_half(0);
+  }
+  __syncthreads();
+  const int total = pre[a.batch], ncta = min((int)gridDim.x, total);
+  if ((int)blockIdx.x >= ncta) return;
+  auto first_of = [&](int cta) { return (int)((long long)total * cta / ncta); };
+  const int u0 = first_of(blockIdx.x), n = first_of(blockIdx.x + 1) - u0;
+
+  Walk c;                                           // the unit in use
+  {
+    int lo = 0, hi = a.batch - 1;                   // the sequence b with pre[b] <= u0 < pre[b + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid + 1] <= u0) lo = mid + 1;
+      else hi = mid;
+    }
+    c.b = lo;
+    c.len = a.lens[lo];
+    c.nch = (c.len + kUnit - 1) / kUnit;
+    const int r = u0 - pre[lo];
+    c.h = r / c.nch;
+    c.chunk = r - c.h * c.nch;
+  }
+  auto advance = [&](Walk& w) {
+    if (++w.chunk < w.nch) return;
+    w.chunk = 0;
+    if (++w.h < a.hu) return;
+    w.h = 0;
+    do ++w.b;
+    while (w.b < a.batch && pre[w.b + 1] == pre[w.b]);
+    if (w.b < a.batch) {
+      w.len = a.lens[w.b];
+      w.nch = (w.len + kUnit - 1) / kUnit;
+    }
+  };
+
+  // ---- the warp's loads, STAGES - 1 units ahead of their use
+  const uint32_t ring = saddr(q2_att_smem) + warp * (STAGES * 2 * S::kTileBytes);
+  Walk p = c;
+  int pu = 0, pslot = 0, ppage = -1;                // unit to load, its stage, the page of this lane's row
+  uint32_t badslots = 0;                            // stages with a row whose page does not exist
+  auto lookup = [&]() {                             // lanes l and l + 16: row l of the tile
+    const int t = p.chunk * kUnit + warp * kTile + (lane & 15);
+    ppage = pu < n && t < p.len ? a.table[p.b * a.table_stride + t / a.page] : -1;
+  };
+  lookup();
+  auto issue = [&]() {
+    if (pu < n) {
+      const int t0 = p.chunk * kUnit + warp * kTile, t = t0 + (lane & 15);
+      if (t0 < p.len) {
+        const bool wanted = t < p.len && !(a.nk && t == p.len - 1);    // the new token does not come from the cache
+        const bool there = (unsigned)ppage < (unsigned)a.npages;
+        const bool bad = __any_sync(0xffffffffu, t < p.len && !there);
+        if (bad && lane == 0) atomicOr(&q2_attend_error, Q2_ERR_PAGE);
+        badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
+        const long long off = wanted && there ? ppage * a.page_stride + (t % a.page) * a.token_stride +
+                                                    (p.h / a.nht) * a.head_stride
+                                              : -1;
+        const uint32_t dst = ring + pslot * (2 * S::kTileBytes);
+        const int piece = lane % CPR;
+#pragma unroll
+        for (int i = 0; i < kTile / RPI; ++i) {
+          const int row = i * RPI + lane / CPR;
+          const long long o = __shfl_sync(0xffffffffu, off, row);
+          const long long e = (o < 0 ? 0 : o) + piece * 8;
+          const uint32_t d = dst + row * (D * 2) + ((piece ^ (row & 7)) << 4);
+          cp16(d, a.k + e, o >= 0);
+          cp16(d + S::kTileBytes, a.v + e, o >= 0);
+        }
+      }
+      ++pu;
+      advance(p);
+      lookup();
+      pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int s = 0; s < STAGES - 1; ++s) issue();
+
+  // ---- sums of the current (sequence, head)
+  uint32_t qa[D / 16][2];                           // the queries: row g, columns 2j.. and 2j + 8.. of each 16
+  uint4 newk, newv;                                 // lane l < CPR: piece l of the new token's key and value
+  float o[NT][4], m = -INFINITY, l = 0.f;
+  bool fresh = true;
+  int seg = c.chunk, slot = 0;                      // first unit of this part of the (sequence, head)
+  for (int i = 0; i < n; ++i) {
+    const int kvh = c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
+    const int qh = kvh * a.group + ht * kHeads;
+    const int t0 = c.chunk * kUnit + warp * kTile;
+    if (fresh) {
+      fresh = false;
+      const __half* q = a.q + c.b * a.ldq + (long long)(qh + g) * D + 2 * j;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        qa[s][0] = g < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * s) : 0u;
+        qa[s][1] = g < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8) : 0u;
+      }
+      if (a.nk && lane < CPR) {
+        const long long e = c.b * a.ldn + kvh * D + lane * 8;
+        newk = *reinterpret_cast<const uint4*>(a.nk + e);
+        newv = *reinterpret_cast<const uint4*>(a.nv + e);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[t][x] = 0.f;
+      m = -INFINITY;
+      l = 0.f;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncwarp();                                   // unit i has arrived for all lanes, unit i - 1 is done with
+    issue();
+    if (t0 < c.len) {
+      const uint32_t kt = ring + slot * (2 * S::kTileBytes), vt = kt + S::kTileBytes;
+      const int fin = c.len - 1 - t0;               // row of the last token, if below kTile
+      if (a.nk && fin < kTile) {                    // the new token's row, and its place in the cache
+        if (lane < CPR) {
+          const uint32_t d = fin * (D * 2) + ((lane ^ (fin & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kt + d), "r"(newk.x), "r"(newk.y), "r"(newk.z),
+                       "r"(newk.w)
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vt + d), "r"(newv.x), "r"(newv.y), "r"(newv.z),
+                       "r"(newv.w)
+                       : "memory");
+          const int page = a.table[c.b * a.table_stride + (c.len - 1) / a.page];
+          if (ht == 0 && (unsigned)page < (unsigned)a.npages) {
+            const long long e = page * a.page_stride + ((c.len - 1) % a.page) * a.token_stride + kvh * a.head_stride +
+                                lane * 8;
+            *reinterpret_cast<uint4*>(a.k + e) = newk;
+            *reinterpret_cast<uint4*>(a.v + e) = newv;
+          }
+        }
+        __syncwarp();
+      }
+      // scores of 16 tokens: columns 2j, 2j + 1 of tokens 0..7 (s0) and 8..15 (s1)
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        uint32_t b[4];
+        ldsm4(b, kt + krow * (D * 2) + (((2 * s + kpiece) ^ (krow & 7)) << 4));
+        mma(s0, qa[s][0], 0u, qa[s][1], 0u, b[0], b[1]);
+        mma(s1, qa[s][0], 0u, qa[s][1], 0u, b[2], b[3]);
+      }
+      float x[4] = {s0[0] * a.sc2, s0[1] * a.sc2, s1[0] * a.sc2, s1[1] * a.sc2};
+      if (fin < kTile - 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (2 * j + (e & 1) + (e >> 1) * 8 > fin) x[e] = -INFINITY;
+      }
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+      if (__any_sync(0xffffffffu, mn > m)) {        // a new maximum somewhere: scale what there is
+        const float al = exp2f(m - ref);
+        l *= al;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {              // rows 0..7 and 8..15 are halves of the same head
+          o[t][0] *= al;
+          o[t][1] *= al;
+          o[t][2] *= al;
+          o[t][3] *= al;
+        }
+        m = mn;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = exp2f(x[e] - ref);
+      l += (x[0] + x[1]) + (x[2] + x[3]);
+      if ((badslots >> slot) & 1u) l = __int_as_float(0x7fc00000);
+      uint32_t p0, p1, p2, p3;
+      split2(x[0], x[1], p0, p1);
+      split2(x[2], x[3], p2, p3);
+      const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t b[4];
+        ldsm4t(b, vt + vrow * (D * 2) + (((t + vpiece) ^ (vrow & 7)) << 4));
+        mma(o[t], p0, p1, p2, p3, b[0], b[1]);
+        mma(o[t + 1], p0, p1, p2, p3, b[2], b[3]);
+      }
+    }
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+
+    const bool ends = c.chunk + 1 == c.nch;
+    if (ends || i + 1 == n) {                       // the end of this (sequence, head), or of this CTA's share of it
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      __syncthreads();                              // the merge buffer is free
+      if (j == 0) wml[warp * kHeads + g] = make_float2(m, l);
+      if (warp) {
+        float* w = merge + ((warp - 1) * kHeads + g) * D + 2 * j;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<float2*>(w + 8 * t) = make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3]);
+      }
+      __syncthreads();
+      const bool whole = ends && seg == 0;
+      const int part = 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0);
+      if (warp == 0) {
+        float wt[kWarps], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, wml[w * kHeads + g].x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = wml[w * kHeads + g];
+          wt[w] = exp2f(v.x - ref);
+          ll += wt[w] * v.y;
+        }
+        if (g < rows) {
+          const float inv = 1.f / ll;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float x = (o[t][0] + o[t][2]) * wt[0], y = (o[t][1] + o[t][3]) * wt[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+              const float2 v = *reinterpret_cast<const float2*>(merge + ((w - 1) * kHeads + g) * D + 8 * t + 2 * j);
+              x += v.x * wt[w];
+              y += v.y * wt[w];
+            }
+            if (whole)
+              *reinterpret_cast<__half2*>(a.o + c.b * a.ldo + (long long)(qh + g) * D + 8 * t + 2 * j) =
+                  __floats2half2_rn(x * inv, y * inv);
+            else
+              *reinterpret_cast<float2*>(a.part + ((size_t)part * kHeads + g) * D + 8 * t + 2 * j) = make_float2(x, y);
+          }
+          if (!whole && j == 0) a.ml[(size_t)part * kHeads + g] = make_float2(mm, ll);
+        }
+      }
+      if (!whole) {
+        // the CTAs that hold parts of this (sequence, head): c0 (from its first unit) .. c1
+        const int s = pre[c.b] + c.h * c.nch;
+        auto cta_of = [&](int u) { return (int)((((long long)u + 1) * ncta - 1) / total); };
+        const int c0 = cta_of(s), c1 = cta_of(s + c.nch - 1);
+        if (warp == 0) {
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            unsigned int* count = a.count + (size_t)c.b * a.hu + c.h;
+            const bool done = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
+            if (done) *count = 0;
+            __threadfence();
+            *last = done;
+          }
+        }
+        __syncthreads();
+        if (*last) {
+          for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), d4 = e % (D / 4);
+            float mm = -INFINITY;
+#pragma unroll 8
+            for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(&a.ml[(size_t)(2 * k + (k == c0)) * kHeads + r]).x);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f, x = 0.f, y = 0.f, z = 0.f, w = 0.f;
+#pragma unroll 4
+            for (int k = c0; k <= c1; ++k) {
+              const size_t at = (size_t)(2 * k + (k == c0)) * kHeads + r;
+              const float2 v = __ldcg(&a.ml[at]);
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + d4);
+              const float wt = exp2f(v.x - ref);
+              ll += wt * v.y;
+              x += wt * f.x;
+              y += wt * f.y;
+              z += wt * f.z;
+              w += wt * f.w;
+            }
+            const float inv = 1.f / ll;
+            __half2 h[2] = {__floats2half2_rn(x * inv, y * inv), __floats2half2_rn(z * inv, w * inv)};
+            *reinterpret_cast<uint2*>(a.o + c.b * a.ldo + (long long)(qh + r) * D + d4 * 4) = *reinterpret_cast<uint2*>(h);
+          }
+        }
+      }
+      fresh = true;
+      seg = 0;
+    }
+    advance(c);
+  }
+}
+
+int most_ctas(int D) { return dev_info().sms * (D <= 128 ? 2 : 1); }
+
+// The workspace: the parts' sums, in a region that fits every head_dim (so the
+// counters behind it have one place for calls of all shapes), then counters.
+size_t part_bytes() {
+  const size_t a = (size_t)2 * most_ctas(128) * kHeads * (128 * 4 + 8), b = (size_t)2 * most_ctas(256) * kHeads * (256 * 4 + 8);
+  return ((a > b ? a : b) + 255) / 256 * 256;
+}
+
+// Shared checks of the head counts; hu: heads of units.
+int check_heads(int batch, int q_heads, int kv_heads, int D, int* hu, int* nht) {
+  if (batch < 0 || batch > Q2_ATT_MAX_BATCH || kv_heads < 1 || kv_heads > 65536 || q_heads < 1 || q_heads % kv_heads)
+    return Q2_ESHAPE;
+  if (q_heads / kv_heads > Q2_ATT_MAX_GROUP || (D != 64 && D != 128 && D != 256)) return Q2_ESHAPE;
+  *nht = (q_heads / kv_heads + kHeads - 1) / kHeads;
+  *hu = kv_heads * *nht;
+  return Q2_OK;
+}
+
+}  // namespace
+}  // namespace q2
+
+using namespace q2;
+
+extern "C" int q2_attend_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim, size_t* bytes) {
+  if (!bytes) return Q2_EINVAL;
+  int hu, nht;
+  const int st = check_heads(batch, q_heads, kv_heads, head_dim, &hu, &nht);
+  if (st) return st;
+  *bytes = part_bytes() + (size_t)batch * hu * 4;
+  return Q2_OK;
+}
+
+extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, const void* new_v,
+                         long long ldn, const int* lens, int batch, int q_heads, float scale, void* out, long long ldo,
+                         void* ws, size_t ws_bytes, q2_stream stream) {
+  if (!kv || (!new_k) != (!new_v)) return Q2_EINVAL;
+  const int D = kv->head_dim;
+  int hu, nht;
+  int st = check_heads(batch, q_heads, kv->kv_heads, D, &hu, &nht);
+  if (st) return st;
+  if (kv->page_size < 1 || kv->npages < 0 || kv->max_pages < 0) return Q2_ESHAPE;
+  if (!(scale == scale) || scale - scale != 0.f) return Q2_EINVAL;
+  if (batch == 0) return Q2_OK;
+  if (!q || !lens || !out || !kv->k || !kv->v || !kv->table) return Q2_EINVAL;
+  const long long qw = (long long)q_heads * D, kw = (long long)kv->kv_heads * D;
+  if (batch > 1 && (ldq < qw || ldo < qw || (new_k && ldn < kw) || kv->table_stride < kv->max_pages)) return Q2_ESHAPE;
+  if (kv->page_stride < 0 || kv->token_stride < 0 || kv->head_stride < 0) return Q2_ESHAPE;
+  auto off = [](const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; };
+  if (off(q, 16) || off(out, 16) || off(new_k, 16) || off(new_v, 16) || off(kv->k, 16) || off(kv->v, 16) ||
+      off(kv->table, 4) || off(lens, 4) || kv->page_stride % 8 || kv->token_stride % 8 || kv->head_stride % 8 ||
+      (batch > 1 && (ldq % 8 || ldo % 8 || (new_k && ldn % 8))))
+    return Q2_EALIGN;
+  size_t need = 0;
+  st = q2_attend_workspace_bytes(batch, q_heads, kv->kv_heads, D, &need);
+  if (st) return st;
+  if (!ws || ws_bytes < need) return Q2_EWORKSPACE;
+  if (off(ws, 256)) return Q2_EALIGN;
+  // tokens of a table row, and of all units: both are counted in 32 bits on the device
+  const long long cap = (long long)kv->max_pages * kv->page_size;
+  const long long units = (cap / kUnit + 1) * hu * batch;
+  if (cap > 0x7fffff00ll || units > 0x7fffffffll) return Q2_ESHAPE;
+  AttendArgs a = {};
+  a.k = static_cast<__half*>(kv->k);
+  a.v = static_cast<__half*>(kv->v);
+  a.page_stride = kv->page_stride;
+  a.token_stride = kv->token_stride;
+  a.head_stride = kv->head_stride;
+  a.table = kv->table;
+  a.table_stride = kv->table_stride;
+  a.lens = lens;
+  a.q = static_cast<const __half*>(q);
+  a.nk = static_cast<const __half*>(new_k);
+  a.nv = static_cast<const __half*>(new_v);
+  a.o = static_cast<__half*>(out);
+  a.ldq = ldq;
+  a.ldn = ldn;
+  a.ldo = ldo;
+  const int most = most_ctas(D);
+  a.part = static_cast<float*>(ws);
+  a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + part_bytes());
+  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most * kHeads * D);
+  a.batch = batch;
+  a.npages = kv->npages;
+  a.page = kv->page_size;
+  a.cap = (int)cap;
+  a.hu = hu;
+  a.nht = nht;
+  a.group = q_heads / kv->kv_heads;
+  a.sc2 = (float)((double)scale * 1.4426950408889634);
+  const int grid = units < most ? (int)units : most;
+  if (D == 64) return launch_pdl(k_attend<64>, a, grid, kThreads, Shape<64>::smem(batch), stream);
+  if (D == 128) return launch_pdl(k_attend<128>, a, grid, kThreads, Shape<128>::smem(batch), stream);
+  return launch_pdl(k_attend<256>, a, grid, kThreads, Shape<256>::smem(batch), stream);
+}
+
+// The error word of the attention kernels, then cleared (q2_device_errors).
+extern "C" int q2_attend_errors(unsigned int* out) {
+  unsigned int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, q2_attend_error, sizeof(v)) != cudaSuccess) return Q2_ECUDA;
+  if (v && cudaMemcpyToSymbol(q2_attend_error, &z, sizeof(z)) != cudaSuccess) return Q2_ECUDA;
+  *out = v;
+  return Q2_OK;
+}

@@ -1116,7 +1116,9 @@ extern "C" int q2_debug_wait_limit(long long polls) {
   return cudaMemcpyToSymbol(q2_tc_stage_wait_limit, &polls, sizeof(polls)) == cudaSuccess ? Q2_OK : Q2_ECUDA;
 }
 
-// Device-side error word of the tensor-core kernels since the last call
+extern "C" int q2_attend_errors(unsigned int* out);   // q2_attend.cu
+
+// Device-side error word of the tensor-core and attention kernels since the last call
 // (then cleared): 0 in normal operation, else the code of a bounded wait
 // that ran out.  Synchronous (reads device memory).
 extern "C" int q2_device_errors(unsigned int* out) {
@@ -1124,6 +1126,8 @@ extern "C" int q2_device_errors(unsigned int* out) {
   unsigned int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, q2_tc_error, sizeof(v)) != cudaSuccess) return Q2_ECUDA;
   if (cudaMemcpyToSymbol(q2_tc_error, &z, sizeof(z)) != cudaSuccess) return Q2_ECUDA;
-  *out = v;
+  unsigned int att = 0;
+  if (q2_attend_errors(&att) != Q2_OK) return Q2_ECUDA;
+  *out = v | att;
   return Q2_OK;
 }

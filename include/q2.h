@@ -323,9 +323,75 @@ int q2_rotate_split(int C, int* nh, int* nq);
 int q2_rmsnorm(const void* x, long long ldx, int ntok, int heads, int C, const void* residual, void* residual_out,
                const void* weight, float eps, void* y, long long ldy, void* y8, float* scale8, q2_stream stream);
 
-/* Device-side error word of the tensor-core (multi-token) kernels, then
- * cleared: 0 in normal operation; nonzero means a bounded wait on the
- * tensor core ran out and the kernel skipped its work (the rows of the tiles
+/* ----------------------------------------------------------------- attention
+ * Attention of one new token per sequence over a paged key-value cache (no
+ * counterpart on the source pages): what lies between the qkv and the output
+ * projection of a decode step.
+ *     o[b][h] = sum_l p_l v_l / sum_l p_l,  p_l = exp(scale * q[b][h] . k_l),
+ * over the tokens l < lens[b] of sequence b, k and v of key-value head
+ * h / (q_heads / kv_heads).  fp16 in and out, fp32 sums.
+ *
+ * The cache: pools k and v of fp16, both with element (page, slot, head, d) at
+ * page * page_stride + slot * token_stride + head * head_stride + d, so pages
+ * may be stored token by token or head by head.  Token l of sequence b is in
+ * slot l % page_size of page table[b * table_stride + l / page_size];
+ * max_pages entries of a table row may be used.  Any page_size >= 1. */
+typedef struct {
+  void* k;                      /* device fp16 pools, 16-byte aligned          */
+  void* v;
+  long long page_stride;        /* elements, multiples of 8                    */
+  long long token_stride;
+  long long head_stride;
+  int npages;                   /* pages in a pool                             */
+  int page_size;                /* tokens of a page                            */
+  int kv_heads;
+  int head_dim;                 /* 64, 128 or 256                              */
+  const int* table;             /* device [batch][table_stride] page numbers   */
+  long long table_stride;
+  int max_pages;
+} q2_kv;
+
+#define Q2_ATT_MAX_BATCH 1024
+#define Q2_ATT_MAX_GROUP 64     /* query heads per key-value head              */
+
+/* out[b] = attention of q[b] over the first lens[b] tokens of sequence b.
+ *   - q: device fp16, head h of sequence b at q + b * ldq + h * head_dim; out
+ *     the same with ldo (so q may lie in the qkv projection's output).
+ *   - new_k, new_v: the new token's keys and values, head h of sequence b at
+ *     + b * ldn + h * head_dim, or both NULL.  When given, lens[b] counts the
+ *     new token: its row is taken from here and also stored in the cache as
+ *     token lens[b] - 1.  When NULL, the cache holds all lens[b] tokens.
+ *   - lens: device int32 [batch].  A sequence of length 0 gives zeros and
+ *     stores nothing.
+ *   - Pointers 16-byte aligned, leading dimensions multiples of 8 (Q2_EALIGN);
+ *     head_dim 64, 128 or 256, q_heads a multiple of kv_heads with at most
+ *     Q2_ATT_MAX_GROUP of them to one, batch <= Q2_ATT_MAX_BATCH (Q2_ESHAPE).
+ *     No two sequences may store to the same place of the cache.
+ *   - ws: device memory of q2_attend_workspace_bytes(), 256-byte aligned, zero
+ *     when first used; completed calls leave its counters at zero.  Calls of
+ *     any shapes that it is large enough for may share it if they are ordered
+ *     on one stream; calls that overlap on the GPU need different ones.
+ *   - What pages hold past a sequence's end, and table entries there, are
+ *     never used.  A length below 0 or above max_pages * page_size, or a page
+ *     number outside 0..npages-1, makes that sequence's output NaN (of the
+ *     heads concerned) and sets Q2_ERR_LENGTH or Q2_ERR_PAGE in
+ *     q2_device_errors(); nothing outside the pools is read or written (the
+ *     new token is stored where its own page is sound).
+ *   - batch == 0 does nothing.  The result does not depend on the order in
+ *     which the GPU runs the parts.  Asynchronous on `stream`, one launch,
+ *     launched like q2_gemv (all inputs are read after the previous kernel
+ *     has finished). */
+int q2_attend_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim, size_t* bytes);
+int q2_attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, const void* new_v, long long ldn,
+              const int* lens, int batch, int q_heads, float scale, void* out, long long ldo, void* ws,
+              size_t ws_bytes, q2_stream stream);
+
+#define Q2_ERR_LENGTH 0x100u    /* a sequence length outside its table row     */
+#define Q2_ERR_PAGE 0x200u      /* a page number outside the pools             */
+
+/* Device-side error word of the tensor-core (multi-token) and the attention
+ * kernels, then cleared: 0 in normal operation; Q2_ERR_LENGTH and Q2_ERR_PAGE
+ * as above; any other bit means a bounded wait on the tensor core ran out and the kernel skipped its work (the rows of the tiles
  * concerned are NaN).  Before such a kernel's CTA exits it waits, with the
  * full bound, for its copies and MMAs in flight, and it still meets the
  * other CTAs of its cluster at both of their barriers.  Synchronous: reads

@@ -22,6 +22,7 @@ Modules:
   fp16     -- the dense fp16 control
   int4     -- 4-bit weights with group scales
   norm     -- root-mean-square norm with the residual's addition
+  attend   -- attention of one new token over a paged key-value cache
   matvec   -- f64 reference product and the pass criterion
   rotate   -- the activation rotation x_rot = (H (x) Q)(S x) applied ahead
               of the GEMV ("Qwen3.8-27B on a 12 GB card", section "What

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 import synth
-from oracle import int4 as oint4, norm as onorm
+from oracle import attend as oatt, int4 as oint4, norm as onorm
 from tests import _blob
 
 
@@ -42,6 +42,47 @@ def test_norm_closed_forms():
     assert (h == 0).all() and np.isnan(y).all()                    # 0 / sqrt(0): eps is what avoids it
     q, s = onorm.quantise_f64(np.array([[0.0, 0.0], [2.54, -1.0]]))
     assert np.array_equal(q, [[0, 0], [127, -50]]) and s[0] == 0 and s[1] == 0.02
+
+
+def test_attend_closed_forms():
+    v = np.arange(12.0).reshape(3, 2, 2)
+    k = np.zeros((3, 2, 2))
+    q = np.ones((4, 2))
+    o, S, Q = oatt.attend_f64(q, k, v, 0.5)                        # equal scores: the mean
+    assert np.allclose(o[:2], v[:, 0].mean(0)) and np.allclose(o[2:], v[:, 1].mean(0)) and np.allclose(S, o) and (Q == 0).all()
+    k[1, 0] = np.log(2)                                            # head 0: weights 1, 2, 1 at scale 1/2
+    assert np.allclose(oatt.attend_f64(q, k, v, 0.5)[0][:2], (v[0, 0] + 2 * v[1, 0] + v[2, 0]) / 4)
+    assert (oatt.attend_f64(q, k[:0], v[:0], 0.5)[0] == 0).all()
+    pool = np.arange(8.0).reshape(4, 2, 1, 1)
+    assert oatt.gather(pool, np.array([3, 0]), 3).ravel().tolist() == [6, 7, 0]
+
+
+def test_attend_refusals(q2):
+    L = q2.load()
+    n = ctypes.c_size_t(0)
+    p = ctypes.c_void_p(1 << 20)                                                # never read
+    assert L.q2_attend_workspace_bytes(2, 7, 2, 128, ctypes.byref(n)) == -2     # heads do not divide
+    assert L.q2_attend_workspace_bytes(2, 8, 2, 96, ctypes.byref(n)) == -2
+    assert L.q2_attend_workspace_bytes(1025, 8, 2, 128, ctypes.byref(n)) == -2
+    assert L.q2_attend_workspace_bytes(2, 130, 2, 128, ctypes.byref(n)) == -2   # 65 heads to one
+    assert L.q2_attend_workspace_bytes(2, 8, 2, 128, None) == -1
+
+    def call(q=p, ldq=1024, nk=None, nv=None, ldn=0, lens=p, batch=2, heads=8, scale=0.1, out=p, ldo=1024, ws=p, wsb=1 << 30, **kv):
+        f = dict(k=p, v=p, page_stride=4096, token_stride=256, head_stride=128, npages=9, page_size=16, kv_heads=2,
+                 head_dim=128, table=p, table_stride=4, max_pages=4)
+        f.update(kv)
+        return L.q2_attend(ctypes.byref(q2._KV(**f)), q, ldq, nk, nv, ldn, lens, batch, heads, scale, out, ldo, ws, wsb, None)
+
+    odd = ctypes.c_void_p((1 << 20) + 8)
+    assert call(batch=0) == 0
+    assert call(q=None) == -1 and call(lens=None) == -1 and call(out=None) == -1 and call(k=None) == -1 and call(table=None) == -1
+    assert call(nk=p) == -1 and call(scale=float("inf")) == -1 and call(scale=float("nan")) == -1
+    assert call(page_size=0) == -2 and call(npages=-1) == -2 and call(ldq=1023) == -2 and call(ldo=8) == -2
+    assert call(table_stride=3) == -2 and call(nk=p, nv=p, ldn=8) == -2 and call(page_stride=-8) == -2
+    assert call(max_pages=1 << 28, table_stride=1 << 28) == -2                  # more tokens than 32 bits count
+    assert call(q=odd) == -3 and call(k=odd) == -3 and call(ldq=1028) == -3 and call(token_stride=260) == -3
+    assert call(lens=ctypes.c_void_p((1 << 20) + 2)) == -3
+    assert call(ws=None) == -7 and call(wsb=100) == -7 and call(ws=ctypes.c_void_p((1 << 20) + 16)) == -3
 
 
 def _codes(blob, R, C, group):
