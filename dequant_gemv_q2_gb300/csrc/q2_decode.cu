@@ -62,20 +62,19 @@ __global__ void k_dec_trellis(const unsigned char* stream, const uint32_t* table
 }
 
 // INT4: one thread per (row, column), s * (q - z).
-__global__ void k_dec_int4(const unsigned char* w, const __half* scale, const unsigned char* zero, float* out, int R,
-                           int C, int nblk, int group) {
+__global__ void k_dec_int4(const unsigned char* w, float* out, int R, int C, int nblk, int group, int zeros, int item) {
   const size_t n = (size_t)R * C;
   const int gpb = Q2_INT4_COLS / group;
   for (size_t e = blockIdx.x * (size_t)kThreads + threadIdx.x; e < n; e += (size_t)gridDim.x * kThreads) {
     const int r = (int)(e / C), c = (int)(e % C), cc = c % Q2_INT4_COLS, p = (r >> 3) & 1;
-    const size_t it = (size_t)(r >> 4) * nblk + c / Q2_INT4_COLS;
+    const unsigned char* it = w + ((size_t)(r >> 4) * nblk + c / Q2_INT4_COLS) * item;
+    const unsigned char* side = it + Q2_INT4_BLOCK_BYTES;
     const int j = (cc >> 3) & 3, t = (cc >> 5) * 2 + ((cc >> 2) & 1), k = cc & 3;
-    const unsigned char* at = w + it * Q2_INT4_BLOCK_BYTES + (t >> 2) * 512 + ((r & 7) * 4 + j) * 16 + (t & 3) * 4;
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(it + (t >> 2) * 512 + ((r & 7) * 4 + j) * 16 + (t & 3) * 4);
     const int nib = (k & 1) * 4 + (k >> 1) * 2 + p;
-    const size_t side = ((it * 8 + (r & 7)) * gpb + cc / group) * 2 + p;
-    const int q = (int)((v >> (4 * nib)) & 15), z = zero ? zero[side] : 8;
-    out[e] = __half2float(scale[side]) * (float)(q - z);
+    const int at = ((r & 7) * gpb + cc / group) * 2 + p;
+    const int q = (int)((v >> (4 * nib)) & 15), z = zeros ? side[gpb * 32 + at] : 8;
+    out[e] = __half2float(reinterpret_cast<const __half*>(side)[at]) * (float)(q - z);
   }
 }
 
@@ -150,10 +149,9 @@ extern "C" int q2_launch_decode(const q2_handle* h, void* out, void* stream) {
           d.Rpad);
       break;
     case Q2_INT4:
-      k_dec_int4<<<grid_for((size_t)d.R * d.C), kThreads, 0, st>>>(
-          h->dev + d.off[SEC_INT4_W], reinterpret_cast<const __half*>(h->dev + d.off[SEC_INT4_SCALE]),
-          d.len[SEC_INT4_ZERO] ? h->dev + d.off[SEC_INT4_ZERO] : nullptr, static_cast<float*>(out), d.R, d.C, d.nblock,
-          d.reserved);
+      k_dec_int4<<<grid_for((size_t)d.R * d.C), kThreads, 0, st>>>(h->dev + d.off[SEC_INT4_W], static_cast<float*>(out),
+                                                                   d.R, d.C, d.nblock, d.reserved, d.layout,
+                                                                   q2_int4_item(d.reserved, d.layout));
       break;
     case Q2_LEECH: {
       k_dec_leech<<<grid_for((size_t)d.R * d.nblock), kThreads, 0, st>>>(

@@ -353,13 +353,12 @@ int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero
   if (R < 1 || C < group || C % group) return Q2_ESHAPE;
   Builder b(Q2_INT4, R, C);
   const int nblk = (C + Q2_INT4_COLS - 1) / Q2_INT4_COLS, ntile = b.hdr.Rpad / 16, gpb = Q2_INT4_COLS / group, G = C / group;
-  const size_t nit = (size_t)ntile * nblk;
+  const int item = q2_int4_item(group, zero != nullptr);
   b.hdr.nslice = (C + Q2_SLICE - 1) / Q2_SLICE;
   b.hdr.nblock = nblk;
   b.hdr.reserved = group;
-  b.section(SEC_INT4_W, nit * Q2_INT4_BLOCK_BYTES);
-  b.section(SEC_INT4_SCALE, nit * 16 * gpb * 2);
-  b.section(SEC_INT4_ZERO, zero ? nit * 16 * gpb : 0);
+  b.hdr.layout = zero ? 1 : 0;
+  b.section(SEC_INT4_W, (size_t)ntile * nblk * item);
   if (out && zero)
     for (size_t i = 0; i < (size_t)R * G; ++i)
       if (zero[i] > 15) return Q2_EINVAL;
@@ -367,8 +366,6 @@ int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero
   int st = finish(b, out, out_bytes, &fill);
   if (st || !fill) return st;
   unsigned char* w = sec(out, b.hdr, SEC_INT4_W);
-  uint16_t* sc = reinterpret_cast<uint16_t*>(sec(out, b.hdr, SEC_INT4_SCALE));
-  unsigned char* zr = zero ? sec(out, b.hdr, SEC_INT4_ZERO) : nullptr;
   const uint8_t none[2] = {0x88, 0x88};          // q = 8 outside the matrix
   for (int rt = 0; rt < ntile; ++rt)
     for (int g = 0; g < 8; ++g) {                // rows rt*16 + g and + 8
@@ -376,21 +373,23 @@ int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero
       const uint8_t* c0 = r0 < R ? code + (size_t)r0 * (C / 2) : nullptr;
       const uint8_t* c1 = r1 < R ? code + (size_t)r1 * (C / 2) : nullptr;
       for (int blk = 0; blk < nblk; ++blk) {
-        const size_t it = (size_t)rt * nblk + blk;
+        unsigned char* it = w + ((size_t)rt * nblk + blk) * item;
+        unsigned char* side = it + Q2_INT4_BLOCK_BYTES;
         for (int k = 0; k < 32; ++k) {           // runs of 4 columns: lane part j, step t
           const int j = (k >> 1) & 3, t = (k >> 3) * 2 + (k & 1), c = blk * Q2_INT4_COLS + 4 * k;
           const uint32_t lo = int4_spread(c0 && c < C ? c0 + c / 2 : none), hi = int4_spread(c1 && c < C ? c1 + c / 2 : none);
           const uint32_t v = lo | hi << 4;
-          std::memcpy(w + it * Q2_INT4_BLOCK_BYTES + (t >> 2) * 512 + (g * 4 + j) * 16 + (t & 3) * 4, &v, 4);
+          std::memcpy(it + (t >> 2) * 512 + (g * 4 + j) * 16 + (t & 3) * 4, &v, 4);
         }
         for (int q = 0; q < gpb; ++q) {
           const int gi = blk * gpb + q;
           for (int p = 0; p < 2; ++p) {
             const int r = p ? r1 : r0;
-            const size_t at = ((it * 8 + g) * gpb + q) * 2 + p;
+            const int at = (g * gpb + q) * 2 + p;
             const bool in = r < R && gi < G;
-            sc[at] = in ? scale[(size_t)r * G + gi] : (uint16_t)0;
-            if (zr) zr[at] = in ? zero[(size_t)r * G + gi] : (uint8_t)8;
+            const uint16_t s = in ? scale[(size_t)r * G + gi] : (uint16_t)0;
+            std::memcpy(side + at * 2, &s, 2);
+            if (zero) side[gpb * 32 + at] = in ? zero[(size_t)r * G + gi] : (uint8_t)8;
           }
         }
       }
@@ -449,16 +448,14 @@ int q2_bind(const void* blob_host, const void* blob_dev, q2_handle** h) {
     return Q2_EBLOB;
   for (int i = 0; i < Q2_MAX_SECTIONS; ++i)
     if (hdr.len[i] && (hdr.off[i] % kAlign || hdr.off[i] + hdr.len[i] > hdr.total_bytes)) return Q2_EBLOB;
-  if (hdr.layout != 0 && !(hdr.fmt == Q2_LEECH && hdr.layout == Q2_LEECH_OFFSET4)) return Q2_EBLOB;
+  if (hdr.layout != 0 && !(hdr.fmt == Q2_LEECH && hdr.layout == Q2_LEECH_OFFSET4) && !(hdr.fmt == Q2_INT4 && hdr.layout == 1))
+    return Q2_EBLOB;
   if (hdr.fmt == Q2_INT4) {
     const int group = hdr.reserved;
     if ((group != 32 && group != 64 && group != 128) || hdr.C % group ||
         hdr.nblock != (hdr.C + Q2_INT4_COLS - 1) / Q2_INT4_COLS || hdr.nslice != (hdr.C + Q2_SLICE - 1) / Q2_SLICE)
       return Q2_EBLOB;
-    const uint64_t units = (uint64_t)(hdr.Rpad / 16) * hdr.nblock, sides = units * 16 * (Q2_INT4_COLS / group);
-    if (hdr.len[SEC_INT4_W] != units * Q2_INT4_BLOCK_BYTES || hdr.len[SEC_INT4_SCALE] != sides * 2 ||
-        (hdr.len[SEC_INT4_ZERO] && hdr.len[SEC_INT4_ZERO] != sides))
-      return Q2_EBLOB;
+    if (hdr.len[SEC_INT4_W] != (uint64_t)(hdr.Rpad / 16) * hdr.nblock * q2_int4_item(group, hdr.layout)) return Q2_EBLOB;
   }
   q2_handle* p = new (std::nothrow) q2_handle;
   if (!p) return Q2_ENOMEM;
@@ -518,7 +515,7 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* bytes) {
   const q2_blob_header& d = h->hdr;
   switch (d.fmt) {
     case Q2_FP16: *bytes = d.len[SEC_FP16_W]; break;
-    case Q2_INT4: *bytes = d.len[SEC_INT4_W] + d.len[SEC_INT4_SCALE] + d.len[SEC_INT4_ZERO]; break;
+    case Q2_INT4: *bytes = d.len[SEC_INT4_W]; break;
     case Q2_BPDQ:
       // batch 1 reads (c0, c1, off); the multi-token path reads the value table
       *bytes = d.len[SEC_BPDQ_BITS] + (ntok == 1 ? d.len[SEC_BPDQ_C01] + d.len[SEC_BPDQ_OFF]

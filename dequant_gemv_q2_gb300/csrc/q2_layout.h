@@ -26,7 +26,7 @@
 // Section indices per format.
 enum { SEC_FP16_W = 0 };
 enum { SEC_BPDQ_BITS = 0, SEC_BPDQ_C01 = 1, SEC_BPDQ_OFF = 2, SEC_BPDQ_VTAB = 3 };
-enum { SEC_INT4_W = 0, SEC_INT4_SCALE = 1, SEC_INT4_ZERO = 2 };
+enum { SEC_INT4_W = 0 };
 enum { SEC_TRL_STREAM = 0, SEC_TRL_TABLE = 1, SEC_TRL_SCALE = 2 };
 enum { SEC_LEECH_PLANES = 0, SEC_LEECH_PARITY = 1, SEC_LEECH_SCALE = 2, SEC_LEECH_TAIL = 3,
        SEC_LEECH_EXCPTR = 4, SEC_LEECH_EXCCOL = 5 };
@@ -47,7 +47,7 @@ struct q2_blob_header {
   uint64_t total_bytes;
   uint64_t off[Q2_MAX_SECTIONS];
   uint64_t len[Q2_MAX_SECTIONS];
-  int32_t layout;     // Leech: Q2_LEECH_PLANES3 or Q2_LEECH_OFFSET4; 0 otherwise
+  int32_t layout;     // Leech: Q2_LEECH_PLANES3 or Q2_LEECH_OFFSET4; INT4: 1 with zero points; 0 otherwise
   int32_t reserved;   // INT4: columns per scale group (32, 64 or 128); 0 otherwise
 };
 
@@ -60,11 +60,16 @@ struct q2_blob_header {
 // Trellis: 16 little-endian words per lane; nibble n (0..127) of the lane's
 //         64 bytes holds symbol 127 - n of the segment, so the state of step
 //         k is the 16 bits at bit offset 4*(127 - k), wrapping modulo 512.
-// INT4:   unit of 16 rows x 128 columns, index it = (row / 16) * nblock + block:
-//         weights 1024 bytes at it*1024: half u, lane, 16 bytes; word i of
-//         lane l = 4*(row % 8) + j is step t = 4*u + i and holds the four
-//         columns 32*(t / 2) + 8*j + 4*(t % 2) + 0..3: from the lowest four
-//         bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, of rows (row % 8) and
-//         (row % 8) + 8 in turn.
-//         Scales (fp16) and zero points (bytes): [it][row % 8][group of the
-//         block][row / 8 % 2].  Rows past R and columns past C hold q = z = 8.
+// INT4:   unit of 16 rows x 128 columns, index it = (row / 16) * nblock + block,
+//         q2_int4_item() bytes each: weights 1024 bytes (half u, lane, 16
+//         bytes; word i of lane l = 4*(row % 8) + j is step t = 4*u + i and
+//         holds the four columns 32*(t / 2) + 8*j + 4*(t % 2) + 0..3: from the
+//         lowest four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, of rows
+//         (row % 8) and (row % 8) + 8 in turn); then scales (fp16) and, where
+//         the matrix has them, zero points (bytes), both in the order
+//         [row % 8][group of the block][row / 8 % 2].  Rows past R and columns
+//         past C hold q = z = 8.
+static inline int q2_int4_item(int group, int zeros) {
+  const int groups = Q2_INT4_COLS / group;
+  return Q2_INT4_BLOCK_BYTES + groups * 32 + (zeros ? groups * 16 : 0);
+}

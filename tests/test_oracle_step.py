@@ -89,9 +89,10 @@ def _codes(blob, R, C, group):
     """(code values, zero points) read back from the packed layout, one element at a time."""
     h = _blob.header(blob)
     nblk, gpb = int(h["nblock"]), 128 // group
-    w = _blob.section(blob, 0).view("<u4").reshape(-1, 2, 32, 4)
-    sc = _blob.section(blob, 1).view(np.float16).reshape(-1, 8, gpb, 2)
-    zr = _blob.section(blob, 2).reshape(-1, 8, gpb, 2) if h["len"][2] else None
+    items = _blob.section(blob, 0).reshape(-1, 1024 + gpb * 32 + (gpb * 16 if h["layout"] else 0))
+    w = items[:, :1024].copy().view("<u4").reshape(-1, 2, 32, 4)
+    sc = items[:, 1024: 1024 + gpb * 32].copy().view(np.float16).reshape(-1, 8, gpb, 2)
+    zr = items[:, 1024 + gpb * 32:].reshape(-1, 8, gpb, 2) if h["layout"] else None
     order = [0, 0, 2, 2, 1, 1, 3, 3]
     q = np.zeros((R, C), dtype=np.int64)
     s = np.zeros((R, C // group), dtype=np.float16)
@@ -140,7 +141,7 @@ def test_int4_pack_and_bind_refusals(q2):
     assert e.value.status == -2
     blob = q2.q2_pack_int4(d["code"], d["scale"], d["zero"], 64)
     h, dev, x = ctypes.c_void_p(), ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
-    for field, value in (("reserved", 48), ("nblock", 9), ("nslice", 7)):
+    for field, value in (("reserved", 48), ("nblock", 9), ("nslice", 7), ("layout", 0), ("layout", 2)):
         bad = blob.copy()
         hdr = np.frombuffer(bad[:_blob.HEADER.itemsize].tobytes(), dtype=_blob.HEADER).copy()
         hdr[field] = value
@@ -148,7 +149,7 @@ def test_int4_pack_and_bind_refusals(q2):
         assert L.q2_bind(bad.ctypes.data, dev, ctypes.byref(h)) == -6, field
     assert L.q2_bind(blob.ctypes.data, dev, ctypes.byref(h)) == 0
     assert L.q2_workspace_bytes(h, 64, N) == 0 and n.value == 0
-    assert L.q2_bytes(h, 1, N) == 0 and n.value == 1024 * 2 + 2 * 64 + 2 * 32        # Rpad 32: two row tiles
+    assert L.q2_bytes(h, 1, N) == 0 and n.value == 2 * (1024 + 64 + 32)              # Rpad 32: two row tiles
     assert L.q2_gemv(1, h, x, x, 1, None) == -4
     assert L.q2_gemv(5, h, x, x, 65, None) == -5
     assert L.q2_gemv(5, h, ctypes.c_void_p((1 << 21) + 8), x, 1, None) == -3
