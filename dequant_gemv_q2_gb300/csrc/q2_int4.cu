@@ -25,9 +25,8 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
-#include <mutex>
-#include <utility>
-#include <vector>
+#include <algorithm>
+#include <type_traits>
 
 #include "q2_common.cuh"
 
@@ -57,12 +56,6 @@ struct Sides {
 // for weights requested after it; 19.1 us instead of 10.3 at 24576 x 4096).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char* src, int item, int lane) {
-  cp16(dst + lane * 16, src + lane * 16);
-  cp16(dst + 512 + lane * 16, src + 512 + lane * 16);
-  if (lane * 16 < item - 1024) cp16(dst + 1024 + lane * 16, src + 1024 + lane * 16);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -157,6 +150,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Four 8-bit integers as two pairs of fp16: the byte plus 128 in the mantissa
 // of 1024, minus 1152.
 __device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
@@ -193,7 +192,7 @@ struct XVec<true> {
   using T = uint2;
 };
 
-// ------------------------------------------------------- up to 8 tokens
+// ------------------------------------------------------- 1 and 2 tokens
 // At one token a block's 2048 weights have to pass in about 50 cycles per SM,
 // so instructions are what is scarce.  Here the four bits are used as they
 // are: in the lowest bits of an fp16 number they are the subnormal q * 2^-24
@@ -204,177 +203,183 @@ struct XVec<true> {
 // with the sums of x over each group computed once per CTA (as a product with
 // ones).  Both terms are of the size of the result, so nothing is lost.
 //
-// A CTA's warps split the columns of MT row tiles (16 rows each) and keep
-// their column range over all row tiles that the CTA takes (every
-// gridDim.x-th), so the weight stream of a warp never stops: its ring of
-// STAGES blocks is filled across the ends of row tiles, the first of them
-// before the wait on the previous kernel.  x goes straight from L1 to
-// registers.  At a row tile's end the warps leave their sums in one of two
-// shared-memory buffers and the first threads add them in warp order: one
-// barrier per row tile, no atomics.
-constexpr int kFewWarps = 8;
+// A CTA's warps split the columns of a row tile (16 rows) and keep their
+// column range over all row tiles that the CTA takes (every gridDim.x-th): a
+// warp's share of x stays in shared memory, and its weight stream never
+// stops: its ring of pairs of blocks is filled across the ends of row tiles,
+// the first of them before the wait on the previous kernel.  At a row tile's
+// end the warps leave their sums in one of two shared-memory buffers and the
+// first threads add them in warp order: one barrier per row tile, no atomics.
+#ifndef MS
+#define MS 3
+#endif
+#ifndef MC
+#define MC 3
+#endif
+constexpr int kFewWarps = 8, kFewTok = 2, kFewStages = 3, kFewCtas = 2;
+constexpr int kFewRed = 2 * kFewWarps * kFewTok * 16 * 4;
 
-// A lane's share of x in one block: its columns of one token (any token where
-// there are fewer: a column of the product that is not stored).
-template <bool X8>
-__device__ __forceinline__ void few_b(uint32_t (&b)[16], const unsigned char* p, int runs) {
-  using V = typename XVec<X8>::T;
-  if (runs >= 4) {
-    load_b<X8>(b, [&](int k) { return *reinterpret_cast<const V*>(p + k * (X8 ? 32 : 64)); });
-  } else {                                          // the last block of a C that 128 does not divide
-    load_b<X8>(b, [&](int k) { return k < runs ? *reinterpret_cast<const V*>(p + k * (X8 ? 32 : 64)) : V{}; });
-  }
-}
-
-template <int MT, int GPB>
-__host__ __device__ constexpr int few_stages() { return 8 / MT; }
-template <int MT>
-__host__ __device__ constexpr int few_ld() { return 16 * MT + 4; }   // floats per token in a buffer: conflict-free writes
-template <int MT>
-__host__ __device__ constexpr int few_red_bytes() { return 2 * kFewWarps * 8 * few_ld<MT>() * 4; }
-
-// red, then a ring of blocks per warp, then the sums of x
-template <int MT, int GPB>
+// The buffers, then a ring of pairs of blocks per warp, x by blocks and tokens
+// (whole blocks, zeros past C), the sums of x.
+template <int GPB, bool X8>
 int few_smem(const Int4Args& a, int nwarp) {
-  return few_red_bytes<MT>() + nwarp * few_stages<MT, GPB>() * MT * a.item + a.nblk * GPB * 32;
+  return kFewRed + nwarp * kFewStages * 2 * a.item + a.nblk * (a.ntok * 128 * (X8 ? 1 : 2) + GPB * kFewTok * 4);
 }
 
-template <int MT, int GPB, bool X8>
-__global__ void __launch_bounds__(kFewWarps * 32, 2) k_int4_few(const __grid_constant__ Int4Args a) {
-  constexpr int LD = few_ld<MT>(), RED = few_red_bytes<MT>();
-  constexpr int esz = X8 ? 1 : 2, STEPS = 8 / GPB, STAGES = few_stages<MT, GPB>();
+template <int GPB, bool Z, bool X8>
+__global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __grid_constant__ Int4Args a) {
+  constexpr int esz = X8 ? 1 : 2, STEPS = 8 / GPB, XB = 128 * esz;      // bytes of x in a block
+  constexpr int ITEM = Q2_INT4_BLOCK_BYTES + GPB * (Z ? 48 : 32), STAGE = 2 * ITEM;
   extern __shared__ __align__(16) unsigned char q2_int4_smem[];
-  float* red = reinterpret_cast<float*>(q2_int4_smem);      // [2][kFewWarps][8 * LD]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
   const int g = lane >> 2, j = lane & 3;
   const int b0 = a.nblk * warp / nwarp, nb = a.nblk * (warp + 1) / nwarp - b0;   // nwarp <= nblk: nb >= 1
-  const int nunit = (a.ntile + MT - 1) / MT;                // row tiles in bundles of MT
-  const int mine = (nunit - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int n = mine * nb;                                  // blocks (times MT) of this warp's stream
-  const uint32_t ring = saddr(q2_int4_smem) + RED + warp * (STAGES * MT * a.item);
-  float* sums = reinterpret_cast<float*>(q2_int4_smem + RED + nwarp * (STAGES * MT * a.item));   // [nblk][GPB][8 tokens]
+  const int mine = (a.ntile - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  float* red = reinterpret_cast<float*>(q2_int4_smem);      // [2][kFewWarps][kFewTok][16]
+  const uint32_t ring = saddr(q2_int4_smem) + kFewRed + warp * (kFewStages * STAGE);
+  unsigned char* xs = q2_int4_smem + kFewRed + nwarp * (kFewStages * STAGE) + b0 * (a.ntok * XB);   // this warp's x
+  float* sums = reinterpret_cast<float*>(xs + (a.nblk - b0) * (a.ntok * XB)) + b0 * (GPB * kFewTok);
 
-  // the stream: block fb of the warp's range in bundle `unit`
-  int left = n, fb = 0, unit = blockIdx.x;
-  uint32_t fslot = ring;
-  const unsigned char* src = a.w + ((size_t)unit * MT * a.nblk + b0) * a.item;
+  // the stream: pairs of blocks (the last of a row tile may be one block)
+  int left = mine, fb = 0;                                  // row tiles to load; block of the row tile at `src`
+  uint32_t fslot = ring + lane * 16;
+  const size_t jump = ((size_t)gridDim.x * a.nblk - nb) * ITEM;
+  const unsigned char* src = a.w + ((size_t)blockIdx.x * a.nblk + b0) * ITEM + lane * 16;
   auto fetch = [&]() {
     if (left > 0) {
-      --left;
+      const int bytes = fb + 1 < nb ? STAGE : ITEM;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)                          // a missing row tile repeats the one before; its rows are not stored
-        copy_block(fslot + m * a.item, src + (m && unit * MT + m < a.ntile ? (size_t)m * a.nblk * a.item : 0), a.item, lane);
-      src += a.item;
-      fslot += MT * a.item;
-      if (fslot == ring + STAGES * MT * a.item) fslot = ring;
-      if (++fb == nb) {
+      for (int k = 0; k < STAGE; k += 512)
+        if (lane * 16 + k < bytes) cp16(fslot + k, src + k);
+      src += bytes;
+      fslot = fslot == ring + (kFewStages - 1) * STAGE + lane * 16 ? ring + lane * 16 : fslot + STAGE;
+      fb += 2;
+      if (fb >= nb) {
         fb = 0;
-        unit += gridDim.x;
-        src = a.w + ((size_t)unit * MT * a.nblk + b0) * a.item;
+        src += jump;
+        --left;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
-  for (int d = 0; d < STAGES - 1; ++d) fetch();
+  for (int d = 0; d < kFewStages - 1; ++d) fetch();
 
   pdl_wait();                                               // x may come from the previous kernel
   pdl_trigger();
-  const unsigned char* xp = static_cast<const unsigned char*>(a.x) + ((size_t)min(g, a.ntok - 1) * a.C + b0 * 128 + j * 8) * esz;
+  for (int e = lane; e < nb * a.ntok * (XB / 16); e += 32) {
+    const int p = e % (XB / 16), kt = e / (XB / 16), k = a.ntok == 2 ? kt >> 1 : kt, t = kt - k * a.ntok;
+    const int c = (b0 + k) * 128 + p * (16 / esz);
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + ((size_t)t * a.C + c) * esz);
+    reinterpret_cast<uint4*>(xs)[e] = c < a.C ? *from : make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
+  // A lane's columns of one token (token g, of two: the other columns of the
+  // products repeat them and are not stored).
+  const uint32_t xl = saddr(xs) + (g & (a.ntok - 1)) * XB + j * (8 * esz);
+  const int xblk = a.ntok * XB;
+  auto xload = [&](uint32_t(&b)[16], uint32_t from) {
+    load_b<X8>(b, [&](int r) {
+      if constexpr (X8) return lds64(from + r * (32 * esz));
+      else return lds128(from + r * (32 * esz));
+    });
+  };
   for (int k = 0; k < nb; ++k) {
     uint32_t b[16];
-    few_b<X8>(b, xp + k * (128 * esz), (a.C - (b0 + k) * 128) / 32);
+    xload(b, xl + k * xblk);
     const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
     for (int q = 0; q < GPB; ++q) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[4];
 #pragma unroll
-      for (int t = 0; t < STEPS; ++t) mma(c, one, b[2 * (q * STEPS + t)], b[2 * (q * STEPS + t) + 1]);
-      if (g == 0) *reinterpret_cast<float2*>(sums + ((b0 + k) * GPB + q) * 8 + 2 * j) = make_float2(c[0], c[1]);
+      for (int t = 0; t < STEPS; ++t) {
+        const int st = q * STEPS + t;
+        if (t == 0) mma_first(c, one, b[2 * st], b[2 * st + 1]);
+        else mma(c, one, b[2 * st], b[2 * st + 1]);
+      }
+      if (lane == 0) *reinterpret_cast<float2*>(sums + (k * GPB + q) * kFewTok) = make_float2(c[0], c[1]);
     }
   }
   __syncwarp();
-  const float xsc0 = X8 && 2 * j < a.ntok ? a.xs[2 * j] : 1.f, xsc1 = X8 && 2 * j + 1 < a.ntok ? a.xs[2 * j + 1] : 1.f;
+  const float xsc0 = X8 ? a.xs[0] : 1.f, xsc1 = X8 && a.ntok > 1 ? a.xs[1] : 1.f;
 
-  float acc[MT][4];
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  // K blocks at `from`, columns from block b on: K independent chains of products
+  auto use = [&](auto kc, uint32_t from, int blk) {
+    constexpr int K = decltype(kc)::value;
+    const uint32_t xat = xl + blk * xblk;
+    const float* sat = sums + blk * (GPB * kFewTok);
+    uint32_t b[K][16];
+    uint4 w[K][2];
+    Sides<GPB> sd[K];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-  int cb = 0, cu = 0;                                       // block and bundle in use
-  uint32_t slot = ring;
-  for (int i = 0; i < n; ++i) {
-    uint32_t b[16];
-    few_b<X8>(b, xp + cb * (128 * esz), (a.C - (b0 + cb) * 128) / 32);
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    __syncwarp();                                           // block i has arrived for all lanes, block i - 1 is done with
-    fetch();
-    uint4 w[MT][2];
-    Sides<GPB> sd[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      w[m][0] = lds128(slot + m * a.item + lane * 16);
-      w[m][1] = lds128(slot + m * a.item + 512 + lane * 16);
-      load_sides(sd[m], slot + m * a.item, a.zeros, g);
+    for (int k = 0; k < K; ++k) {
+      w[k][0] = lds128(from + k * ITEM + lane * 16);
+      w[k][1] = lds128(from + k * ITEM + 512 + lane * 16);
+      load_sides(sd[k], from + k * ITEM, Z, g);
+      xload(b[k], xat + k * xblk);
     }
-    slot += MT * a.item;
-    if (slot == ring + STAGES * MT * a.item) slot = ring;
 #pragma unroll
     for (int q = 0; q < GPB; ++q) {
-      float c[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+      float c[K][4];
 #pragma unroll
       for (int t = 0; t < STEPS; ++t) {
         const int st = q * STEPS + t;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t v = word(w[m][st >> 2], st & 3), v8 = v >> 8;
+        for (int k = 0; k < K; ++k) {
+          const uint32_t v = word(w[k][st >> 2], st & 3), v8 = v >> 8;
           const uint32_t A[4] = {v & 0x000f000fu, v & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u};
-          mma(c[m], A, b[2 * st], b[2 * st + 1]);
+          if (t == 0) mma_first(c[k], A, b[k][2 * st], b[k][2 * st + 1]);
+          else mma(c[k], A, b[k][2 * st], b[k][2 * st + 1]);
         }
       }
-      const float2 X = *reinterpret_cast<const float2*>(sums + ((b0 + cb) * GPB + q) * 8 + 2 * j);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
-        const uint32_t zz = sd[m].z[q >> 1] >> (16 * (q & 1));
-        const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
-        acc[m][0] = fmaf(sc.x, fmaf(c[m][0], 16777216.f, -z0 * X.x), acc[m][0]);
-        acc[m][1] = fmaf(sc.x, fmaf(c[m][1], 16777216.f, -z0 * X.y), acc[m][1]);
-        acc[m][2] = fmaf(sc.y, fmaf(c[m][2], 1048576.f, -z1 * X.x), acc[m][2]);
-        acc[m][3] = fmaf(sc.y, fmaf(c[m][3], 1048576.f, -z1 * X.y), acc[m][3]);
+      for (int k = 0; k < K; ++k) {
+        const float2 X = *reinterpret_cast<const float2*>(sat + (k * GPB + q) * kFewTok);
+        const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[k].s[q]));
+        const uint32_t zz = sd[k].z[q >> 1] >> (16 * (q & 1));
+        const float z0 = Z ? (float)(zz & 0xffu) : 8.f, z1 = Z ? (float)((zz >> 8) & 0xffu) : 8.f;
+        acc[0] = fmaf(sc.x, fmaf(c[k][0], 16777216.f, -z0 * X.x), acc[0]);
+        acc[1] = fmaf(sc.x, fmaf(c[k][1], 16777216.f, -z0 * X.y), acc[1]);
+        acc[2] = fmaf(sc.y, fmaf(c[k][2], 1048576.f, -z1 * X.x), acc[2]);
+        acc[3] = fmaf(sc.y, fmaf(c[k][3], 1048576.f, -z1 * X.y), acc[3]);
       }
     }
-    if (++cb == nb) {                                       // the bundle's end
-      float* r = red + ((cu & 1) * kFewWarps + warp) * (8 * LD);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        r[(2 * j) * LD + 16 * m + g] = acc[m][0] * xsc0;
-        r[(2 * j + 1) * LD + 16 * m + g] = acc[m][1] * xsc1;
-        r[(2 * j) * LD + 16 * m + g + 8] = acc[m][2] * xsc0;
-        r[(2 * j + 1) * LD + 16 * m + g + 8] = acc[m][3] * xsc1;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[m][q] = 0.f;
-      }
-      __syncthreads();
-      const int row0 = ((int)blockIdx.x + cu * (int)gridDim.x) * MT * 16;
-      for (int e = threadIdx.x; e < a.ntok * MT * 16; e += blockDim.x) {
-        const int t = e / (MT * 16), rr = e % (MT * 16);
-        float v = 0.f;
-        for (int k = 0; k < nwarp; ++k) v += red[((cu & 1) * kFewWarps + k) * (8 * LD) + t * LD + rr];
-        if (row0 + rr < a.R) a.y[(size_t)t * a.R + row0 + rr] = __float2half_rn(v);
-      }
-      cb = 0;
-      ++cu;
+  };
+  uint32_t slot = ring;
+  for (int u = 0; u < mine; ++u) {
+    for (int cb = 0; cb < nb; cb += 2) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
+      __syncwarp();                                         // the pair has arrived for all lanes, the one before is done with
+      fetch();
+      if (cb + 1 < nb) use(std::integral_constant<int, 2>(), slot, cb);
+      else use(std::integral_constant<int, 1>(), slot, cb);
+      slot = slot == ring + (kFewStages - 1) * STAGE ? ring : slot + STAGE;
+    }
+    float* r = red + ((u & 1) * kFewWarps + warp) * (kFewTok * 16);
+    if (j == 0) {                                           // tokens 0 and 1
+      r[g] = acc[0] * xsc0;
+      r[16 + g] = acc[1] * xsc1;
+      r[g + 8] = acc[2] * xsc0;
+      r[16 + g + 8] = acc[3] * xsc1;
+    }
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    __syncthreads();
+    const int row = ((int)blockIdx.x + u * (int)gridDim.x) * 16 + (threadIdx.x & 15), t = threadIdx.x >> 4;
+    if (t < a.ntok && row < a.R) {
+      float v = 0.f;
+      for (int k = 0; k < nwarp; ++k) v += red[((u & 1) * kFewWarps + k) * (kFewTok * 16) + threadIdx.x];
+      a.y[(size_t)t * a.R + row] = __float2half_rn(v);
     }
   }
 }
 
-// ------------------------------------------------------- 9..64 tokens
-// A CTA takes 128 rows and a range of 256-column stages.  Its eight warps are
-// four pairs of row tiles times the two 128-column blocks of a stage.  x of
-// all tokens (a token's row is padded so that the lanes that load together
+// ------------------------------------------------------- 3..64 tokens
+// A CTA takes 128 rows and a range of 128-column blocks.  Its eight warps are
+// two groups of four, which take alternate blocks and run on their own (the
+// two warps of a scheduler belong to different groups, so one unpacks while
+// the other multiplies); each warp of a group has two row tiles.  A group's x
+// of all tokens (a token's row is padded so that the lanes that load together
 // fall on different banks) and each warp's own weights come through a ring of
 // shared-memory stages by asynchronous 16-byte copies.  A block's A operands
 // (here q - z itself: the tensor cores, not the instructions, are what is
@@ -382,62 +387,86 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) k_int4_few(const __grid_con
 // and two row tiles at a time, so that four chains of dependent products are
 // in flight.  When the column range is split over CTAs, they form a cluster
 // and add their fp32 sums through distributed shared memory in rank order.
-constexpr int kManyWarps = 8, kManyRows = 128, kManyStages = 3;
+#ifndef INT4_SUB
+#define INT4_SUB 1
+#endif
+constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
-__host__ __device__ constexpr int x_row_bytes() { return X8 ? 256 + 32 : 512 + 64; }
+__host__ __device__ constexpr int x_row_bytes() { return X8 ? 128 + 32 : 256 + 64; }
+template <int NT>
+__host__ __device__ constexpr int many_stages() { return NT == 8 || NT == 2 ? 3 : NT == 1 ? MS : 4; }
+template <int NT>
+__host__ __device__ constexpr int many_ctas() { return NT == 1 ? MC : NT <= 2 ? 2 : 1; }   // per SM
 
 constexpr int kOutLd = kManyRows + 4;
 
 template <int NT, bool X8>
 int many_smem(const Int4Args& a) {
-  const int ring = kManyStages * (NT * 8 * x_row_bytes<X8>() + kManyWarps * 2 * a.item), out = NT * 8 * kOutLd * 4;
+  const int ring = 2 * many_stages<NT>() * (NT * 8 * x_row_bytes<X8>() + 8 * a.item), out = NT * 8 * kOutLd * 4;
   return ring > out ? ring : out;
 }
 
-template <int NT, int GPB, bool X8>
-__global__ void __launch_bounds__(kManyWarps * 32, 1) k_int4_many(const __grid_constant__ Int4Args a, const int nsplit) {
-  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB;
-  constexpr int esz = X8 ? 1 : 2, PIECES = 256 * esz / 16;
+template <int NT, int GPB, bool X8, bool SUB>
+__global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
+    k_int4_many(const __grid_constant__ Int4Args a, const int nsplit) {
+  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB, STAGES = many_stages<NT>();
+  constexpr int esz = X8 ? 1 : 2, PIECES = 128 * esz / 16, PASS = 128 / PIECES;   // pieces of a row; tokens of a pass
+  constexpr int HT = NT == 1 ? 1 : 2;                       // tiles of 8 tokens at a time
   extern __shared__ __align__(16) unsigned char q2_int4_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, j = lane & 3, wm = warp & 3, wk = warp >> 2;
   const int rank = (int)blockIdx.x % nsplit, tile0 = (int)blockIdx.x / nsplit * (kManyRows / 16) + wm * MT;
-  const int nstage = (a.nblk + 1) / 2;
-  const int s0 = nstage * rank / nsplit, n = nstage * (rank + 1) / nsplit - s0;   // stages of this CTA
-  const uint32_t sx = saddr(q2_int4_smem), sw = sx + kManyStages * (NTOK * ROWB) + warp * (MT * a.item);
-  const int wstage = kManyWarps * MT * a.item;
+  const int b0 = a.nblk * rank / nsplit + wk, n = (a.nblk * (rank + 1) / nsplit - b0 + 1) / 2;   // this group: b0, b0 + 2, ..
+  const int stage = NTOK * ROWB + 8 * a.item;
+  const uint32_t ring = saddr(q2_int4_smem) + wk * (STAGES * stage);
 
-  auto weights = [&](int i) {
-    if (i < n) {
-      const int blk = min(2 * (s0 + i) + wk, a.nblk - 1);   // past the last block: any block, its x is zero
+  const unsigned char* wsrc[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)                          // a missing row tile: any; its rows are not stored
-        copy_block(sw + (i % kManyStages) * wstage + m * a.item,
-                   a.w + ((size_t)min(tile0 + m, a.ntile - 1) * a.nblk + blk) * a.item, a.item, lane);
+  for (int m = 0; m < MT; ++m)                              // a missing row tile: the last one; its rows are not stored
+    wsrc[m] = a.w + ((size_t)min(tile0 + m, a.ntile - 1) * a.nblk + b0) * a.item + lane * 16;
+  const bool sides = lane * 16 < a.item - 1024;
+  const uint32_t wdst = ring + NTOK * ROWB + wm * MT * a.item + lane * 16;
+  auto weights = [&](int i, int st) {
+    if (i < n) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint32_t d = wdst + st * stage + m * a.item;
+        cp16(d, wsrc[m]);
+        cp16(d + 512, wsrc[m] + 512);
+        if (sides) cp16(d + 1024, wsrc[m] + 1024);
+        wsrc[m] += 2 * a.item;
+      }
     }
   };
-  auto xstage = [&](int i) {
+  const int xp = (threadIdx.x & 127) % PIECES, xt = (threadIdx.x & 127) / PIECES;   // this thread's piece and first token
+  const unsigned char* xsrc = static_cast<const unsigned char*>(a.x) + ((size_t)xt * a.C + b0 * 128) * esz + xp * 16;
+  const size_t xpass = (size_t)PASS * a.C * esz;
+  const uint32_t xdst = ring + xt * ROWB + xp * 16;
+  int xleft = a.C - b0 * 128 - xp * (16 / esz);             // columns from this piece to the end of the row
+  auto xstage = [&](int i, int st) {
     if (i < n) {
-      const uint32_t base = sx + (i % kManyStages) * (NTOK * ROWB);
-      for (int e = threadIdx.x; e < NTOK * PIECES; e += kManyWarps * 32) {
-        const int t = e / PIECES, p = e % PIECES;
-        const int c = (s0 + i) * 256 + p * (16 / esz);
-        const bool live = t < a.ntok && c < a.C;
-        const unsigned char* from = static_cast<const unsigned char*>(a.x) + (live ? ((size_t)t * a.C + c) * esz : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + t * ROWB + p * 16), "l"(from),
-                     "r"(live ? 16 : 0)
-                     : "memory");
+      const unsigned char* from = xsrc;
+#pragma unroll
+      for (int t = 0; t < NTOK; t += PASS) {
+        const bool live = xt + t < a.ntok && xleft > 0;
+        if (PASS <= NTOK || xt + t < NTOK)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(xdst + st * stage + t * ROWB),
+                       "l"(live ? from : static_cast<const unsigned char*>(a.x)), "r"(live ? 16 : 0)
+                       : "memory");
+        from += xpass;
       }
+      xsrc += 256 * esz;
+      xleft -= 256;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int d = 0; d < kManyStages - 1; ++d) weights(d);
+  for (int d = 0; d < STAGES - 1; ++d) weights(d, d);
   pdl_wait();                                               // x may come from the previous kernel
   pdl_trigger();
 #pragma unroll
-  for (int d = 0; d < kManyStages - 1; ++d) xstage(d);
+  for (int d = 0; d < STAGES - 1; ++d) xstage(d, d);
 
   float acc[MT][NT][4];
 #pragma unroll
@@ -447,59 +476,112 @@ __global__ void __launch_bounds__(kManyWarps * 32, 1) k_int4_many(const __grid_c
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
 
+  int st = 0, last = STAGES - 1;                            // stage in use, stage before it (free)
   for (int i = 0; i < n; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kManyStages - 2) : "memory");
-    __syncthreads();                                        // stage i has arrived for all, stage i - 1 is free
-    weights(i + kManyStages - 1);
-    xstage(i + kManyStages - 1);
-    uint32_t A[MT][8][4];
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + wk) : "memory");   // block i has arrived for the group, block i - 1 is done with
+    weights(i + STAGES - 1, last);
+    xstage(i + STAGES - 1, last);
     Sides<GPB> sd[MT];
+    const uint32_t base = ring + st * stage, xb = base + g * ROWB + j * (8 * esz);
+    auto xload = [&](uint32_t(&b)[16], int t) {
+      load_b<X8>(b, [&](int k) {
+        const uint32_t at = xb + t * 8 * ROWB + k * (32 * esz);
+        if constexpr (X8) return lds64(at);
+        else return lds128(at);
+      });
+    };
+    uint4 w[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint32_t at = sw + (i % kManyStages) * wstage + m * a.item;
-      const uint4 w[2] = {lds128(at + lane * 16), lds128(at + 512 + lane * 16)};
+      const uint32_t at = base + NTOK * ROWB + (wm * MT + m) * a.item;
+      w[m][0] = lds128(at + lane * 16);
+      w[m][1] = lds128(at + 512 + lane * 16);
       load_sides(sd[m], at, a.zeros, g);
-      unpack(w, sd[m], A[m]);
     }
-    const uint32_t xb = sx + (i % kManyStages) * (NTOK * ROWB) + g * ROWB + wk * (128 * esz) + j * (8 * esz);
+    if constexpr (SUB) {
+      const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+      uint32_t b[NT][16];
 #pragma unroll
-    for (int t = 0; t < NT; t += 2) {
-      uint32_t b[2][16];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        load_b<X8>(b[h], [&](int k) {
-          const uint32_t at = xb + (t + h) * 8 * ROWB + k * (32 * esz);
-          if constexpr (X8) return lds64(at);
-          else return lds128(at);
-        });
+      for (int t = 0; t < NT; ++t) xload(b[t], t);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
-        float c[MT][2][4];
+        float c[MT][NT][4], X[NT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int k = q * STEPS; k < (q + 1) * STEPS; ++k) {
+          uint32_t A[MT][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) c[m][h][0] = c[m][h][1] = c[m][h][2] = c[m][h][3] = 0.f;
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t v = word(w[m][k >> 2], k & 3), v8 = v >> 8;
+            A[m][0] = v & 0x000f000fu;
+            A[m][1] = v & 0x00f000f0u;
+            A[m][2] = v8 & 0x000f000fu;
+            A[m][3] = v8 & 0x00f000f0u;
+          }
 #pragma unroll
-        for (int st = q * STEPS; st < (q + 1) * STEPS; ++st)
+          for (int t = 0; t < NT; ++t) {
+            if (k == q * STEPS) mma_first(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
+            else mma(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) mma(c[m][h], A[m][st], b[h][2 * st], b[h][2 * st + 1]);
+            for (int m = 0; m < MT; ++m) {
+              if (k == q * STEPS) mma_first(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
+              else mma(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
+            }
+          }
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
+          const uint32_t zz = sd[m].z[q >> 1] >> (16 * (q & 1));
+          const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            acc[m][t + h][0] = fmaf(sc.x, c[m][h][0], acc[m][t + h][0]);
-            acc[m][t + h][1] = fmaf(sc.x, c[m][h][1], acc[m][t + h][1]);
-            acc[m][t + h][2] = fmaf(sc.y, c[m][h][2], acc[m][t + h][2]);
-            acc[m][t + h][3] = fmaf(sc.y, c[m][h][3], acc[m][t + h][3]);
+          for (int t = 0; t < NT; ++t) {
+            acc[m][t][0] = fmaf(sc.x, fmaf(c[m][t][0], 16777216.f, -z0 * X[t][0]), acc[m][t][0]);
+            acc[m][t][1] = fmaf(sc.x, fmaf(c[m][t][1], 16777216.f, -z0 * X[t][1]), acc[m][t][1]);
+            acc[m][t][2] = fmaf(sc.y, fmaf(c[m][t][2], 1048576.f, -z1 * X[t][0]), acc[m][t][2]);
+            acc[m][t][3] = fmaf(sc.y, fmaf(c[m][t][3], 1048576.f, -z1 * X[t][1]), acc[m][t][3]);
+          }
+        }
+      }
+    } else {
+      uint32_t A[MT][8][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) unpack(w[m], sd[m], A[m]);
+#pragma unroll
+      for (int t = 0; t < NT; t += HT) {
+        uint32_t b[HT][16];
+#pragma unroll
+        for (int h = 0; h < HT; ++h) xload(b[h], t + h);
+#pragma unroll
+        for (int q = 0; q < GPB; ++q) {
+          float c[MT][HT][4];
+#pragma unroll
+          for (int k = q * STEPS; k < (q + 1) * STEPS; ++k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int h = 0; h < HT; ++h) {
+                if (k == q * STEPS) mma_first(c[m][h], A[m][k], b[h][2 * k], b[h][2 * k + 1]);
+                else mma(c[m][h], A[m][k], b[h][2 * k], b[h][2 * k + 1]);
+              }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+              acc[m][t + h][0] = fmaf(sc.x, c[m][h][0], acc[m][t + h][0]);
+              acc[m][t + h][1] = fmaf(sc.x, c[m][h][1], acc[m][t + h][1]);
+              acc[m][t + h][2] = fmaf(sc.y, c[m][h][2], acc[m][t + h][2]);
+              acc[m][t + h][3] = fmaf(sc.y, c[m][h][3], acc[m][t + h][3]);
+            }
           }
         }
       }
     }
+    last = st;
+    st = st + 1 == STAGES ? 0 : st + 1;
   }
-  // the second block's warps add to the first block's, in shared memory
+  // the second group's warps add to the first group's, in shared memory
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   float* out = reinterpret_cast<float*>(q2_int4_smem);
@@ -522,16 +604,17 @@ __global__ void __launch_bounds__(kManyWarps * 32, 1) k_int4_many(const __grid_c
   if (nsplit > 1) cluster.sync();
   const int row0 = (int)blockIdx.x / nsplit * kManyRows;
   const int all = a.ntok * kManyRows, e0 = all * rank / nsplit, e1 = all * (rank + 1) / nsplit;
-  const float* peer[8];
-  for (int k = 0; k < 8; ++k) peer[k] = k < nsplit && nsplit > 1 ? cluster.map_shared_rank(out, k) : out;
+  const float* peer[kManyMax];
+#pragma unroll
+  for (int k = 0; k < kManyMax; ++k) peer[k] = k < nsplit && nsplit > 1 ? cluster.map_shared_rank(out, k) : out;
   for (int e = e0 + threadIdx.x; e < e1; e += kManyWarps * 32) {
     const int t = e / kManyRows, r = e % kManyRows;
-    float p[8];
+    float p[kManyMax];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = k < nsplit ? peer[k][t * kOutLd + r] : 0.f;
+    for (int k = 0; k < kManyMax; ++k) p[k] = k < nsplit ? peer[k][t * kOutLd + r] : 0.f;
     float v = p[0];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += p[k];
+    for (int k = 1; k < kManyMax; ++k) v += p[k];
     if (X8) v *= a.xs[t];
     if (row0 + r < a.R) a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(v);
   }
@@ -539,45 +622,26 @@ __global__ void __launch_bounds__(kManyWarps * 32, 1) k_int4_many(const __grid_c
 }
 
 // ------------------------------------------------------- launch
-template <int MT, int GPB, bool X8>
-int launch_few(const Int4Args& a, void* stream) {
-  const int nwarp = a.nblk < kFewWarps ? a.nblk : kFewWarps;
-  const int nunit = (a.ntile + MT - 1) / MT, most = 2 * dev_info().sms;
-  return launch_pdl(k_int4_few<MT, GPB, X8>, a, nunit < most ? nunit : most, nwarp * 32, few_smem<MT, GPB>(a, nwarp), stream);
-}
+constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
-template <int NT, int GPB, bool X8>
-int launch_many(const Int4Args& a, void* stream) {
-  auto kernel = k_int4_many<NT, GPB, X8>;
-  const int smem = many_smem<NT, X8>(a);
-  if (set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
-  const int tiles = (a.ntile + kManyRows / 16 - 1) / (kManyRows / 16), nstage = (a.nblk + 1) / 2;
-  const int slots = dev_info().sms;
-  // Waves of CTAs times their stages plus a fixed cost of about six stages.
-  int nsplit = 1;
-  double best = 0;
-  for (int s = 1; s <= 8 && s <= nstage; s *= 2) {
-    const double cost = (double)((tiles * s + slots - 1) / slots) * ((nstage + s - 1) / s + 6);
-    if (s == 1 || cost < best) {
-      best = cost;
-      nsplit = s;
-    }
-  }
+// Launch in clusters of cs CTAs, programmatic stream serialization allowed.
+template <typename... A, typename... B>
+int launch_clusters(void (*kernel)(A...), int clusters, int cs, int threads, int smem, void* stream, const B&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * nsplit);
-  cfg.blockDim = dim3(kManyWarps * 32);
+  cfg.gridDim = dim3(clusters * cs);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = nsplit;
+  attr[0].val.clusterDim.x = cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kernel, a, nsplit) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return Q2_ECUDA;
   }
@@ -585,9 +649,43 @@ int launch_many(const Int4Args& a, void* stream) {
 }
 
 template <int GPB, bool X8>
+int launch_few(const Int4Args& a, int slots, void* stream) {
+  const int nwarp = a.nblk < kFewWarps ? a.nblk : kFewWarps, smem = few_smem<GPB, X8>(a, nwarp);
+  const int grid = a.ntile < slots ? a.ntile : slots;
+  return a.zeros ? launch_pdl(k_int4_few<GPB, true, X8>, a, grid, nwarp * 32, smem, stream)
+                 : launch_pdl(k_int4_few<GPB, false, X8>, a, grid, nwarp * 32, smem, stream);
+}
+
+template <int NT, int GPB, bool X8>
+int launch_many(const Int4Args& a, void* stream) {
+  auto kernel = k_int4_many<NT, GPB, X8, (NT <= INT4_SUB)>;
+  const int smem = many_smem<NT, X8>(a);
+  if (set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
+  const int tiles = (a.ntile + kManyRows / 16 - 1) / (kManyRows / 16);
+  const int slots = dev_info().sms * std::max(1, std::min(many_ctas<NT>(), kSmemPerSm / (smem + 1024)));
+  // Waves of CTAs times their blocks plus a fixed cost of about eight blocks.
+  int nsplit = 1;
+  long long best = 0;
+  for (int s = 1; s <= kManyMax && 2 * s <= a.nblk; ++s) {
+    const long long cost = (long long)((tiles * s + slots - 1) / slots) * ((a.nblk + s - 1) / s + 8);
+    if (s == 1 || cost < best) {
+      best = cost;
+      nsplit = s;
+    }
+  }
+  return launch_clusters(kernel, tiles, nsplit, kManyWarps * 32, smem, stream, a, nsplit);
+}
+
+template <int GPB, bool X8>
 int launch_tokens(const Int4Args& a, void* stream) {
-  if (a.ntok <= 2) return launch_few<1, GPB, X8>(a, stream);
-  if (a.ntok <= 8) return launch_few<2, GPB, X8>(a, stream);
+  if (a.ntok <= kFewTok) {
+    // k_int4_few keeps x in shared memory and hands out whole row tiles, so it
+    // is taken where x fits and the last round of row tiles is mostly full.
+    const int slots = std::min(kFewCtas, kSmemPerSm / (few_smem<GPB, X8>(a, kFewWarps) + 1024)) * dev_info().sms;
+    const int rounds = slots ? (a.ntile + slots - 1) / slots : 0;
+    if (slots && 5ll * a.ntile >= 4ll * rounds * slots) return launch_few<GPB, X8>(a, slots, stream);
+  }
+  if (a.ntok <= 8) return launch_many<1, GPB, X8>(a, stream);
   if (a.ntok <= 16) return launch_many<2, GPB, X8>(a, stream);
   if (a.ntok <= 32) return launch_many<4, GPB, X8>(a, stream);
   return launch_many<8, GPB, X8>(a, stream);
