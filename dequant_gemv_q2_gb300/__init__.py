@@ -375,6 +375,18 @@ class RmsNorm:
         _check_tensor("RmsNorm", "weight", w, torch.float16, (w.numel(),))
         self.weight, self.eps, self.C, self._w = w, float(eps), w.numel(), w.data_ptr()
 
+    def _ld(self, name: str, t, shape, heads: int) -> int:
+        """The token stride of fp16 rows [ntok][heads][C] of which each token's are contiguous."""
+        import torch
+        if not (t.dtype is torch.float16 and t.is_cuda and t.shape == shape):
+            _check_tensor("q2_rmsnorm", name, t, torch.float16, shape)
+        if t.is_contiguous():
+            return heads * self.C
+        st = t.stride()
+        if (self.C > 1 and st[-1] != 1) or (heads > 1 and st[1] != self.C):
+            raise Q2Error(ESHAPE, f"q2_rmsnorm: {name} has strides {st}")
+        return st[0] if shape[0] > 1 else heads * self.C
+
     def apply(self, x, residual=None, residual_out=None, out=None, out8=None, scale8=None, stream=None):
         """Norm of the rows x [ntok][C] or [ntok][heads][C] (fp16; a token's rows contiguous, any token stride).
 
@@ -389,17 +401,15 @@ class RmsNorm:
         if dims not in (2, 3) or shape[-1] != C:
             raise Q2Error(ESHAPE, f"q2_rmsnorm: x has shape {tuple(shape)}, not [ntok][{C}] or [ntok][heads][{C}]")
         ntok, heads = shape[0], shape[1] if dims == 3 else 1
-        ldx = ldy = heads * C
         if out is None and out8 is None:
             out = torch.empty(shape, dtype=f16, device=x.device)
+        ldx = ldy = heads * C
         if not (x.dtype is f16 and x.is_cuda and x.is_contiguous()):
-            _check_tensor("q2_rmsnorm", "x", x, f16, shape, (x.stride(0),) + (C, 1)[3 - dims:])
-            ldx = x.stride(0) if ntok > 1 else ldx
+            ldx = self._ld("x", x, shape, heads)
         y = y8 = s8 = r = ro = None
         if out is not None:
             if not (out.dtype is f16 and out.is_cuda and out.shape == shape and out.is_contiguous()):
-                _check_tensor("q2_rmsnorm", "out", out, f16, shape, (out.stride(0),) + (C, 1)[3 - dims:])
-                ldy = out.stride(0) if ntok > 1 else ldy
+                ldy = self._ld("out", out, shape, heads)
             y = out.data_ptr()
         if residual is not None:
             residual_out = residual if residual_out is None else residual_out

@@ -12,8 +12,11 @@
 // A row is read once and stays in registers between the sum, the maximum and
 // the stores, so the bytes of the inputs and outputs are all that moves.  Rows
 // of up to 512 columns take 16 or 32 threads each (a reduction is five
-// shuffles, no barrier); longer ones a block each.
+// shuffles, no barrier); longer ones a block, which goes on to further rows
+// with the next row's loads in flight during the reductions of the one before.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "q2_common.cuh"
 
@@ -56,131 +59,149 @@ __device__ __forceinline__ T row_reduce(T v, T* part) {
   return v;
 }
 
-// TPR: threads per row (16 or 32, several rows per block; 0: one row per
-// block).  CH: pieces of 8 columns a thread holds.  VEC: pieces are 16-byte
-// loads; otherwise a thread's columns are strided by the row's threads.
-template <int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR ? 256 : 1024) k_rmsnorm(const __grid_constant__ NormArgs a) {
-  __shared__ float psum[32];
-  __shared__ uint32_t pmax[32];
-  const int nt = TPR ? TPR : blockDim.x;
-  const int tid = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
-  const long long row = TPR ? (long long)blockIdx.x * (256 / (TPR ? TPR : 1)) + threadIdx.x / (TPR ? TPR : 1)
-                            : (long long)blockIdx.x;
-  const bool live = !TPR || row < a.rows;
-  const long long t = row / a.heads;
-  const int C = a.C;
-  const __half* x = a.x + t * a.ldx + (row - t * a.heads) * C;
-  const size_t flat = (size_t)row * C;
-  auto col = [&](int c, int i) { return VEC ? (c * nt + tid) * 8 + i : (c * 8 + i) * nt + tid; };
-  auto load8 = [&](const __half* p, int c, float* v) {
-    if (VEC) {
-      if (live && col(c, 0) < C) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(p + col(c, 0));
-        const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
+// One thread's share of a row: CH pieces of 8 columns.  VEC: a piece is one
+// 16-byte access; otherwise its columns are strided by the row's nt threads.
+template <int CH, bool VEC>
+struct Row {
+  int tid, nt, C;
+  bool live;
+  __device__ __forceinline__ int col(int c, int i) const { return VEC ? (c * nt + tid) * 8 + i : (c * 8 + i) * nt + tid; }
+
+  __device__ __forceinline__ void load(const __half* p, uint4 (&r)[CH]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(h2[i]);
-          v[2 * i] = f.x;
-          v[2 * i + 1] = f.y;
-        }
+    for (int c = 0; c < CH; ++c) {
+      if (VEC) {
+        r[c] = live && col(c, 0) < C ? *reinterpret_cast<const uint4*>(p + col(c, 0)) : make_uint4(0, 0, 0, 0);
+      } else {
+        uint16_t* h = reinterpret_cast<uint16_t*>(&r[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          h[i] = live && col(c, i) < C ? reinterpret_cast<const uint16_t*>(p)[col(c, i)] : (uint16_t)0;
+      }
+    }
+  }
+  __device__ __forceinline__ static void floats(const uint4& r, float (&v)[8]) {
+    const __half2* h2 = reinterpret_cast<const __half2*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h2[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void store(__half* p, const float (&v)[CH][8]) const {
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (VEC) {
+        uint4 raw;
+        __half2* h2 = reinterpret_cast<__half2*>(&raw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[c][2 * i], v[c][2 * i + 1]);
+        if (col(c, 0) < C) *reinterpret_cast<uint4*>(p + col(c, 0)) = raw;
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        for (int i = 0; i < 8; ++i)
+          if (col(c, i) < C) p[col(c, i)] = __float2half_rn(v[c][i]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = live && col(c, i) < C ? __half2float(p[col(c, i)]) : 0.f;
     }
-  };
-  auto store8 = [&](__half* p, int c, const float* v) {
+  }
+  __device__ __forceinline__ void store8(int8_t* p, const float (&v)[CH][8], float inv) const {
     if (!live) return;
-    if (VEC) {
-      if (col(c, 0) >= C) return;
-      uint4 raw;
-      __half2* h2 = reinterpret_cast<__half2*>(&raw);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<uint4*>(p + col(c, 0)) = raw;
-    } else {
+    for (int c = 0; c < CH; ++c) {
+      if (VEC) {
+        uint32_t lo = 0, hi = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col(c, i) < C) p[col(c, i)] = __float2half_rn(v[i]);
+        for (int i = 0; i < 4; ++i) {
+          lo |= (uint32_t)(__float2int_rn(v[c][i] * inv) & 0xff) << (8 * i);
+          hi |= (uint32_t)(__float2int_rn(v[c][i + 4] * inv) & 0xff) << (8 * i);
+        }
+        if (col(c, 0) < C) *reinterpret_cast<uint2*>(p + col(c, 0)) = make_uint2(lo, hi);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col(c, i) < C) p[col(c, i)] = (int8_t)__float2int_rn(v[c][i] * inv);
+      }
     }
-  };
+  }
+};
 
+// TPR: threads per row (16 or 32, several rows per block; 0: a block per row,
+// then every gridDim.x-th).  NT: threads of a block at most.
+template <int TPR, int CH, bool VEC, int NT>
+__global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs a) {
+  // Rows ahead: where the registers hold them (wider rows wait for theirs).
+  constexpr bool AHEAD = TPR == 0 && CH <= 2;
+  __shared__ float psum[2][32];
+  __shared__ uint32_t pmax[2][32];
+  Row<CH, VEC> me;
+  me.nt = TPR ? TPR : blockDim.x;
+  me.tid = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
+  me.C = a.C;
+  long long row = TPR ? (long long)blockIdx.x * (256 / (TPR ? TPR : 1)) + threadIdx.x / (TPR ? TPR : 1)
+                      : (long long)blockIdx.x;
+  me.live = !TPR || row < a.rows;
+  auto place = [&](long long r, long long ld) {                  // element offset of row r = (token, head)
+    const long long t = a.heads == 1 ? r : r / a.heads;
+    return t * ld + (r - t * a.heads) * a.C;
+  };
+  uint4 xr[CH], rr[CH], wr[CH];
   pdl_wait();                                   // x and the residual may come from the previous kernel
   pdl_trigger();
-  float h[CH][8];
+  me.load(a.x + place(row, a.ldx), xr);
+  if (a.res) me.load(a.res + (size_t)row * a.C, rr);
+  if (CH <= 2) me.load(a.w, wr);
+  for (int turn = 0;; turn ^= 1) {
+    float h[CH][8];
+    float ss = 0.f;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) load8(x, c, h[c]);
-  if (a.res) {
-    float r[CH][8];
+    for (int c = 0; c < CH; ++c) {
+      me.floats(xr[c], h[c]);
+      if (a.res) {
+        float r[8];
+        me.floats(rr[c], r);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) load8(a.res + flat, c, r[c]);
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[c][i] += r[c][i];
-  }
-  float w[CH][8];
-  if (CH < 4) {                                 // in flight with the row; wider rows have no registers for it
-#pragma unroll
-    for (int c = 0; c < CH; ++c) load8(a.w, c, w[c]);
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
-  ss = row_reduce<TPR, false>(ss, psum);
-  if (a.res_out) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) store8(a.res_out + flat, c, h[c]);
-  }
-  const float k = rsqrtf(ss / (float)C + a.eps);
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    if (CH >= 4) load8(a.w, c, w[c]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * k * w[c][i];
-  }
-  if (a.y) {
-    __half* y = a.y + t * a.ldy + (row - t * a.heads) * C;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) store8(y, c, h[c]);
-  }
-  if (a.y8) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[c][i]) & 0x7fffffffu);
-    m = row_reduce<TPR, true>(m, pmax);
-    const float top = __uint_as_float(m);
-    // A zero row has scale 0 and zeros; a row with a NaN (or an infinity) has
-    // a scale that is NaN (or infinite), which its consumer multiplies by.
-    const float inv = top > 0.f ? 127.f / top : 0.f;
-    if (live && tid == 0) a.s8[row] = top / 127.f;
-    if (live) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (VEC) {
-          if (col(c, 0) < C) {
-            uint32_t lo = 0, hi = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              lo |= (uint32_t)(__float2int_rn(h[c][i] * inv) & 0xff) << (8 * i);
-              hi |= (uint32_t)(__float2int_rn(h[c][i + 4] * inv) & 0xff) << (8 * i);
-            }
-            *reinterpret_cast<uint2*>(a.y8 + flat + col(c, 0)) = make_uint2(lo, hi);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col(c, i) < C) a.y8[flat + col(c, i)] = (int8_t)__float2int_rn(h[c][i] * inv);
-        }
+        for (int i = 0; i < 8; ++i) h[c][i] += r[i];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
+    }
+    const long long next = row + gridDim.x;
+    if (AHEAD && next < a.rows) {
+      me.load(a.x + place(next, a.ldx), xr);
+      if (a.res) me.load(a.res + (size_t)next * a.C, rr);
+    }
+    if (CH > 2) me.load(a.w, wr);
+    ss = row_reduce<TPR, false>(ss, psum[turn]);
+    if (a.res_out) me.store(a.res_out + (size_t)row * a.C, h);
+    const float k = rsqrtf(ss / (float)a.C + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[8];
+      me.floats(wr[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * k * w[i];
+    }
+    if (a.y) me.store(a.y + place(row, a.ldy), h);
+    if (a.y8) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[c][i]) & 0x7fffffffu);
+      m = row_reduce<TPR, true>(m, pmax[turn]);
+      const float top = __uint_as_float(m);
+      // A zero row has scale 0 and zeros; a row with a NaN (or an infinity) has
+      // a scale that is NaN (or infinite), which its consumer multiplies by.
+      if (me.live && me.tid == 0) a.s8[row] = top / 127.f;
+      me.store8(a.y8 + (size_t)row * a.C, h, top > 0.f ? 127.f / top : 0.f);
+    }
+    if (TPR || next >= a.rows) return;
+    row = next;
+    if (!AHEAD) {
+      me.load(a.x + place(row, a.ldx), xr);
+      if (a.res) me.load(a.res + (size_t)row * a.C, rr);
     }
   }
 }
@@ -189,18 +210,25 @@ template <bool VEC>
 int launch_norm(const NormArgs& a, void* stream) {
   const int pieces = (a.C + 7) / 8;
   auto blocks = [&](int per) { return (int)((a.rows + per - 1) / per); };
-  if (pieces <= 16) return launch_pdl(k_rmsnorm<16, 1, VEC>, a, blocks(16), 256, 0, stream);
-  if (pieces <= 32) return launch_pdl(k_rmsnorm<32, 1, VEC>, a, blocks(8), 256, 0, stream);
-  if (pieces <= 64) return launch_pdl(k_rmsnorm<32, 2, VEC>, a, blocks(8), 256, 0, stream);
+  if (pieces <= 16) return launch_pdl(k_rmsnorm<16, 1, VEC, 256>, a, blocks(16), 256, 0, stream);
+  if (pieces <= 32) return launch_pdl(k_rmsnorm<32, 1, VEC, 256>, a, blocks(8), 256, 0, stream);
+  if (pieces <= 64) return launch_pdl(k_rmsnorm<32, 2, VEC, 256>, a, blocks(8), 256, 0, stream);
+  // A block per row, up to as many blocks as fit 1024 threads on every SM.
   auto threads = [&](int ch) { return ((pieces + ch - 1) / ch + 31) / 32 * 32; };
-  if (pieces <= 512) return launch_pdl(k_rmsnorm<0, 1, VEC>, a, blocks(1), threads(1), 0, stream);
-  if (pieces <= 1024) return launch_pdl(k_rmsnorm<0, 2, VEC>, a, blocks(1), threads(2), 0, stream);
-  return launch_pdl(k_rmsnorm<0, 4, VEC>, a, blocks(1), threads(4), 0, stream);
+  auto grid = [&](int nt) {
+    const long long most = (long long)dev_info().sms * std::max(1, 1024 / nt);
+    return (int)std::min(a.rows, most);
+  };
+  // Few rows: more threads, for the latency; many: two pieces in flight each.
+  const bool few = a.rows <= 2 * dev_info().sms;
+  if (few && pieces <= 512) return launch_pdl(k_rmsnorm<0, 1, VEC, 512>, a, (int)a.rows, threads(1), 0, stream);
+  if (pieces <= 512) return launch_pdl(k_rmsnorm<0, 2, VEC, 256>, a, grid(threads(2)), threads(2), 0, stream);
+  if (pieces <= 1024) return launch_pdl(k_rmsnorm<0, 2, VEC, 512>, a, grid(threads(2)), threads(2), 0, stream);
+  return launch_pdl(k_rmsnorm<0, 4, VEC, 1024>, a, grid(threads(4)), threads(4), 0, stream);
 }
 
 }  // namespace
 }  // namespace q2
-
 extern "C" int q2_rmsnorm(const void* x, long long ldx, int ntok, int heads, int C, const void* residual,
                           void* residual_out, const void* weight, float eps, void* y, long long ldy, void* y8,
                           float* scale8, q2_stream stream) {
