@@ -61,8 +61,16 @@ struct AttendArgs {
   float2* ml;                 // [2 * CTAs][kHeads] maximum, denominator
   int batch, npages, page, cap;   // cap: tokens that a table row can hold
   int hu, nht, group;         // heads of units = kv_heads * nht; query heads of a key-value head
+  uint32_t page_mul, page_sh; // t / page = (high half of t * page_mul, + t) >> page_sh, t < 2^31
+  int aligned;                // page % 16 == 0: a tile lies in one page
   float sc2;                  // scale * log2(e)
 };
+
+// Division by an invariant with a multiplication (Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication", 1994).
+__device__ __forceinline__ int page_of(const AttendArgs& a, int t) {
+  return (int)((__umulhi((uint32_t)t, a.page_mul) + (uint32_t)t) >> a.page_sh);
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -101,15 +109,21 @@ struct Walk {
   int b, h, chunk, nch, len;
 };
 
+// What the end of a (sequence, head) costs a CTA, in units: the shares are cut
+// by units plus this, so that a CTA with many short sequences gets fewer units
+// (16 sequences of 1 to 4096 tokens, 40 query heads of 128: 31.6 us; 34.2 with
+// 0, 31.9 with 4).
+constexpr int kEnd = 2;
+
 template <int D>
 struct Shape {
   static constexpr int STAGES = D == 64 ? 6 : 3;
   static constexpr int kTileBytes = kTile * D * 2;                     // keys or values of a tile
   static constexpr int kRing = kWarps * STAGES * 2 * kTileBytes;
-  static constexpr int kMerge = (kWarps - 1) * kHeads * D * 4;
   static constexpr int kMl = kWarps * kHeads * 8;
-  static constexpr int fixed = kRing + kMerge + kMl + 16;
-  static int smem(int batch) { return fixed + 4 * (batch + 1); }
+  static constexpr int fixed = kRing + kMl + 48;
+  static_assert(kHeads * D * 4 == kTileBytes, "a warp's numerators take the place of a tile's keys");
+  static int smem(int batch) { return fixed + 4 * (2 * batch + 1); }
 };
 
 template <int D>
@@ -117,21 +131,25 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
   using S = Shape<D>;
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
   extern __shared__ __align__(16) unsigned char q2_att_smem[];
-  float* merge = reinterpret_cast<float*>(q2_att_smem + S::kRing);     // [kWarps - 1][kHeads][D]
-  float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing + S::kMerge);   // [kWarps][kHeads]
-  int* last = reinterpret_cast<int*>(q2_att_smem + S::kRing + S::kMerge + S::kMl);
-  int* pre = last + 4;                                                 // [batch + 1] units before each sequence
+  float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing);     // [kWarps][kHeads] maximum, denominator
+  int4* owe = reinterpret_cast<int4*>(q2_att_smem + S::kRing + S::kMl);   // joins that are this CTA's: sequence, head, CTAs
+  int* nowed = reinterpret_cast<int*>(owe + 2);                           // at first: how many CTAs have work
+  int* pre = nowed + 4;                                                // [batch + 1] units before each sequence
+  int* lens = pre + a.batch + 1;                                       // [batch] lengths; what cannot be is 0
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
 
   pdl_wait();                                       // everything may come from the previous kernel
   pdl_trigger();
   if (warp == 0) {                                  // the units before each sequence
-    int carry = 0;
+    int carry = 0, longest = 0, used = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       const int b = b0 + lane;
       int len = b < a.batch ? a.lens[b] : 0;
       if (len < 0 || len > a.cap) len = 0;
-      int v = (len + kUnit - 1) / kUnit * a.hu;
+      if (b < a.batch) lens[b] = len;
+      longest = max(longest, (len + kUnit - 1) / kUnit);
+      used += __popc(__ballot_sync(0xffffffffu, len > 0));
+      int v = len ? ((len + kUnit - 1) / kUnit + kEnd) * a.hu : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -140,7 +158,16 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
       if (b < a.batch) pre[b + 1] = carry + v;
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) pre[0] = 0;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      pre[0] = 0;
+      // How many CTAs.  Each part of a (sequence, head) costs its join about a
+      // quarter of what a unit costs its CTA, so n units are best cut into
+      // about 2 sqrt(n) parts; with few (sequence, head)s, a multiple of their
+      // number, so that sequences of one length are cut at their heads.
+      const int heads = used * a.hu, parts = max(1, (int)(2.f * sqrtf((float)longest)));
+      *nowed = heads * 4 > (int)gridDim.x ? (int)gridDim.x : heads * min(parts, (int)gridDim.x / max(heads, 1));
+    }
   }
   // sequences without a token give zeros, lengths that the table cannot hold NaN
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -152,10 +179,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
       a.o[b * a.ldo + e] = len ? __ushort_as_half(0x7e00) : __ushort_as_half(0);
   }
   __syncthreads();
-  const int total = pre[a.batch], ncta = min((int)gridDim.x, total);
+    // The order of units: each (sequence, head) has its units and kEnd places
+  // without one.  This CTA takes the units at places u0 .. u1 - 1.
+  const int total = pre[a.batch], ncta = min(*nowed, total);
   if ((int)blockIdx.x >= ncta) return;
   auto first_of = [&](int cta) { return (int)((long long)total * cta / ncta); };
-  const int u0 = first_of(blockIdx.x), n = first_of(blockIdx.x + 1) - u0;
+  int u0 = first_of(blockIdx.x);
+  const int u1 = first_of(blockIdx.x + 1);
 
   Walk c;                                           // the unit in use
   {
@@ -166,77 +196,113 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
       else hi = mid;
     }
     c.b = lo;
-    c.len = a.lens[lo];
+    c.len = lens[lo];
     c.nch = (c.len + kUnit - 1) / kUnit;
     const int r = u0 - pre[lo];
-    c.h = r / c.nch;
-    c.chunk = r - c.h * c.nch;
+    c.h = r / (c.nch + kEnd);
+    c.chunk = r - c.h * (c.nch + kEnd);
   }
+  // to the next unit; how many places further it is
   auto advance = [&](Walk& w) {
-    if (++w.chunk < w.nch) return;
+    if (++w.chunk < w.nch) return 1;
+    const int skipped = w.nch + kEnd - w.chunk;
     w.chunk = 0;
-    if (++w.h < a.hu) return;
-    w.h = 0;
-    do ++w.b;
-    while (w.b < a.batch && pre[w.b + 1] == pre[w.b]);
-    if (w.b < a.batch) {
-      w.len = a.lens[w.b];
-      w.nch = (w.len + kUnit - 1) / kUnit;
+    if (++w.h == a.hu) {
+      w.h = 0;
+      do ++w.b;
+      while (w.b < a.batch && pre[w.b + 1] == pre[w.b]);
+      if (w.b < a.batch) {
+        w.len = lens[w.b];
+        w.nch = (w.len + kUnit - 1) / kUnit;
+      }
     }
+    return 1 + skipped;
   };
+  if (c.chunk >= c.nch) {                           // the share begins behind the last unit of a (sequence, head)
+    --c.chunk;
+    u0 += advance(c) - 1;
+  }
+  if (u0 >= u1) return;
 
   // ---- the warp's loads, STAGES - 1 units ahead of their use
   const uint32_t ring = saddr(q2_att_smem) + warp * (STAGES * 2 * S::kTileBytes);
   Walk p = c;
-  int pu = 0, pslot = 0, ppage = -1;                // unit to load, its stage, the page of this lane's row
+  int pu = u0, pslot = 0, ppage = -1;               // place of the unit to load, its stage, the page of this lane's row
   uint32_t badslots = 0;                            // stages with a row whose page does not exist
-  auto lookup = [&]() {                             // lanes l and l + 16: row l of the tile
-    const int t = p.chunk * kUnit + warp * kTile + (lane & 15);
-    ppage = pu < n && t < p.len ? a.table[p.b * a.table_stride + t / a.page] : -1;
+  const int piece = lane % CPR, row0 = lane / CPR;
+  const long long lrow = row0 * a.token_stride + piece * 8;            // this lane's place in a tile that lies in one page
+  const uint32_t ldst = ring + row0 * (D * 2);
+  auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
+    const int t = p.chunk * kUnit + warp * kTile + (a.aligned ? 0 : lane & 15);
+    ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
   };
   lookup();
   auto issue = [&]() {
-    if (pu < n) {
-      const int t0 = p.chunk * kUnit + warp * kTile, t = t0 + (lane & 15);
+    if (pu < u1) {
+      const int t0 = p.chunk * kUnit + warp * kTile;
       if (t0 < p.len) {
-        const bool wanted = t < p.len && !(a.nk && t == p.len - 1);    // the new token does not come from the cache
-        const bool there = (unsigned)ppage < (unsigned)a.npages;
-        const bool bad = __any_sync(0xffffffffu, t < p.len && !there);
+        const int have = p.len - t0 - (a.nk ? 1 : 0);                  // rows to copy: the new token does not come from the cache
+        const int kvh = a.nht == 1 ? p.h : p.h / a.nht;
+        const uint32_t dst = ldst + pslot * (2 * S::kTileBytes);
+        bool bad;
+        if (a.aligned) {
+          bad = (unsigned)ppage >= (unsigned)a.npages;
+          const long long off = bad ? 0 : ppage * a.page_stride + (t0 - page_of(a, t0) * a.page) * a.token_stride +
+                                              kvh * a.head_stride + lrow;
+          const __half* k = a.k + off;
+          const __half* v = a.v + off;
+          const long long step = RPI * a.token_stride;
+          const int rows = bad ? 0 : have - row0;                      // live rows from this lane's first on
+#pragma unroll
+          for (int i = 0; i < kTile / RPI; ++i) {
+            const uint32_t d = dst + i * (RPI * D * 2) + ((piece ^ ((i * RPI + row0) & 7)) << 4);
+            const bool live = i * RPI < rows;
+            cp16(d, live ? k : a.k, live);
+            cp16(d + S::kTileBytes, live ? v : a.v, live);
+            k += step;
+            v += step;
+          }
+        } else {
+          const int t = t0 + (lane & 15);
+          const bool there = (unsigned)ppage < (unsigned)a.npages;
+          bad = __any_sync(0xffffffffu, t < p.len && !there);
+          const long long off = (lane & 15) < have && there
+                                    ? ppage * a.page_stride + (t - page_of(a, t) * a.page) * a.token_stride + kvh * a.head_stride
+                                    : -1;
+#pragma unroll 2
+          for (int i = 0; i < kTile / RPI; ++i) {
+            const int row = i * RPI + row0;
+            const long long o = __shfl_sync(0xffffffffu, off, row);
+            const long long e = (o < 0 ? 0 : o) + piece * 8;
+            const uint32_t d = dst + i * (RPI * D * 2) + ((piece ^ (row & 7)) << 4);
+            cp16(d, a.k + e, o >= 0);
+            cp16(d + S::kTileBytes, a.v + e, o >= 0);
+          }
+        }
         if (bad && lane == 0) atomicOr(&q2_attend_error, Q2_ERR_PAGE);
         badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
-        const long long off = wanted && there ? ppage * a.page_stride + (t % a.page) * a.token_stride +
-                                                    (p.h / a.nht) * a.head_stride
-                                              : -1;
-        const uint32_t dst = ring + pslot * (2 * S::kTileBytes);
-        const int piece = lane % CPR;
-#pragma unroll
-        for (int i = 0; i < kTile / RPI; ++i) {
-          const int row = i * RPI + lane / CPR;
-          const long long o = __shfl_sync(0xffffffffu, off, row);
-          const long long e = (o < 0 ? 0 : o) + piece * 8;
-          const uint32_t d = dst + row * (D * 2) + ((piece ^ (row & 7)) << 4);
-          cp16(d, a.k + e, o >= 0);
-          cp16(d + S::kTileBytes, a.v + e, o >= 0);
-        }
       }
-      ++pu;
-      advance(p);
+      pu += advance(p);
       lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll 1
-  for (int s = 0; s < STAGES - 1; ++s) issue();
-
   // ---- sums of the current (sequence, head)
   uint32_t qa[D / 16][2];                           // the queries: row g, columns 2j.. and 2j + 8.. of each 16
   uint4 newk, newv;                                 // lane l < CPR: piece l of the new token's key and value
   float o[NT][4], m = -INFINITY, l = 0.f;
   bool fresh = true;
   int seg = c.chunk, slot = 0;                      // first unit of this part of the (sequence, head)
-  for (int i = 0; i < n; ++i) {
-    const int kvh = c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
+  int ahead = STAGES - 1;                           // units still to be requested before the first is used
+  int owed = 0;                                     // parts of this CTA that were the last of their (sequence, head)
+  for (int u = u0; u < u1;) {
+    if (ahead) {
+      --ahead;
+      issue();
+      continue;
+    }
+    const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
     const int qh = kvh * a.group + ht * kHeads;
     const int t0 = c.chunk * kUnit + warp * kTile;
     if (fresh) {
@@ -260,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
       l = 0.f;
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    __syncwarp();                                   // unit i has arrived for all lanes, unit i - 1 is done with
+    __syncwarp();                                   // this unit has arrived for all lanes, the one before is done with
     issue();
     if (t0 < c.len) {
       const uint32_t kt = ring + slot * (2 * S::kTileBytes), vt = kt + S::kTileBytes;
@@ -274,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vt + d), "r"(newv.x), "r"(newv.y), "r"(newv.z),
                        "r"(newv.w)
                        : "memory");
-          const int page = a.table[c.b * a.table_stride + (c.len - 1) / a.page];
+          const int at = page_of(a, c.len - 1), page = a.table[c.b * a.table_stride + at];
           if (ht == 0 && (unsigned)page < (unsigned)a.npages) {
-            const long long e = page * a.page_stride + ((c.len - 1) % a.page) * a.token_stride + kvh * a.head_stride +
+            const long long e = page * a.page_stride + (c.len - 1 - at * a.page) * a.token_stride + kvh * a.head_stride +
                                 lane * 8;
             *reinterpret_cast<uint4*>(a.k + e) = newk;
             *reinterpret_cast<uint4*>(a.v + e) = newv;
@@ -332,100 +398,139 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
         mma(o[t + 1], p0, p1, p2, p3, b[2], b[3]);
       }
     }
+    const uint32_t mine = slot * (2 * S::kTileBytes);       // this unit's stage, free until the next issue()
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
-    const bool ends = c.chunk + 1 == c.nch;
-    if (ends || i + 1 == n) {                       // the end of this (sequence, head), or of this CTA's share of it
+    const Walk w = c;
+    u += advance(c);
+    const bool ends = w.chunk + 1 == w.nch, all = u >= u1;
+    if (ends || all) {                              // the end of this (sequence, head), or of this CTA's share of it
+      // Every warp leaves its sums (the numerators in place of the keys it has
+      // just used, 16-byte pieces exchanged by the row as the keys were), then
+      // joins a quarter of the columns of all warps.
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      __syncthreads();                              // the merge buffer is free
+      unsigned char* sums = q2_att_smem + warp * (STAGES * 2 * S::kTileBytes) + mine;
+      __syncwarp();
       if (j == 0) wml[warp * kHeads + g] = make_float2(m, l);
-      if (warp) {
-        float* w = merge + ((warp - 1) * kHeads + g) * D + 2 * j;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<float2*>(w + 8 * t) = make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3]);
-      }
+      for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<float2*>(sums + g * (D * 4) + (((2 * t + (j >> 1)) ^ g) << 4) + (j & 1) * 8) =
+            make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3]);
       __syncthreads();
       const bool whole = ends && seg == 0;
       const int part = 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0);
-      if (warp == 0) {
-        float wt[kWarps], mm = -INFINITY, ll = 0.f;
+      constexpr int PPL = D / kWarps / 16;          // 16-byte pieces of a lane: row lane / 4, a quarter of the warp's columns
+      float wt[kWarps], mm = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, wml[w * kHeads + g].x);
-        const float ref = mm == -INFINITY ? 0.f : mm;
+      for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, wml[k * kHeads + g].x);
+      const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 v = wml[w * kHeads + g];
-          wt[w] = exp2f(v.x - ref);
-          ll += wt[w] * v.y;
-        }
-        if (g < rows) {
-          const float inv = 1.f / ll;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            float x = (o[t][0] + o[t][2]) * wt[0], y = (o[t][1] + o[t][3]) * wt[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(merge + ((w - 1) * kHeads + g) * D + 8 * t + 2 * j);
-              x += v.x * wt[w];
-              y += v.y * wt[w];
-            }
-            if (whole)
-              *reinterpret_cast<__half2*>(a.o + c.b * a.ldo + (long long)(qh + g) * D + 8 * t + 2 * j) =
-                  __floats2half2_rn(x * inv, y * inv);
-            else
-              *reinterpret_cast<float2*>(a.part + ((size_t)part * kHeads + g) * D + 8 * t + 2 * j) = make_float2(x, y);
-          }
-          if (!whole && j == 0) a.ml[(size_t)part * kHeads + g] = make_float2(mm, ll);
-        }
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 v = wml[k * kHeads + g];
+        wt[k] = exp2f(v.x - ref);
+        ll += wt[k] * v.y;
       }
+      if (g < rows) {
+        const float inv = 1.f / ll;
+#pragma unroll
+        for (int q = 0; q < PPL; ++q) {
+          const int piece4 = (warp * 4 + j) * PPL + q;      // columns 4 * piece4 ..
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(q2_att_smem + k * (STAGES * 2 * S::kTileBytes) + mine +
+                                                              g * (D * 4) + ((piece4 ^ g) << 4));
+            x.x += v.x * wt[k];
+            x.y += v.y * wt[k];
+            x.z += v.z * wt[k];
+            x.w += v.w * wt[k];
+          }
+          if (whole) {
+            __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
+            *reinterpret_cast<uint2*>(a.o + w.b * a.ldo + (long long)(qh + g) * D + piece4 * 4) = *reinterpret_cast<uint2*>(h);
+          } else {
+            *reinterpret_cast<float4*>(a.part + ((size_t)part * kHeads + g) * D + piece4 * 4) = x;
+          }
+        }
+        if (!whole && warp == 0 && j == 0) a.ml[(size_t)part * kHeads + g] = make_float2(mm, ll);
+      }
+      __syncthreads();                              // the stages may be filled again; the part is written
       if (!whole) {
         // the CTAs that hold parts of this (sequence, head): c0 (from its first unit) .. c1
-        const int s = pre[c.b] + c.h * c.nch;
-        auto cta_of = [&](int u) { return (int)((((long long)u + 1) * ncta - 1) / total); };
-        const int c0 = cta_of(s), c1 = cta_of(s + c.nch - 1);
-        if (warp == 0) {
+        const int s = pre[w.b] + w.h * (w.nch + kEnd);
+        auto cta_of = [&](int v) { return (int)((((long long)v + 1) * ncta - 1) / total); };
+        const int c0 = cta_of(s), c1 = cta_of(s + w.nch - 1);
+        // The part that completes a (sequence, head) owes its join; a CTA has
+        // two parts at most (the one it begins with and the one it ends with)
+        // and joins at its end, so that nothing waits for the counter here.
+        if (threadIdx.x == 0) {
+          unsigned int* count = a.count + (size_t)w.b * a.hu + w.h;
           __threadfence();
-          __syncwarp();
-          if (lane == 0) {
-            unsigned int* count = a.count + (size_t)c.b * a.hu + c.h;
-            const bool done = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
-            if (done) *count = 0;
-            __threadfence();
-            *last = done;
-          }
-        }
-        __syncthreads();
-        if (*last) {
-          for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
-            const int r = e / (D / 4), d4 = e % (D / 4);
-            float mm = -INFINITY;
-#pragma unroll 8
-            for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(&a.ml[(size_t)(2 * k + (k == c0)) * kHeads + r]).x);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f, x = 0.f, y = 0.f, z = 0.f, w = 0.f;
-#pragma unroll 4
-            for (int k = c0; k <= c1; ++k) {
-              const size_t at = (size_t)(2 * k + (k == c0)) * kHeads + r;
-              const float2 v = __ldcg(&a.ml[at]);
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + d4);
-              const float wt = exp2f(v.x - ref);
-              ll += wt * v.y;
-              x += wt * f.x;
-              y += wt * f.y;
-              z += wt * f.z;
-              w += wt * f.w;
-            }
-            const float inv = 1.f / ll;
-            __half2 h[2] = {__floats2half2_rn(x * inv, y * inv), __floats2half2_rn(z * inv, w * inv)};
-            *reinterpret_cast<uint2*>(a.o + c.b * a.ldo + (long long)(qh + r) * D + d4 * 4) = *reinterpret_cast<uint2*>(h);
+          const bool done = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
+          if (done) {
+            *count = 0;
+            owe[owed++] = make_int4(w.b, w.h, c0, c1);
           }
         }
       }
       fresh = true;
       seg = 0;
     }
-    advance(c);
+  }
+
+  if (threadIdx.x == 0) {
+    __threadfence();
+    *nowed = owed;
+  }
+  __syncthreads();
+  for (int q = 0; q < *nowed; ++q) {
+    const int4 w = owe[q];
+    const int kvh = a.nht == 1 ? w.y : w.y / a.nht, ht = w.y - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
+    const int parts = w.w - w.z + 1;
+    for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), d4 = e % (D / 4);
+      float mj = -INFINITY, lj = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int k0 = 0; k0 < parts; k0 += 8) {       // eight parts' loads at a time
+        float2 v[8];
+        float4 f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // the first CTA's second part, the others' first
+          const size_t at = (size_t)(2 * (w.z + min(k0 + k, parts - 1)) + (k0 + k == 0)) * kHeads + r;
+          v[k] = __ldcg(&a.ml[at]);
+          f[k] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + d4);
+          if (k0 + k >= parts) v[k].x = -INFINITY;
+        }
+        float mn = mj;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, v[k].x);
+        const float ref = mn == -INFINITY ? 0.f : mn, old = exp2f(mj - ref);
+        mj = mn;
+        lj *= old;
+        x.x *= old;
+        x.y *= old;
+        x.z *= old;
+        x.w *= old;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k0 + k < parts) {
+            const float wk = exp2f(v[k].x - ref);
+            lj += wk * v[k].y;
+            x.x += wk * f[k].x;
+            x.y += wk * f[k].y;
+            x.z += wk * f[k].z;
+            x.w += wk * f[k].w;
+          }
+        }
+      }
+      const float inv = 1.f / lj;
+      __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
+      *reinterpret_cast<uint2*>(a.o + w.x * a.ldo + (long long)(kvh * a.group + ht * kHeads + r) * D + d4 * 4) =
+          *reinterpret_cast<uint2*>(h);
+    }
   }
 }
 
@@ -489,7 +594,7 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
   if (off(ws, 256)) return Q2_EALIGN;
   // tokens of a table row, and of all units: both are counted in 32 bits on the device
   const long long cap = (long long)kv->max_pages * kv->page_size;
-  const long long units = (cap / kUnit + 1) * hu * batch;
+  const long long units = (cap / kUnit + 1 + kEnd) * hu * batch;
   if (cap > 0x7fffff00ll || units > 0x7fffffffll) return Q2_ESHAPE;
   AttendArgs a = {};
   a.k = static_cast<__half*>(kv->k);
@@ -514,6 +619,9 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
   a.batch = batch;
   a.npages = kv->npages;
   a.page = kv->page_size;
+  a.aligned = kv->page_size % kTile == 0;
+  while ((1ll << a.page_sh) < a.page) ++a.page_sh;
+  a.page_mul = (uint32_t)(((1ull << 32) * ((1ull << a.page_sh) - a.page)) / a.page + 1);
   a.cap = (int)cap;
   a.hu = hu;
   a.nht = nht;
