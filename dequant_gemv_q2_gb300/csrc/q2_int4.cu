@@ -28,169 +28,12 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "q2_common.cuh"
+#include "q2_int4.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace q2 {
 namespace {
-
-struct Int4Args {
-  const unsigned char* w;     // [ntile][nblk] blocks of `item` bytes: weights, scales, zero points
-  const void* x;              // [ntok][C] fp16 or int8
-  const float* xs;            // [ntok], 8-bit x only
-  __half* y;                  // [ntok][R]
-  int R, C, nblk, ntile, ntok, item;
-  int zeros;                  // blocks hold zero points; else 8 everywhere
-};
-
-// The scales (rows g and g + 8) and zero points of a lane's rows in one block.
-template <int GPB>            // groups per block: 1, 2 or 4
-struct Sides {
-  uint32_t s[GPB];
-  uint32_t z[(GPB + 1) / 2];
-};
-
-// Blocks go to shared memory by asynchronous 16-byte copies (a register ring
-// was bound by the six scoreboards a warp has: waiting for x meant waiting
-// for weights requested after it; 19.1 us instead of 10.3 at 24576 x 4096).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t lds16(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return v;
-}
-
-template <int GPB>
-__device__ __forceinline__ void load_sides(Sides<GPB>& k, uint32_t blk, int zeros, int g) {
-  const uint32_t s = blk + 1024 + g * (GPB * 4), z = blk + 1024 + GPB * 32 + g * (GPB * 2);
-  if constexpr (GPB == 1) {
-    k.s[0] = lds32(s);
-    k.z[0] = zeros ? lds16(z) : 0x0808u;
-  } else if constexpr (GPB == 2) {
-    const uint2 v = lds64(s);
-    k.s[0] = v.x;
-    k.s[1] = v.y;
-    k.z[0] = zeros ? lds32(z) : 0x08080808u;
-  } else {
-    const uint4 v = lds128(s);
-    k.s[0] = v.x;
-    k.s[1] = v.y;
-    k.s[2] = v.z;
-    k.s[3] = v.w;
-    const uint2 u = zeros ? lds64(z) : make_uint2(0x08080808u, 0x08080808u);
-    k.z[0] = u.x;
-    k.z[1] = u.y;
-  }
-}
-
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// The block's q - z as the A operands of its eight 16-column steps: rows g
-// (a0, a2) and g + 8 (a1, a3) of lane group g = lane / 4.  A word holds, from
-// its lowest four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3 of the step's four,
-// rows g and g + 8 in turn.
-template <int GPB>
-__device__ __forceinline__ void unpack(const uint4 (&w)[2], const Sides<GPB>& k, uint32_t (&A)[8][4]) {
-#pragma unroll
-  for (int q = 0; q < GPB; ++q) {
-    const uint32_t zz = k.z[q >> 1] >> (16 * (q & 1));
-    const uint32_t z0 = and_or(zz, 0xffu, 0x6400u) * 0x10001u;                  // 1024 + z of row g
-    const uint32_t z1 = and_or(zz >> 4, 0xff0u, 0xd400u) * 0x10001u;            // -(64 + z) of row g + 8
-#pragma unroll
-    for (int t = 0; t < 8 / GPB; ++t) {
-      const int st = q * (8 / GPB) + t;
-      const uint32_t v = word(w[st >> 2], st & 3), v8 = v >> 8;
-      A[st][0] = hsub2(and_or(v, 0x000f000fu, 0x64006400u), z0);
-      A[st][1] = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
-      A[st][2] = hsub2(and_or(v8, 0x000f000fu, 0x64006400u), z0);
-      A[st][3] = hfma2(and_or(v8, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
-    }
-  }
-}
-
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Four 8-bit integers as two pairs of fp16: the byte plus 128 in the mantissa
-// of 1024, minus 1152.
-__device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  v ^= 0x80808080u;
-  lo = hsub2(__byte_perm(v, 0x64646464u, 0x4140), 0x64806480u);
-  hi = hsub2(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u);
-}
-
-// The B operands of one block for one token: 8 consecutive columns in each of
-// the block's four runs of 32, 16 bytes of fp16 or 8 bytes of 8-bit integers.
-template <bool X8, typename L>
-__device__ __forceinline__ void load_b(uint32_t (&b)[16], L&& load) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const auto v = load(k);
-    if constexpr (X8) {
-      int8x4(v.x, b[4 * k], b[4 * k + 1]);
-      int8x4(v.y, b[4 * k + 2], b[4 * k + 3]);
-    } else {
-      b[4 * k] = v.x;
-      b[4 * k + 1] = v.y;
-      b[4 * k + 2] = v.z;
-      b[4 * k + 3] = v.w;
-    }
-  }
-}
-
-template <bool X8>
-struct XVec {
-  using T = uint4;
-};
-template <>
-struct XVec<true> {
-  using T = uint2;
-};
 
 // ------------------------------------------------------- 1 and 2 tokens
 // At one token a block's 2048 weights have to pass in about 50 cycles per SM,
@@ -622,32 +465,6 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
 }
 
 // ------------------------------------------------------- launch
-constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
-
-// Launch in clusters of cs CTAs, programmatic stream serialization allowed.
-template <typename... A, typename... B>
-int launch_clusters(void (*kernel)(A...), int clusters, int cs, int threads, int smem, void* stream, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * cs);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return Q2_ECUDA;
-  }
-  return cudaGetLastError() == cudaSuccess ? Q2_OK : Q2_ECUDA;
-}
-
 template <int GPB, bool X8>
 int launch_few(const Int4Args& a, int slots, void* stream) {
   const int nwarp = a.nblk < kFewWarps ? a.nblk : kFewWarps, smem = few_smem<GPB, X8>(a, nwarp);
@@ -686,6 +503,10 @@ int launch_tokens(const Int4Args& a, void* stream) {
     if (slots && 5ll * a.ntile >= 4ll * rounds * slots) return launch_few<GPB, X8>(a, slots, stream);
   }
   if (a.ntok <= 8) return launch_many<1, GPB, X8>(a, stream);
+#ifndef TCN
+#define TCN 9
+#endif
+  if (a.ntok >= TCN) return q2_int4_tc(a, Q2_INT4_COLS / GPB, X8, stream);
   if (a.ntok <= 16) return launch_many<2, GPB, X8>(a, stream);
   if (a.ntok <= 32) return launch_many<4, GPB, X8>(a, stream);
   return launch_many<8, GPB, X8>(a, stream);

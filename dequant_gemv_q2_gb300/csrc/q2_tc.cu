@@ -59,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include "q2_common.cuh"
+#include "q2_tcgen.cuh"
 
 extern __shared__ __align__(1024) unsigned char q2_smem[];
 
@@ -89,23 +90,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAcol0 = 64;               // D takes TMEM columns 0..63
 constexpr int kOneCtaSmem = 116 * 1024;       // two CTAs never share an SM (each holds all of TMEM)
 
-// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B fp16
-// (7-9, 10-12 = 0), both K-major (15, 16 = 0), N >> 3 in 17-22, M >> 4 in 24-28.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// D[tmem] (+)= A[tmem] x B[smem descriptor]
-__device__ __forceinline__ void mma_f16_ta(uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dtmem),
-      "r"(atmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // 16 consecutive 32-bit columns of this thread's TMEM lane (the warp's 32 lanes).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -119,7 +103,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, uint4 a, uint4 b, uint
   const uint32_t r[16] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
   tmem_st16(taddr, r);
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Lane un-rotation.  Lane l = 4a + r stores its 32-byte plane row rotated:
 // rotated byte j holds column-byte (j + l) mod 32, so canonical word c
@@ -133,28 +116,6 @@ __device__ __forceinline__ uint32_t unrot(uint32_t lo, uint32_t hi, uint32_t sh)
 // Byte offset, inside the lane's part of an item (after lane * 16), of
 // rotated word w of plane q: half w / 4 of the plane is chunk 2q + w / 4.
 __device__ __forceinline__ int rot_word_offset(int q, int w) { return (2 * q + (w >> 2)) * 512 + (w & 3) * 4; }
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-// 16 fp32 columns of this warp's 32 TMEM lanes (one row per lane).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // Decode of 4 column-bytes (32 columns) of one row.  w0, w1: the 4 plane-0
 // and plane-1 bytes.  The 2-bit code of column 8q + i is b0_i | b1_i << 1;
@@ -195,9 +156,6 @@ __device__ __forceinline__ uint4 decode_q(const Codes4& c, uint32_t tlo, uint32_
   return r;
 }
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // one arrival that also expects `bytes` of asynchronous copies
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -280,17 +238,6 @@ struct TcShape {
   static constexpr int planes = FMT == Q2_BPDQ ? 2 : FMT == Q2_LEECH ? (OFF4 ? 4 : 3) : 0;
 };
 static_assert(kAcol0 + kStagesA * TcShape<Q2_LEECH>::acols <= kTmemCols, "A stages exceed TMEM");
-
-// Shared-memory matrix descriptor (tcgen05) of a K-major operand with the
-// 128-byte swizzle: start >> 4 in bits 0-13, leading byte offset field 1
-// (not used by swizzled K-major layouts), stride byte offset 1024 >> 4 in
-// 32-45 (8 rows x 128 bytes), version 1 in 46-47, base offset 0, swizzle
-// mode 2 (128-byte) in 61-63.  A K step inside an atom adds its byte offset
-// to the start address.
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 
 // Leech: 3-bit codes b0 | b1 << 1 | b2 << 2 of the columns of 4 column-bytes
 // in nibble fields (the BPDQ split of codes4, with bit 2 from plane 2).
@@ -1109,14 +1056,18 @@ extern "C" int q2_tc_leech(const q2_handle* h, const void* x, void* y, int ntok,
   return q2::launch_tc<Q2_LEECH, false>(h, x, y, ntok, stream);
 }
 
+extern "C" int q2_int4_wait_limit(long long polls);    // q2_int4_tc.cu
+
 // Test hook: the poll limit of the tensor-core kernel's stage waits (0 = the
 // normal bound), on the current device.
 extern "C" int q2_debug_wait_limit(long long polls) {
   if (polls < 0) return Q2_EINVAL;
+  if (q2_int4_wait_limit(polls) != Q2_OK) return Q2_ECUDA;
   return cudaMemcpyToSymbol(q2_tc_stage_wait_limit, &polls, sizeof(polls)) == cudaSuccess ? Q2_OK : Q2_ECUDA;
 }
 
 extern "C" int q2_attend_errors(unsigned int* out);   // q2_attend.cu
+extern "C" int q2_int4_errors(unsigned int* out);     // q2_int4_tc.cu
 
 // Device-side error word of the tensor-core and attention kernels since the last call
 // (then cleared): 0 in normal operation, else the code of a bounded wait
@@ -1126,8 +1077,8 @@ extern "C" int q2_device_errors(unsigned int* out) {
   unsigned int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, q2_tc_error, sizeof(v)) != cudaSuccess) return Q2_ECUDA;
   if (cudaMemcpyToSymbol(q2_tc_error, &z, sizeof(z)) != cudaSuccess) return Q2_ECUDA;
-  unsigned int att = 0;
-  if (q2_attend_errors(&att) != Q2_OK) return Q2_ECUDA;
-  *out = v | att;
+  unsigned int att = 0, int4 = 0;
+  if (q2_attend_errors(&att) != Q2_OK || q2_int4_errors(&int4) != Q2_OK) return Q2_ECUDA;
+  *out = v | att | int4;
   return Q2_OK;
 }
