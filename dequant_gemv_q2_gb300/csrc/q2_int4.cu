@@ -506,7 +506,7 @@ int launch_tokens(const Int4Args& a, void* stream) {
 #ifndef TCN
 #define TCN 9
 #endif
-  if (a.ntok >= TCN) return q2_int4_tc(a, Q2_INT4_COLS / GPB, X8, stream);
+  if (a.ntok >= TCN && a.nblk >= 2) return q2_int4_tc(a, Q2_INT4_COLS / GPB, X8, stream);
   if (a.ntok <= 16) return launch_many<2, GPB, X8>(a, stream);
   if (a.ntok <= 32) return launch_many<4, GPB, X8>(a, stream);
   return launch_many<8, GPB, X8>(a, stream);

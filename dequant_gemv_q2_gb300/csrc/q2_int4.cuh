@@ -88,31 +88,45 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
+// (v & mask) | bits as one instruction (from two constants the compiler makes two)
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// What unpack_step takes off: 1024 + z of row g and -(64 + z) of row g + 8, as
+// pairs, from the rows' zero points as two bytes.
+struct Zeros {
+  uint32_t z0, z1;
+};
+__device__ __forceinline__ Zeros zeros_of(uint32_t zz) {
+  return Zeros{and_or(zz, 0xffu, 0x6400u) * 0x10001u, and_or(zz >> 4, 0xff0u, 0xd400u) * 0x10001u};
+}
+
 // One step's q - z (four columns of rows g and g + 8) as an operand fragment:
 // a0 and a2 of row g, a1 and a3 of row g + 8.  The word holds, from its lowest
-// four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, rows g and g + 8 in turn; zz
-// the rows' zero points as two bytes.
-__device__ __forceinline__ void unpack_step(uint32_t v, uint32_t zz, uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
-  const uint32_t z0 = and_or(zz, 0xffu, 0x6400u) * 0x10001u;                    // 1024 + z of row g
-  const uint32_t z1 = and_or(zz >> 4, 0xff0u, 0xd400u) * 0x10001u;              // -(64 + z) of row g + 8
+// four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, rows g and g + 8 in turn.
+__device__ __forceinline__ void unpack_step(uint32_t v, const Zeros& z, uint32_t& a0, uint32_t& a1, uint32_t& a2,
+                                            uint32_t& a3) {
   const uint32_t v8 = v >> 8;
-  a0 = hsub2(and_or(v, 0x000f000fu, 0x64006400u), z0);
-  a1 = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
-  a2 = hsub2(and_or(v8, 0x000f000fu, 0x64006400u), z0);
-  a3 = hfma2(and_or(v8, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
+  a0 = hsub2(and_or(v, 0x000f000fu, 0x64006400u), z.z0);
+  a1 = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z.z1);
+  a2 = hsub2(and_or(v8, 0x000f000fu, 0x64006400u), z.z0);
+  a3 = hfma2(and_or(v8, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z.z1);
 }
 
 // The block's eight steps.
 template <int GPB>
 __device__ __forceinline__ void unpack(const uint4 (&w)[2], const Sides<GPB>& k, uint32_t (&A)[8][4]) {
 #pragma unroll
-  for (int st = 0; st < 8; ++st) {
-    const int q = st / (8 / GPB);
-    unpack_step(word(w[st >> 2], st & 3), k.z[q >> 1] >> (16 * (q & 1)), A[st][0], A[st][1], A[st][2], A[st][3]);
+  for (int q = 0; q < GPB; ++q) {
+    const Zeros z = zeros_of(k.z[q >> 1] >> (16 * (q & 1)));
+#pragma unroll
+    for (int st = q * (8 / GPB); st < (q + 1) * (8 / GPB); ++st)
+      unpack_step(word(w[st >> 2], st & 3), z, A[st][0], A[st][1], A[st][2], A[st][3]);
   }
 }
 

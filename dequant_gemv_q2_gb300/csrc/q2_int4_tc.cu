@@ -2,27 +2,31 @@
 // 5th-generation tensor cores (tcgen05); the formula, the weights' layout and
 // the exact operands q - z are those of q2_int4.cuh.
 //
-// A CTA owns 128 rows (the instruction's M) and a range of 128-column blocks,
-// and runs them through rings of stages with four roles:
-//   - 8 decoder warps, two per TMEM lane quarter, copy their weights to
-//     shared memory RAW blocks ahead, unpack them to q - z in fp16 and store
-//     them to tensor memory.  The packed order is that of a 16 x 16 operand
-//     fragment, which is what tcgen05.st's 16x128b shape stores: no exchange;
-//   - 4 staging warps bring x of all tokens to shared memory in the 128-byte
-//     swizzle, columns in the packed order (a thread's 32 columns are four
-//     16-byte pieces transposed in registers) and 8-bit x turned to fp16;
+// Tiles of 128 rows (the instruction's M) are shared out over clusters of
+// CTAs, and the 128-column blocks of a cluster's tiles evenly over its CTAs,
+// one per SM: a CTA runs its run of blocks, across the ends of tiles, through
+// rings of stages with four roles:
+//   - 8 decoder warps, two per TMEM lane quarter taking blocks in turn, copy
+//     their weights to shared memory kRaw - 1 of their blocks ahead, unpack
+//     them to q - z in fp16 and store them to tensor memory.  The packed order
+//     is that of a 16 x 16 operand fragment, which is what tcgen05.st's
+//     16x128b shape stores: no exchange;
+//   - 8 staging warps bring x of all tokens to shared memory in the 128-byte
+//     swizzle, columns in the packed order (a thread's 32 columns of one token
+//     are four 16-byte pieces transposed in registers) and 8-bit x turned to
+//     fp16; a thread's loads run kAhead blocks ahead;
 //   - 2 issuing warps take blocks in turn: lane 0 issues the block's eight
 //     M = 128, K = 16 products and commits them.  An issuing thread that
 //     touches memory waits for its own queue of products, so with two of them
 //     one waits while the other's products run;
-//   - 4 summing warps, one per lane quarter, a row per lane, read each scale
-//     group's product from one of kAccs accumulators, multiply it by the
+//   - 8 summing warps, two per lane quarter (half of the tokens each), a row
+//     per lane, read each scale group's product from one of kAccs accumulators, multiply it by the
 //     group's scale and add it to the row's fp32 sums in registers: group
 //     scales cost no rounding, and the accumulator is free for another group.
-// An instruction costs the same for 16 to 64 tokens, so nothing depends on
-// the token count but the bytes of x.  The column range is split over a
-// cluster's CTAs where there are few row tiles, whose sums meet in rank order
-// in distributed shared memory.
+// A tile that begins and ends inside a CTA's run is written from those
+// registers while the next one's products run.  The others' sums meet at the
+// end in distributed shared memory, after one barrier of the cluster, and are
+// added in column order.
 //
 // Every wait is bounded: one that runs out sets the error word
 // (q2_device_errors) and a flag on which the other roles give up; the
@@ -31,6 +35,8 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 #include "q2_int4.cuh"
 #include "q2_tcgen.cuh"
@@ -43,31 +49,78 @@ __device__ long long q2_int4_stage_wait_limit = 0;           // 0: the normal bo
 namespace q2 {
 namespace {
 
-constexpr int kRows = 128, kDec = 8, kStage = 4, kIssue = 2, kSum = 4;   // rows; warps of each role
+constexpr int kRows = 128, kDec = 8, kStage = 8, kIssue = 2, kSum = 8;   // rows; warps of each role
+constexpr int kTurn = 2;                      // decoder warps of a lane quarter, blocks in turn
 constexpr int kThreads = (kDec + kStage + kIssue + kSum) * 32;
 constexpr int kRing = 4;                      // blocks in flight: A in tensor memory, x in shared memory
-constexpr int kAccs = 4;                      // accumulators of 64 columns
-constexpr int kRaw = 4;                       // blocks of packed weights in shared memory per decoder warp
-constexpr int kRawBytes = 2 * (512 + 64);     // two row tiles: half a block and the zero points
+constexpr int kAccs = 2 * kIssue;             // accumulators of 64 columns, two of each issuing warp (which so sees all their phases)
+constexpr int kRaw = 3;                       // its blocks of packed weights in shared memory per decoder warp
+constexpr int kRawTile = 1024 + 64, kRawBytes = 2 * kRawTile;   // two row tiles: a block and the zero points
 constexpr uint32_t kTmem = 512, kAcol = 64 * kAccs;
-constexpr int kOutLd = kRows + 4, kMaxSplit = 8;
-#ifndef TCB
-#define TCB (1ll << 22)
-#endif
-constexpr long long kBound = TCB;
+constexpr int kScales = 4;                    // blocks of scales in shared memory per summing warp
+constexpr int kStageWarps = kStage / 2;       // of a group
+constexpr int kOutLd = kRows + 4, kMaxCluster = 8;
 constexpr int kOneCta = 116 * 1024;           // at most one CTA of this or the other tcgen05 kernels per SM (each holds all of TMEM)
+constexpr int kBound = 1 << 20;               // polls of a wait (each may sleep for some microseconds)
+
+// Wait for the phase of the given parity, for at most `limit` polls; false
+// when they run out or `give_up` is set.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int limit, const volatile int* give_up) {
+  for (int i = 0; i < limit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (give_up && (i & 31) == 31 && *give_up) return false;
+  }
+  return false;
+}
+
+// One product, issued by lane 0 of a converged warp: outside a divergent
+// branch the operands stay in uniform registers (inside one each of them was
+// moved there again, about 115 cycles per product).
+__device__ __forceinline__ void mma_lane0(int lane, uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.eq.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lane)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lane0(int lane, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.eq.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lane)
+      : "memory");
+}
+
+// c += a * b, a pair at a time
+__device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
+  uint64_t& cc = reinterpret_cast<uint64_t&>(c);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+}
 
 struct TcArgs {
   Int4Args a;
-  int N, nsplit;                              // tokens rounded up to 16; CTAs of a row tile
+  int N, cs, ntiles;                          // tokens rounded up to 16; CTAs of a cluster; tiles of 128 rows
 };
 
-// 16 rows x 64 columns of operand fragments (four 16-column steps).
-__device__ __forceinline__ void tmem_st_frag(uint32_t at, const uint32_t (&r)[16]) {
+// 16 rows x 128 columns of operand fragments (eight 16-column steps).
+__device__ __forceinline__ void tmem_st_frag(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -87,23 +140,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
   const Int4Args& a = ta.a;
   constexpr int STEPS = 8 / GPB, esz = X8 ? 1 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = ta.N, nsplit = ta.nsplit, atom = N * 128, bbytes = 2 * atom;
-  const int rank = (int)blockIdx.x % nsplit, tile0 = (int)blockIdx.x / nsplit * (kRows / 16);
-  const int b0 = (int)((long long)a.nblk * rank / nsplit), n = (int)((long long)a.nblk * (rank + 1) / nsplit) - b0;
+  const int N = ta.N, cs = ta.cs, atom = N * 128, bbytes = 2 * atom;
+  // this CTA's run: blocks u0 .. u0 + n - 1 of the cluster's T, tile by tile
+  const int rank = (int)blockIdx.x % cs, cl = (int)blockIdx.x / cs, ncl = (int)gridDim.x / cs;
+  const int t0 = (int)((long long)ta.ntiles * cl / ncl), t1 = (int)((long long)ta.ntiles * (cl + 1) / ncl);
+  const int T = (t1 - t0) * a.nblk;
+  auto first_of = [&](int r) { return (int)((long long)T * r / cs); };
+  const int u0 = first_of(rank), n = first_of(rank + 1) - u0;
+  struct Place {
+    int tile, blk;
+  };
+  auto place_of = [&](int u) { return Place{t0 + u / a.nblk, u % a.nblk}; };
+  auto move = [&](Place& p, int by) {               // by <= kTurn <= nblk; whether it is another tile
+    p.blk += by;
+    if (p.blk < a.nblk) return false;
+    p.blk -= a.nblk;
+    ++p.tile;
+    return true;
+  };
   const uint32_t sB = (saddr(q2_int4tc_smem) + 1023u) & ~1023u;
   unsigned char* B = q2_int4tc_smem + (sB - saddr(q2_int4tc_smem));
-  const uint32_t sraw = sB + kRing * bbytes;
-  Bars* bar = reinterpret_cast<Bars*>(B + std::max(kRing * bbytes + kDec * kRaw * kRawBytes, N * kOutLd * 4));
+  const uint32_t sraw = sB + kRing * bbytes, ssc = sraw + kDec * kRaw * kRawBytes;
+  // the sums of a tile begun before this run, and of one not finished in it
+  float* part = reinterpret_cast<float*>(B + kRing * bbytes + kDec * kRaw * kRawBytes + kSum * kScales * 512);   // [2][N][kOutLd]
+  Bars* bar = reinterpret_cast<Bars*>(part + 2 * N * kOutLd);
   volatile int* give_up = &bar->abort;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(saddr(&bar->full[i]), kDec + kStage);
+      mbar_init(saddr(&bar->full[i]), kDec / kTurn + (N < 8 * kStageWarps ? N / 8 : kStageWarps));
       mbar_init(saddr(&bar->done[i]), 1);
     }
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(saddr(&bar->ready[i]), 1);
-      mbar_init(saddr(&bar->taken[i]), kSum);
+      mbar_init(saddr(&bar->taken[i]), N > 32 ? kSum : kSum / 2);
     }
     for (int i = 0; i < kIssue; ++i) mbar_init(saddr(&bar->drain[i]), 1);
     bar->abort = 0;
@@ -127,88 +197,126 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
     }
     return false;
   };
-  auto wait = [&](uint64_t& b, int phase, unsigned int code, long long limit = kBound) {
-    return __all_sync(~0u, mbar_wait(saddr(&b), (uint32_t)phase & 1u, limit, give_up)) ? true : failed(code);
+  auto wait = [&](uint64_t& b, int phase, unsigned int code, int limit = kBound) {
+    return __all_sync(~0u, wait_phase(saddr(&b), (uint32_t)phase & 1u, limit, give_up)) ? true : failed(code);
   };
-  float acc[64];
+  float2 acc[16];                                   // 32 tokens
 
   if (warp < kDec) {
-    // ---- decoders: half `hf` of the blocks of row tiles 2 * quarter, + 1
-    const int quarter = warp & 3, hf = warp >> 2, g = lane >> 2;
+    // ---- decoders: row tiles 2 * quarter, + 1 of every kTurn-th block
+    const int quarter = warp & 3, turn = warp >> 2, g = lane >> 2;
     const uint32_t raw = sraw + warp * (kRaw * kRawBytes);
+    const bool zcopy = a.zeros && lane < GPB;
+    Place at = place_of(u0 + turn);                 // of the next block to copy
     const unsigned char* src[2];
-    for (int m = 0; m < 2; ++m)                     // a missing row tile: the last one; its rows are not stored
-      src[m] = a.w + ((size_t)min(tile0 + 2 * quarter + m, a.ntile - 1) * a.nblk + b0) * a.item;
-    auto copy = [&](int i) {
+    auto point = [&]() {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)                   // a missing row tile: the last one; its rows are not stored
+        src[m] = a.w + ((size_t)min(at.tile * (kRows / 16) + 2 * quarter + m, a.ntile - 1) * a.nblk + at.blk) * a.item +
+                 lane * 16;
+    };
+    point();
+    auto copy = [&](int i, uint32_t slot) {
       if (i < n) {
-        const uint32_t d = raw + (i % kRaw) * kRawBytes;
+        const uint32_t d = slot + lane * 16;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          cp16(d + m * 576 + lane * 16, src[m] + hf * 512 + lane * 16);
-          if (a.zeros && lane < GPB) cp16(d + m * 576 + 512 + lane * 16, src[m] + 1024 + GPB * 32 + lane * 16);
-          src[m] += a.item;
+          cp16(d + m * kRawTile, src[m]);
+          cp16(d + m * kRawTile + 512, src[m] + 512);
+          if (zcopy) cp16(d + m * kRawTile + 1024, src[m] + 1024 + GPB * 32);
+          src[m] += kTurn * a.item;
         }
+        if (move(at, kTurn)) point();
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int i = 0; i < kRaw - 1; ++i) copy(i);
-    for (int i = 0; i < n && ok; ++i) {
+    for (int k = 0; k < kRaw - 1; ++k) copy(turn + k * kTurn, raw + k * kRawBytes);
+    uint32_t slot = raw, before = raw + (kRaw - 1) * kRawBytes;
+    int stored = -1;                                // stage whose stores are under way
+    auto arrive = [&]() {
+      if (stored >= 0) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(saddr(&bar->full[stored]));
+      }
+    };
+    for (int i = turn; i < n; i += kTurn) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
       __syncwarp();
-      copy(i + kRaw - 1);
+      copy(i + (kRaw - 1) * kTurn, before);
       const int st = i % kRing;
-      uint32_t A[2][16];
+      if (i - kRing < kTurn && i >= kRing) pdl_wait();       // no bounded wait may have to wait for the previous kernel
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const uint32_t at = raw + (i % kRaw) * kRawBytes + m * 576;
-        const uint4 w = lds128(at + lane * 16);
+        const uint32_t from = slot + m * kRawTile;
+        const uint4 w[2] = {lds128(from + lane * 16), lds128(from + 512 + lane * 16)};
+        uint32_t A[32];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int q = GPB == 1 ? 0 : GPB == 2 ? hf : 2 * hf + (t >> 1);          // the step's scale group
-          const uint32_t zz = a.zeros ? lds16(at + 512 + (g * GPB + q) * 2) : 0x0808u;
-          unpack_step(word(w, t), zz, A[m][4 * t], A[m][4 * t + 1], A[m][4 * t + 2], A[m][4 * t + 3]);
+        for (int q = 0; q < GPB; ++q) {
+          const Zeros z = a.zeros ? zeros_of(lds16(from + 1024 + (g * GPB + q) * 2)) : Zeros{0x64086408u, 0xd480d480u};
+#pragma unroll
+          for (int t = q * STEPS; t < (q + 1) * STEPS; ++t)
+            unpack_step(word(w[t >> 2], t & 3), z, A[4 * t], A[4 * t + 1], A[4 * t + 2], A[4 * t + 3]);
         }
+        if (m == 0) {
+          arrive();                                 // for the block before
+          stored = -1;
+          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 1u);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st_frag(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + kAcol + st * 64, A);
       }
-      if (i == kRing) pdl_wait();                   // no bounded wait may have to wait for the previous kernel
-      if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 1u);
       if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-        tmem_st_frag(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + kAcol + st * 64 + hf * 32, A[m]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
+      stored = st;
+      before = slot;
+      slot = slot == raw + (kRaw - 1) * kRawBytes ? raw : slot + kRawBytes;
     }
+    arrive();
+    tmem_wait_st();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < kDec + kStage) {
-    // ---- x: task (token t, run q of 32 columns): 64 (32) bytes in, four 16-byte pieces out
-    const int tid = threadIdx.x - kDec * 32, ntask = N * 4;
-    uint4 v[2][4];
+    // (two groups of warps, blocks in turn: a block's loads are under way for
+    // two blocks' time)
+    const int group = (warp - kDec) / kStageWarps, tid = threadIdx.x - (kDec + group * kStageWarps) * 32;
+    constexpr int TASKS = 256 / (kStageWarps * 32), PIECES = X8 ? 2 : 4;
+    if (tid / 32 < N / 8) {                         // a warp for 32 of the 4 * N tasks
+    const unsigned char* row[TASKS];
+    unsigned char* to[TASKS];
+    int key[TASKS], last[TASKS];                    // blocks in which the token has this run
+#pragma unroll
+    for (int k = 0; k < TASKS; ++k) {
+      const int e = tid + k * (kStageWarps * 32), t = e % N, q = e / N;
+      const bool live = q < 4 && t < a.ntok;
+      row[k] = static_cast<const unsigned char*>(a.x) + ((size_t)(live ? t : 0) * a.C + q * 32) * esz;
+      to[k] = B + (q >> 1) * atom + t * 128;
+      key[k] = (4 * (q & 1)) ^ (t & 7);
+      last[k] = live ? (a.C - q * 32 + 127) / 128 : 0;
+    }
+    const bool second = TASKS > 1 && tid + kStageWarps * 32 < 4 * N;
+    uint4 v[TASKS][PIECES];
+    Place at = place_of(u0 + group);                // of the next block to load
     auto load = [&](int i) {
       if (i < n) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int e = tid + k * (kStage * 32), t = e % N, q = e / N, c = (b0 + i) * 128 + q * 32;
-          const bool live = e < ntask && t < a.ntok && c < a.C;
-          const uint4* from =
-              reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + ((size_t)t * a.C + c) * esz);
+        for (int k = 0; k < TASKS; ++k) {
+          const uint4* from = reinterpret_cast<const uint4*>(row[k] + at.blk * (128 * esz));
 #pragma unroll
-          for (int p = 0; p < (X8 ? 2 : 4); ++p) v[k][p] = live ? from[p] : make_uint4(0, 0, 0, 0);
+          for (int p = 0; p < PIECES; ++p) v[k][p] = at.blk < last[k] ? from[p] : make_uint4(0, 0, 0, 0);
         }
+        move(at, 2);
       }
     };
     pdl_wait();                                     // x may come from the previous kernel
-    load(0);
-    for (int i = 0; i < n && ok; ++i) {
+    load(group);
+    for (int i = group; i < n; i += 2) {
       const int st = i % kRing;
       if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
       if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int e = tid + k * (kStage * 32), t = e % N, q = e / N;
-        if (e < ntask) {
+      for (int k = 0; k < TASKS; ++k) {
+        if (k == 0 || second) {
           uint32_t in[4][4];                        // run j of 8 columns, pair p
           if constexpr (X8) {
 #pragma unroll
@@ -222,153 +330,223 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
 #pragma unroll
               for (int p = 0; p < 4; ++p) in[j][p] = word(v[k][j], p);
           }
-          unsigned char* d = B + st * bbytes + (q >> 1) * atom + t * 128;
+          unsigned char* d = to[k] + st * bbytes;
 #pragma unroll
           for (int p = 0; p < 4; ++p)
-            *reinterpret_cast<uint4*>(d + (((4 * (q & 1) + p) ^ (t & 7)) << 4)) =
-                make_uint4(in[0][p], in[1][p], in[2][p], in[3][p]);
+            *reinterpret_cast<uint4*>(d + ((key[k] ^ p) << 4)) = make_uint4(in[0][p], in[1][p], in[2][p], in[3][p]);
         }
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
-      load(i + 1);
+      load(i + 2);
+    }
     }
   } else if (warp < kDec + kStage + kIssue) {
     // ---- products of every kIssue-th block
     pdl_wait();
-    const int me = warp - kDec - kStage;
+    const int me = __shfl_sync(~0u, warp, 0) - kDec - kStage;
     const uint32_t idesc = idesc_f16(kRows, N);
-    const long long limit = q2_int4_stage_wait_limit > 0 ? q2_int4_stage_wait_limit : kBound;
+    const int limit = q2_int4_stage_wait_limit > 0 ? (int)std::min(q2_int4_stage_wait_limit, (long long)kBound) : kBound;
     for (int i = me; i < n && ok; i += kIssue) {
       const int st = i % kRing;
       ok = wait(bar->full[st], i / kRing, 3u, limit);
-      for (int q = 0; q < GPB && ok; ++q) {
-        const int gi = i * GPB + q, d = gi % kAccs;
-        if (gi >= kAccs) ok = wait(bar->taken[d], gi / kAccs - 1, 4u);
+#pragma unroll
+      for (int q = 0; q < GPB; ++q) {
+        if (!ok) break;
+        const int gi = i / kIssue * GPB + q, d = 2 * me + (gi & 1);    // this warp's groups in turn
+        if (gi >= 2) ok = wait(bar->taken[d], gi / 2 - 1, 4u);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t bs = sB + st * bbytes, at = tmem + kAcol + st * 64;
+        const uint32_t at = tmem + kAcol + st * 64 + q * (STEPS * 8), acc0 = tmem + d * 64;
+        const uint64_t lo = sdesc_sw128(sB + st * bbytes), hi = sdesc_sw128(sB + st * bbytes + atom);
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const int k = q * STEPS + s;
-            mma_f16_ta(tmem + d * 64, at + k * 8, sdesc_sw128(bs + (k >> 2) * atom + (k & 3) * 32), idesc, s > 0 ? 1u : 0u);
-          }
-          mma_commit(saddr(&bar->ready[d]));
-          if (q + 1 == GPB) mma_commit(saddr(&bar->done[st]));
+        for (int s = 0; s < STEPS; ++s) {
+          const int k = q * STEPS + s;
+          mma_lane0(lane, acc0, at + s * 8, (k < 4 ? lo : hi) + (k & 3) * 2, idesc, s > 0 ? 1u : 0u);
         }
+        commit_lane0(lane, saddr(&bar->ready[d]));
+        if (q + 1 == GPB) commit_lane0(lane, saddr(&bar->done[st]));
         __syncwarp();
       }
     }
     // whatever was issued is waited for, with the full bound, on every path
     if (lane == 0) mma_commit(saddr(&bar->drain[me]));
     __syncwarp();
-    if (!__all_sync(~0u, mbar_wait(saddr(&bar->drain[me]), 0u, kBound))) ok = failed(5u);
+    if (!__all_sync(~0u, wait_phase(saddr(&bar->drain[me]), 0u, kBound, nullptr))) ok = failed(5u);
   } else {
-    // ---- sums: lane = row `row` of the tile
-    const int quarter = warp & 3, row = quarter * 32 + lane, g = row & 7, half = (row >> 3) & 1;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    const unsigned char* side = a.w + ((size_t)min(tile0 + (row >> 4), a.ntile - 1) * a.nblk + b0) * a.item + 1024;
-    auto scales = [&](__half(&s)[GPB], int i) {
+    // ---- sums: lane = row `row` of the tile, tokens c0 .. c0 + 31
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const int c0 = (warp - kDec - kStage - kIssue) / 4 * 32;
+    if (c0 < N) {
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+    // the scales of rows row % 8 and row % 8 + 8 of the row tile, kScales - 1 blocks ahead
+    Place at = place_of(u0), now = at;              // of the next scales to copy, of the block in use
+    const uint32_t ring = ssc + (warp - kDec - kStage - kIssue) * (kScales * 32 * GPB * 4) + lane * (GPB * 4);
+    const unsigned char* side;
+    auto point = [&]() {
+      side = a.w + ((size_t)min(at.tile * (kRows / 16) + (row >> 4), a.ntile - 1) * a.nblk + at.blk) * a.item + 1024 +
+             (row & 7) * (GPB * 4);
+    };
+    point();
+    auto copy = [&](int i) {
       if (i < n) {
-        const __half* p = reinterpret_cast<const __half*>(side + (size_t)i * a.item) + g * (2 * GPB) + half;
-#pragma unroll
-        for (int q = 0; q < GPB; ++q) s[q] = p[2 * q];
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ring + (i % kScales) * (32 * GPB * 4)), "l"(side),
+                     "n"(GPB * 4)
+                     : "memory");
+        side += a.item;
+        if (move(at, 1)) point();
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int t = 0; t < 64; ++t) acc[t] = 0.f;
+    for (int t = 0; t < 16; ++t) acc[t] = make_float2(0.f, 0.f);
+    for (int k = 0; k < kScales - 1; ++k) copy(k);
     pdl_wait();
-    __half s0[GPB], s1[GPB], s2[GPB];
-    scales(s0, 0);
-    scales(s1, 1);
-    for (int i = 0; i < n && ok; ++i) {
-      scales(s2, i + 2);
+    bool begun = now.blk == 0;                      // the tile in use began in this run
+    for (int i = 0; i < n; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kScales - 2) : "memory");
+      copy(i + kScales - 1);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
-        const int gi = i * GPB + q, d = gi % kAccs;
-        if (ok) ok = wait(bar->ready[d], gi / kAccs, 6u);
-        if (!ok) break;
-        tc_fence_after();
-        const float s = __half2float(s0[q]);
+        const int gi = i / kIssue * GPB + q, d = 2 * (i % kIssue) + (gi & 1);
+        if (ok) ok = wait(bar->ready[d], gi / 2, 6u);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t sw = lds16(ring + (i % kScales) * (32 * GPB * 4) + q * 4 + ((row >> 3) & 1) * 2);
+          const float s1 = __half2float(__ushort_as_half((unsigned short)sw));
+          const float2 s2 = make_float2(s1, s1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c * 16 < N) {
-            float v[16];
-            tmem_ld16(tl + d * 64 + c * 16, v);
+          for (int h = 0; h < 2; ++h)
+            if (c0 + 16 * h < N) {
+              float v[16];
+              tmem_ld16(tl + d * 64 + 16 * h, v);
 #pragma unroll
-            for (int t = 0; t < 16; ++t) acc[c * 16 + t] = fmaf(s, v[t], acc[c * 16 + t]);
+              for (int t = 0; t < 8; ++t) fma2(acc[8 * h + t], s2, make_float2(v[2 * t], v[2 * t + 1]));
+            }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(saddr(&bar->taken[d]));
+        }
+      }
+      const bool ends = now.blk + 1 == a.nblk;
+      if (ends || i + 1 == n) {                     // a tile's end, or the run's; NaN where a wait ran out
+        const int r = now.tile * kRows + row;
+        float* o = part + (begun ? N * kOutLd : 0) + c0 * kOutLd + row;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) {
+          const float v = ok ? (t & 1 ? acc[t >> 1].y : acc[t >> 1].x) : __int_as_float(0x7fc00000);
+          if (!(ends && begun)) {
+            if (c0 + t < N) o[t * kOutLd] = v;
+          } else if (r < a.R && c0 + t < a.ntok) {
+            a.y[(size_t)(c0 + t) * a.R + r] = __float2half_rn(X8 ? v * a.xs[c0 + t] : v);
           }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(saddr(&bar->taken[d]));
-      }
+        }
 #pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        s0[q] = s1[q];
-        s1[q] = s2[q];
+        for (int t = 0; t < 16; ++t) acc[t] = make_float2(0.f, 0.f);
+        begun = true;
       }
+      move(now, 1);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
   pdl_wait();                                       // before anything writes y (returns at once if done)
-  ok = __syncthreads_and(ok);
-  // ---- the sums, or NaN where a wait ran out, over the rings (all copies and products are done)
-  float* out = reinterpret_cast<float*>(B);
-  if (warp >= kDec + kStage + kIssue) {
-    const int row = (warp & 3) * 32 + lane;
-#pragma unroll
-    for (int t = 0; t < 64; ++t)
-      if (t < N) out[t * kOutLd + row] = ok ? acc[t] : __int_as_float(0x7fc00000);
-  }
   cg::cluster_group cluster = cg::this_cluster();
-  if (nsplit > 1) cluster.sync();
-  else __syncthreads();
-  const int row0 = tile0 * 16, all = a.ntok * kRows;
-  const int e0 = (int)((long long)all * rank / nsplit), e1 = (int)((long long)all * (rank + 1) / nsplit);
-  for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
-    const int t = e / kRows, r = e % kRows;
-    float v;
-    if (nsplit == 1) {
-      v = out[t * kOutLd + r];
-    } else {
-      float p[kMaxSplit];
+  if (cs > 1) {
+    cluster.sync();
+    // the tile that this run begins in the middle of, and the one it leaves
+    // unfinished: this CTA's share of the rows of each
+    const int head = u0 / a.nblk, tail = (u0 + n - 1) / a.nblk;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int tile = k ? tail : head, s = tile * a.nblk, e = s + a.nblk;
+      const bool open = k ? tail != head && e > u0 + n : s < u0 || e > u0 + n;
+      if (!open) continue;
+      auto rank_of = [&](int u) { return (int)((((long long)u + 1) * cs - 1) / T); };
+      const int r0 = rank_of(s), cnt = rank_of(e - 1) - r0 + 1, all = a.ntok * kRows;
+      const int e0 = all * (rank - r0) / cnt, e1 = all * (rank - r0 + 1) / cnt;
+      for (int x = e0 + threadIdx.x; x < e1; x += kThreads) {
+        const int t = x / kRows, r = x % kRows;
+        float p[kMaxCluster];
 #pragma unroll
-      for (int k = 0; k < kMaxSplit; ++k) p[k] = k < nsplit ? cluster.map_shared_rank(out, k)[t * kOutLd + r] : 0.f;
-      v = p[0];
+        for (int c = 0; c < kMaxCluster; ++c)       // the first CTA has the tile as its last, the others as their first
+          p[c] = c < cnt ? cluster.map_shared_rank(part, r0 + c)[(c ? 0 : N * kOutLd) + t * kOutLd + r] : 0.f;
+        float v = p[0];
 #pragma unroll
-      for (int k = 1; k < kMaxSplit; ++k) v += p[k];
+        for (int c = 1; c < kMaxCluster; ++c) v += p[c];
+        const int row = (t0 + tile) * kRows + r;
+        if (X8) v *= a.xs[t];
+        if (row < a.R) a.y[(size_t)t * a.R + row] = __float2half_rn(v);
+      }
     }
-    if (X8) v *= a.xs[t];
-    if (row0 + r < a.R) a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(v);
+    cluster.sync();                                 // every CTA's sums stay readable until all are done
   }
-  if (nsplit > 1) cluster.sync();                   // every CTA's sums stay readable until all are done
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
+// Clusters of cs CTAs that the device runs at once (a cluster lives in one
+// GPC, so this is not SMs / cs); asked for once.
+int clusters_at_once(const void* fn, int cs, int smem) {
+  struct Known {
+    int dev, cs, smem, n;
+    const void* fn;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known& k : known)
+    if (k.dev == dev && k.cs == cs && k.smem == smem && k.fn == fn) return k.n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = 1;
+  }
+  known.push_back({dev, cs, smem, n, fn});
+  return n;
+}
+
 template <int GPB, bool X8>
 int launch_tc(const Int4Args& a, void* stream) {
+  auto kernel = k_int4_tc<GPB, X8>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
   TcArgs ta = {};
   ta.a = a;
   ta.N = (a.ntok + 15) / 16 * 16;
-  const int work = std::max(kRing * ta.N * 256 + kDec * kRaw * kRawBytes, ta.N * kOutLd * 4);
+  ta.ntiles = (a.ntile + kRows / 16 - 1) / (kRows / 16);
+  const int work = kRing * ta.N * 256 + kDec * kRaw * kRawBytes + kSum * kScales * 512 + 2 * ta.N * kOutLd * 4;
   const int smem = std::max(kOneCta, 1024 + work + (int)sizeof(Bars));
-  if (set_smem(reinterpret_cast<const void*>(k_int4_tc<GPB, X8>), smem)) return Q2_ECUDA;
-  const int tiles = (a.ntile + kRows / 16 - 1) / (kRows / 16), sms = dev_info().sms;
-  // Waves of CTAs (one per SM) times their blocks plus a fixed cost of about ten.
-  ta.nsplit = 1;
-  long long best = 0;
-  for (int s = 1; s <= kMaxSplit && 2 * s <= a.nblk; ++s) {
-    const long long cost = (long long)((tiles * s + sms - 1) / sms) * ((a.nblk + s - 1) / s + 10);
-    if (s == 1 || cost < best) {
+  if (set_smem(fn, smem)) return Q2_ECUDA;
+  // The cluster size with the shortest run of blocks, each doubling of it
+  // counted as three blocks (its barriers and the meeting of its sums).
+  int clusters = 1;
+  double best = 0;
+  for (int cs = 1, lg = 0; cs <= kMaxCluster && cs <= a.nblk; cs *= 2, ++lg) {
+    const int n = std::min(ta.ntiles, cs == 1 ? dev_info().sms : clusters_at_once(fn, cs, smem));
+    const double cost = (double)((ta.ntiles + n - 1) / n) * a.nblk / cs + 3 * lg;
+    if (cs == 1 || cost < best) {
       best = cost;
-      ta.nsplit = s;
+      ta.cs = cs;
+      clusters = n;
     }
   }
-  return launch_clusters(k_int4_tc<GPB, X8>, tiles, ta.nsplit, kThreads, smem, stream, ta);
+  return launch_clusters(kernel, clusters, ta.cs, kThreads, smem, stream, ta);
 }
 
 }  // namespace
