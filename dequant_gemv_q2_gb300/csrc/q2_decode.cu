@@ -69,7 +69,7 @@ __global__ void k_dec_int4(const unsigned char* w, float* out, int R, int C, int
     const int r = (int)(e / C), c = (int)(e % C), cc = c % Q2_INT4_COLS, p = (r >> 3) & 1;
     const unsigned char* it = w + ((size_t)(r >> 4) * nblk + c / Q2_INT4_COLS) * item;
     const unsigned char* side = it + Q2_INT4_BLOCK_BYTES;
-    const int j = (cc >> 3) & 3, t = (cc >> 5) * 2 + ((cc >> 2) & 1), k = cc & 3;
+    const int j = (cc >> 1) & 3, t = cc >> 4, k = ((cc >> 3) & 1) * 2 + (cc & 1);
     const uint32_t v = *reinterpret_cast<const uint32_t*>(it + (t >> 2) * 512 + ((r & 7) * 4 + j) * 16 + (t & 3) * 4);
     const int nib = (k & 1) * 4 + (k >> 1) * 2 + p;
     const int at = ((r & 7) * gpb + cc / group) * 2 + p;

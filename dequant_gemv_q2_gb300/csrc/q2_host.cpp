@@ -340,10 +340,10 @@ int q2_pack_leech(const int8_t* v, const uint16_t* tail, const uint16_t* scale,
   return Q2_OK;
 }
 
-// The step's four columns of one row, spread to every eighth bit: column 0 to
-// bit 0, 2 to bit 8, 1 to bit 16, 3 to bit 24 (two code bytes in).
-static inline uint32_t int4_spread(const uint8_t* c) {
-  return (uint32_t)(c[0] & 15) | (uint32_t)(c[1] & 15) << 8 | (uint32_t)(c[0] >> 4) << 16 | (uint32_t)(c[1] >> 4) << 24;
+// Four columns of one row, two code bytes, spread to every eighth bit: low
+// halves to bits 0 and 8, high halves to bits 16 and 24.
+static inline uint32_t int4_spread(uint8_t a, uint8_t b) {
+  return (uint32_t)(a & 15) | (uint32_t)(b & 15) << 8 | (uint32_t)(a >> 4) << 16 | (uint32_t)(b >> 4) << 24;
 }
 
 int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero,
@@ -366,7 +366,6 @@ int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero
   int st = finish(b, out, out_bytes, &fill);
   if (st || !fill) return st;
   unsigned char* w = sec(out, b.hdr, SEC_INT4_W);
-  const uint8_t none[2] = {0x88, 0x88};          // q = 8 outside the matrix
   for (int rt = 0; rt < ntile; ++rt)
     for (int g = 0; g < 8; ++g) {                // rows rt*16 + g and + 8
       const int r0 = rt * 16 + g, r1 = r0 + 8;
@@ -375,9 +374,11 @@ int q2_pack_int4(const uint8_t* code, const uint16_t* scale, const uint8_t* zero
       for (int blk = 0; blk < nblk; ++blk) {
         unsigned char* it = w + ((size_t)rt * nblk + blk) * item;
         unsigned char* side = it + Q2_INT4_BLOCK_BYTES;
-        for (int k = 0; k < 32; ++k) {           // runs of 4 columns: lane part j, step t
-          const int j = (k >> 1) & 3, t = (k >> 3) * 2 + (k & 1), c = blk * Q2_INT4_COLS + 4 * k;
-          const uint32_t lo = int4_spread(c0 && c < C ? c0 + c / 2 : none), hi = int4_spread(c1 && c < C ? c1 + c / 2 : none);
+        for (int k = 0; k < 32; ++k) {           // lane part j, step t: code bytes j and j + 4 of the step's eight
+          const int j = k & 3, t = k >> 2, at = blk * (Q2_INT4_COLS / 2) + 8 * t + j;
+          const bool in = 2 * at < C;            // q = 8 outside the matrix
+          const uint32_t lo = c0 && in ? int4_spread(c0[at], c0[at + 4]) : 0x08080808u;
+          const uint32_t hi = c1 && in ? int4_spread(c1[at], c1[at + 4]) : 0x08080808u;
           const uint32_t v = lo | hi << 4;
           std::memcpy(it + (t >> 2) * 512 + (g * 4 + j) * 16 + (t & 3) * 4, &v, 4);
         }

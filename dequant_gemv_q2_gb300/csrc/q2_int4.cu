@@ -110,11 +110,27 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 
   pdl_wait();                                               // x may come from the previous kernel
   pdl_trigger();
+  // x in the order of the products' operands: a lane's words of two steps are
+  // consecutive (16 bytes of fp16, 8 of 8-bit integers)
   for (int e = lane; e < nb * a.ntok * (XB / 16); e += 32) {
     const int p = e % (XB / 16), kt = e / (XB / 16), k = a.ntok == 2 ? kt >> 1 : kt, t = kt - k * a.ntok;
     const int c = (b0 + k) * 128 + p * (16 / esz);
     const uint4* from = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + ((size_t)t * a.C + c) * esz);
-    reinterpret_cast<uint4*>(xs)[e] = c < a.C ? *from : make_uint4(0, 0, 0, 0);
+    const uint4 v = c < a.C ? *from : make_uint4(0, 0, 0, 0);
+    uint32_t* to = reinterpret_cast<uint32_t*>(xs + kt * XB);
+    if constexpr (X8) {                                     // columns 16p ..: step p
+      to += (p >> 1) * 8 + (p & 1);
+      to[0] = __byte_perm(v.x, v.z, 0x5410);
+      to[2] = __byte_perm(v.x, v.z, 0x7632);
+      to[4] = __byte_perm(v.y, v.w, 0x5410);
+      to[6] = __byte_perm(v.y, v.w, 0x7632);
+    } else {                                                // columns 8p ..: half p % 2 of step p / 2
+      to += (p >> 2) * 16 + (p & 3);
+      to[0] = v.x;
+      to[4] = v.y;
+      to[8] = v.z;
+      to[12] = v.w;
+    }
   }
   __syncwarp();
   // A lane's columns of one token (token g, of two: the other columns of the
@@ -122,10 +138,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   const uint32_t xl = saddr(xs) + (g & (a.ntok - 1)) * XB + j * (8 * esz);
   const int xblk = a.ntok * XB;
   auto xload = [&](uint32_t(&b)[16], uint32_t from) {
-    load_b<X8>(b, [&](int r) {
-      if constexpr (X8) return lds64(from + r * (32 * esz));
-      else return lds128(from + r * (32 * esz));
-    });
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (X8) {
+        const uint2 v = lds64(from + r * 32);
+        int8x4(v.x, b[4 * r], b[4 * r + 1]);
+        int8x4(v.y, b[4 * r + 2], b[4 * r + 3]);
+      } else {
+        const uint4 v = lds128(from + r * 64);
+        b[4 * r] = v.x;
+        b[4 * r + 1] = v.y;
+        b[4 * r + 2] = v.z;
+        b[4 * r + 3] = v.w;
+      }
+    }
   };
   for (int k = 0; k < nb; ++k) {
     uint32_t b[16];
@@ -236,7 +262,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
-__host__ __device__ constexpr int x_row_bytes() { return X8 ? 128 + 32 : 256 + 64; }
+__host__ __device__ constexpr int x_row_bytes() { return X8 ? 128 + 16 : 256 + 16; }
 template <int NT>
 __host__ __device__ constexpr int many_stages() { return NT == 8 || NT == 2 ? 3 : NT == 1 ? MS : 4; }
 template <int NT>
@@ -326,13 +352,23 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
     weights(i + STAGES - 1, last);
     xstage(i + STAGES - 1, last);
     Sides<GPB> sd[MT];
-    const uint32_t base = ring + st * stage, xb = base + g * ROWB + j * (8 * esz);
+    const uint32_t base = ring + st * stage;
+    // 8-bit x: this lane's pairs of token g; fp16: the row and piece whose address this lane gives a matrix load
+    const uint32_t xb = base + (X8 ? g * ROWB + 2 * j : (lane & 7) * ROWB + (lane >> 3) * 16);
     auto xload = [&](uint32_t(&b)[16], int t) {
-      load_b<X8>(b, [&](int k) {
-        const uint32_t at = xb + t * 8 * ROWB + k * (32 * esz);
-        if constexpr (X8) return lds64(at);
-        else return lds128(at);
-      });
+      if constexpr (X8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = xb + t * 8 * ROWB + k * 16;
+          int8x4(lds16(at) | lds16(at + 8) << 16, b[2 * k], b[2 * k + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(b[4 * k]), "=r"(b[4 * k + 1]), "=r"(b[4 * k + 2]), "=r"(b[4 * k + 3])
+                       : "r"(xb + t * 8 * ROWB + k * 64));
+      }
     };
     uint4 w[MT][2];
 #pragma unroll

@@ -150,34 +150,6 @@ __device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
   hi = hsub2(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u);
 }
 
-// The B operands of one block for one token: 8 consecutive columns in each of
-// the block's four runs of 32, 16 bytes of fp16 or 8 bytes of 8-bit integers.
-template <bool X8, typename L>
-__device__ __forceinline__ void load_b(uint32_t (&b)[16], L&& load) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const auto v = load(k);
-    if constexpr (X8) {
-      int8x4(v.x, b[4 * k], b[4 * k + 1]);
-      int8x4(v.y, b[4 * k + 2], b[4 * k + 3]);
-    } else {
-      b[4 * k] = v.x;
-      b[4 * k + 1] = v.y;
-      b[4 * k + 2] = v.z;
-      b[4 * k + 3] = v.w;
-    }
-  }
-}
-
-template <bool X8>
-struct XVec {
-  using T = uint4;
-};
-template <>
-struct XVec<true> {
-  using T = uint2;
-};
-
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
 // Launch in clusters of cs CTAs, programmatic stream serialization allowed.

@@ -11,10 +11,9 @@
 //     them to q - z in fp16 and store them to tensor memory.  The packed order
 //     is that of a 16 x 16 operand fragment, which is what tcgen05.st's
 //     16x128b shape stores: no exchange;
-//   - 8 staging warps bring x of all tokens to shared memory in the 128-byte
-//     swizzle, columns in the packed order (a thread's 32 columns of one token
-//     are four 16-byte pieces transposed in registers) and 8-bit x turned to
-//     fp16; a thread's loads run kAhead blocks ahead;
+//   - x of all tokens comes to shared memory in the 128-byte swizzle: fp16 by
+//     TMA, which one warp asks for; 8-bit x through the registers of 8 staging
+//     warps, which turn it to fp16;
 //   - 2 issuing warps take blocks in turn: lane 0 issues the block's eight
 //     M = 128, K = 16 products and commits them.  An issuing thread that
 //     touches memory waits for its own queue of products, so with two of them
@@ -33,6 +32,7 @@
 // products issued are waited for before tensor memory is released, and the
 // CTA's rows come out NaN.
 #include <cooperative_groups.h>
+#include <cuda.h>
 
 #include <algorithm>
 #include <mutex>
@@ -49,16 +49,19 @@ __device__ long long q2_int4_stage_wait_limit = 0;           // 0: the normal bo
 namespace q2 {
 namespace {
 
-constexpr int kRows = 128, kDec = 8, kStage = 8, kIssue = 2, kSum = 8;   // rows; warps of each role
+constexpr int kRows = 128, kDec = 8, kIssue = 2, kSum = 8;   // rows; warps of the roles but staging
+template <bool X8>
+__host__ __device__ constexpr int stage_warps() { return X8 ? 8 : 2; }
+template <bool X8>
+__host__ __device__ constexpr int tc_threads() { return (kDec + stage_warps<X8>() + kIssue + kSum) * 32; }
 constexpr int kTurn = 2;                      // decoder warps of a lane quarter, blocks in turn
-constexpr int kThreads = (kDec + kStage + kIssue + kSum) * 32;
 constexpr int kRing = 4;                      // blocks in flight: A in tensor memory, x in shared memory
 constexpr int kAccs = 2 * kIssue;             // accumulators of 64 columns, two of each issuing warp (which so sees all their phases)
 constexpr int kRaw = 3;                       // its blocks of packed weights in shared memory per decoder warp
 constexpr int kRawTile = 1024 + 64, kRawBytes = 2 * kRawTile;   // two row tiles: a block and the zero points
 constexpr uint32_t kTmem = 512, kAcol = 64 * kAccs;
 constexpr int kScales = 4;                    // blocks of scales in shared memory per summing warp
-constexpr int kStageWarps = kStage / 2;       // of a group
+constexpr int kStageWarps = 4;                // staging warps of a group (8-bit x)
 constexpr int kOutLd = kRows + 4, kMaxCluster = 8;
 constexpr int kOneCta = 116 * 1024;           // at most one CTA of this or the other tcgen05 kernels per SM (each holds all of TMEM)
 constexpr int kBound = 1 << 20;               // polls of a wait (each may sleep for some microseconds)
@@ -108,6 +111,7 @@ __device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
 }
 
 struct TcArgs {
+  CUtensorMap xmap;                           // fp16 x: box of 64 columns x N tokens, 128-byte swizzle, zeros outside
   Int4Args a;
   int N, cs, ntiles;                          // tokens rounded up to 16; CTAs of a cluster; tiles of 128 rows
 };
@@ -135,10 +139,10 @@ struct Bars {
 };
 
 template <int GPB, bool X8>
-__global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__ TcArgs ta) {
+__global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_constant__ TcArgs ta) {
   extern __shared__ __align__(1024) unsigned char q2_int4tc_smem[];
   const Int4Args& a = ta.a;
-  constexpr int STEPS = 8 / GPB, esz = X8 ? 1 : 2;
+  constexpr int STEPS = 8 / GPB, kStage = stage_warps<X8>();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = ta.N, cs = ta.cs, atom = N * 128, bbytes = 2 * atom;
   // this CTA's run: blocks u0 .. u0 + n - 1 of the cluster's T, tile by tile
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(saddr(&bar->full[i]), kDec / kTurn + (N < 8 * kStageWarps ? N / 8 : kStageWarps));
+      mbar_init(saddr(&bar->full[i]), kDec / kTurn + (!X8 ? 1 : N < 8 * kStageWarps ? N / 8 : kStageWarps));
       mbar_init(saddr(&bar->done[i]), 1);
     }
     for (int i = 0; i < kAccs; ++i) {
@@ -190,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
   const uint32_t tmem = bar->tmem;
   pdl_trigger();
   bool ok = true;
+  int copied = 0;                                   // blocks of x requested by TMA
   auto failed = [&](unsigned int code) {
     if (lane == 0) {
       atomicExch(&q2_int4_error, code);
@@ -277,70 +282,82 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
     tmem_wait_st();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < kDec + kStage) {
-    // (two groups of warps, blocks in turn: a block's loads are under way for
-    // two blocks' time)
-    const int group = (warp - kDec) / kStageWarps, tid = threadIdx.x - (kDec + group * kStageWarps) * 32;
-    constexpr int TASKS = 256 / (kStageWarps * 32), PIECES = X8 ? 2 : 4;
-    if (tid / 32 < N / 8) {                         // a warp for 32 of the 4 * N tasks
-    const unsigned char* row[TASKS];
-    unsigned char* to[TASKS];
-    int key[TASKS], last[TASKS];                    // blocks in which the token has this run
-#pragma unroll
-    for (int k = 0; k < TASKS; ++k) {
-      const int e = tid + k * (kStageWarps * 32), t = e % N, q = e / N;
-      const bool live = q < 4 && t < a.ntok;
-      row[k] = static_cast<const unsigned char*>(a.x) + ((size_t)(live ? t : 0) * a.C + q * 32) * esz;
-      to[k] = B + (q >> 1) * atom + t * 128;
-      key[k] = (4 * (q & 1)) ^ (t & 7);
-      last[k] = live ? (a.C - q * 32 + 127) / 128 : 0;
-    }
-    const bool second = TASKS > 1 && tid + kStageWarps * 32 < 4 * N;
-    uint4 v[TASKS][PIECES];
-    Place at = place_of(u0 + group);                // of the next block to load
-    auto load = [&](int i) {
-      if (i < n) {
+    // ---- x of all tokens: copied as it is by TMA (fp16), or turned to fp16 on the way
+    pdl_wait();                                     // x may come from the previous kernel
+    if constexpr (!X8) {
+      if (warp == kDec) {
+        Place at = place_of(u0);
+        for (int i = 0; i < n; ++i) {
+          const int st = i % kRing;
+          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t full = saddr(&bar->full[st]), d = sB + st * bbytes;
+            mbar_expect_tx(full, (uint32_t)bbytes);
+            tma_load_2d(d, &ta.xmap, at.blk * 128, 0, full);
+            tma_load_2d(d + atom, &ta.xmap, at.blk * 128 + 64, 0, full);
+          }
+          __syncwarp();
+          copied = i + 1;
+          move(at, 1);
+        }
+      }
+    } else {
+      // two groups of warps, blocks in turn; task (token t, run q of 32
+      // columns): 32 bytes in, four 16-byte pieces out
+      const int group = (warp - kDec) / kStageWarps, tid = threadIdx.x - (kDec + group * kStageWarps) * 32;
+      constexpr int TASKS = 256 / (kStageWarps * 32);
+      if (tid / 32 < N / 8) {                       // a warp for 32 of the 4 * N tasks
+        const unsigned char* row[TASKS];
+        unsigned char* to[TASKS];
+        int key[TASKS], last[TASKS];                // blocks in which the token has this run
 #pragma unroll
         for (int k = 0; k < TASKS; ++k) {
-          const uint4* from = reinterpret_cast<const uint4*>(row[k] + at.blk * (128 * esz));
-#pragma unroll
-          for (int p = 0; p < PIECES; ++p) v[k][p] = at.blk < last[k] ? from[p] : make_uint4(0, 0, 0, 0);
+          const int e = tid + k * (kStageWarps * 32), t = e % N, q = e / N;
+          const bool live = q < 4 && t < a.ntok;
+          row[k] = static_cast<const unsigned char*>(a.x) + (size_t)(live ? t : 0) * a.C + q * 32;
+          to[k] = B + (q >> 1) * atom + t * 128;
+          key[k] = (4 * (q & 1)) ^ (t & 7);
+          last[k] = live ? (a.C - q * 32 + 127) / 128 : 0;
         }
-        move(at, 2);
-      }
-    };
-    pdl_wait();                                     // x may come from the previous kernel
-    load(group);
-    for (int i = group; i < n; i += 2) {
-      const int st = i % kRing;
-      if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
-      if (!ok) break;
+        const bool second = TASKS > 1 && tid + kStageWarps * 32 < 4 * N;
+        uint4 v[TASKS][2];
+        Place at = place_of(u0 + group);            // of the next block to load
+        auto load = [&](int i) {
+          if (i < n) {
 #pragma unroll
-      for (int k = 0; k < TASKS; ++k) {
-        if (k == 0 || second) {
-          uint32_t in[4][4];                        // run j of 8 columns, pair p
-          if constexpr (X8) {
+            for (int k = 0; k < TASKS; ++k) {
+              const uint4* from = reinterpret_cast<const uint4*>(row[k] + at.blk * 128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              int8x4(word(v[k][j >> 1], 2 * (j & 1)), in[j][0], in[j][1]);
-              int8x4(word(v[k][j >> 1], 2 * (j & 1) + 1), in[j][2], in[j][3]);
+              for (int p = 0; p < 2; ++p) v[k][p] = at.blk < last[k] ? from[p] : make_uint4(0, 0, 0, 0);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int p = 0; p < 4; ++p) in[j][p] = word(v[k][j], p);
+            move(at, 2);
           }
-          unsigned char* d = to[k] + st * bbytes;
+        };
+        load(group);
+        for (int i = group; i < n; i += 2) {
+          const int st = i % kRing;
+          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
+          if (!ok) break;
 #pragma unroll
-          for (int p = 0; p < 4; ++p)
-            *reinterpret_cast<uint4*>(d + ((key[k] ^ p) << 4)) = make_uint4(in[0][p], in[1][p], in[2][p], in[3][p]);
+          for (int k = 0; k < TASKS; ++k) {
+            if (k == 0 || second) {
+              unsigned char* d = to[k] + st * bbytes;
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                uint4 o;
+                int8x4(word(v[k][p >> 1], 2 * (p & 1)), o.x, o.y);
+                int8x4(word(v[k][p >> 1], 2 * (p & 1) + 1), o.z, o.w);
+                *reinterpret_cast<uint4*>(d + ((key[k] ^ p) << 4)) = o;
+              }
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
+          load(i + 2);
         }
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
-      load(i + 2);
-    }
     }
   } else if (warp < kDec + kStage + kIssue) {
     // ---- products of every kIssue-th block
@@ -451,6 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
+  // no copy may land after the CTA has gone: on an error, wait for those under way
+  if (!ok && !X8 && warp == kDec)
+    for (int i = copied - kRing > 0 ? copied - kRing : 0; i < copied; ++i)
+      (void)wait_phase(saddr(&bar->full[i % kRing]), (uint32_t)(i / kRing) & 1u, 1 << 12, nullptr);
   pdl_wait();                                       // before anything writes y (returns at once if done)
   cg::cluster_group cluster = cg::this_cluster();
   if (cs > 1) {
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
       auto rank_of = [&](int u) { return (int)((((long long)u + 1) * cs - 1) / T); };
       const int r0 = rank_of(s), cnt = rank_of(e - 1) - r0 + 1, all = a.ntok * kRows;
       const int e0 = all * (rank - r0) / cnt, e1 = all * (rank - r0 + 1) / cnt;
-      for (int x = e0 + threadIdx.x; x < e1; x += kThreads) {
+      for (int x = e0 + threadIdx.x; x < e1; x += blockDim.x) {
         const int t = x / kRows, r = x % kRows;
         float p[kMaxCluster];
 #pragma unroll
@@ -490,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_tc(const __grid_constant__
 
 // Clusters of cs CTAs that the device runs at once (a cluster lives in one
 // GPC, so this is not SMs / cs); asked for once.
-int clusters_at_once(const void* fn, int cs, int smem) {
+int clusters_at_once(const void* fn, int cs, int threads, int smem) {
   struct Known {
     int dev, cs, smem, n;
     const void* fn;
@@ -504,7 +525,7 @@ int clusters_at_once(const void* fn, int cs, int smem) {
     if (k.dev == dev && k.cs == cs && k.smem == smem && k.fn == fn) return k.n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -538,7 +559,7 @@ int launch_tc(const Int4Args& a, void* stream) {
   int clusters = 1;
   double best = 0;
   for (int cs = 1, lg = 0; cs <= kMaxCluster && cs <= a.nblk; cs *= 2, ++lg) {
-    const int n = std::min(ta.ntiles, cs == 1 ? dev_info().sms : clusters_at_once(fn, cs, smem));
+    const int n = std::min(ta.ntiles, cs == 1 ? dev_info().sms : clusters_at_once(fn, cs, tc_threads<X8>(), smem));
     const double cost = (double)((ta.ntiles + n - 1) / n) * a.nblk / cs + 3 * lg;
     if (cs == 1 || cost < best) {
       best = cost;
@@ -546,7 +567,8 @@ int launch_tc(const Int4Args& a, void* stream) {
       clusters = n;
     }
   }
-  return launch_clusters(kernel, clusters, ta.cs, kThreads, smem, stream, ta);
+  if (!X8 && !encode_x_map(&ta.xmap, a.x, a.C, a.ntok, ta.N)) return Q2_ECUDA;
+  return launch_clusters(kernel, clusters, ta.cs, tc_threads<X8>(), smem, stream, ta);
 }
 
 }  // namespace

@@ -63,9 +63,9 @@ struct q2_blob_header {
 // INT4:   unit of 16 rows x 128 columns, index it = (row / 16) * nblock + block,
 //         q2_int4_item() bytes each: weights 1024 bytes (half u, lane, 16
 //         bytes; word i of lane l = 4*(row % 8) + j is step t = 4*u + i and
-//         holds the four columns 32*(t / 2) + 8*j + 4*(t % 2) + 0..3: from the
-//         lowest four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, of rows
-//         (row % 8) and (row % 8) + 8 in turn); then scales (fp16) and, where
+//         holds columns 16*t + 2*j + (0, 8, 1, 9), the share of one lane of a
+//         16 x 16 operand fragment, from the lowest eight bits up, each of
+//         rows (row % 8) and (row % 8) + 8 in turn); then scales (fp16) and, where
 //         the matrix has them, zero points (bytes), both in the order
 //         [row % 8][group of the block][row / 8 % 2].  Rows past R and columns
 //         past C hold q = z = 8.

@@ -156,19 +156,6 @@ __device__ __forceinline__ uint4 decode_q(const Codes4& c, uint32_t tlo, uint32_
   return r;
 }
 
-// one arrival that also expects `bytes` of asynchronous copies
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// 2D TMA tile load of box (x, y) of the tensor map into shared memory; the
-// bytes are reported to the mbarrier.  x * 2 bytes is a multiple of 128.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void sleep_us(int us) {
   for (int k = 0; k < us; ++k) __nanosleep(1000);
 }
@@ -875,6 +862,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+}  // namespace
+
 // Tensor map of x [ntok][C] fp16 for the B tiles: box of 64 columns (128
 // bytes, the swizzle span) x N token rows, rows past ntok and columns past C
 // read as zero.  False when the rows are not 16-byte aligned or the driver
@@ -891,6 +880,8 @@ bool encode_x_map(CUtensorMap* map, const void* x, int C, int ntok, int N) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // The K split of the tensor-core launch.  One CTA per SM at a time, so the
 // makespan is (waves of tiles) x (slices per CTA + the CTA's fixed cost in

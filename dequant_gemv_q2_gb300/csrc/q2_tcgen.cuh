@@ -1,5 +1,6 @@
 // 5th-generation tensor core helpers shared by the kernels that use them.
 #pragma once
+#include <cuda.h>
 #include <stdint.h>
 
 namespace q2 {
@@ -59,5 +60,22 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+
+// one arrival that also expects `bytes` of asynchronous copies
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// 2D TMA tile load of box (x, y) of the tensor map into shared memory; the
+// bytes are reported to the mbarrier.  x * 2 bytes is a multiple of 128.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// Tensor map of x [ntok][C] fp16 for the kernels' B tiles (q2_tc.cu).
+bool encode_x_map(CUtensorMap* map, const void* x, int C, int ntok, int N);
 
 }  // namespace q2

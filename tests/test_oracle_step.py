@@ -93,16 +93,16 @@ def _codes(blob, R, C, group):
     w = items[:, :1024].copy().view("<u4").reshape(-1, 2, 32, 4)
     sc = items[:, 1024: 1024 + gpb * 32].copy().view(np.float16).reshape(-1, 8, gpb, 2)
     zr = items[:, 1024 + gpb * 32:].reshape(-1, 8, gpb, 2) if h["layout"] else None
-    order = [0, 0, 2, 2, 1, 1, 3, 3]
+    order = [0, 0, 8, 8, 1, 1, 9, 9]
     q = np.zeros((R, C), dtype=np.int64)
     s = np.zeros((R, C // group), dtype=np.float16)
     z = np.full((R, C // group), 8, dtype=np.int64)
     for r in range(R):
         for c in range(C):
             it, cc, half = (r // 16) * nblk + c // 128, c % 128, (r // 8) % 2
-            step = 2 * (cc // 32) + (cc % 8) // 4
-            v = int(w[it, step // 4, (r % 8) * 4 + (cc % 32) // 8, step % 4])
-            nib = [n for n in range(8) if order[n] == cc % 4 and n % 2 == half][0]
+            step = cc // 16
+            v = int(w[it, step // 4, (r % 8) * 4 + (cc % 8) // 2, step % 4])
+            nib = [n for n in range(8) if order[n] == cc % 2 + cc % 16 // 8 * 8 and n % 2 == half][0]
             q[r, c] = (v >> (4 * nib)) & 15
             s[r, c // group] = sc[it, r % 8, cc // group, half]
             if zr is not None:
