@@ -1,27 +1,26 @@
-// y = W x for 4-bit weights with group scales, 1..64 tokens,
+// y = W x for 4-bit weights with group scales, 1..64 tokens (up to 16 here),
 //
 //   y[t][r] = sum_g s[r][g] * sum_{c in g} (q[r][c] - z[r][g]) * x[t][c],
 //
 // for x in fp16, or in 8 bits with one fp32 scale per token.
 //
 // The inner sums run on the tensor cores, 16 rows x 16 columns of weights
-// against 8 tokens per instruction, fp32 accumulators.  q - z is a small
-// integer and exact in fp16: four bits OR-ed into the mantissa of 1024 (or,
-// shifted left by four, of 64 after a multiplication by 1/16) give 1024 + q
-// (64 + q) without a conversion, and one subtraction (one fused
-// multiply-add) takes 1024 + z (64 + z) off again, so 8 weights cost 9
-// instructions.  The group's fp32 sum is multiplied by the scale and added to
-// the row's fp32 sum: nothing but y itself is rounded to fp16.  For 8-bit x
-// the group sums are sums of at most 128 products of magnitude at most
-// 15 * 128 each and thus exact.
+// against 8 tokens per instruction, fp32 accumulators.  The four bits are used
+// as they are: in the lowest bits of an fp16 number they are the subnormal
+// q * 2^-24 (shifted left by four: q * 2^-20), which the tensor cores multiply
+// exactly, so 8 weights cost 5 instructions.  The powers of two go into the
+// scales, and the zero point is taken off the group's sum,
+//   sum (q - z) x = 2^24 sum (q 2^-24) x - z sum x,
+// with the sums of x over each group from a product with ones.  Both terms are
+// fp32 sums of the group's products, at most 15 sum |x| each, so the
+// difference keeps the rounding of such a sum; nothing but y itself is rounded
+// to fp16.  For 8-bit x both are integers below 2^18 and thus exact.
 //
 // Weights are stored in the order in which lanes use them: the unit is a
 // block of 16 rows x 128 columns, 1 KB as two 16-byte loads per lane, with
-// its scales and zero points behind it, so that a warp reads one stream.  The
-// columns that a lane holds are its own choice of the contraction's order
-// (any bijection is right as long as x uses it too, and as long as a step
-// stays inside a scale group); it is the one that makes a lane's share of x in
-// 32 columns of a token, 8 consecutive ones, contiguous.
+// its scales and zero points behind it, so that a warp reads one stream.
+//
+// Up to 2 tokens: k_int4_few.  3 to 16: k_int4_many.  More: q2_int4_tc.cu.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -37,14 +36,8 @@ namespace {
 
 // ------------------------------------------------------- 1 and 2 tokens
 // At one token a block's 2048 weights have to pass in about 50 cycles per SM,
-// so instructions are what is scarce.  Here the four bits are used as they
-// are: in the lowest bits of an fp16 number they are the subnormal q * 2^-24
-// (shifted left by four: q * 2^-20), which the tensor cores multiply exactly,
-// so 8 weights cost 5 instructions.  The powers of two go into the scales,
-// and the zero point is taken off the group's sum,
-//   sum (q - z) x = 2^24 sum (q 2^-24) x - z sum x,
-// with the sums of x over each group computed once per CTA (as a product with
-// ones).  Both terms are of the size of the result, so nothing is lost.
+// so instructions are what is scarce: k_int4_few computes the sums of x once
+// per CTA.
 //
 // A CTA's warps split the columns of a row tile (16 rows) and keep their
 // column range over all row tiles that the CTA takes (every gridDim.x-th): a
@@ -53,12 +46,13 @@ namespace {
 // the first of them before the wait on the previous kernel.  At a row tile's
 // end the warps leave their sums in one of two shared-memory buffers and the
 // first threads add them in warp order: one barrier per row tile, no atomics.
-#ifndef MS
-#define MS 3
-#endif
-#ifndef MC
-#define MC 3
-#endif
+//
+// 24576 x 4096 at one token, groups of 128 with zero points: 11.2 us on the
+// device, 4.7 TB/s (4096 x 4096: 3.6 us, of which 2 are the launch and the
+// first bytes' way).  Issue slots are 70% full and what remains is the ends:
+// the first loads, x and its sums before them, the last row tiles.  Steps:
+// register ring 19.1 us, shared-memory ring 14.3, the bits as subnormals and
+// sums of x once per CTA 11.2.
 constexpr int kFewWarps = 8, kFewTok = 2, kFewStages = 3, kFewCtas = 2;
 constexpr int kFewRed = 2 * kFewWarps * kFewTok * 16 * 4;
 
@@ -243,45 +237,47 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   }
 }
 
-// ------------------------------------------------------- 3..64 tokens
+// ------------------------------------------------------- 3..16 tokens
 // A CTA takes 128 rows and a range of 128-column blocks.  Its eight warps are
 // two groups of four, which take alternate blocks and run on their own (the
-// two warps of a scheduler belong to different groups, so one unpacks while
-// the other multiplies); each warp of a group has two row tiles.  A group's x
-// of all tokens (a token's row is padded so that the lanes that load together
-// fall on different banks) and each warp's own weights come through a ring of
-// shared-memory stages by asynchronous 16-byte copies.  A block's A operands
-// (here q - z itself: the tensor cores, not the instructions, are what is
-// scarce) are unpacked once and used for all tokens, two tiles of 8 tokens
-// and two row tiles at a time, so that four chains of dependent products are
-// in flight.  When the column range is split over CTAs, they form a cluster
-// and add their fp32 sums through distributed shared memory in rank order.
-#ifndef INT4_SUB
-#define INT4_SUB 1
-#endif
+// two warps of a scheduler belong to different groups, so one waits or unpacks
+// while the other multiplies); each warp of a group has two row tiles.  A
+// group's x of all tokens (a token's row is padded so that the lanes that load
+// together fall on different banks) and each warp's own weights come through a
+// ring of shared-memory stages by asynchronous 16-byte copies.  A block's
+// operands are unpacked once and used for all tokens; two row tiles and the
+// product with ones (per 8 tokens) give three chains of products in flight.
+// When the column range is split over CTAs, they form a cluster and add their
+// fp32 sums through distributed shared memory in rank order.
+//
+// What bounds it at 8 tokens is bytes in flight and the ends, 3.0 TB/s at
+// 5120 x 17408 (8-bit x, groups of 64: 15.9 us) and 3.6 at 24576 x 4096 (14.5
+// us); at 16 tokens the products: an instruction takes the tensor cores 2
+// cycles of an SM whatever its operands are worth, 12.5 us of the 22.2 at
+// 24576 x 4096.  More than 16 tokens would cost another product with ones and
+// 48 accumulators more per thread: they go to the kernel in q2_int4_tc.cu
+// (24576 x 4096 at 32 tokens 28.8 us, twice the 16-token time here 44).
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
 __host__ __device__ constexpr int x_row_bytes() { return X8 ? 128 + 16 : 256 + 16; }
+constexpr int kManyStages = 3;
 template <int NT>
-__host__ __device__ constexpr int many_stages() { return NT == 8 || NT == 2 ? 3 : NT == 1 ? MS : 4; }
-template <int NT>
-__host__ __device__ constexpr int many_ctas() { return NT == 1 ? MC : NT <= 2 ? 2 : 1; }   // per SM
+__host__ __device__ constexpr int many_ctas() { return NT == 1 ? 3 : 2; }   // per SM, at most
 
 constexpr int kOutLd = kManyRows + 4;
 
 template <int NT, bool X8>
 int many_smem(const Int4Args& a) {
-  const int ring = 2 * many_stages<NT>() * (NT * 8 * x_row_bytes<X8>() + 8 * a.item), out = NT * 8 * kOutLd * 4;
+  const int ring = 2 * kManyStages * (NT * 8 * x_row_bytes<X8>() + 8 * a.item), out = NT * 8 * kOutLd * 4;
   return ring > out ? ring : out;
 }
 
-template <int NT, int GPB, bool X8, bool SUB>
+template <int NT, int GPB, bool X8>
 __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
     k_int4_many(const __grid_constant__ Int4Args a, const int nsplit) {
-  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB, STAGES = many_stages<NT>();
+  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB, STAGES = kManyStages;
   constexpr int esz = X8 ? 1 : 2, PIECES = 128 * esz / 16, PASS = 128 / PIECES;   // pieces of a row; tokens of a pass
-  constexpr int HT = NT == 1 ? 1 : 2;                       // tiles of 8 tokens at a time
   extern __shared__ __align__(16) unsigned char q2_int4_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, j = lane & 3, wm = warp & 3, wk = warp >> 2;
@@ -378,82 +374,46 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
       w[m][1] = lds128(at + 512 + lane * 16);
       load_sides(sd[m], at, a.zeros, g);
     }
-    if constexpr (SUB) {
-      const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-      uint32_t b[NT][16];
+    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+    uint32_t b[NT][16];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) xload(b[t], t);
+    for (int t = 0; t < NT; ++t) xload(b[t], t);
 #pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        float c[MT][NT][4], X[NT][4];
+    for (int q = 0; q < GPB; ++q) {
+      float c[MT][NT][4], X[NT][4];
 #pragma unroll
-        for (int k = q * STEPS; k < (q + 1) * STEPS; ++k) {
-          uint32_t A[MT][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t v = word(w[m][k >> 2], k & 3), v8 = v >> 8;
-            A[m][0] = v & 0x000f000fu;
-            A[m][1] = v & 0x00f000f0u;
-            A[m][2] = v8 & 0x000f000fu;
-            A[m][3] = v8 & 0x00f000f0u;
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (k == q * STEPS) mma_first(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
-            else mma(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              if (k == q * STEPS) mma_first(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
-              else mma(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
-            }
-          }
-        }
+      for (int k = q * STEPS; k < (q + 1) * STEPS; ++k) {
+        uint32_t A[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
-          const uint32_t zz = sd[m].z[q >> 1] >> (16 * (q & 1));
-          const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
+          const uint32_t v = word(w[m][k >> 2], k & 3), v8 = v >> 8;
+          A[m][0] = v & 0x000f000fu;
+          A[m][1] = v & 0x00f000f0u;
+          A[m][2] = v8 & 0x000f000fu;
+          A[m][3] = v8 & 0x00f000f0u;
+        }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            acc[m][t][0] = fmaf(sc.x, fmaf(c[m][t][0], 16777216.f, -z0 * X[t][0]), acc[m][t][0]);
-            acc[m][t][1] = fmaf(sc.x, fmaf(c[m][t][1], 16777216.f, -z0 * X[t][1]), acc[m][t][1]);
-            acc[m][t][2] = fmaf(sc.y, fmaf(c[m][t][2], 1048576.f, -z1 * X[t][0]), acc[m][t][2]);
-            acc[m][t][3] = fmaf(sc.y, fmaf(c[m][t][3], 1048576.f, -z1 * X[t][1]), acc[m][t][3]);
+        for (int t = 0; t < NT; ++t) {
+          if (k == q * STEPS) mma_first(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
+          else mma(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (k == q * STEPS) mma_first(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
+            else mma(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
           }
         }
       }
-    } else {
-      uint32_t A[MT][8][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) unpack(w[m], sd[m], A[m]);
+      for (int m = 0; m < MT; ++m) {
+        const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
+        const uint32_t zz = sd[m].z[q >> 1] >> (16 * (q & 1));
+        const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
 #pragma unroll
-      for (int t = 0; t < NT; t += HT) {
-        uint32_t b[HT][16];
-#pragma unroll
-        for (int h = 0; h < HT; ++h) xload(b[h], t + h);
-#pragma unroll
-        for (int q = 0; q < GPB; ++q) {
-          float c[MT][HT][4];
-#pragma unroll
-          for (int k = q * STEPS; k < (q + 1) * STEPS; ++k)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int h = 0; h < HT; ++h) {
-                if (k == q * STEPS) mma_first(c[m][h], A[m][k], b[h][2 * k], b[h][2 * k + 1]);
-                else mma(c[m][h], A[m][k], b[h][2 * k], b[h][2 * k + 1]);
-              }
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-              acc[m][t + h][0] = fmaf(sc.x, c[m][h][0], acc[m][t + h][0]);
-              acc[m][t + h][1] = fmaf(sc.x, c[m][h][1], acc[m][t + h][1]);
-              acc[m][t + h][2] = fmaf(sc.y, c[m][h][2], acc[m][t + h][2]);
-              acc[m][t + h][3] = fmaf(sc.y, c[m][h][3], acc[m][t + h][3]);
-            }
-          }
+        for (int t = 0; t < NT; ++t) {
+          acc[m][t][0] = fmaf(sc.x, fmaf(c[m][t][0], 16777216.f, -z0 * X[t][0]), acc[m][t][0]);
+          acc[m][t][1] = fmaf(sc.x, fmaf(c[m][t][1], 16777216.f, -z0 * X[t][1]), acc[m][t][1]);
+          acc[m][t][2] = fmaf(sc.y, fmaf(c[m][t][2], 1048576.f, -z1 * X[t][0]), acc[m][t][2]);
+          acc[m][t][3] = fmaf(sc.y, fmaf(c[m][t][3], 1048576.f, -z1 * X[t][1]), acc[m][t][3]);
         }
       }
     }
@@ -509,43 +469,66 @@ int launch_few(const Int4Args& a, int slots, void* stream) {
                  : launch_pdl(k_int4_few<GPB, false, X8>, a, grid, nwarp * 32, smem, stream);
 }
 
+// The split of the columns over a cluster, from the time of a CTA: its blocks
+// (about 0.22 us each for a CTA alone on its SM, 0.2 + 0.8 n of that with n of
+// them on it), three blocks for the cluster's barriers, and waves where the
+// clusters do not all run at once.  Against all sizes and spreads timed (8
+// shapes of the 8B and 14B stacks, 1 to 16 tokens) the choice is within 10%.
 template <int NT, int GPB, bool X8>
 int launch_many(const Int4Args& a, void* stream) {
-  auto kernel = k_int4_many<NT, GPB, X8, (NT <= INT4_SUB)>;
+  static ClusterCounts counts;
+  auto kernel = k_int4_many<NT, GPB, X8>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
   const int smem = many_smem<NT, X8>(a);
-  if (set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
-  const int tiles = (a.ntile + kManyRows / 16 - 1) / (kManyRows / 16);
-  const int slots = dev_info().sms * std::max(1, std::min(many_ctas<NT>(), kSmemPerSm / (smem + 1024)));
-  // Waves of CTAs times their blocks plus a fixed cost of about eight blocks.
-  int nsplit = 1;
+  const int tiles = (a.ntile + kManyRows / 16 - 1) / (kManyRows / 16), sms = dev_info().sms;
+  if (set_smem(fn, kSmemPerSm - 1024)) return Q2_ECUDA;
+  // No more CTAs on an SM than an even spread needs (the next one's shared
+  // memory is taken): left alone they fill some SMs and leave others idle
+  // (256 CTAs of 4096 x 4096: 5.6 us instead of 4.4).
+  auto smem_of = [&](int share) { return share < many_ctas<NT>() ? std::max(smem, kSmemPerSm / (share + 1)) : smem; };
+  int nsplit = 1, with = smem;
   long long best = 0;
   for (int s = 1; s <= kManyMax && 2 * s <= a.nblk; ++s) {
-    const long long cost = (long long)((tiles * s + slots - 1) / slots) * ((a.nblk + s - 1) / s + 8);
+    int share = std::min((tiles * s + sms - 1) / sms, many_ctas<NT>()), fit = 0;
+    for (; share <= many_ctas<NT>(); ++share) {               // the clusters that run at once with so many CTAs per SM
+      fit = counts.get(fn, s, kManyWarps * 32, smem_of(share));
+      if (fit >= tiles) break;
+    }
+    share = std::min(share, many_ctas<NT>());
+    const long long waves = (tiles + fit - 1) / fit, cost = (a.nblk + s - 1) / s * (1 + 4 * share) * waves + (s > 1 ? 15 : 0);
     if (s == 1 || cost < best) {
       best = cost;
       nsplit = s;
+      with = smem_of(share);
     }
   }
-  return launch_clusters(kernel, tiles, nsplit, kManyWarps * 32, smem, stream, a, nsplit);
+  return launch_clusters(kernel, tiles, nsplit, kManyWarps * 32, with, stream, a, nsplit);
 }
 
 template <int GPB, bool X8>
 int launch_tokens(const Int4Args& a, void* stream) {
   if (a.ntok <= kFewTok) {
-    // k_int4_few keeps x in shared memory and hands out whole row tiles, so it
-    // is taken where x fits and the last round of row tiles is mostly full.
+    // k_int4_few keeps x in shared memory and hands out whole row tiles: it is
+    // taken where x fits, unless the last of several rounds is mostly empty
+    // (5120 x 17408 at one token, 1.05 rounds: 14.2 us, 12.3 with k_int4_many;
+    // 6144 x 4096, 1.26 rounds: 4.9 and 5.4; 24576 x 4096, 5.05: 11.1 and 13.4).
     const int slots = std::min(kFewCtas, kSmemPerSm / (few_smem<GPB, X8>(a, kFewWarps) + 1024)) * dev_info().sms;
     const int rounds = slots ? (a.ntile + slots - 1) / slots : 0;
-    if (slots && 5ll * a.ntile >= 4ll * rounds * slots) return launch_few<GPB, X8>(a, slots, stream);
+    if (rounds == 1 || (slots && 5ll * a.ntile >= 3ll * rounds * slots)) return launch_few<GPB, X8>(a, slots, stream);
   }
   if (a.ntok <= 8) return launch_many<1, GPB, X8>(a, stream);
-#ifndef TCN
-#define TCN 9
-#endif
-  if (a.ntok >= TCN && a.nblk >= 2) return q2_int4_tc(a, Q2_INT4_COLS / GPB, X8, stream);
   if (a.ntok <= 16) return launch_many<2, GPB, X8>(a, stream);
-  if (a.ntok <= 32) return launch_many<4, GPB, X8>(a, stream);
-  return launch_many<8, GPB, X8>(a, stream);
+  if (a.nblk > 1) return q2_int4_tc(a, Q2_INT4_COLS / GPB, X8, stream);
+  // One block per row tile (up to 128 columns): q2_int4_tc takes two in turn.
+  for (int t = 0; t < a.ntok; t += 16) {
+    Int4Args b = a;
+    b.x = static_cast<const unsigned char*>(a.x) + (size_t)t * a.C * (X8 ? 1 : 2);
+    b.xs = X8 ? a.xs + t : nullptr;
+    b.y = a.y + (size_t)t * a.R;
+    b.ntok = std::min(16, a.ntok - t);
+    if (const int e = launch_many<2, GPB, X8>(b, stream)) return e;
+  }
+  return Q2_OK;
 }
 
 template <bool X8>

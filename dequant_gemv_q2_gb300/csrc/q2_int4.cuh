@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_fp16.h>
 
+#include <mutex>
+
 #include "q2_common.cuh"
 
 namespace q2 {
@@ -24,7 +26,7 @@ struct Sides {
 
 // Blocks go to shared memory by asynchronous 16-byte copies (a register ring
 // was bound by the six scoreboards a warp has: waiting for x meant waiting
-// for weights requested after it; 19.1 us instead of 10.3 at 24576 x 4096).
+// for weights requested after it; 19.1 us instead of 14.3 at 24576 x 4096).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -118,18 +120,6 @@ __device__ __forceinline__ void unpack_step(uint32_t v, const Zeros& z, uint32_t
   a3 = hfma2(and_or(v8, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z.z1);
 }
 
-// The block's eight steps.
-template <int GPB>
-__device__ __forceinline__ void unpack(const uint4 (&w)[2], const Sides<GPB>& k, uint32_t (&A)[8][4]) {
-#pragma unroll
-  for (int q = 0; q < GPB; ++q) {
-    const Zeros z = zeros_of(k.z[q >> 1] >> (16 * (q & 1)));
-#pragma unroll
-    for (int st = q * (8 / GPB); st < (q + 1) * (8 / GPB); ++st)
-      unpack_step(word(w[st >> 2], st & 3), z, A[st][0], A[st][1], A[st][2], A[st][3]);
-  }
-}
-
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -151,6 +141,44 @@ __device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
 }
 
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
+
+// How many clusters of cs CTAs of a kernel the device runs at once (a cluster
+// lives in one GPC, so this is not SMs / cs), each asked for once.
+class ClusterCounts {
+  struct Known {
+    int dev, cs, smem, n;
+  };
+  std::mutex mu;
+  Known known[64];
+  int nknown = 0;
+
+ public:
+  int get(const void* fn, int cs, int threads, int smem) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < nknown; ++i)
+      if (known[i].dev == dev && known[i].cs == cs && known[i].smem == smem) return known[i].n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return 1;
+    }
+    if (nknown < 64) known[nknown++] = {dev, cs, smem, n};
+    return n;
+  }
+};
 
 // Launch in clusters of cs CTAs, programmatic stream serialization allowed.
 template <typename... A, typename... B>
@@ -178,5 +206,5 @@ int launch_clusters(void (*kernel)(A...), int clusters, int cs, int threads, int
 
 }  // namespace q2
 
-// 9..64 tokens on the 5th-generation tensor cores (q2_int4_tc.cu).
+// 17..64 tokens on the 5th-generation tensor cores (q2_int4_tc.cu).
 int q2_int4_tc(const q2::Int4Args& a, int group, bool x8, void* stream);

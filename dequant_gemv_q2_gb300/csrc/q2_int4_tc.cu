@@ -35,8 +35,6 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <mutex>
-#include <vector>
 
 #include "q2_int4.cuh"
 #include "q2_tcgen.cuh"
@@ -64,25 +62,6 @@ constexpr int kScales = 4;                    // blocks of scales in shared memo
 constexpr int kStageWarps = 4;                // staging warps of a group (8-bit x)
 constexpr int kOutLd = kRows + 4, kMaxCluster = 8;
 constexpr int kOneCta = 116 * 1024;           // at most one CTA of this or the other tcgen05 kernels per SM (each holds all of TMEM)
-constexpr int kBound = 1 << 20;               // polls of a wait (each may sleep for some microseconds)
-
-// Wait for the phase of the given parity, for at most `limit` polls; false
-// when they run out or `give_up` is set.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int limit, const volatile int* give_up) {
-  for (int i = 0; i < limit; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (give_up && (i & 31) == 31 && *give_up) return false;
-  }
-  return false;
-}
 
 // One product, issued by lane 0 of a converged warp: outside a divergent
 // branch the operands stay in uniform registers (inside one each of them was
@@ -135,7 +114,7 @@ struct Bars {
   uint64_t taken[kAccs];      // it has been read (summing warps)
   uint64_t drain[kIssue];     // everything an issuing warp has issued is done
   uint32_t tmem;
-  int abort;
+  int abort, copied;          // a wait ran out; blocks of x requested by TMA
 };
 
 template <int GPB, bool X8>
@@ -155,7 +134,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     int tile, blk;
   };
   auto place_of = [&](int u) { return Place{t0 + u / a.nblk, u % a.nblk}; };
-  auto move = [&](Place& p, int by) {               // by <= kTurn <= nblk; whether it is another tile
+  auto move = [&](Place& p, int by) {               // by <= 2 <= nblk; whether it is another tile
     p.blk += by;
     if (p.blk < a.nblk) return false;
     p.blk -= a.nblk;
@@ -194,7 +173,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
   const uint32_t tmem = bar->tmem;
   pdl_trigger();
   bool ok = true;
-  int copied = 0;                                   // blocks of x requested by TMA
+  int undone = n;                                   // a decoder's next block when it gave up
   auto failed = [&](unsigned int code) {
     if (lane == 0) {
       atomicExch(&q2_int4_error, code);
@@ -202,8 +181,8 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     }
     return false;
   };
-  auto wait = [&](uint64_t& b, int phase, unsigned int code, int limit = kBound) {
-    return __all_sync(~0u, wait_phase(saddr(&b), (uint32_t)phase & 1u, limit, give_up)) ? true : failed(code);
+  auto wait = [&](uint64_t& b, int phase, unsigned int code) {
+    return __all_sync(~0u, mbar_wait(saddr(&b), (uint32_t)phase & 1u, kSpinLimit, give_up)) ? true : failed(code);
   };
   float2 acc[16];                                   // 32 tokens
 
@@ -237,15 +216,6 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     };
     for (int k = 0; k < kRaw - 1; ++k) copy(turn + k * kTurn, raw + k * kRawBytes);
     uint32_t slot = raw, before = raw + (kRaw - 1) * kRawBytes;
-    int stored = -1;                                // stage whose stores are under way
-    auto arrive = [&]() {
-      if (stored >= 0) {
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(saddr(&bar->full[stored]));
-      }
-    };
     for (int i = turn; i < n; i += kTurn) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
       __syncwarp();
@@ -265,21 +235,23 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
             unpack_step(word(w[t >> 2], t & 3), z, A[4 * t], A[4 * t + 1], A[4 * t + 2], A[4 * t + 3]);
         }
         if (m == 0) {
-          arrive();                                 // for the block before
-          stored = -1;
           if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 1u);
           if (!ok) break;
           tc_fence_after();
         }
         tmem_st_frag(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + kAcol + st * 64, A);
       }
-      if (!ok) break;
-      stored = st;
+      if (!ok) {
+        undone = i;
+        break;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
       before = slot;
       slot = slot == raw + (kRaw - 1) * kRawBytes ? raw : slot + kRawBytes;
     }
-    arrive();
-    tmem_wait_st();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < kDec + kStage) {
     // ---- x of all tokens: copied as it is by TMA (fp16), or turned to fp16 on the way
@@ -287,6 +259,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     if constexpr (!X8) {
       if (warp == kDec) {
         Place at = place_of(u0);
+        int copied = 0;
         for (int i = 0; i < n; ++i) {
           const int st = i % kRing;
           if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
@@ -301,6 +274,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
           copied = i + 1;
           move(at, 1);
         }
+        if (lane == 0) bar->copied = copied;
       }
     } else {
       // two groups of warps, blocks in turn; task (token t, run q of 32
@@ -364,10 +338,11 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     pdl_wait();
     const int me = __shfl_sync(~0u, warp, 0) - kDec - kStage;
     const uint32_t idesc = idesc_f16(kRows, N);
-    const int limit = q2_int4_stage_wait_limit > 0 ? (int)std::min(q2_int4_stage_wait_limit, (long long)kBound) : kBound;
+    const long long limit = q2_int4_stage_wait_limit;         // in plain polls, which do not sleep
     for (int i = me; i < n && ok; i += kIssue) {
       const int st = i % kRing;
-      ok = wait(bar->full[st], i / kRing, 3u, limit);
+      if (limit > 0 && !__all_sync(~0u, mbar_wait(saddr(&bar->full[st]), (uint32_t)(i / kRing) & 1u, limit))) ok = failed(3u);
+      if (ok) ok = wait(bar->full[st], i / kRing, 3u);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
         if (!ok) break;
@@ -390,7 +365,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     // whatever was issued is waited for, with the full bound, on every path
     if (lane == 0) mma_commit(saddr(&bar->drain[me]));
     __syncwarp();
-    if (!__all_sync(~0u, wait_phase(saddr(&bar->drain[me]), 0u, kBound, nullptr))) ok = failed(5u);
+    if (!__all_sync(~0u, mbar_wait(saddr(&bar->drain[me]), 0u))) ok = failed(5u);
   } else {
     // ---- sums: lane = row `row` of the tile, tokens c0 .. c0 + 31
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -468,10 +443,18 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
-  // no copy may land after the CTA has gone: on an error, wait for those under way
-  if (!ok && !X8 && warp == kDec)
-    for (int i = copied - kRing > 0 ? copied - kRing : 0; i < copied; ++i)
-      (void)wait_phase(saddr(&bar->full[i % kRing]), (uint32_t)(i / kRing) & 1u, 1 << 12, nullptr);
+  // no copy may land after the CTA has gone: on an error the decoders make up
+  // for the arrivals that they left out, and the copies under way are waited for
+  if (__syncthreads_or(!ok) && !X8 && warp <= kDec) {
+    const int copied = bar->copied;
+    if (warp < kDec) {
+      if (lane == 0)
+        for (int i = undone; i < copied; i += kTurn) mbar_arrive(saddr(&bar->full[i % kRing]));
+    } else {
+      for (int i = copied - kRing > 0 ? copied - kRing : 0; i < copied; ++i)
+        (void)mbar_wait(saddr(&bar->full[i % kRing]), (uint32_t)(i / kRing) & 1u);
+    }
+  }
   pdl_wait();                                       // before anything writes y (returns at once if done)
   cg::cluster_group cluster = cg::this_cluster();
   if (cs > 1) {
@@ -509,42 +492,9 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
-// Clusters of cs CTAs that the device runs at once (a cluster lives in one
-// GPC, so this is not SMs / cs); asked for once.
-int clusters_at_once(const void* fn, int cs, int threads, int smem) {
-  struct Known {
-    int dev, cs, smem, n;
-    const void* fn;
-  };
-  static std::mutex mu;
-  static std::vector<Known> known;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lk(mu);
-  for (const Known& k : known)
-    if (k.dev == dev && k.cs == cs && k.smem == smem && k.fn == fn) return k.n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    n = 1;
-  }
-  known.push_back({dev, cs, smem, n, fn});
-  return n;
-}
-
 template <int GPB, bool X8>
 int launch_tc(const Int4Args& a, void* stream) {
+  static ClusterCounts counts;
   auto kernel = k_int4_tc<GPB, X8>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   TcArgs ta = {};
@@ -559,7 +509,7 @@ int launch_tc(const Int4Args& a, void* stream) {
   int clusters = 1;
   double best = 0;
   for (int cs = 1, lg = 0; cs <= kMaxCluster && cs <= a.nblk; cs *= 2, ++lg) {
-    const int n = std::min(ta.ntiles, cs == 1 ? dev_info().sms : clusters_at_once(fn, cs, tc_threads<X8>(), smem));
+    const int n = std::min(ta.ntiles, cs == 1 ? dev_info().sms : counts.get(fn, cs, tc_threads<X8>(), smem));
     const double cost = (double)((ta.ntiles + n - 1) / n) * a.nblk / cs + 3 * lg;
     if (cs == 1 || cost < best) {
       best = cost;

@@ -181,7 +181,7 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* weight_bytes_read_per_call);
  * token's BPDQ result at 1..6 tokens is bit-identical whatever the batch.
  * Leech at 2 tokens runs two single-token launches when C and R are
  * multiples of 8.  The tensor-core path (7..64 tokens, or 2..64 for trellis
- * and the other Leech cases) is one launch: a tile's K splits (at most 8,
+ * and the other Leech cases; Q2_INT4 has its own, below) is one launch: a tile's K splits (at most 8,
  * one thread-block cluster) add their fp32 partials in split order, so the
  * result does not depend on which finished first, and the same pass applies
  * the format's row epilogue (trellis: scale; Leech: exceptions, scale,
@@ -189,9 +189,16 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* weight_bytes_read_per_call);
  * matrix from its largest weight magnitude so that no fp16 x can overflow
  * it; each term then carries an absolute rounding error of at most
  * 2^-(F+1), about 2e-8 per 256-column slice for weights of magnitude
- * 0.05.  An inf or NaN in a token's x makes that token's outputs NaN (the
- * IEEE result is non-finite for every row; the fixed-point sums carry a
- * sticky flag for it).  Launches use programmatic dependent launch: weights are
+ * 0.05.  Q2_INT4 needs no workspace: 1 and 2 tokens take a kernel that keeps
+ * x in shared memory (where the rows fill its rounds), up to 16 one on the
+ * warps' tensor instructions, 17..64 one on the 5th-generation tensor cores,
+ * each one launch whose K splits are summed in split order (matrices of up to
+ * 128 columns: a launch per 16 tokens).  There q * x is exact; up to 16
+ * tokens the zero point is taken off a group's fp32 sum, so a group's error
+ * is that of an fp32 sum of s * (q + z) * |x|, from 17 tokens on that of
+ * s * |q - z| * |x|.  An inf or NaN in a token's x makes that token's outputs
+ * NaN, of Q2_INT4 not finite (the IEEE result is non-finite for every row;
+ * the fixed-point sums carry a sticky flag for it).  Launches use programmatic dependent launch: weights are
  * fetched before the previous kernel on the stream has finished; x, y and
  * the workspace are touched only after it has.  Returns Q2_ECUDA if a
  * launch fails. */
@@ -214,7 +221,8 @@ int q2_gemv(q2_fmt fmt, const q2_handle* h, const void* x, void* y, int ntok, q2
  * (packed)", Kernels (at up to 8 tokens a second stream loads each weight
  * matrix into L2 two matmuls ahead of its use, paced by a progress flag);
  * here the launch order itself paces it, so nothing waits on a flag.
- * Results are bit-identical to the same q2_gemv calls.  Every handle needs
+ * The weights of a Q2_INT4 GEMV are not fetched ahead, nor does its launch
+ * fetch those of others.  Results are bit-identical to the same q2_gemv calls.  Every handle needs
  * its workspace as for q2_gemv (handles may share one workspace: the calls
  * are ordered).  All handles and pointers are checked before anything is
  * launched; a launch failure returns its status with the launches before
@@ -389,17 +397,18 @@ int q2_attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, 
 #define Q2_ERR_LENGTH 0x100u    /* a sequence length outside its table row     */
 #define Q2_ERR_PAGE 0x200u      /* a page number outside the pools             */
 
-/* Device-side error word of the tensor-core (multi-token) and the attention
- * kernels, then cleared: 0 in normal operation; Q2_ERR_LENGTH and Q2_ERR_PAGE
- * as above; any other bit means a bounded wait on the tensor core ran out and the kernel skipped its work (the rows of the tiles
+/* Device-side error word of the tensor-core (7..64 tokens; Q2_INT4 17..64) and
+ * the attention kernels, then cleared: 0 in normal operation; Q2_ERR_LENGTH
+ * and Q2_ERR_PAGE as above; any other bit means a bounded wait on the tensor
+ * core ran out and the kernel skipped its work (the rows of the tiles
  * concerned are NaN).  Before such a kernel's CTA exits it waits, with the
  * full bound, for its copies and MMAs in flight, and it still meets the
  * other CTAs of its cluster at both of their barriers.  Synchronous: reads
  * device memory of the current device. */
 int q2_device_errors(unsigned int* out);
 
-/* Test hook, not for production use: limits the tensor-core kernel's stage
- * waits (the helper warp's wait for a slice's decoded weights and x tile) to
+/* Test hook, not for production use: limits the tensor-core kernels' stage
+ * waits (the issuing warps' wait for a slice's decoded weights and x tile) to
  * `polls` polls on the current device (0 restores the normal bound), so a
  * test can make them run out and check the error path above without
  * faulting or hanging the GPU.  Synchronous.  Q2_EINVAL for polls < 0. */
