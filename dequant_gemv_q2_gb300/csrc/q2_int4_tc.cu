@@ -14,10 +14,10 @@
 //   - x of all tokens comes to shared memory in the 128-byte swizzle: fp16 by
 //     TMA, which one warp asks for; 8-bit x through the registers of 8 staging
 //     warps, which turn it to fp16;
-//   - 2 issuing warps take blocks in turn: lane 0 issues the block's eight
+//   - 2 warps issue the products: one waits for a block and a free accumulator
+//     and grants the group at a named barrier, lane 0 of the other issues its
 //     M = 128, K = 16 products and commits them.  An issuing thread that
-//     touches memory waits for its own queue of products, so with two of them
-//     one waits while the other's products run;
+//     touches memory waits for its own queue of products; this one does not;
 //   - 8 summing warps, two per lane quarter (half of the tokens each), a row
 //     per lane, read each scale group's product from one of kAccs accumulators, multiply it by the
 //     group's scale and add it to the row's fp32 sums in registers: group
@@ -28,9 +28,10 @@
 // added in column order.
 //
 // Every wait is bounded: one that runs out sets the error word
-// (q2_device_errors) and a flag on which the other roles give up; the
-// products issued are waited for before tensor memory is released, and the
-// CTA's rows come out NaN.
+// (q2_device_errors) and a flag on which the other roles give up (the issuing
+// warp, which reads no memory, is led to its end by the granting one: its
+// products then work on whatever is there).  The products issued are waited
+// for before tensor memory is released, and the CTA's rows come out NaN.
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -54,7 +55,8 @@ template <bool X8>
 __host__ __device__ constexpr int tc_threads() { return (kDec + stage_warps<X8>() + kIssue + kSum) * 32; }
 constexpr int kTurn = 2;                      // decoder warps of a lane quarter, blocks in turn
 constexpr int kRing = 4;                      // blocks in flight: A in tensor memory, x in shared memory
-constexpr int kAccs = 2 * kIssue;             // accumulators of 64 columns, two of each issuing warp (which so sees all their phases)
+constexpr int kAccs = 4;                      // accumulators of 64 columns
+constexpr int kGrants = 8;                    // named barriers of the granting and the issuing warp, more than kAccs
 constexpr int kRaw = 3;                       // its blocks of packed weights in shared memory per decoder warp
 constexpr int kRawTile = 1024 + 64, kRawBytes = 2 * kRawTile;   // two row tiles: a block and the zero points
 constexpr uint32_t kTmem = 512, kAcol = 64 * kAccs;
@@ -112,7 +114,7 @@ struct Bars {
   uint64_t done[kRing];       // its products are done: the stage is free (commit)
   uint64_t ready[kAccs];      // an accumulator holds a group's product (commit)
   uint64_t taken[kAccs];      // it has been read (summing warps)
-  uint64_t drain[kIssue];     // everything an issuing warp has issued is done
+  uint64_t drain;             // everything issued is done
   uint32_t tmem;
   int abort, copied;          // a wait ran out; blocks of x requested by TMA
 };
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       mbar_init(saddr(&bar->ready[i]), 1);
       mbar_init(saddr(&bar->taken[i]), N > 32 ? kSum : kSum / 2);
     }
-    for (int i = 0; i < kIssue; ++i) mbar_init(saddr(&bar->drain[i]), 1);
+    mbar_init(saddr(&bar->drain), 1);
     bar->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
         int copied = 0;
         for (int i = 0; i < n; ++i) {
           const int st = i % kRing;
-          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
+          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u) && !__any_sync(~0u, *give_up);   // (done is also told of products given up)
           if (!ok) break;
           if (lane == 0) {
             const uint32_t full = saddr(&bar->full[st]), d = sB + st * bbytes;
@@ -334,38 +336,50 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       }
     }
   } else if (warp < kDec + kStage + kIssue) {
-    // ---- products of every kIssue-th block
+    // ---- products: a granting and an issuing warp, which meet at named barriers
     pdl_wait();
-    const int me = __shfl_sync(~0u, warp, 0) - kDec - kStage;
-    const uint32_t idesc = idesc_f16(kRows, N);
-    const long long limit = q2_int4_stage_wait_limit;         // in plain polls, which do not sleep
-    for (int i = me; i < n && ok; i += kIssue) {
-      const int st = i % kRing;
-      if (limit > 0 && !__all_sync(~0u, mbar_wait(saddr(&bar->full[st]), (uint32_t)(i / kRing) & 1u, limit))) ok = failed(3u);
-      if (ok) ok = wait(bar->full[st], i / kRing, 3u);
+    if (__shfl_sync(~0u, warp, 0) == kDec + kStage) {
+      const long long limit = q2_int4_stage_wait_limit;       // in plain polls, which do not sleep
+      for (int i = 0; i < n; ++i) {
+        const int st = i % kRing;
+        if (ok && limit > 0 && !__all_sync(~0u, mbar_wait(saddr(&bar->full[st]), (uint32_t)(i / kRing) & 1u, limit)))
+          ok = failed(3u);
+        if (ok) ok = wait(bar->full[st], i / kRing, 3u);
 #pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        if (!ok) break;
-        const int gi = i / kIssue * GPB + q, d = 2 * me + (gi & 1);    // this warp's groups in turn
-        if (gi >= 2) ok = wait(bar->taken[d], gi / 2 - 1, 4u);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem + kAcol + st * 64 + q * (STEPS * 8), acc0 = tmem + d * 64;
+        for (int q = 0; q < GPB; ++q) {
+          const int gi = i * GPB + q, d = gi % kAccs;
+          if (ok && gi >= kAccs) ok = wait(bar->taken[d], gi / kAccs - 1, 4u);
+          tc_fence_after();
+          tc_fence_before();
+          if (ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + gi % kGrants) : "memory");
+          else asm volatile("bar.sync %0, 64;" ::"r"(1 + gi % kGrants) : "memory");
+        }
+      }
+    } else {
+      const uint32_t idesc = idesc_f16(kRows, N);
+      for (int i = 0; i < n; ++i) {
+        const int st = i % kRing;
         const uint64_t lo = sdesc_sw128(sB + st * bbytes), hi = sdesc_sw128(sB + st * bbytes + atom);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const int k = q * STEPS + s;
-          mma_lane0(lane, acc0, at + s * 8, (k < 4 ? lo : hi) + (k & 3) * 2, idesc, s > 0 ? 1u : 0u);
+        for (int q = 0; q < GPB; ++q) {
+          const int gi = i * GPB + q, d = gi % kAccs;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + gi % kGrants) : "memory");
+          tc_fence_after();
+          const uint32_t at = tmem + kAcol + st * 64 + q * (STEPS * 8), acc0 = tmem + d * 64;
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) {
+            const int k = q * STEPS + s;
+            mma_lane0(lane, acc0, at + s * 8, (k < 4 ? lo : hi) + (k & 3) * 2, idesc, s > 0 ? 1u : 0u);
+          }
+          commit_lane0(lane, saddr(&bar->ready[d]));
+          if (q + 1 == GPB) commit_lane0(lane, saddr(&bar->done[st]));
         }
-        commit_lane0(lane, saddr(&bar->ready[d]));
-        if (q + 1 == GPB) commit_lane0(lane, saddr(&bar->done[st]));
-        __syncwarp();
       }
+      // whatever was issued is waited for, on every path
+      if (lane == 0) mma_commit(saddr(&bar->drain));
+      __syncwarp();
+      if (!__all_sync(~0u, mbar_wait(saddr(&bar->drain), 0u))) ok = failed(5u);
     }
-    // whatever was issued is waited for, with the full bound, on every path
-    if (lane == 0) mma_commit(saddr(&bar->drain[me]));
-    __syncwarp();
-    if (!__all_sync(~0u, mbar_wait(saddr(&bar->drain[me]), 0u))) ok = failed(5u);
   } else {
     // ---- sums: lane = row `row` of the tile, tokens c0 .. c0 + 31
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -401,8 +415,8 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       copy(i + kScales - 1);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
-        const int gi = i / kIssue * GPB + q, d = 2 * (i % kIssue) + (gi & 1);
-        if (ok) ok = wait(bar->ready[d], gi / 2, 6u);
+        const int gi = i * GPB + q, d = gi % kAccs;
+        if (ok) ok = wait(bar->ready[d], gi / kAccs, 6u);
         if (ok) {
           tc_fence_after();
           const uint32_t sw = lds16(ring + (i % kScales) * (32 * GPB * 4) + q * 4 + ((row >> 3) & 1) * 2);
@@ -423,6 +437,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       }
       const bool ends = now.blk + 1 == a.nblk;
       if (ends || i + 1 == n) {                     // a tile's end, or the run's; NaN where a wait ran out
+        if (__any_sync(~0u, *give_up)) ok = false;
         const int r = now.tile * kRows + row;
         float* o = part + (begun ? N * kOutLd : 0) + c0 * kOutLd + row;
 #pragma unroll
