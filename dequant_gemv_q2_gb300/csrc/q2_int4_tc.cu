@@ -6,11 +6,12 @@
 // CTAs, and the 128-column blocks of a cluster's tiles evenly over its CTAs,
 // one per SM: a CTA runs its run of blocks, across the ends of tiles, through
 // rings of stages with four roles:
-//   - 8 decoder warps, two per TMEM lane quarter taking blocks in turn, copy
-//     their weights to shared memory kRaw - 1 of their blocks ahead, unpack
-//     them to q - z in fp16 and store them to tensor memory.  The packed order
-//     is that of a 16 x 16 operand fragment, which is what tcgen05.st's
-//     16x128b shape stores: no exchange;
+//   - 8 decoder warps, two per TMEM lane quarter taking blocks in turn, bring
+//     their weights to shared memory kRaw - 1 of their blocks ahead (one bulk
+//     copy per row tile, scales and zero points with it), unpack them to q - z
+//     in fp16 and store them to tensor memory.  The packed order is that of a
+//     16 x 16 operand fragment, which is what tcgen05.st's 16x128b shape
+//     stores: no exchange.  The scales go to a ring for the summing warps;
 //   - x of all tokens comes to shared memory in the 128-byte swizzle: fp16 by
 //     TMA, which one warp asks for; 8-bit x through the registers of 8 staging
 //     warps, which turn it to fp16;
@@ -19,13 +20,26 @@
 //     M = 128, K = 16 products and commits them.  An issuing thread that
 //     touches memory waits for its own queue of products; this one does not;
 //   - 8 summing warps, two per lane quarter (half of the tokens each), a row
-//     per lane, read each scale group's product from one of kAccs accumulators, multiply it by the
-//     group's scale and add it to the row's fp32 sums in registers: group
-//     scales cost no rounding, and the accumulator is free for another group.
+//     per lane, read each scale group's product from one of kAccs
+//     accumulators, multiply it by the group's scale and add it to the row's
+//     fp32 sums in registers: group scales cost no rounding, and the
+//     accumulator is free for another group.
 // A tile that begins and ends inside a CTA's run is written from those
 // registers while the next one's products run.  The others' sums meet at the
 // end in distributed shared memory, after one barrier of the cluster, and are
 // added in column order.
+//
+// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 41.8 us on the
+// device, 2.3 TB/s, 0.55 PFLOP/s (a block of 128 x 128 every 800 cycles of an
+// SM).  What bounds it is not one unit: the decoders (850 cycles per block and
+// pair of warps, their 9 instructions per 8 weights being half of the issue
+// slots used), the way of x from L2 (1400 to 1900 cycles from the request to
+// the stage, 16 KB of x per 8.8 KB of weights) and the chain block - grant -
+// products - free stage (1000) all come to about the same.  12 or 16 decoder
+// warps, deeper rings of weights or x, one barrier less or products left out
+// each change it by less than 5%.  What the waits cost shows in the steps:
+// addresses that the compiler cannot show to be uniform cost 200 cycles and
+// more at each wait (58 -> 42 us at 24576 x 4096 in groups of 32).
 //
 // Every wait is bounded: one that runs out sets the error word
 // (q2_device_errors) and a flag on which the other roles give up (the issuing
@@ -56,11 +70,14 @@ __host__ __device__ constexpr int tc_threads() { return (kDec + stage_warps<X8>(
 constexpr int kTurn = 2;                      // decoder warps of a lane quarter, blocks in turn
 constexpr int kRing = 4;                      // blocks in flight: A in tensor memory, x in shared memory
 constexpr int kAccs = 4;                      // accumulators of 64 columns
+static_assert(kAccs == kRing, "with one group to a block its accumulator's barrier tells of its stage too");
 constexpr int kGrants = 8;                    // named barriers of the granting and the issuing warp, more than kAccs
 constexpr int kRaw = 3;                       // its blocks of packed weights in shared memory per decoder warp
-constexpr int kRawTile = 1024 + 64, kRawBytes = 2 * kRawTile;   // two row tiles: a block and the zero points
+template <int GPB>
+__host__ __device__ constexpr int raw_tile() { return Q2_INT4_BLOCK_BYTES + GPB * 48; }   // a row tile's block with its sides
 constexpr uint32_t kTmem = 512, kAcol = 64 * kAccs;
-constexpr int kScales = 4;                    // blocks of scales in shared memory per summing warp
+constexpr int kScales = kRing + kAccs;        // blocks of scales in shared memory: a block's products done means that the
+                                              // scales kAccs blocks before have been used
 constexpr int kStageWarps = 4;                // staging warps of a group (8-bit x)
 constexpr int kOutLd = kRows + 4, kMaxCluster = 8;
 constexpr int kOneCta = 116 * 1024;           // at most one CTA of this or the other tcgen05 kernels per SM (each holds all of TMEM)
@@ -91,6 +108,26 @@ __device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
 }
 
+// Whether the phase of the given parity is complete (after a short sleep at most).
+__device__ __forceinline__ uint32_t try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
+
+// `bytes` of global memory to shared memory, reported to the mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 struct TcArgs {
   CUtensorMap xmap;                           // fp16 x: box of 64 columns x N tokens, 128-byte swizzle, zeros outside
   Int4Args a;
@@ -110,6 +147,7 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t at, const uint32_t (&r)[32
 }
 
 struct Bars {
+  uint64_t raw[kDec][kRaw];   // a decoder warp's packed weights are there
   uint64_t full[kRing];       // A and x of a block are there (decoder and staging warps)
   uint64_t done[kRing];       // its products are done: the stage is free (commit)
   uint64_t ready[kAccs];      // an accumulator holds a group's product (commit)
@@ -123,8 +161,8 @@ template <int GPB, bool X8>
 __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_constant__ TcArgs ta) {
   extern __shared__ __align__(1024) unsigned char q2_int4tc_smem[];
   const Int4Args& a = ta.a;
-  constexpr int STEPS = 8 / GPB, kStage = stage_warps<X8>();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int STEPS = 8 / GPB, kStage = stage_warps<X8>(), TILE = raw_tile<GPB>();
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform, and so are the barriers' addresses
   const int N = ta.N, cs = ta.cs, atom = N * 128, bbytes = 2 * atom;
   // this CTA's run: blocks u0 .. u0 + n - 1 of the cluster's T, tile by tile
   const int rank = (int)blockIdx.x % cs, cl = (int)blockIdx.x / cs, ncl = (int)gridDim.x / cs;
@@ -145,9 +183,9 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
   };
   const uint32_t sB = (saddr(q2_int4tc_smem) + 1023u) & ~1023u;
   unsigned char* B = q2_int4tc_smem + (sB - saddr(q2_int4tc_smem));
-  const uint32_t sraw = sB + kRing * bbytes, ssc = sraw + kDec * kRaw * kRawBytes;
+  const uint32_t sraw = sB + kRing * bbytes, ssc = sraw + kDec * kRaw * 2 * TILE;
   // the sums of a tile begun before this run, and of one not finished in it
-  float* part = reinterpret_cast<float*>(B + kRing * bbytes + kDec * kRaw * kRawBytes + kSum * kScales * 512);   // [2][N][kOutLd]
+  float* part = reinterpret_cast<float*>(B + kRing * bbytes + kDec * kRaw * 2 * TILE + kScales * kRows * 2 * GPB);   // [2][N][kOutLd]
   Bars* bar = reinterpret_cast<Bars*>(part + 2 * N * kOutLd);
   volatile int* give_up = &bar->abort;
 
@@ -161,6 +199,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       mbar_init(saddr(&bar->taken[i]), N > 32 ? kSum : kSum / 2);
     }
     mbar_init(saddr(&bar->drain), 1);
+    for (int i = 0; i < kDec * kRaw; ++i) mbar_init(saddr(&bar->raw[0][i]), 1);
     bar->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -183,63 +222,76 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     }
     return false;
   };
-  auto wait = [&](uint64_t& b, int phase, unsigned int code) {
-    return __all_sync(~0u, mbar_wait(saddr(&b), (uint32_t)phase & 1u, kSpinLimit, give_up)) ? true : failed(code);
+  // A block's products are done when its last group's are (with several groups
+  // to a block an accumulator's barrier may be phases ahead of a stage's).
+  auto done = [&](unsigned st) -> uint64_t& { return GPB == 1 ? bar->ready[st] : bar->done[st]; };
+  // All lanes poll and leave together: the loop and what it reads stay uniform.
+  auto wait = [&](uint64_t& b, unsigned phase, unsigned int code) {
+    const uint32_t at = saddr(&b), parity = phase & 1u;
+    for (int k = 0; k < (int)kSpinLimit; ++k) {
+      if (__all_sync(~0u, try_phase(at, parity))) return true;
+      if ((k & 31) == 31 && __any_sync(~0u, *give_up)) break;
+    }
+    return failed(code);
   };
   float2 acc[16];                                   // 32 tokens
 
   if (warp < kDec) {
     // ---- decoders: row tiles 2 * quarter, + 1 of every kTurn-th block
     const int quarter = warp & 3, turn = warp >> 2, g = lane >> 2;
-    const uint32_t raw = sraw + warp * (kRaw * kRawBytes);
-    const bool zcopy = a.zeros && lane < GPB;
+    const uint32_t raw = sraw + warp * (kRaw * 2 * TILE);
     Place at = place_of(u0 + turn);                 // of the next block to copy
     const unsigned char* src[2];
     auto point = [&]() {
 #pragma unroll
       for (int m = 0; m < 2; ++m)                   // a missing row tile: the last one; its rows are not stored
-        src[m] = a.w + ((size_t)min(at.tile * (kRows / 16) + 2 * quarter + m, a.ntile - 1) * a.nblk + at.blk) * a.item +
-                 lane * 16;
+        src[m] = a.w + ((size_t)min(at.tile * (kRows / 16) + 2 * quarter + m, a.ntile - 1) * a.nblk + at.blk) * a.item;
     };
     point();
-    auto copy = [&](int i, uint32_t slot) {
+    auto copy = [&](int i, int k) {                 // block i to slot k
       if (i < n) {
-        const uint32_t d = slot + lane * 16;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          cp16(d + m * kRawTile, src[m]);
-          cp16(d + m * kRawTile + 512, src[m] + 512);
-          if (zcopy) cp16(d + m * kRawTile + 1024, src[m] + 1024 + GPB * 32);
-          src[m] += kTurn * a.item;
+        if (lane == 0) {
+          const uint32_t b = saddr(&bar->raw[warp][k]), d = raw + k * (2 * TILE);
+          mbar_expect_tx(b, 2u * a.item);
+          bulk_load(d, src[0], a.item, b);
+          bulk_load(d + TILE, src[1], a.item, b);
         }
+        src[0] += kTurn * a.item;
+        src[1] += kTurn * a.item;
         if (move(at, kTurn)) point();
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int k = 0; k < kRaw - 1; ++k) copy(turn + k * kTurn, raw + k * kRawBytes);
-    uint32_t slot = raw, before = raw + (kRaw - 1) * kRawBytes;
-    for (int i = turn; i < n; i += kTurn) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 2) : "memory");
-      __syncwarp();
-      copy(i + (kRaw - 1) * kTurn, before);
-      const int st = i % kRing;
-      if (i - kRing < kTurn && i >= kRing) pdl_wait();       // no bounded wait may have to wait for the previous kernel
+    for (int k = 0; k < kRaw - 1; ++k) copy(turn + k * kTurn, k);
+    int k = 0, free = kRaw - 1;                     // slot in use, slot before it
+    unsigned turned = 0;                            // phase of the slot in use
+    for (unsigned i = turn; i < (unsigned)n; i += kTurn) {
+      const unsigned st = i % kRing;
+      if (i >= kRing && i < kRing + kTurn) pdl_wait();       // no bounded wait may have to wait for the previous kernel
+      ok = wait(bar->raw[warp][k], turned, 7u);
+      copy(i + (kRaw - 1) * kTurn, free);
+      const uint32_t slot = raw + k * (2 * TILE);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const uint32_t from = slot + m * kRawTile;
+        const uint32_t from = slot + m * TILE;
         const uint4 w[2] = {lds128(from + lane * 16), lds128(from + 512 + lane * 16)};
         uint32_t A[32];
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
-          const Zeros z = a.zeros ? zeros_of(lds16(from + 1024 + (g * GPB + q) * 2)) : Zeros{0x64086408u, 0xd480d480u};
+          const Zeros z = a.zeros ? zeros_of(lds16(from + Q2_INT4_BLOCK_BYTES + GPB * 32 + (g * GPB + q) * 2)) : Zeros{0x64086408u, 0xd480d480u};
 #pragma unroll
           for (int t = q * STEPS; t < (q + 1) * STEPS; ++t)
             unpack_step(word(w[t >> 2], t & 3), z, A[4 * t], A[4 * t + 1], A[4 * t + 2], A[4 * t + 3]);
         }
         if (m == 0) {
-          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 1u);
+          if (ok && i >= kRing) ok = wait(done(st), i / kRing - 1, 1u);
           if (!ok) break;
           tc_fence_after();
+          // the scales of both row tiles, as they are, for the summing warps
+          if (lane < 4 * GPB) {
+            const int e = lane % (2 * GPB), mm = lane / (2 * GPB);
+            const uint4 v = lds128(slot + mm * TILE + Q2_INT4_BLOCK_BYTES + e * 16);
+            sts128(ssc + (i % kScales) * (kRows * 2 * GPB) + (2 * quarter + mm) * (32 * GPB) + e * 16, v);
+          }
         }
         tmem_st_frag(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + kAcol + st * 64, A);
       }
@@ -251,10 +303,18 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(saddr(&bar->full[st]));
-      before = slot;
-      slot = slot == raw + (kRaw - 1) * kRawBytes ? raw : slot + kRawBytes;
+      free = k;
+      k = k + 1 == kRaw ? 0 : k + 1;
+      turned ^= k == 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // no copy may land after the CTA has gone: those asked for when this warp gave up
+    if (!ok)
+      for (int e = 0; e < kRaw; ++e) {
+        (void)mbar_wait(saddr(&bar->raw[warp][k]), turned);
+        k = k + 1 == kRaw ? 0 : k + 1;
+        turned ^= k == 0;
+        if (undone + (e + 1) * kTurn >= n || e + 1 == kRaw) break;
+      }
   } else if (warp < kDec + kStage) {
     // ---- x of all tokens: copied as it is by TMA (fp16), or turned to fp16 on the way
     pdl_wait();                                     // x may come from the previous kernel
@@ -262,9 +322,9 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       if (warp == kDec) {
         Place at = place_of(u0);
         int copied = 0;
-        for (int i = 0; i < n; ++i) {
-          const int st = i % kRing;
-          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u) && !__any_sync(~0u, *give_up);   // (done is also told of products given up)
+        for (unsigned i = 0; i < (unsigned)n; ++i) {
+          const unsigned st = i % kRing;
+          if (i >= kRing) ok = wait(done(st), i / kRing - 1, 2u) && !__any_sync(~0u, *give_up);   // (done is also told of products given up)
           if (!ok) break;
           if (lane == 0) {
             const uint32_t full = saddr(&bar->full[st]), d = sB + st * bbytes;
@@ -311,9 +371,9 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
           }
         };
         load(group);
-        for (int i = group; i < n; i += 2) {
-          const int st = i % kRing;
-          if (i >= kRing) ok = wait(bar->done[st], i / kRing - 1, 2u);
+        for (unsigned i = group; i < (unsigned)n; i += 2) {
+          const unsigned st = i % kRing;
+          if (i >= kRing) ok = wait(done(st), i / kRing - 1, 2u);
           if (!ok) break;
 #pragma unroll
           for (int k = 0; k < TASKS; ++k) {
@@ -338,16 +398,16 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
   } else if (warp < kDec + kStage + kIssue) {
     // ---- products: a granting and an issuing warp, which meet at named barriers
     pdl_wait();
-    if (__shfl_sync(~0u, warp, 0) == kDec + kStage) {
+    if (warp == kDec + kStage) {
       const long long limit = q2_int4_stage_wait_limit;       // in plain polls, which do not sleep
-      for (int i = 0; i < n; ++i) {
-        const int st = i % kRing;
+      for (unsigned i = 0; i < (unsigned)n; ++i) {
+        const unsigned st = i % kRing;
         if (ok && limit > 0 && !__all_sync(~0u, mbar_wait(saddr(&bar->full[st]), (uint32_t)(i / kRing) & 1u, limit)))
           ok = failed(3u);
         if (ok) ok = wait(bar->full[st], i / kRing, 3u);
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
-          const int gi = i * GPB + q, d = gi % kAccs;
+          const unsigned gi = i * GPB + q, d = gi % kAccs;
           if (ok && gi >= kAccs) ok = wait(bar->taken[d], gi / kAccs - 1, 4u);
           tc_fence_after();
           tc_fence_before();
@@ -357,12 +417,12 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       }
     } else {
       const uint32_t idesc = idesc_f16(kRows, N);
-      for (int i = 0; i < n; ++i) {
-        const int st = i % kRing;
+      for (unsigned i = 0; i < (unsigned)n; ++i) {
+        const unsigned st = i % kRing;
         const uint64_t lo = sdesc_sw128(sB + st * bbytes), hi = sdesc_sw128(sB + st * bbytes + atom);
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
-          const int gi = i * GPB + q, d = gi % kAccs;
+          const unsigned gi = i * GPB + q, d = gi % kAccs;
           asm volatile("bar.sync %0, 64;" ::"r"(1 + gi % kGrants) : "memory");
           tc_fence_after();
           const uint32_t at = tmem + kAcol + st * 64 + q * (STEPS * 8), acc0 = tmem + d * 64;
@@ -372,7 +432,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
             mma_lane0(lane, acc0, at + s * 8, (k < 4 ? lo : hi) + (k & 3) * 2, idesc, s > 0 ? 1u : 0u);
           }
           commit_lane0(lane, saddr(&bar->ready[d]));
-          if (q + 1 == GPB) commit_lane0(lane, saddr(&bar->done[st]));
+          if (GPB > 1 && q + 1 == GPB) commit_lane0(lane, saddr(&bar->done[st]));
         }
       }
       // whatever was issued is waited for, on every path
@@ -386,57 +446,35 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     const int c0 = (warp - kDec - kStage - kIssue) / 4 * 32;
     if (c0 < N) {
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-    // the scales of rows row % 8 and row % 8 + 8 of the row tile, kScales - 1 blocks ahead
-    Place at = place_of(u0), now = at;              // of the next scales to copy, of the block in use
-    const uint32_t ring = ssc + (warp - kDec - kStage - kIssue) * (kScales * 32 * GPB * 4) + lane * (GPB * 4);
-    const unsigned char* side;
-    auto point = [&]() {
-      side = a.w + ((size_t)min(at.tile * (kRows / 16) + (row >> 4), a.ntile - 1) * a.nblk + at.blk) * a.item + 1024 +
-             (row & 7) * (GPB * 4);
-    };
-    point();
-    auto copy = [&](int i) {
-      if (i < n) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ring + (i % kScales) * (32 * GPB * 4)), "l"(side),
-                     "n"(GPB * 4)
-                     : "memory");
-        side += a.item;
-        if (move(at, 1)) point();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+    const uint32_t sc = ssc + (row >> 4) * (32 * GPB) + (row & 7) * (GPB * 4) + ((row >> 3) & 1) * 2;   // this row's scales
+    Place now = place_of(u0);
 #pragma unroll
     for (int t = 0; t < 16; ++t) acc[t] = make_float2(0.f, 0.f);
-    for (int k = 0; k < kScales - 1; ++k) copy(k);
     pdl_wait();
     bool begun = now.blk == 0;                      // the tile in use began in this run
-    for (int i = 0; i < n; ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kScales - 2) : "memory");
-      copy(i + kScales - 1);
+    for (unsigned i = 0; i < (unsigned)n; ++i) {
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
-        const int gi = i * GPB + q, d = gi % kAccs;
+        const unsigned gi = i * GPB + q, d = gi % kAccs;
         if (ok) ok = wait(bar->ready[d], gi / kAccs, 6u);
         if (ok) {
           tc_fence_after();
-          const uint32_t sw = lds16(ring + (i % kScales) * (32 * GPB * 4) + q * 4 + ((row >> 3) & 1) * 2);
-          const float s1 = __half2float(__ushort_as_half((unsigned short)sw));
+          const float s1 = __half2float(__ushort_as_half((unsigned short)lds16(sc + (i % kScales) * (kRows * 2 * GPB) + q * 4)));
           const float2 s2 = make_float2(s1, s1);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (c0 + 16 * h < N) {
-              float v[16];
-              tmem_ld16(tl + d * 64 + 16 * h, v);
+          for (int h = 0; h < 2; ++h) {             // (past N: whatever is there)
+            float v[16];
+            tmem_ld16(tl + d * 64 + 16 * h, v);
 #pragma unroll
-              for (int t = 0; t < 8; ++t) fma2(acc[8 * h + t], s2, make_float2(v[2 * t], v[2 * t + 1]));
-            }
+            for (int t = 0; t < 8; ++t) fma2(acc[8 * h + t], s2, make_float2(v[2 * t], v[2 * t + 1]));
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(saddr(&bar->taken[d]));
         }
       }
       const bool ends = now.blk + 1 == a.nblk;
-      if (ends || i + 1 == n) {                     // a tile's end, or the run's; NaN where a wait ran out
+      if (ends || i + 1 == (unsigned)n) {                     // a tile's end, or the run's; NaN where a wait ran out
         if (__any_sync(~0u, *give_up)) ok = false;
         const int r = now.tile * kRows + row;
         float* o = part + (begun ? N * kOutLd : 0) + c0 * kOutLd + row;
@@ -455,7 +493,6 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       }
       move(now, 1);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
   // no copy may land after the CTA has gone: on an error the decoders make up
@@ -516,7 +553,7 @@ int launch_tc(const Int4Args& a, void* stream) {
   ta.a = a;
   ta.N = (a.ntok + 15) / 16 * 16;
   ta.ntiles = (a.ntile + kRows / 16 - 1) / (kRows / 16);
-  const int work = kRing * ta.N * 256 + kDec * kRaw * kRawBytes + kSum * kScales * 512 + 2 * ta.N * kOutLd * 4;
+  const int work = kRing * ta.N * 256 + kDec * kRaw * 2 * raw_tile<GPB>() + kScales * kRows * 2 * GPB + 2 * ta.N * kOutLd * 4;
   const int smem = std::max(kOneCta, 1024 + work + (int)sizeof(Bars));
   if (set_smem(fn, smem)) return Q2_ECUDA;
   // The cluster size with the shortest run of blocks, each doubling of it
