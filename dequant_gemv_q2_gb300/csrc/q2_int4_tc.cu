@@ -29,17 +29,18 @@
 // end in distributed shared memory, after one barrier of the cluster, and are
 // added in column order.
 //
-// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 41.8 us on the
-// device, 2.3 TB/s, 0.55 PFLOP/s (a block of 128 x 128 every 800 cycles of an
-// SM).  What bounds it is not one unit: the decoders (850 cycles per block and
-// pair of warps, their 9 instructions per 8 weights being half of the issue
-// slots used), the way of x from L2 (1400 to 1900 cycles from the request to
-// the stage, 16 KB of x per 8.8 KB of weights) and the chain block - grant -
-// products - free stage (1000) all come to about the same.  12 or 16 decoder
-// warps, deeper rings of weights or x, one barrier less or products left out
-// each change it by less than 5%.  What the waits cost shows in the steps:
-// addresses that the compiler cannot show to be uniform cost 200 cycles and
-// more at each wait (58 -> 42 us at 24576 x 4096 in groups of 32).
+// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 38.5 us on the
+// device, 2.5 TB/s, 0.59 PFLOP/s (a block of 128 x 128 every 900 cycles of an
+// SM).  What bounds it is not one unit: the decoders (about 800 cycles per
+// block, their 9 instructions per 8 weights being half of the issue slots
+// used), the way of x from L2 (1400 to 1900 cycles from the request to the
+// stage, 16 KB of x per 8.8 KB of weights) and the chain block - grant -
+// products - free stage (1000, four blocks in it) come to about the same: in
+// trials without the unpacking it took 14% less, without the products 10%,
+// without x 2%; 12 or 16 decoder warps and deeper rings of weights or x gain
+// nothing.  What waits cost shows in the steps: a barrier's address that the
+// compiler cannot show to be uniform costs 200 cycles and more at each wait
+// (58 -> 42 us at 24576 x 4096 in groups of 32).
 //
 // Every wait is bounded: one that runs out sets the error word
 // (q2_device_errors) and a flag on which the other roles give up (the issuing
@@ -268,19 +269,29 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       const unsigned st = i % kRing;
       if (i >= kRing && i < kRing + kTurn) pdl_wait();       // no bounded wait may have to wait for the previous kernel
       ok = wait(bar->raw[warp][k], turned, 7u);
-      copy(i + (kRaw - 1) * kTurn, free);
       const uint32_t slot = raw + k * (2 * TILE);
+      uint4 w[2][2];
+      uint32_t zz[2][GPB];
+      auto read = [&](int m) {
+        const uint32_t from = slot + m * TILE;
+        w[m][0] = lds128(from + lane * 16);
+        w[m][1] = lds128(from + 512 + lane * 16);
+#pragma unroll
+        for (int q = 0; q < GPB; ++q)
+          zz[m][q] = a.zeros ? lds16(from + Q2_INT4_BLOCK_BYTES + GPB * 32 + (g * GPB + q) * 2) : 0x0808u;
+      };
+      read(0);
+      if constexpr (!X8) read(1);                   // both at once where registers allow (37.2 -> 34.5 us at 19456 x 10240)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const uint32_t from = slot + m * TILE;
-        const uint4 w[2] = {lds128(from + lane * 16), lds128(from + 512 + lane * 16)};
+        if (X8 && m == 1) read(1);
         uint32_t A[32];
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
-          const Zeros z = a.zeros ? zeros_of(lds16(from + Q2_INT4_BLOCK_BYTES + GPB * 32 + (g * GPB + q) * 2)) : Zeros{0x64086408u, 0xd480d480u};
+          const Zeros z = zeros_of(zz[m][q]);
 #pragma unroll
           for (int t = q * STEPS; t < (q + 1) * STEPS; ++t)
-            unpack_step(word(w[t >> 2], t & 3), z, A[4 * t], A[4 * t + 1], A[4 * t + 2], A[4 * t + 3]);
+            unpack_step(word(w[m][t >> 2], t & 3), z, A[4 * t], A[4 * t + 1], A[4 * t + 2], A[4 * t + 3]);
         }
         if (m == 0) {
           if (ok && i >= kRing) ok = wait(done(st), i / kRing - 1, 1u);
@@ -299,6 +310,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
         undone = i;
         break;
       }
+      copy(i + (kRaw - 1) * kTurn, free);           // while the stores are on their way
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -309,11 +321,10 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
     }
     // no copy may land after the CTA has gone: those asked for when this warp gave up
     if (!ok)
-      for (int e = 0; e < kRaw; ++e) {
+      for (int i = undone, e = 0; e < kRaw - 1 && i < n; i += kTurn, ++e) {
         (void)mbar_wait(saddr(&bar->raw[warp][k]), turned);
         k = k + 1 == kRaw ? 0 : k + 1;
         turned ^= k == 0;
-        if (undone + (e + 1) * kTurn >= n || e + 1 == kRaw) break;
       }
   } else if (warp < kDec + kStage) {
     // ---- x of all tokens: copied as it is by TMA (fp16), or turned to fp16 on the way
