@@ -30,7 +30,16 @@
 // the group's query heads as rows 0..7.  The probabilities are split into two
 // fp16 numbers, p = hi + lo, and lo takes rows 8..15 of the same
 // instructions: the numerators are as exact as with fp32 probabilities (an
-// error of 2^-22 instead of 2^-11 per term) at no cost.
+// error of 2^-22 instead of 2^-11 per term) at no cost.  More than eight query
+// heads to a key-value head are taken eight at a time, each reading the tokens
+// again (the second time mostly from L2).
+//
+// 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 319 us
+// on the device, 6.7 TB/s, the rate of a copy; one of 131072: 88 us, 6.1; 16
+// of 1 to 4096 with 40 query heads 30 us, 4.5 (each CTA's start, its ends of
+// sequences and the joins are 9 of them); one of 777 tokens 7.5 us: the
+// lengths, the first pages' numbers, the first rows and the join behind one
+// another.
 #include <cuda_fp16.h>
 
 #include "q2_common.cuh"

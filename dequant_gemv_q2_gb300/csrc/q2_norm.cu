@@ -6,14 +6,19 @@
 //   r' = fp16(h),  y16 = fp16(y),  s = max|y| / 127,  y8 = rint(y / s),
 //
 // all in fp32 from the fp16 inputs; h, y and s are each rounded once.  The sum
-// of squares is a tree over the row's threads in a fixed order, so a row's
-// result does not depend on the batch.
+// of squares is a tree over the row's threads in a fixed order (one up to as
+// many rows as SMs and one beyond), wherever the row lies.
 //
 // A row is read once and stays in registers between the sum, the maximum and
 // the stores, so the bytes of the inputs and outputs are all that moves.  Rows
 // of up to 512 columns take 16 or 32 threads each (a reduction is five
 // shuffles, no barrier); longer ones a block, which goes on to further rows
 // with the next row's loads in flight during the reductions of the one before.
+//
+// 16384 rows of 4096 with residual and both outputs: 107 us on the device, 5.6
+// of the 6.7 TB/s that a copy reaches (one row per block and no row ahead:
+// 164).  One row of 4096: 1.6 us, which is a launch, one trip to memory and
+// one block reduction; 64 rows of 5120 to 8 bits 2.3.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -59,24 +64,59 @@ __device__ __forceinline__ T row_reduce(T v, T* part) {
   return v;
 }
 
-// One thread's share of a row: CH pieces of 8 columns.  VEC: a piece is one
-// 16-byte access; otherwise its columns are strided by the row's nt threads.
-template <int CH, bool VEC>
+// 16 bytes that begin m bytes (even) into the 32 of a and b.
+__device__ __forceinline__ uint4 cut16(const uint4& a, const uint4& b, uint32_t m) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t t[6], u[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) t[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = m & 4 ? t[i + 1] : t[i];
+  const uint32_t s = (m & 2) * 8;
+  return make_uint4(__funnelshift_r(u[0], u[1], s), __funnelshift_r(u[1], u[2], s), __funnelshift_r(u[2], u[3], s),
+                    __funnelshift_r(u[3], u[4], s));
+}
+// 8 bytes that begin m bytes into the 16 of a and b.
+__device__ __forceinline__ uint2 cut8(const uint2& a, const uint2& b, uint32_t m) {
+  const uint32_t w0 = m & 4 ? a.y : a.x, w1 = m & 4 ? b.x : a.y, w2 = m & 4 ? b.y : b.x, s = (m & 3) * 8;
+  return make_uint2(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s));
+}
+
+// One thread's share of a row: CH pieces of 8 columns, in turn with the row's
+// other nt - 1 threads.  VEC: a piece is one 16-byte access.  Otherwise rows
+// may begin anywhere: a piece is cut out of two 16-byte loads, and written
+// through shared memory in pieces of 16 bytes as they lie in global memory;
+// the ends of a row go element by element (4096 rows of 5125 columns with
+// residual 50 us, 91 with every element by itself; 16 rows of 3001, where
+// only the latency counts, 4.3 and 2.7).  A thread's columns, and with them
+// the order of the sums, do not depend on where a row begins.
+template <int TPR, int CH, bool VEC>
 struct Row {
   int tid, nt, C;
   bool live;
-  __device__ __forceinline__ int col(int c, int i) const { return VEC ? (c * nt + tid) * 8 + i : (c * 8 + i) * nt + tid; }
+  __device__ __forceinline__ int col(int c) const { return (c * nt + tid) * 8; }
+  __device__ __forceinline__ static void sync() {
+    if (TPR) __syncwarp();
+    else __syncthreads();
+  }
 
   __device__ __forceinline__ void load(const __half* p, uint4 (&r)[CH]) const {
+    const uint32_t m = VEC ? 0 : (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (VEC) {
-        r[c] = live && col(c, 0) < C ? *reinterpret_cast<const uint4*>(p + col(c, 0)) : make_uint4(0, 0, 0, 0);
+      const int k = col(c);
+      r[c] = make_uint4(0, 0, 0, 0);
+      if (!live || k >= C) continue;
+      if (VEC || (m == 0 && k + 8 <= C)) {
+        r[c] = *reinterpret_cast<const uint4*>(p + k);
+      } else if (m && k > 0 && k + 16 <= C) {          // both loads lie inside the row
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + k) - m);
+        r[c] = cut16(from[0], from[1], m);
       } else {
         uint16_t* h = reinterpret_cast<uint16_t*>(&r[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          h[i] = live && col(c, i) < C ? reinterpret_cast<const uint16_t*>(p)[col(c, i)] : (uint16_t)0;
+          if (k + i < C) h[i] = reinterpret_cast<const uint16_t*>(p)[k + i];
       }
     }
   }
@@ -89,59 +129,95 @@ struct Row {
       v[2 * i + 1] = f.y;
     }
   }
-  __device__ __forceinline__ void store(__half* p, const float (&v)[CH][8]) const {
-    if (!live) return;
+  // buf: the row's place in shared memory (not VEC), 8 columns to an element
+  __device__ __forceinline__ void store(__half* p, const float (&v)[CH][8], uint4* buf) const {
+    const uint32_t m = VEC ? 0 : (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (VEC) {
-        uint4 raw;
-        __half2* h2 = reinterpret_cast<__half2*>(&raw);
+      const int k = col(c);
+      uint4 raw;
+      __half2* h2 = reinterpret_cast<__half2*>(&raw);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[c][2 * i], v[c][2 * i + 1]);
-        if (col(c, 0) < C) *reinterpret_cast<uint4*>(p + col(c, 0)) = raw;
-      } else {
+      for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[c][2 * i], v[c][2 * i + 1]);
+      if (!live || k >= C) continue;
+      if (VEC || (m == 0 && k + 8 <= C)) *reinterpret_cast<uint4*>(p + k) = raw;
+      else buf[k / 8] = raw;
+    }
+    if (VEC) return;
+    sync();
+    if (!live) return;
+    for (int g = m ? tid : C / 8; g * 8 < C + (int)m / 2; g += m ? nt : C) {   // columns k .. k + 7 (m == 0: the last ones)
+      const int k = g * 8 - (int)m / 2;
+      if (m && k >= 0 && k + 8 <= C) {
+        *reinterpret_cast<uint4*>(p + k) = cut16(buf[g - 1], buf[g], 16 - m);
+      } else if (m || tid == 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (col(c, i) < C) p[col(c, i)] = __float2half_rn(v[c][i]);
+          if (k + i >= 0 && k + i < C) p[k + i] = reinterpret_cast<const __half*>(buf)[k + i];
       }
     }
   }
-  __device__ __forceinline__ void store8(int8_t* p, const float (&v)[CH][8], float inv) const {
-    if (!live) return;
+  __device__ __forceinline__ void store8(int8_t* p, const float (&v)[CH][8], float inv, uint2* buf) const {
+    const uint32_t m = VEC ? 0 : (uint32_t)reinterpret_cast<uintptr_t>(p) & 7u;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (VEC) {
-        uint32_t lo = 0, hi = 0;
+      const int k = col(c);
+      uint32_t lo = 0, hi = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo |= (uint32_t)(__float2int_rn(v[c][i] * inv) & 0xff) << (8 * i);
-          hi |= (uint32_t)(__float2int_rn(v[c][i + 4] * inv) & 0xff) << (8 * i);
-        }
-        if (col(c, 0) < C) *reinterpret_cast<uint2*>(p + col(c, 0)) = make_uint2(lo, hi);
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        lo |= (uint32_t)(__float2int_rn(v[c][i] * inv) & 0xff) << (8 * i);
+        hi |= (uint32_t)(__float2int_rn(v[c][i + 4] * inv) & 0xff) << (8 * i);
+      }
+      if (!live || k >= C) continue;
+      if (VEC || (m == 0 && k + 8 <= C)) *reinterpret_cast<uint2*>(p + k) = make_uint2(lo, hi);
+      else buf[k / 8] = make_uint2(lo, hi);
+    }
+    if (VEC) return;
+    sync();
+    if (!live) return;
+    for (int g = m ? tid : C / 8; g * 8 < C + (int)m; g += m ? nt : C) {
+      const int k = g * 8 - (int)m;
+      if (m && k >= 0 && k + 8 <= C) {
+        *reinterpret_cast<uint2*>(p + k) = cut8(buf[g - 1], buf[g], 8 - m);
+      } else if (m || tid == 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (col(c, i) < C) p[col(c, i)] = (int8_t)__float2int_rn(v[c][i] * inv);
+          if (k + i >= 0 && k + i < C) p[k + i] = reinterpret_cast<const int8_t*>(buf)[k + i];
       }
     }
   }
 };
 
+// Shared memory of a block of `rows` rows: the outputs' images (not VEC).
+template <bool VEC>
+int norm_smem(const NormArgs& a, int rows) {
+  if (VEC) return 0;
+  const int pieces = (a.C + 7) / 8;
+  return rows * pieces * ((a.res_out ? 16 : 0) + (a.y ? 16 : 0) + (a.y8 ? 8 : 0));
+}
+
 // TPR: threads per row (16 or 32, several rows per block; 0: a block per row,
 // then every gridDim.x-th).  NT: threads of a block at most.
 template <int TPR, int CH, bool VEC, int NT>
-__global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs a) {
-  // Rows ahead: where the registers hold them (wider rows wait for theirs).
-  constexpr bool AHEAD = TPR == 0 && CH <= 2;
+__global__ void __launch_bounds__(NT, VEC || TPR || CH > 1 ? 0 : 2048 / NT) k_rmsnorm(const __grid_constant__ NormArgs a) {
+  // Rows ahead: where the registers hold them (wider rows wait for theirs, rows
+  // that may begin anywhere leave it to the other blocks of their SM).
+  constexpr bool AHEAD = VEC && TPR == 0 && CH <= 2;
   __shared__ float psum[2][32];
   __shared__ uint32_t pmax[2][32];
-  Row<CH, VEC> me;
+  extern __shared__ __align__(16) unsigned char q2_norm_smem[];
+  Row<TPR, CH, VEC> me;
   me.nt = TPR ? TPR : blockDim.x;
   me.tid = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
   me.C = a.C;
   long long row = TPR ? (long long)blockIdx.x * (256 / (TPR ? TPR : 1)) + threadIdx.x / (TPR ? TPR : 1)
                       : (long long)blockIdx.x;
   me.live = !TPR || row < a.rows;
+  // the images of this row's outputs: all rows' sums, then y, then y8
+  const int pieces = (a.C + 7) / 8, rows = TPR ? 256 / (TPR ? TPR : 1) : 1, at = TPR ? threadIdx.x / (TPR ? TPR : 1) : 0;
+  uint4* hbuf = reinterpret_cast<uint4*>(q2_norm_smem) + at * pieces;
+  uint4* ybuf = hbuf + (a.res_out ? rows * pieces : 0);
+  uint2* qbuf = reinterpret_cast<uint2*>(q2_norm_smem) + ((a.res_out ? 2 : 0) + (a.y ? 2 : 0)) * rows * pieces + at * pieces;
   auto place = [&](long long r, long long ld) {                  // element offset of row r = (token, head)
     const long long t = a.heads == 1 ? r : r / a.heads;
     return t * ld + (r - t * a.heads) * a.C;
@@ -174,7 +250,7 @@ __global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs
     }
     if (CH > 2) me.load(a.w, wr);
     ss = row_reduce<TPR, false>(ss, psum[turn]);
-    if (a.res_out) me.store(a.res_out + (size_t)row * a.C, h);
+    if (a.res_out) me.store(a.res_out + (size_t)row * a.C, h, hbuf);
     const float k = rsqrtf(ss / (float)a.C + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -183,7 +259,7 @@ __global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * k * w[i];
     }
-    if (a.y) me.store(a.y + place(row, a.ldy), h);
+    if (a.y) me.store(a.y + place(row, a.ldy), h, ybuf);
     if (a.y8) {
       uint32_t m = 0;
 #pragma unroll
@@ -195,7 +271,7 @@ __global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs
       // A zero row has scale 0 and zeros; a row with a NaN (or an infinity) has
       // a scale that is NaN (or infinite), which its consumer multiplies by.
       if (me.live && me.tid == 0) a.s8[row] = top / 127.f;
-      me.store8(a.y8 + (size_t)row * a.C, h, top > 0.f ? 127.f / top : 0.f);
+      me.store8(a.y8 + (size_t)row * a.C, h, top > 0.f ? 127.f / top : 0.f, qbuf);
     }
     if (TPR || next >= a.rows) return;
     row = next;
@@ -206,29 +282,49 @@ __global__ void __launch_bounds__(NT) k_rmsnorm(const __grid_constant__ NormArgs
   }
 }
 
+template <int TPR, int CH, bool VEC, int NT>
+int launch_rows(const NormArgs& a, int grid, int threads, void* stream) {
+  auto kernel = k_rmsnorm<TPR, CH, VEC, NT>;
+  const int smem = norm_smem<VEC>(a, TPR ? 256 / (TPR ? TPR : 1) : 1);
+  if (smem > 47 * 1024 && set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
+  return launch_pdl(kernel, a, grid, threads, smem, stream);
+}
+
 template <bool VEC>
 int launch_norm(const NormArgs& a, void* stream) {
   const int pieces = (a.C + 7) / 8;
   auto blocks = [&](int per) { return (int)((a.rows + per - 1) / per); };
-  if (pieces <= 16) return launch_pdl(k_rmsnorm<16, 1, VEC, 256>, a, blocks(16), 256, 0, stream);
-  if (pieces <= 32) return launch_pdl(k_rmsnorm<32, 1, VEC, 256>, a, blocks(8), 256, 0, stream);
-  if (pieces <= 64) return launch_pdl(k_rmsnorm<32, 2, VEC, 256>, a, blocks(8), 256, 0, stream);
-  // A block per row, up to as many blocks as fit 1024 threads on every SM.
+  // Short rows by half warps and warps (64 x 40 rows of 128: 1.6 us, 2.9 with
+  // a block per row; 4096 rows of 512 with residual: 3.0 and 4.5; a few rows
+  // of 512 1.9 and 1.8).
+  if (pieces <= 16) return launch_rows<16, 1, VEC, 256>(a, blocks(16), 256, stream);
+  if (pieces <= 32) return launch_rows<32, 1, VEC, 256>(a, blocks(8), 256, stream);
+  if (pieces <= 64) return launch_rows<32, 2, VEC, 256>(a, blocks(8), 256, stream);
+  // A block per row, up to as many blocks as fit 1024 threads on every SM; rows
+  // that may begin anywhere, which have more barriers, 2048 threads of 32
+  // registers (4096 rows of 5125: 50 us, 72 with 1024 threads).
   auto threads = [&](int ch) { return ((pieces + ch - 1) / ch + 31) / 32 * 32; };
   auto grid = [&](int nt) {
-    const long long most = (long long)dev_info().sms * std::max(1, 1024 / nt);
+    const long long most = (long long)dev_info().sms * std::max(1, (VEC ? 1024 : 2048) / nt);
     return (int)std::min(a.rows, most);
   };
-  // Few rows: more threads, for the latency; many: two pieces in flight each.
-  const bool few = a.rows <= 2 * dev_info().sms;
-  if (few && pieces <= 512) return launch_pdl(k_rmsnorm<0, 1, VEC, 512>, a, (int)a.rows, threads(1), 0, stream);
-  if (pieces <= 512) return launch_pdl(k_rmsnorm<0, 2, VEC, 256>, a, grid(threads(2)), threads(2), 0, stream);
-  if (pieces <= 1024) return launch_pdl(k_rmsnorm<0, 2, VEC, 512>, a, grid(threads(2)), threads(2), 0, stream);
-  return launch_pdl(k_rmsnorm<0, 4, VEC, 1024>, a, grid(threads(4)), threads(4), 0, stream);
+  if (!VEC && pieces <= 256) return launch_rows<0, 1, false, 256>(a, grid(threads(1)), threads(1), stream);
+  if (!VEC && pieces <= 512) return launch_rows<0, 1, false, 512>(a, grid(threads(1)), threads(1), stream);
+  if (!VEC && pieces <= 1024) return launch_rows<0, 1, false, 1024>(a, grid(threads(1)), threads(1), stream);
+  if (!VEC) return launch_rows<0, 4, false, 1024>(a, grid(threads(4)), threads(4), stream);
+  // Few rows: more threads, for the latency (1 or 64 rows of 4096: 1.71 us,
+  // 1.78 with two pieces per thread); many: two pieces in flight each (600
+  // rows 3.1 us, 3.9 with one).
+  const bool few = a.rows <= dev_info().sms;
+  if (few && pieces <= 512) return launch_rows<0, 1, true, 512>(a, (int)a.rows, threads(1), stream);
+  if (pieces <= 512) return launch_rows<0, 2, true, 256>(a, grid(threads(2)), threads(2), stream);
+  if (pieces <= 1024) return launch_rows<0, 2, true, 512>(a, grid(threads(2)), threads(2), stream);
+  return launch_rows<0, 4, true, 1024>(a, grid(threads(4)), threads(4), stream);
 }
 
 }  // namespace
 }  // namespace q2
+
 extern "C" int q2_rmsnorm(const void* x, long long ldx, int ntok, int heads, int C, const void* residual,
                           void* residual_out, const void* weight, float eps, void* y, long long ldy, void* y8,
                           float* scale8, q2_stream stream) {

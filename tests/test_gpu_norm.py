@@ -94,6 +94,36 @@ def test_misaligned_rows(q2, off):
     _close16(rd, h)                                                                    # the residual was updated in place
 
 
+@pytest.mark.parametrize("C,ntok", [(65, 40), (127, 33), (255, 9), (510, 21), (513, 700), (4099, 400), (5125, 333), (8201, 160), (17401, 5)])
+@pytest.mark.parametrize("offs", [(0, 0, 0, 0), (1, 2, 3, 5), (7, 7, 7, 7)])
+def test_rows_that_begin_anywhere(q2, C, ntok, offs):
+    """Odd widths, each tensor at its own offset inside a buffer whose other elements have to stay as they are."""
+    _, x, w, r = _draw(ntok, 1, C, C + ntok)
+    sizes = {"x": x[:, 0], "r": r[:, 0], "y": None, "q": None}
+    bufs, views = {}, {}
+    for (name, data), off in zip(sizes.items(), offs):
+        dt = torch.int8 if name == "q" else torch.float16
+        bufs[name] = torch.full((ntok * C + 32,), 77, dtype=dt, device="cuda")
+        views[name] = bufs[name][off: off + ntok * C].view(ntok, C)
+        if data is not None:
+            views[name].copy_(torch.from_numpy(data.copy()))
+    s8 = torch.zeros(ntok, device="cuda")
+    q2.RmsNorm(w, EPS).apply(views["x"], residual=views["r"], out=views["y"], out8=views["q"], scale8=s8)
+    h, y = onorm.rmsnorm_f64(x[:, 0], w, EPS, r[:, 0])
+    _close16(views["r"], h)
+    _close16(views["y"], y)
+    _close8(views["q"], s8, y)
+    assert np.array_equal(views["x"].cpu().numpy(), x[:, 0])
+    for name, off in zip(sizes, offs):
+        assert (bufs[name][:off] == 77).all() and (bufs[name][off + ntok * C:] == 77).all()
+    # 8 bits alone, and fp16 alone in place
+    q2.RmsNorm(w, EPS).apply(views["x"], out8=views["q"], scale8=s8)
+    y = onorm.rmsnorm_f64(x[:, 0], w, EPS)[1]
+    _close8(views["q"], s8, y)
+    q2.RmsNorm(w, EPS).apply(views["x"], out=views["x"])
+    _close16(views["x"], y)
+
+
 def test_rows_do_not_depend_on_the_batch(q2):
     _, x, w, r = _draw(64, 1, 5120, 80)
     n = q2.RmsNorm(w, EPS)
