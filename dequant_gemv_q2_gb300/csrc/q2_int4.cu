@@ -47,12 +47,12 @@ namespace {
 // end the warps leave their sums in one of two shared-memory buffers and the
 // first threads add them in warp order: one barrier per row tile, no atomics.
 //
-// 24576 x 4096 at one token, groups of 128 with zero points: 11.2 us on the
+// 24576 x 4096 at one token, groups of 128 with zero points: 11.0 us on the
 // device, 4.7 TB/s (4096 x 4096: 3.6 us, of which 2 are the launch and the
 // first bytes' way).  Issue slots are 70% full and what remains is the ends:
 // the first loads, x and its sums before them, the last row tiles.  Steps:
 // register ring 19.1 us, shared-memory ring 14.3, the bits as subnormals and
-// sums of x once per CTA 11.2.
+// sums of x once per CTA 11.2, sums added a pair of tokens at a time 11.0.
 constexpr int kFewWarps = 8, kFewTok = 2, kFewStages = 3, kFewCtas = 2;
 constexpr int kFewRed = 2 * kFewWarps * kFewTok * 16 * 4;
 
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   __syncwarp();
   const float xsc0 = X8 ? a.xs[0] : 1.f, xsc1 = X8 && a.ntok > 1 ? a.xs[1] : 1.f;
 
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // rows g and g + 8, tokens 0 and 1
   // K blocks at `from`, columns from block b on: K independent chains of products
   auto use = [&](auto kc, uint32_t from, int blk) {
     constexpr int K = decltype(kc)::value;
@@ -202,10 +202,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
         const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[k].s[q]));
         const uint32_t zz = sd[k].z[q >> 1] >> (16 * (q & 1));
         const float z0 = Z ? (float)(zz & 0xffu) : 8.f, z1 = Z ? (float)((zz >> 8) & 0xffu) : 8.f;
-        acc[0] = fmaf(sc.x, fmaf(c[k][0], 16777216.f, -z0 * X.x), acc[0]);
-        acc[1] = fmaf(sc.x, fmaf(c[k][1], 16777216.f, -z0 * X.y), acc[1]);
-        acc[2] = fmaf(sc.y, fmaf(c[k][2], 1048576.f, -z1 * X.x), acc[2]);
-        acc[3] = fmaf(sc.y, fmaf(c[k][3], 1048576.f, -z1 * X.y), acc[3]);
+        add_group(acc[0], sc.x, z0, make_float2(c[k][0], c[k][1]), X, 16777216.f);
+        add_group(acc[1], sc.y, z1, make_float2(c[k][2], c[k][3]), X, 1048576.f);
       }
     }
   };
@@ -221,12 +219,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
     }
     float* r = red + ((u & 1) * kFewWarps + warp) * (kFewTok * 16);
     if (j == 0) {                                           // tokens 0 and 1
-      r[g] = acc[0] * xsc0;
-      r[16 + g] = acc[1] * xsc1;
-      r[g + 8] = acc[2] * xsc0;
-      r[16 + g + 8] = acc[3] * xsc1;
+      r[g] = acc[0].x * xsc0;
+      r[16 + g] = acc[0].y * xsc1;
+      r[g + 8] = acc[1].x * xsc0;
+      r[16 + g + 8] = acc[1].y * xsc1;
     }
-    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    acc[0] = acc[1] = make_float2(0.f, 0.f);
     __syncthreads();
     const int row = ((int)blockIdx.x + u * (int)gridDim.x) * 16 + (threadIdx.x & 15), t = threadIdx.x >> 4;
     if (t < a.ntok && row < a.R) {
@@ -250,13 +248,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 // When the column range is split over CTAs, they form a cluster and add their
 // fp32 sums through distributed shared memory in rank order.
 //
-// What bounds it at 8 tokens is bytes in flight and the ends, 3.0 TB/s at
-// 5120 x 17408 (8-bit x, groups of 64: 15.9 us) and 3.6 at 24576 x 4096 (14.5
+// What bounds it at 8 tokens is instructions and uneven SMs (240 CTAs, two on
+// some and one on others: an even spread would save 20%), 3.1 TB/s at
+// 5120 x 17408 (8-bit x, groups of 64: 15.3 us) and 3.6 at 24576 x 4096 (14.5
 // us); at 16 tokens the products: an instruction takes the tensor cores 2
 // cycles of an SM whatever its operands are worth, 12.5 us of the 22.2 at
 // 24576 x 4096.  More than 16 tokens would cost another product with ones and
 // 48 accumulators more per thread: they go to the kernel in q2_int4_tc.cu
-// (24576 x 4096 at 32 tokens 28.8 us, twice the 16-token time here 44).
+// (24576 x 4096 at 32 tokens 26.3 us, twice the 16-token time here 44).
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
@@ -333,13 +332,13 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
 #pragma unroll
   for (int d = 0; d < STAGES - 1; ++d) xstage(d, d);
 
-  float acc[MT][NT][4];
+  float2 acc[MT][NT][2];                                    // rows g and g + 8, tokens 2j and 2j + 1
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
+      for (int q = 0; q < 2; ++q) acc[m][t][q] = make_float2(0.f, 0.f);
 
   int st = 0, last = STAGES - 1;                            // stage in use, stage before it (free)
   for (int i = 0; i < n; ++i) {
@@ -410,10 +409,9 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
         const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          acc[m][t][0] = fmaf(sc.x, fmaf(c[m][t][0], 16777216.f, -z0 * X[t][0]), acc[m][t][0]);
-          acc[m][t][1] = fmaf(sc.x, fmaf(c[m][t][1], 16777216.f, -z0 * X[t][1]), acc[m][t][1]);
-          acc[m][t][2] = fmaf(sc.y, fmaf(c[m][t][2], 1048576.f, -z1 * X[t][0]), acc[m][t][2]);
-          acc[m][t][3] = fmaf(sc.y, fmaf(c[m][t][3], 1048576.f, -z1 * X[t][1]), acc[m][t][3]);
+          const float2 x2 = make_float2(X[t][0], X[t][1]);
+          add_group(acc[m][t][0], sc.x, z0, make_float2(c[m][t][0], c[m][t][1]), x2, 16777216.f);
+          add_group(acc[m][t][1], sc.y, z1, make_float2(c[m][t][2], c[m][t][3]), x2, 1048576.f);
         }
       }
     }
@@ -434,7 +432,8 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float* o = out + (t * 8 + 2 * j + (q & 1)) * kOutLd + wm * 32 + m * 16 + g + (q >> 1) * 8;
-            *o = half ? acc[m][t][q] : *o + acc[m][t][q];
+            const float v = q & 1 ? acc[m][t][q >> 1].y : acc[m][t][q >> 1].x;
+            *o = half ? v : *o + v;
           }
     }
     __syncthreads();

@@ -144,6 +144,19 @@ __device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
   hi = hsub2(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u);
 }
 
+// c += a * b, a pair at a time
+__device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
+  uint64_t& cc = reinterpret_cast<uint64_t&>(c);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+}
+
+// A group's sums of two tokens onto the row's: acc += s (2^e c - z X).
+__device__ __forceinline__ void add_group(float2& acc, float s, float z, float2 c, float2 X, float two_e) {
+  float2 t = make_float2(-z * X.x, -z * X.y);
+  fma2(t, c, make_float2(two_e, two_e));
+  fma2(acc, make_float2(s, s), t);
+}
+
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
 // How many clusters of cs CTAs of a kernel the device runs at once (a cluster

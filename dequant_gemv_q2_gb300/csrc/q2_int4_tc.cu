@@ -103,12 +103,6 @@ __device__ __forceinline__ void commit_lane0(int lane, uint32_t bar) {
       : "memory");
 }
 
-// c += a * b, a pair at a time
-__device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
-  uint64_t& cc = reinterpret_cast<uint64_t&>(c);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-}
-
 // Whether the phase of the given parity is complete (after a short sleep at most).
 __device__ __forceinline__ uint32_t try_phase(uint32_t bar, uint32_t parity) {
   uint32_t done;
