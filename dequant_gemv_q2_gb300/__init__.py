@@ -374,6 +374,7 @@ class RmsNorm:
         w = weight if isinstance(weight, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(weight)).to(device)
         _check_tensor("RmsNorm", "weight", w, torch.float16, (w.numel(),))
         self.weight, self.eps, self.C, self._w = w, float(eps), w.numel(), w.data_ptr()
+        self._fn, self._f16 = load().q2_rmsnorm, torch.float16
 
     def _ld(self, name: str, t, shape, heads: int) -> int:
         """The token stride of fp16 rows [ntok][heads][C] of which each token's are contiguous."""
@@ -395,15 +396,13 @@ class RmsNorm:
         neither ``out`` nor ``out8`` is given.  ``out8`` (int8, x's shape) and ``scale8`` (fp32, a scale per row)
         take the 8-bit output.  Returns ``out`` (asynchronous).
         """
-        import torch
-        f16, C, shape = torch.float16, self.C, x.shape
+        f16, C, shape = self._f16, self.C, x.shape
         dims = len(shape)
         if dims not in (2, 3) or shape[-1] != C:
             raise Q2Error(ESHAPE, f"q2_rmsnorm: x has shape {tuple(shape)}, not [ntok][{C}] or [ntok][heads][{C}]")
         ntok, heads = shape[0], shape[1] if dims == 3 else 1
-        if out is None and out8 is None:
-            out = torch.empty(shape, dtype=f16, device=x.device)
         ldx = ldy = heads * C
+        # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
         if not (x.dtype is f16 and x.is_cuda and x.is_contiguous()):
             ldx = self._ld("x", x, shape, heads)
         y = y8 = s8 = r = ro = None
@@ -411,21 +410,27 @@ class RmsNorm:
             if not (out.dtype is f16 and out.is_cuda and out.shape == shape and out.is_contiguous()):
                 ldy = self._ld("out", out, shape, heads)
             y = out.data_ptr()
+        elif out8 is None:
+            import torch
+            out = torch.empty(shape, dtype=f16, device=x.device)
+            y = out.data_ptr()
         if residual is not None:
-            residual_out = residual if residual_out is None else residual_out
-            _check_tensor("q2_rmsnorm", "residual", residual, f16, shape)
-            r = residual.data_ptr()
+            if not (residual.dtype is f16 and residual.is_cuda and residual.shape == shape and residual.is_contiguous()):
+                _check_tensor("q2_rmsnorm", "residual", residual, f16, shape)
+            ro = r = residual.data_ptr()
         if residual_out is not None:
-            _check_tensor("q2_rmsnorm", "residual_out", residual_out, f16, shape)
+            if not (residual_out.dtype is f16 and residual_out.is_cuda and residual_out.shape == shape
+                    and residual_out.is_contiguous()):
+                _check_tensor("q2_rmsnorm", "residual_out", residual_out, f16, shape)
             ro = residual_out.data_ptr()
         if out8 is not None:
+            import torch
             _check_tensor("q2_rmsnorm", "out8", out8, torch.int8, shape)
             if scale8 is None:
                 raise Q2Error(EINVAL, "q2_rmsnorm: out8 needs scale8")
             _check_tensor("q2_rmsnorm", "scale8", scale8, torch.float32, shape[:-1])
             y8, s8 = out8.data_ptr(), scale8.data_ptr()
-        st = load().q2_rmsnorm(x.data_ptr(), ldx, ntok, heads, C, r, ro, self._w, self.eps, y, ldy, y8, s8,
-                               _stream_ptr(stream))
+        st = self._fn(x.data_ptr(), ldx, ntok, heads, C, r, ro, self._w, self.eps, y, ldy, y8, s8, _stream_ptr(stream))
         if st:
             raise Q2Error(st, "q2_rmsnorm")
         return out
