@@ -32,7 +32,7 @@
 // instructions: the numerators are as exact as with fp32 probabilities (an
 // error of 2^-22 instead of 2^-11 per term) at no cost.  More than eight query
 // heads to a key-value head are taken eight at a time, each reading the tokens
-// again (the second time mostly from L2).
+// again.
 //
 // 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 319 us
 // on the device, 6.7 TB/s, the rate of a copy; one of 131072: 88 us, 6.1; 16
@@ -41,6 +41,8 @@
 // lengths, the first pages' numbers, the first rows and the join behind one
 // another.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "q2_common.cuh"
 
@@ -124,9 +126,15 @@ struct Walk {
 // 0, 31.9 with 4).
 constexpr int kEnd = 2;
 
+// CTAs per SM: what registers and the rings of three stages leave room for, but
+// no more than three (64 sequences of 8192 tokens, heads of 64: 163 us; with two
+// CTAs of six stages 199, with four of three 169).
+template <int D>
+__host__ __device__ constexpr int att_ctas() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
+
 template <int D>
 struct Shape {
-  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int STAGES = 3;
   static constexpr int kTileBytes = kTile * D * 2;                     // keys or values of a tile
   static constexpr int kRing = kWarps * STAGES * 2 * kTileBytes;
   static constexpr int kMl = kWarps * kHeads * 8;
@@ -136,7 +144,7 @@ struct Shape {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid_constant__ AttendArgs a) {
   using S = Shape<D>;
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
   extern __shared__ __align__(16) unsigned char q2_att_smem[];
@@ -543,13 +551,14 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attend(const __g
   }
 }
 
-int most_ctas(int D) { return dev_info().sms * (D <= 128 ? 2 : 1); }
+int most_ctas(int D) { return dev_info().sms * (D == 64 ? att_ctas<64>() : D == 128 ? att_ctas<128>() : att_ctas<256>()); }
 
 // The workspace: the parts' sums, in a region that fits every head_dim (so the
 // counters behind it have one place for calls of all shapes), then counters.
 size_t part_bytes() {
-  const size_t a = (size_t)2 * most_ctas(128) * kHeads * (128 * 4 + 8), b = (size_t)2 * most_ctas(256) * kHeads * (256 * 4 + 8);
-  return ((a > b ? a : b) + 255) / 256 * 256;
+  size_t n = 0;
+  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D) * kHeads * (D * 4 + 8));
+  return (n + 255) / 256 * 256;
 }
 
 // Shared checks of the head counts; hu: heads of units.
