@@ -29,10 +29,10 @@
 // Both products run on the tensor cores (16 x 8 x 16, fp32 accumulators) with
 // the group's query heads as rows 0..7.  The probabilities are split into two
 // fp16 numbers, p = hi + lo, and lo takes rows 8..15 of the same
-// instructions: the numerators are as exact as with fp32 probabilities (an
-// error of 2^-22 instead of 2^-11 per term) at no cost.  More than eight query
-// heads to a key-value head are taken eight at a time, each reading the tokens
-// again.
+// instructions (with more than eight heads its own): the numerators are as exact as with fp32 probabilities (an
+// error of 2^-22 instead of 2^-11 per term) at no cost.  More than 16
+// query heads to a key-value head (eight of 256 columns) are taken 16 (eight)
+// at a time, each reading the tokens again.
 //
 // 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 319 us
 // on the device, 6.7 TB/s, the rate of a copy; one of 131072: 88 us, 6.1; 16
@@ -53,7 +53,7 @@ __device__ unsigned int q2_attend_error;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 16, kUnit = kTile * kWarps;   // tokens of a warp's tile, of a unit
-constexpr int kHeads = 8;                           // query heads of a unit (rows of the products)
+constexpr int kMostHeads = 16;                      // query heads of a unit at most
 
 struct AttendArgs {
   __half* k;
@@ -68,8 +68,8 @@ struct AttendArgs {
   __half* o;
   long long ldq, ldn, ldo;
   unsigned int* count;        // [batch][units' heads] arrivals, zero between calls
-  float* part;                // [2 * CTAs][kHeads][D] numerators
-  float2* ml;                 // [2 * CTAs][kHeads] maximum, denominator
+  float* part;                // [2 * CTAs][H][D] numerators, H the query heads of a unit
+  float2* ml;                 // [2 * CTAs][H] maximum, denominator
   int batch, npages, page, cap;   // cap: tokens that a table row can hold
   int hu, nht, group;         // heads of units = kv_heads * nht; query heads of a key-value head
   uint32_t page_mul, page_sh; // t / page = (high half of t * page_mul, + t) >> page_sh, t < 2^31
@@ -132,23 +132,25 @@ constexpr int kEnd = 2;
 template <int D>
 __host__ __device__ constexpr int att_ctas() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 
-template <int D>
+template <int D, int H>
 struct Shape {
   static constexpr int STAGES = 3;
   static constexpr int kTileBytes = kTile * D * 2;                     // keys or values of a tile
   static constexpr int kRing = kWarps * STAGES * 2 * kTileBytes;
-  static constexpr int kMl = kWarps * kHeads * 8;
+  static constexpr int kMl = kWarps * H * 8;
   static constexpr int fixed = kRing + kMl + 48;
-  static_assert(kHeads * D * 4 == kTileBytes, "a warp's numerators take the place of a tile's keys");
+  static_assert(H * D * 4 <= 2 * kTileBytes, "a warp's numerators take the place of a tile's keys and values");
   static int smem(int batch) { return fixed + 4 * (2 * batch + 1); }
 };
 
-template <int D>
+// H: query heads of a unit, 8 or 16 (rows of the products)
+template <int D, int H>
 __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid_constant__ AttendArgs a) {
-  using S = Shape<D>;
+  using S = Shape<D, H>;
+  constexpr int RH = H / 8;                         // rows g, g + 8 of a lane that are heads
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
   extern __shared__ __align__(16) unsigned char q2_att_smem[];
-  float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing);     // [kWarps][kHeads] maximum, denominator
+  float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing);     // [kWarps][H] maximum, denominator
   int4* owe = reinterpret_cast<int4*>(q2_att_smem + S::kRing + S::kMl);   // joins that are this CTA's: sequence, head, CTAs
   int* nowed = reinterpret_cast<int*>(owe + 2);                           // at first: how many CTAs have work
   int* pre = nowed + 4;                                                // [batch + 1] units before each sequence
@@ -306,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // ---- sums of the current (sequence, head)
-  uint32_t qa[D / 16][2];                           // the queries: row g, columns 2j.. and 2j + 8.. of each 16
+  uint32_t qa[D / 16][2 * RH];                      // the queries: rows g (+ 8), columns 2j.. and 2j + 8.. of each 16
   uint4 newk, newv;                                 // lane l < CPR: piece l of the new token's key and value
-  float o[NT][4], m = -INFINITY, l = 0.f;
+  float o[NT][4], m[RH], l[RH];
   bool fresh = true;
   int seg = c.chunk, slot = 0;                      // first unit of this part of the (sequence, head)
   int ahead = STAGES - 1;                           // units still to be requested before the first is used
@@ -319,17 +321,20 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       issue();
       continue;
     }
-    const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
-    const int qh = kvh * a.group + ht * kHeads;
+    const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
+    const int qh = kvh * a.group + ht * H;
     const int t0 = c.chunk * kUnit + warp * kTile;
     if (fresh) {
       fresh = false;
       const __half* q = a.q + c.b * a.ldq + (long long)(qh + g) * D + 2 * j;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        qa[s][0] = g < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * s) : 0u;
-        qa[s][1] = g < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8) : 0u;
-      }
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int y = 0; y < RH; ++y) {
+          const bool is = g + 8 * y < rows;
+          qa[s][2 * y] = is ? *reinterpret_cast<const uint32_t*>(q + 8 * y * D + 16 * s) : 0u;
+          qa[s][2 * y + 1] = is ? *reinterpret_cast<const uint32_t*>(q + 8 * y * D + 16 * s + 8) : 0u;
+        }
       if (a.nk && lane < CPR) {
         const long long e = c.b * a.ldn + kvh * D + lane * 8;
         newk = *reinterpret_cast<const uint4*>(a.nk + e);
@@ -339,8 +344,11 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[t][x] = 0.f;
-      m = -INFINITY;
-      l = 0.f;
+#pragma unroll
+      for (int y = 0; y < RH; ++y) {
+        m[y] = -INFINITY;
+        l[y] = 0.f;
+      }
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     __syncwarp();                                   // this unit has arrived for all lanes, the one before is done with
@@ -374,45 +382,66 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       for (int s = 0; s < D / 16; ++s) {
         uint32_t b[4];
         ldsm4(b, kt + krow * (D * 2) + (((2 * s + kpiece) ^ (krow & 7)) << 4));
-        mma(s0, qa[s][0], 0u, qa[s][1], 0u, b[0], b[1]);
-        mma(s1, qa[s][0], 0u, qa[s][1], 0u, b[2], b[3]);
+        const uint32_t a1 = RH == 2 ? qa[s][2 * RH - 2] : 0u, a3 = RH == 2 ? qa[s][2 * RH - 1] : 0u;
+        mma(s0, qa[s][0], a1, qa[s][1], a3, b[0], b[1]);
+        mma(s1, qa[s][0], a1, qa[s][1], a3, b[2], b[3]);
       }
-      float x[4] = {s0[0] * a.sc2, s0[1] * a.sc2, s1[0] * a.sc2, s1[1] * a.sc2};
-      if (fin < kTile - 1) {
+      float x[RH][4], al[RH];
+      bool rise = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (2 * j + (e & 1) + (e >> 1) * 8 > fin) x[e] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-      if (__any_sync(0xffffffffu, mn > m)) {        // a new maximum somewhere: scale what there is
-        const float al = exp2f(m - ref);
-        l *= al;
+      for (int y = 0; y < RH; ++y) {
+        x[y][0] = s0[2 * y] * a.sc2;
+        x[y][1] = s0[2 * y + 1] * a.sc2;
+        x[y][2] = s1[2 * y] * a.sc2;
+        x[y][3] = s1[2 * y + 1] * a.sc2;
+        if (fin < kTile - 1) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {              // rows 0..7 and 8..15 are halves of the same head
-          o[t][0] *= al;
-          o[t][1] *= al;
-          o[t][2] *= al;
-          o[t][3] *= al;
+          for (int e = 0; e < 4; ++e)
+            if (2 * j + (e & 1) + (e >> 1) * 8 > fin) x[y][e] = -INFINITY;
         }
-        m = mn;
-      }
+        float top = fmaxf(fmaxf(x[y][0], x[y][1]), fmaxf(x[y][2], x[y][3]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m[y], top), ref = mn == -INFINITY ? 0.f : mn;
+        rise = rise || mn > m[y];
+        al[y] = exp2f(m[y] - ref);
+        m[y] = mn;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = exp2f(x[e] - ref);
-      l += (x[0] + x[1]) + (x[2] + x[3]);
-      if ((badslots >> slot) & 1u) l = __int_as_float(0x7fc00000);
-      uint32_t p0, p1, p2, p3;
-      split2(x[0], x[1], p0, p1);
-      split2(x[2], x[3], p2, p3);
+        for (int e = 0; e < 4; ++e) x[y][e] = exp2f(x[y][e] - ref);
+      }
+      if (__any_sync(0xffffffffu, rise)) {          // a new maximum somewhere: scale what there is
+#pragma unroll
+        for (int y = 0; y < RH; ++y) l[y] *= al[y];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {              // of 8 heads rows 0..7 and 8..15 are halves of the same head
+          o[t][0] *= al[0];
+          o[t][1] *= al[0];
+          o[t][2] *= al[RH - 1];
+          o[t][3] *= al[RH - 1];
+        }
+      }
+      uint32_t hi[RH][2], lo[RH][2];
+#pragma unroll
+      for (int y = 0; y < RH; ++y) {
+        l[y] += (x[y][0] + x[y][1]) + (x[y][2] + x[y][3]);
+        if ((badslots >> slot) & 1u) l[y] = __int_as_float(0x7fc00000);
+        split2(x[y][0], x[y][1], hi[y][0], lo[y][0]);
+        split2(x[y][2], x[y][3], hi[y][1], lo[y][1]);
+      }
       const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
 #pragma unroll
       for (int t = 0; t < NT; t += 2) {
         uint32_t b[4];
         ldsm4t(b, vt + vrow * (D * 2) + (((t + vpiece) ^ (vrow & 7)) << 4));
-        mma(o[t], p0, p1, p2, p3, b[0], b[1]);
-        mma(o[t + 1], p0, p1, p2, p3, b[2], b[3]);
+        if constexpr (RH == 1) {                    // hi in rows 0..7, lo in rows 8..15
+          mma(o[t], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[0], b[1]);
+          mma(o[t + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2], b[3]);
+        } else {
+          mma(o[t], hi[0][0], hi[1][0], hi[0][1], hi[1][1], b[0], b[1]);
+          mma(o[t + 1], hi[0][0], hi[1][0], hi[0][1], hi[1][1], b[2], b[3]);
+          mma(o[t], lo[0][0], lo[1][0], lo[0][1], lo[1][1], b[0], b[1]);
+          mma(o[t + 1], lo[0][0], lo[1][0], lo[0][1], lo[1][1], b[2], b[3]);
+        }
       }
     }
     const uint32_t mine = slot * (2 * S::kTileBytes);       // this unit's stage, free until the next issue()
@@ -425,52 +454,58 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       // Every warp leaves its sums (the numerators in place of the keys it has
       // just used, 16-byte pieces exchanged by the row as the keys were), then
       // joins a quarter of the columns of all warps.
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
       unsigned char* sums = q2_att_smem + warp * (STAGES * 2 * S::kTileBytes) + mine;
       __syncwarp();
-      if (j == 0) wml[warp * kHeads + g] = make_float2(m, l);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        *reinterpret_cast<float2*>(sums + g * (D * 4) + (((2 * t + (j >> 1)) ^ g) << 4) + (j & 1) * 8) =
-            make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3]);
+      for (int y = 0; y < RH; ++y) {
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+        if (j == 0) wml[warp * H + g + 8 * y] = make_float2(m[y], l[y]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          *reinterpret_cast<float2*>(sums + (g + 8 * y) * (D * 4) + (((2 * t + (j >> 1)) ^ g) << 4) + (j & 1) * 8) =
+              RH == 1 ? make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3]) : make_float2(o[t][2 * y], o[t][2 * y + 1]);
+      }
       __syncthreads();
       const bool whole = ends && seg == 0;
       const int part = 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0);
       constexpr int PPL = D / kWarps / 16;          // 16-byte pieces of a lane: row lane / 4, a quarter of the warp's columns
-      float wt[kWarps], mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, wml[k * kHeads + g].x);
-      const float ref = mm == -INFINITY ? 0.f : mm;
+      for (int row = g; row < H; row += 8) {
+        float wt[kWarps], mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float2 v = wml[k * kHeads + g];
-        wt[k] = exp2f(v.x - ref);
-        ll += wt[k] * v.y;
-      }
-      if (g < rows) {
-        const float inv = 1.f / ll;
+        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, wml[k * H + row].x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-        for (int q = 0; q < PPL; ++q) {
-          const int piece4 = (warp * 4 + j) * PPL + q;      // columns 4 * piece4 ..
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < kWarps; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(q2_att_smem + k * (STAGES * 2 * S::kTileBytes) + mine +
-                                                              g * (D * 4) + ((piece4 ^ g) << 4));
-            x.x += v.x * wt[k];
-            x.y += v.y * wt[k];
-            x.z += v.z * wt[k];
-            x.w += v.w * wt[k];
-          }
-          if (whole) {
-            __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
-            *reinterpret_cast<uint2*>(a.o + w.b * a.ldo + (long long)(qh + g) * D + piece4 * 4) = *reinterpret_cast<uint2*>(h);
-          } else {
-            *reinterpret_cast<float4*>(a.part + ((size_t)part * kHeads + g) * D + piece4 * 4) = x;
-          }
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 v = wml[k * H + row];
+          wt[k] = exp2f(v.x - ref);
+          ll += wt[k] * v.y;
         }
-        if (!whole && warp == 0 && j == 0) a.ml[(size_t)part * kHeads + g] = make_float2(mm, ll);
+        if (row < rows) {
+          const float inv = 1.f / ll;
+#pragma unroll
+          for (int q = 0; q < PPL; ++q) {
+            const int piece4 = (warp * 4 + j) * PPL + q;      // columns 4 * piece4 ..
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+              const float4 v = *reinterpret_cast<const float4*>(q2_att_smem + k * (STAGES * 2 * S::kTileBytes) + mine +
+                                                                row * (D * 4) + ((piece4 ^ g) << 4));
+              x.x += v.x * wt[k];
+              x.y += v.y * wt[k];
+              x.z += v.z * wt[k];
+              x.w += v.w * wt[k];
+            }
+            if (whole) {
+              __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
+              *reinterpret_cast<uint2*>(a.o + w.b * a.ldo + (long long)(qh + row) * D + piece4 * 4) = *reinterpret_cast<uint2*>(h);
+            } else {
+              *reinterpret_cast<float4*>(a.part + ((size_t)part * H + row) * D + piece4 * 4) = x;
+            }
+          }
+          if (!whole && warp == 0 && j == 0) a.ml[(size_t)part * H + row] = make_float2(mm, ll);
+        }
       }
       __syncthreads();                              // the stages may be filled again; the part is written
       if (!whole) {
@@ -503,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   __syncthreads();
   for (int q = 0; q < *nowed; ++q) {
     const int4 w = owe[q];
-    const int kvh = a.nht == 1 ? w.y : w.y / a.nht, ht = w.y - kvh * a.nht, rows = min(kHeads, a.group - ht * kHeads);
+    const int kvh = a.nht == 1 ? w.y : w.y / a.nht, ht = w.y - kvh * a.nht, rows = min(H, a.group - ht * H);
     const int parts = w.w - w.z + 1;
     for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), d4 = e % (D / 4);
@@ -516,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           // the first CTA's second part, the others' first
-          const size_t at = (size_t)(2 * (w.z + min(k0 + k, parts - 1)) + (k0 + k == 0)) * kHeads + r;
+          const size_t at = (size_t)(2 * (w.z + min(k0 + k, parts - 1)) + (k0 + k == 0)) * H + r;
           v[k] = __ldcg(&a.ml[at]);
           f[k] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + d4);
           if (k0 + k >= parts) v[k].x = -INFINITY;
@@ -545,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       }
       const float inv = 1.f / lj;
       __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
-      *reinterpret_cast<uint2*>(a.o + w.x * a.ldo + (long long)(kvh * a.group + ht * kHeads + r) * D + d4 * 4) =
+      *reinterpret_cast<uint2*>(a.o + w.x * a.ldo + (long long)(kvh * a.group + ht * H + r) * D + d4 * 4) =
           *reinterpret_cast<uint2*>(h);
     }
   }
@@ -557,16 +592,23 @@ int most_ctas(int D) { return dev_info().sms * (D == 64 ? att_ctas<64>() : D == 
 // counters behind it have one place for calls of all shapes), then counters.
 size_t part_bytes() {
   size_t n = 0;
-  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D) * kHeads * (D * 4 + 8));
+  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D) * kMostHeads * (D * 4 + 8));
   return (n + 255) / 256 * 256;
 }
+
+// Query heads of a unit.  Sixteen where a key-value head has more than eight
+// and the registers hold them, so that its tokens are read once for sixteen:
+// there lo has its own products (55 us instead of 89 for 8 sequences of 8192
+// tokens, 128 query and 8 key-value heads of 128).
+int unit_heads(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 
 // Shared checks of the head counts; hu: heads of units.
 int check_heads(int batch, int q_heads, int kv_heads, int D, int* hu, int* nht) {
   if (batch < 0 || batch > Q2_ATT_MAX_BATCH || kv_heads < 1 || kv_heads > 65536 || q_heads < 1 || q_heads % kv_heads)
     return Q2_ESHAPE;
   if (q_heads / kv_heads > Q2_ATT_MAX_GROUP || (D != 64 && D != 128 && D != 256)) return Q2_ESHAPE;
-  *nht = (q_heads / kv_heads + kHeads - 1) / kHeads;
+  const int H = unit_heads(q_heads / kv_heads, D);
+  *nht = (q_heads / kv_heads + H - 1) / H;
   *hu = kv_heads * *nht;
   return Q2_OK;
 }
@@ -633,7 +675,7 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
   const int most = most_ctas(D);
   a.part = static_cast<float*>(ws);
   a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + part_bytes());
-  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most * kHeads * D);
+  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most * unit_heads(q_heads / kv->kv_heads, D) * D);
   a.batch = batch;
   a.npages = kv->npages;
   a.page = kv->page_size;
@@ -646,9 +688,12 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
   a.group = q_heads / kv->kv_heads;
   a.sc2 = (float)((double)scale * 1.4426950408889634);
   const int grid = units < most ? (int)units : most;
-  if (D == 64) return launch_pdl(k_attend<64>, a, grid, kThreads, Shape<64>::smem(batch), stream);
-  if (D == 128) return launch_pdl(k_attend<128>, a, grid, kThreads, Shape<128>::smem(batch), stream);
-  return launch_pdl(k_attend<256>, a, grid, kThreads, Shape<256>::smem(batch), stream);
+  auto launch = [&](auto kernel, int smem) { return launch_pdl(kernel, a, grid, kThreads, smem, stream); };
+  const bool wide = unit_heads(a.group, D) == 16;
+  if (D == 64) return wide ? launch(k_attend<64, 16>, Shape<64, 16>::smem(batch)) : launch(k_attend<64, 8>, Shape<64, 8>::smem(batch));
+  if (D == 128)
+    return wide ? launch(k_attend<128, 16>, Shape<128, 16>::smem(batch)) : launch(k_attend<128, 8>, Shape<128, 8>::smem(batch));
+  return launch(k_attend<256, 8>, Shape<256, 8>::smem(batch));
 }
 
 // The error word of the attention kernels, then cleared (q2_device_errors).

@@ -124,6 +124,18 @@ def test_head_layouts(q2, kv_heads, group, D):
     c.check_stored()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group", [9, 15, 16, 17, 32])
+@pytest.mark.parametrize("lens,page", [([1, 17, 64], 16), ([4000, 700, 0, 33], 24)])
+def test_many_query_heads_to_one(q2, D, group, lens, page):
+    c = Case(lens, 2, group, D, page, group + D, new=True, peak=2.0)
+    cache = c.cache(q2)
+    out = c.run(cache)
+    c.check(out)
+    c.check_stored()
+    assert torch.equal(out, c.run(cache)) and q2.device_errors() == 0
+
+
 @pytest.mark.parametrize("lens", [[20000], [9000, 3, 5000], [3000] * 5])
 def test_long_sequences_are_split_and_joined(q2, lens):
     c = Case(lens, 2, 4, 128, 64, len(lens), new=True)
