@@ -37,7 +37,7 @@
 // 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 319 us
 // on the device, 6.7 TB/s, the rate of a copy; one of 131072: 88 us, 6.1; 16
 // of 1 to 4096 with 40 query heads 30 us, 4.5 (each CTA's start, its ends of
-// sequences and the joins are 9 of them); one of 777 tokens 7.5 us: the
+// sequences and the joins are 9 of them); one of 777 tokens 7.0 us: the
 // lengths, the first pages' numbers, the first rows and the join behind one
 // another.
 #include <cuda_fp16.h>
@@ -143,13 +143,23 @@ struct Shape {
   static int smem(int batch) { return fixed + 4 * (2 * batch + 1); }
 };
 
+constexpr int kJoin = 8;                            // parts whose loads are in flight together in a join
+
+// Counts a part in; before it what this CTA wrote becomes visible, and behind
+// it what the parts counted before wrote.
+__device__ __forceinline__ unsigned count_part(unsigned* count) {
+  unsigned before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+  return before;
+}
+
 // H: query heads of a unit, 8 or 16 (rows of the products)
 template <int D, int H>
 __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid_constant__ AttendArgs a) {
   using S = Shape<D, H>;
   constexpr int RH = H / 8;                         // rows g, g + 8 of a lane that are heads
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
-  extern __shared__ __align__(16) unsigned char q2_att_smem[];
+  extern __shared__ __align__(128) unsigned char q2_att_smem[];
   float2* wml = reinterpret_cast<float2*>(q2_att_smem + S::kRing);     // [kWarps][H] maximum, denominator
   int4* owe = reinterpret_cast<int4*>(q2_att_smem + S::kRing + S::kMl);   // joins that are this CTA's: sequence, head, CTAs
   int* nowed = reinterpret_cast<int*>(owe + 2);                           // at first: how many CTAs have work
@@ -202,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   // without one.  This CTA takes the units at places u0 .. u1 - 1.
   const int total = pre[a.batch], ncta = min(*nowed, total);
   if ((int)blockIdx.x >= ncta) return;
-  auto first_of = [&](int cta) { return (int)((long long)total * cta / ncta); };
+  const int each = total / ncta, over = total - each * ncta;
+  auto first_of = [&](int cta) { return each * cta + over * cta / ncta; };   // total * cta / ncta in 32 bits
   int u0 = first_of(blockIdx.x);
   const int u1 = first_of(blockIdx.x + 1);
 
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   uint32_t badslots = 0;                            // stages with a row whose page does not exist
   const int piece = lane % CPR, row0 = lane / CPR;
   const long long lrow = row0 * a.token_stride + piece * 8;            // this lane's place in a tile that lies in one page
-  const uint32_t ldst = ring + row0 * (D * 2);
+  const uint32_t ldst = ring + row0 * (D * 2), lpiece = (uint32_t)((piece ^ row0) << 4);   // row0 < 8; ring and rows on 128 bytes
   auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
     const int t = p.chunk * kUnit + warp * kTile + (a.aligned ? 0 : lane & 15);
     ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
@@ -274,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
           const int rows = bad ? 0 : have - row0;                      // live rows from this lane's first on
 #pragma unroll
           for (int i = 0; i < kTile / RPI; ++i) {
-            const uint32_t d = dst + i * (RPI * D * 2) + ((piece ^ ((i * RPI + row0) & 7)) << 4);
-            const bool live = i * RPI < rows;
-            cp16(d, live ? k : a.k, live);
-            cp16(d + S::kTileBytes, live ? v : a.v, live);
+            const uint32_t d = ((dst + lpiece) ^ (((i * RPI) & 7) << 4)) + i * (RPI * D * 2);
+            const bool live = i * RPI < rows;       // else nothing is read: a row of the page all the same
+            cp16(d, k, live);
+            cp16(d + S::kTileBytes, v, live);
             k += step;
             v += step;
           }
@@ -316,11 +327,6 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   int ahead = STAGES - 1;                           // units still to be requested before the first is used
   int owed = 0;                                     // parts of this CTA that were the last of their (sequence, head)
   for (int u = u0; u < u1;) {
-    if (ahead) {
-      --ahead;
-      issue();
-      continue;
-    }
     const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
     const int qh = kvh * a.group + ht * H;
     const int t0 = c.chunk * kUnit + warp * kTile;
@@ -350,9 +356,15 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
         l[y] = 0.f;
       }
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    __syncwarp();                                   // this unit has arrived for all lanes, the one before is done with
-    issue();
+    if (!ahead) {                                   // this unit has arrived for all lanes, the one before is done with
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      __syncwarp();
+    }
+    issue();                                        // (in one place: a short call's time is a good part instruction fetch)
+    if (ahead) {
+      --ahead;
+      continue;
+    }
     if (t0 < c.len) {
       const uint32_t kt = ring + slot * (2 * S::kTileBytes), vt = kt + S::kTileBytes;
       const int fin = c.len - 1 - t0;               // row of the last token, if below kTile
@@ -509,21 +521,16 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       }
       __syncthreads();                              // the stages may be filled again; the part is written
       if (!whole) {
-        // the CTAs that hold parts of this (sequence, head): c0 (from its first unit) .. c1
-        const int s = pre[w.b] + w.h * (w.nch + kEnd);
-        auto cta_of = [&](int v) { return (int)((((long long)v + 1) * ncta - 1) / total); };
-        const int c0 = cta_of(s), c1 = cta_of(s + w.nch - 1);
         // The part that completes a (sequence, head) owes its join; a CTA has
         // two parts at most (the one it begins with and the one it ends with)
         // and joins at its end, so that nothing waits for the counter here.
         if (threadIdx.x == 0) {
-          unsigned int* count = a.count + (size_t)w.b * a.hu + w.h;
-          __threadfence();
-          const bool done = atomicAdd(count, 1u) == (unsigned)(c1 - c0);
-          if (done) {
-            *count = 0;
-            owe[owed++] = make_int4(w.b, w.h, c0, c1);
-          }
+          const unsigned before = count_part(a.count + (size_t)w.b * a.hu + w.h);
+          // the CTAs that hold parts of this (sequence, head): c0 (from its first unit) .. c1
+          const int s = pre[w.b] + w.h * (w.nch + kEnd);
+          auto cta_of = [&](int v) { return (int)((((long long)v + 1) * ncta - 1) / total); };
+          const int c0 = cta_of(s), c1 = cta_of(s + w.nch - 1);
+          if (before == (unsigned)(c1 - c0)) owe[owed++] = make_int4(w.b, w.h, c0, c1);
         }
       }
       fresh = true;
@@ -531,25 +538,23 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
     }
   }
 
-  if (threadIdx.x == 0) {
-    __threadfence();
-    *nowed = owed;
-  }
+  if (threadIdx.x == 0) *nowed = owed;
   __syncthreads();
   for (int q = 0; q < *nowed; ++q) {
     const int4 w = owe[q];
     const int kvh = a.nht == 1 ? w.y : w.y / a.nht, ht = w.y - kvh * a.nht, rows = min(H, a.group - ht * H);
     const int parts = w.w - w.z + 1;
+    if (threadIdx.x == 0) a.count[(size_t)w.x * a.hu + w.y] = 0;
     for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), d4 = e % (D / 4);
       float mj = -INFINITY, lj = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int k0 = 0; k0 < parts; k0 += 8) {       // eight parts' loads at a time
-        float2 v[8];
-        float4 f[8];
+      for (int k0 = 0; k0 < parts; k0 += kJoin) {       // kJoin parts' loads at a time
+        float2 v[kJoin];
+        float4 f[kJoin];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kJoin; ++k) {
           // the first CTA's second part, the others' first
           const size_t at = (size_t)(2 * (w.z + min(k0 + k, parts - 1)) + (k0 + k == 0)) * H + r;
           v[k] = __ldcg(&a.ml[at]);
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
         }
         float mn = mj;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, v[k].x);
+        for (int k = 0; k < kJoin; ++k) mn = fmaxf(mn, v[k].x);
         const float ref = mn == -INFINITY ? 0.f : mn, old = exp2f(mj - ref);
         mj = mn;
         lj *= old;
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
         x.z *= old;
         x.w *= old;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kJoin; ++k) {
           if (k0 + k < parts) {
             const float wk = exp2f(v[k].x - ref);
             lj += wk * v[k].y;
