@@ -477,6 +477,7 @@ class PagedKV:
         self.scale = self.dim ** -0.5
         self._qshape = torch.Size((self.batch, self.q_heads, self.dim))
         self._kvshape = torch.Size((self.batch, self.kv_heads, self.dim))
+        self._fn, self._f16, self._i32 = load().q2_attend, torch.float16, torch.int32
         self._kv = _KV(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), pages, page, self.kv_heads,
                        self.dim, table.data_ptr(), table.stride(0) if self.batch > 1 else table.shape[1], table.shape[1])
         self._ref = ctypes.byref(self._kv)
@@ -496,28 +497,32 @@ class PagedKV:
         lens[b] - 1.  q, new_k, new_v and ``out`` may have any batch stride (slices of a projection's output).
         ``scale``: dim ** -0.5 if None.  Returns ``out`` (asynchronous).
         """
-        import torch
-        f16, shape = torch.float16, self._qshape
+        f16, shape = self._f16, self._qshape
+        # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
         if out is None:
+            import torch
             out = torch.empty(shape, dtype=f16, device=q.device)
         ldq = ldo = self.q_heads * self.dim
         if not (q.dtype is f16 and q.is_cuda and q.shape == shape and q.is_contiguous()):
             ldq = _rows("q", q, shape)
         if not (out.dtype is f16 and out.is_cuda and out.shape == shape and out.is_contiguous()):
             ldo = _rows("out", out, shape)
-        _check_tensor("q2_attend", "lens", lens, torch.int32, shape[:1])
+        if not (lens.dtype is self._i32 and lens.is_cuda and lens.shape == shape[:1] and lens.is_contiguous()):
+            _check_tensor("q2_attend", "lens", lens, self._i32, shape[:1])
         nk = nv = None
         ldn = 0
         if new_k is not None and new_v is not None:
-            ldn = _rows("new_k", new_k, self._kvshape)
-            if _rows("new_v", new_v, self._kvshape) != ldn:
-                raise Q2Error(ESHAPE, "q2_attend: new_k and new_v have different batch strides")
+            shape = self._kvshape
+            ldn = _rows("new_k", new_k, shape)
+            if not (new_v.dtype is f16 and new_v.is_cuda and new_v.shape == shape and new_v.stride() == new_k.stride()):
+                if _rows("new_v", new_v, shape) != ldn:
+                    raise Q2Error(ESHAPE, "q2_attend: new_k and new_v have different batch strides")
             nk, nv = new_k.data_ptr(), new_v.data_ptr()
         elif new_k is not None or new_v is not None:
             raise Q2Error(EINVAL, "q2_attend: new_k and new_v go together")
-        st = load().q2_attend(self._ref, q.data_ptr(), ldq, nk, nv, ldn, lens.data_ptr(), self.batch, self.q_heads,
-                              self.scale if scale is None else scale, out.data_ptr(), ldo, self._ws, self._ws_bytes,
-                              _stream_ptr(stream))
+        st = self._fn(self._ref, q.data_ptr(), ldq, nk, nv, ldn, lens.data_ptr(), self.batch, self.q_heads,
+                      self.scale if scale is None else scale, out.data_ptr(), ldo, self._ws, self._ws_bytes,
+                      _stream_ptr(stream))
         if st:
             raise Q2Error(st, "q2_attend")
         return out

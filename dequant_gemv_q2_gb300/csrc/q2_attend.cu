@@ -591,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   }
 }
 
-int most_ctas(int D) { return dev_info().sms * (D == 64 ? att_ctas<64>() : D == 128 ? att_ctas<128>() : att_ctas<256>()); }
+int most_ctas(int D, int sms) { return sms * (D == 64 ? att_ctas<64>() : D == 128 ? att_ctas<128>() : att_ctas<256>()); }
 
 // The workspace: the parts' sums, in a region that fits every head_dim (so the
 // counters behind it have one place for calls of all shapes), then counters.
-size_t part_bytes() {
+size_t part_bytes(int sms) {
   size_t n = 0;
-  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D) * kMostHeads * (D * 4 + 8));
+  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D, sms) * kMostHeads * (D * 4 + 8));
   return (n + 255) / 256 * 256;
 }
 
@@ -628,7 +628,7 @@ extern "C" int q2_attend_workspace_bytes(int batch, int q_heads, int kv_heads, i
   int hu, nht;
   const int st = check_heads(batch, q_heads, kv_heads, head_dim, &hu, &nht);
   if (st) return st;
-  *bytes = part_bytes() + (size_t)batch * hu * 4;
+  *bytes = part_bytes(dev_info().sms) + (size_t)batch * hu * 4;
   return Q2_OK;
 }
 
@@ -652,9 +652,8 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
       off(kv->table, 4) || off(lens, 4) || kv->page_stride % 8 || kv->token_stride % 8 || kv->head_stride % 8 ||
       (batch > 1 && (ldq % 8 || ldo % 8 || (new_k && ldn % 8))))
     return Q2_EALIGN;
-  size_t need = 0;
-  st = q2_attend_workspace_bytes(batch, q_heads, kv->kv_heads, D, &need);
-  if (st) return st;
+  const int sms = dev_info().sms;
+  const size_t parts = part_bytes(sms), need = parts + (size_t)batch * hu * 4;
   if (!ws || ws_bytes < need) return Q2_EWORKSPACE;
   if (off(ws, 256)) return Q2_EALIGN;
   // tokens of a table row, and of all units: both are counted in 32 bits on the device
@@ -677,9 +676,9 @@ extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const vo
   a.ldq = ldq;
   a.ldn = ldn;
   a.ldo = ldo;
-  const int most = most_ctas(D);
+  const int most = most_ctas(D, sms);
   a.part = static_cast<float*>(ws);
-  a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + part_bytes());
+  a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + parts);
   a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most * unit_heads(q_heads / kv->kv_heads, D) * D);
   a.batch = batch;
   a.npages = kv->npages;
