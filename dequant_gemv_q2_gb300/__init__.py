@@ -263,15 +263,20 @@ class Packed:
         import torch
         if x8.dim() == 1:
             x8 = x8.view(1, -1)
-        ntok = x8.shape[0]
-        _check_tensor("q2_gemv_x8", "x8", x8, torch.int8, (ntok, self.C))
-        _check_tensor("q2_gemv_x8", "xscale", xscale, torch.float32, (ntok,))
+        shape = x8.shape
+        ntok = shape[0]
+        # what each tensor has to be is tested here at once, and put into words by the function called otherwise
+        if not (x8.dtype is torch.int8 and x8.is_cuda and shape[1:] == (self.C,) and x8.is_contiguous()):
+            _check_tensor("q2_gemv_x8", "x8", x8, torch.int8, (ntok, self.C))
+        if not (xscale.dtype is torch.float32 and xscale.is_cuda and xscale.shape == (ntok,) and xscale.is_contiguous()):
+            _check_tensor("q2_gemv_x8", "xscale", xscale, torch.float32, (ntok,))
         if y is None:
             y = torch.empty((ntok, self.R), dtype=torch.float16, device=x8.device)
-        else:
+        elif not (y.dtype is torch.float16 and y.is_cuda and y.shape == (ntok, self.R) and y.is_contiguous()):
             _check_tensor("q2_gemv_x8", "y", y, torch.float16, (ntok, self.R))
-        _check(load().q2_gemv_x8(self.h, x8.data_ptr(), xscale.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream)),
-               "q2_gemv_x8")
+        st = load().q2_gemv_x8(self.h, x8.data_ptr(), xscale.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_gemv_x8")
         return y
 
     def decode(self, stream=None):

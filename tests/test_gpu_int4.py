@@ -7,6 +7,9 @@ them; the group sums are scaled and added with at most C / group + 16 further
 roundings of 2^-24.  y is rounded once.  So with S = sum |w x|:
 |y - ref| <= 2^-11 |ref| + 2^-25 + (2 group + C / group + 16) 2^-24 S,
 and for 8-bit x, whose group sums are exact, without the term 2 group.
+(Up to 16 tokens the kernels take the zero point off a group's sum; the bound
+for that is wider, see test_gpu_int4_limits.py, and these inputs stay inside
+this one.)
 """
 import numpy as np
 import pytest
