@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
   for (int k = 0; k < kManyMax; ++k) peer[k] = k < nsplit && nsplit > 1 ? cluster.map_shared_rank(out, k) : out;
   for (int e = e0 + threadIdx.x; e < e1; e += kManyWarps * 32) {
     const int t = e / kManyRows, r = e % kManyRows;
+    if (row0 + r >= a.R) continue;                          // (before its loads: see cluster_leave)
     float p[kManyMax];
 #pragma unroll
     for (int k = 0; k < kManyMax; ++k) p[k] = k < nsplit ? peer[k][t * kOutLd + r] : 0.f;
@@ -454,9 +455,9 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
 #pragma unroll
     for (int k = 1; k < kManyMax; ++k) v += p[k];
     if (X8) v *= a.xs[t];
-    if (row0 + r < a.R) a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(v);
+    a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(v);
   }
-  if (nsplit > 1) cluster.sync();                           // every CTA's sums stay readable until all are done
+  if (nsplit > 1) cluster_leave();                          // every CTA's sums stay readable until all are done
 }
 
 // ------------------------------------------------------- launch

@@ -157,6 +157,15 @@ __device__ __forceinline__ void add_group(float2& acc, float s, float z, float2 
   fma2(acc, make_float2(s, s), t);
 }
 
+// The cluster's barrier behind the last reads of other CTAs' shared memory,
+// each of whose values has gone into a store by then: nothing is handed over,
+// so what was written before need not be waited for, as a releasing arrival
+// would (4096 x 4096 at 8 tokens 4.4 -> 3.8 us).
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
 // How many clusters of cs CTAs of a kernel the device runs at once (a cluster

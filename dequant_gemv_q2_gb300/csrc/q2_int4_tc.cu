@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
       const int r0 = rank_of(s), cnt = rank_of(e - 1) - r0 + 1, all = a.ntok * kRows;
       const int e0 = all * (rank - r0) / cnt, e1 = all * (rank - r0 + 1) / cnt;
       for (int x = e0 + threadIdx.x; x < e1; x += blockDim.x) {
-        const int t = x / kRows, r = x % kRows;
+        const int t = x / kRows, r = x % kRows, row = (t0 + tile) * kRows + r;
+        if (row >= a.R) continue;                   // (before its loads: see cluster_leave)
         float p[kMaxCluster];
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)       // the first CTA has the tile as its last, the others as their first
@@ -536,12 +537,11 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
         float v = p[0];
 #pragma unroll
         for (int c = 1; c < kMaxCluster; ++c) v += p[c];
-        const int row = (t0 + tile) * kRows + r;
         if (X8) v *= a.xs[t];
-        if (row < a.R) a.y[(size_t)t * a.R + row] = __float2half_rn(v);
+        a.y[(size_t)t * a.R + row] = __float2half_rn(v);
       }
     }
-    cluster.sync();                                 // every CTA's sums stay readable until all are done
+    cluster_leave();                                // every CTA's sums stay readable until all are done
   }
   tc_fence_before();
   __syncthreads();
