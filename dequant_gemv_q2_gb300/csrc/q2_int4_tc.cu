@@ -29,8 +29,8 @@
 // end in distributed shared memory, after one barrier of the cluster, and are
 // added in column order.
 //
-// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 38.5 us on the
-// device, 2.5 TB/s, 0.59 PFLOP/s (a block of 128 x 128 every 900 cycles of an
+// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 37.2 us on the
+// device, 2.6 TB/s, 0.61 PFLOP/s (a block of 128 x 128 every 900 cycles of an
 // SM).  What bounds it is not one unit: the decoders (about 800 cycles per
 // block, their 9 instructions per 8 weights being half of the issue slots
 // used), the way of x from L2 (1400 to 1900 cycles from the request to the
