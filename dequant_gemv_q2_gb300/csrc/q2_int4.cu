@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
     __syncthreads();
   }
   cg::cluster_group cluster = cg::this_cluster();
-  if (nsplit > 1) cluster.sync();
+  if (nsplit > 1) cluster_meet();
   const int row0 = (int)blockIdx.x / nsplit * kManyRows;
   const int all = a.ntok * kManyRows, e0 = all * rank / nsplit, e1 = all * (rank + 1) / nsplit;
   const float* peer[kManyMax];

@@ -162,8 +162,15 @@ __device__ __forceinline__ void add_group(float2& acc, float s, float z, float2 
 // so what was written before need not be waited for, as a releasing arrival
 // would (4096 x 4096 at 8 tokens 4.4 -> 3.8 us).
 __device__ __forceinline__ void cluster_leave() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// The one in front: what each CTA has left in its shared memory is there.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own

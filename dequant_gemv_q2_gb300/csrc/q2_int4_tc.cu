@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
   pdl_wait();                                       // before anything writes y (returns at once if done)
   cg::cluster_group cluster = cg::this_cluster();
   if (cs > 1) {
-    cluster.sync();
+    cluster_meet();
     // the tile that this run begins in the middle of, and the one it leaves
     // unfinished: this CTA's share of the rows of each
     const int head = u0 / a.nblk, tail = (u0 + n - 1) / a.nblk;
