@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 // What bounds it at 8 tokens is instructions and uneven SMs (240 CTAs, two on
 // some and one on others: an even spread would save 20%), 3.2 TB/s at
 // 5120 x 17408 (8-bit x, groups of 64: 14.9 us) and 3.6 at 24576 x 4096 (14.5
-// us); at 16 tokens the products: an instruction takes the tensor cores 2
+// us); at 16 tokens the products (an instruction takes the tensor cores 2
 // cycles of an SM whatever its operands are worth, 12.5 us of the 21.3 at
-// 24576 x 4096.  More than 16 tokens would cost another product with ones and
+// 24576 x 4096) and, with two CTAs per SM, the latencies between them.  More than 16 tokens would cost another product with ones and
 // 48 accumulators more per thread: they go to the kernel in q2_int4_tc.cu
 // (24576 x 4096 at 32 tokens 25.1 us, twice the 16-token time here 43).
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
