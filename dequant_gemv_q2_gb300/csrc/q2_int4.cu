@@ -249,33 +249,38 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 // fp32 sums through distributed shared memory in rank order.
 //
 // What bounds it at 8 tokens is instructions and uneven SMs (240 CTAs, two on
-// some and one on others: an even spread would save 20%), 3.2 TB/s at
-// 5120 x 17408 (8-bit x, groups of 64: 14.9 us) and 3.6 at 24576 x 4096 (14.5
+// some and one on others: an even spread would save 20%), 3.3 TB/s at
+// 5120 x 17408 (8-bit x, groups of 64: 14.4 us) and 3.6 at 24576 x 4096 (14.5
 // us); at 16 tokens the products (an instruction takes the tensor cores 2
 // cycles of an SM whatever its operands are worth, 12.5 us of the 21.3 at
-// 24576 x 4096) and, with two CTAs per SM, the latencies between them.  More than 16 tokens would cost another product with ones and
-// 48 accumulators more per thread: they go to the kernel in q2_int4_tc.cu
+// 24576 x 4096) and, with two CTAs per SM, the latencies between them.  More than
+// 16 tokens would cost another product with ones and 48 accumulators more per
+// thread: they go to the kernel in q2_int4_tc.cu
 // (24576 x 4096 at 32 tokens 25.1 us, twice the 16-token time here 43).
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
 __host__ __device__ constexpr int x_row_bytes() { return X8 ? 128 + 16 : 256 + 16; }
-constexpr int kManyStages = 3;
+// Stages of a group's ring with so many CTAs per SM.  At up to 8 tokens one or
+// two take four, and 128 registers a thread instead of 80 (34816 x 5120 from
+// 8-bit x at 7 tokens 22.4 us, 23.5 with what three CTAs per SM leave room for).
+template <int NT>
+__host__ __device__ constexpr int many_stages(int share) { return NT == 1 && share <= 2 ? 4 : 3; }
 template <int NT>
 __host__ __device__ constexpr int many_ctas() { return NT == 1 ? 3 : 2; }   // per SM, at most
 
 constexpr int kOutLd = kManyRows + 4;
 
 template <int NT, bool X8>
-int many_smem(const Int4Args& a) {
-  const int ring = 2 * kManyStages * (NT * 8 * x_row_bytes<X8>() + 8 * a.item), out = NT * 8 * kOutLd * 4;
+int many_smem(const Int4Args& a, int stages) {
+  const int ring = 2 * stages * (NT * 8 * x_row_bytes<X8>() + 8 * a.item), out = NT * 8 * kOutLd * 4;
   return ring > out ? ring : out;
 }
 
-template <int NT, int GPB, bool X8>
-__global__ void __launch_bounds__(kManyWarps * 32, many_ctas<NT>())
+template <int NT, int GPB, bool X8, int STAGES>
+__global__ void __launch_bounds__(kManyWarps * 32, STAGES == 4 ? 2 : many_ctas<NT>())
     k_int4_many(const __grid_constant__ Int4Args a, const int nsplit) {
-  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB, STAGES = kManyStages;
+  constexpr int MT = 2, NTOK = NT * 8, ROWB = x_row_bytes<X8>(), STEPS = 8 / GPB;
   constexpr int esz = X8 ? 1 : 2, PIECES = 128 * esz / 16, PASS = 128 / PIECES;   // pieces of a row; tokens of a pass
   extern __shared__ __align__(16) unsigned char q2_int4_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -477,21 +482,25 @@ int launch_few(const Int4Args& a, int slots, void* stream) {
 template <int NT, int GPB, bool X8>
 int launch_many(const Int4Args& a, void* stream) {
   static ClusterCounts counts;
-  auto kernel = k_int4_many<NT, GPB, X8>;
-  const void* fn = reinterpret_cast<const void*>(kernel);
-  const int smem = many_smem<NT, X8>(a);
+  auto kernel_of = [](int share) {
+    return many_stages<NT>(share) == 4 ? k_int4_many<NT, GPB, X8, many_stages<NT>(1)> : k_int4_many<NT, GPB, X8, 3>;
+  };
+  auto fn_of = [&](int share) { return reinterpret_cast<const void*>(kernel_of(share)); };
   const int tiles = (a.ntile + kManyRows / 16 - 1) / (kManyRows / 16), sms = dev_info().sms;
-  if (set_smem(fn, kSmemPerSm - 1024)) return Q2_ECUDA;
+  if (set_smem(fn_of(1), kSmemPerSm - 1024) || set_smem(fn_of(3), kSmemPerSm - 1024)) return Q2_ECUDA;
   // No more CTAs on an SM than an even spread needs (the next one's shared
   // memory is taken): left alone they fill some SMs and leave others idle
   // (256 CTAs of 4096 x 4096: 5.6 us instead of 4.4).
-  auto smem_of = [&](int share) { return share < many_ctas<NT>() ? std::max(smem, kSmemPerSm / (share + 1)) : smem; };
-  int nsplit = 1, with = smem;
+  auto smem_of = [&](int share) {
+    const int smem = many_smem<NT, X8>(a, many_stages<NT>(share));
+    return share < many_ctas<NT>() ? std::max(smem, kSmemPerSm / (share + 1)) : smem;
+  };
+  int nsplit = 1, with = 1;
   long long best = 0;
   for (int s = 1; s <= kManyMax && 2 * s <= a.nblk; ++s) {
     int share = std::min((tiles * s + sms - 1) / sms, many_ctas<NT>()), fit = 0;
     for (; share <= many_ctas<NT>(); ++share) {               // the clusters that run at once with so many CTAs per SM
-      fit = counts.get(fn, s, kManyWarps * 32, smem_of(share));
+      fit = counts.get(fn_of(share), s, kManyWarps * 32, smem_of(share));
       if (fit >= tiles) break;
     }
     share = std::min(share, many_ctas<NT>());
@@ -499,10 +508,10 @@ int launch_many(const Int4Args& a, void* stream) {
     if (s == 1 || cost < best) {
       best = cost;
       nsplit = s;
-      with = smem_of(share);
+      with = share;
     }
   }
-  return launch_clusters(kernel, tiles, nsplit, kManyWarps * 32, with, stream, a, nsplit);
+  return launch_clusters(kernel_of(with), tiles, nsplit, kManyWarps * 32, smem_of(with), stream, a, nsplit);
 }
 
 template <int GPB, bool X8>
