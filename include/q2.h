@@ -309,7 +309,7 @@ int q2_rotate_split(int C, int* nh, int* nq);
  *     h = x + residual                       (fp32; residual may be NULL)
  *     y = h * weight / sqrt(mean(h^2) + eps) (fp32)
  *     residual_out = fp16(h); y = fp16(y);
- *     scale8 = max|y| / 127 over the row, y8 = rint(y / scale8).
+ *     scale8 = max|y| / 127 over the row, y8 = rint(y / scale8) (ties to even).
  * heads = 1 is the norm of a hidden state; heads > 1 that of each head of a
  * projection's output, read where it lies.
  *   - x: device fp16, row (t, k) at x + t * ldx + k * C elements; y: the same
