@@ -27,10 +27,14 @@
 // rows of one piece (what one matrix load takes) lie in different banks.
 //
 // Both products run on the tensor cores (16 x 8 x 16, fp32 accumulators) with
-// the group's query heads as rows 0..7.  The probabilities are split into two
-// fp16 numbers, p = hi + lo, and lo takes rows 8..15 of the same
-// instructions (with more than eight heads its own): the numerators are as exact as with fp32 probabilities (an
-// error of 2^-22 instead of 2^-11 per term) at no cost.  More than 16
+// the group's query heads as rows 0..7.  The probabilities, at most 1, are
+// split into two fp16 numbers, 2^15 p = hi + lo, and lo takes rows 8..15 of the
+// same instructions: an error of 2^-22 instead of 2^-11 per term at no cost
+// (with more than eight heads lo has its own instructions).  The factor keeps
+// small ones apart from fp16's smallest numbers: without it a p below 2^-14
+// lost bits and one below 2^-25 was zero, and behind a token that takes nearly
+// all of the weight and has a value near zero the output is made of those (8192
+// tokens behind one with a score 18 above theirs: 1 % off, behind four 4 %).  More than 16
 // query heads to a key-value head (eight of 256 columns) are taken 16 (eight)
 // at a time, each reading the tokens again.
 //
@@ -106,11 +110,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// p0, p1 as pairs of fp16 numbers whose sums they are (to 2^-22).
+// 2^15 p0 and 2^15 p1 (p <= 1) as pairs of fp16 numbers whose sums they are, to
+// 2^-22 of each or half of fp16's smallest, 2^-40 of the largest p.
+constexpr float kUp = 32768.f;
 __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(p0, p1);
+  const __half2 h = __floats2half2_rn(p0 * kUp, p1 * kUp);
   const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(p0 - f.x, p1 - f.y);
+  const __half2 l = __floats2half2_rn(fmaf(p0, kUp, -f.x), fmaf(p1, kUp, -f.y));
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
           ll += wt[k] * v.y;
         }
         if (row < rows) {
-          const float inv = 1.f / ll;
+          const float inv = 1.f / (kUp * ll);      // (the numerators are 2^15 too large)
 #pragma unroll
           for (int q = 0; q < PPL; ++q) {
             const int piece4 = (warp * 4 + j) * PPL + q;      // columns 4 * piece4 ..
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
           }
         }
       }
-      const float inv = 1.f / lj;
+      const float inv = 1.f / (kUp * lj);
       __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
       *reinterpret_cast<uint2*>(a.o + w.x * a.ldo + (long long)(kvh * a.group + ht * H + r) * D + d4 * 4) =
           *reinterpret_cast<uint2*>(h);
