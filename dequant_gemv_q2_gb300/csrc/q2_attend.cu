@@ -29,7 +29,7 @@
 // Both products run on the tensor cores (16 x 8 x 16, fp32 accumulators) with
 // the group's query heads as rows 0..7.  The probabilities, at most 1, are
 // split into two fp16 numbers, 2^15 p = hi + lo, and lo takes rows 8..15 of the
-// same instructions: an error of 2^-22 instead of 2^-11 per term at no cost
+// same instructions: an error of 2^-20 instead of 2^-11 per term at no cost
 // (with more than eight heads lo has its own instructions).  The factor keeps
 // small ones apart from fp16's smallest numbers: without it a p below 2^-14
 // lost bits and one below 2^-25 was zero, and behind a token that takes nearly
@@ -110,14 +110,17 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^15 p0 and 2^15 p1 (p <= 1) as pairs of fp16 numbers whose sums they are, to
-// 2^-22 of each or half of fp16's smallest, 2^-40 of the largest p.
+// 2^15 p0 and 2^15 p1 (0 <= p <= 1) as pairs of fp16 numbers whose sums they
+// are, to 2^-20 of each or half of fp16's smallest, 2^-40 of the largest p.
+// hi is cut off a little below 2^15 p and lo is the rest, so both are above
+// zero where p is at least 2^-37: an infinite value times either has its sign
+// (0 * inf and inf - inf would make NaN of it).
 constexpr float kUp = 32768.f;
 __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(p0 * kUp, p1 * kUp);
-  const float2 f = __half22float2(h);
+  constexpr float kCut = kUp * (1.f - 1.f / 4096.f), kLeast = 1.f / 16777216.f;
+  asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(fmaf(p1, kCut, -kLeast)), "f"(fmaf(p0, kCut, -kLeast)));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   const __half2 l = __floats2half2_rn(fmaf(p0, kUp, -f.x), fmaf(p1, kUp, -f.y));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 

@@ -379,6 +379,9 @@ typedef struct {
  *     when first used; completed calls leave its counters at zero.  Calls of
  *     any shapes that it is large enough for may share it if they are ordered
  *     on one stream; calls that overlap on the GPU need different ones.
+ *   - Infinite values in the cache make their column of the output infinite,
+ *     of their sign (NaN where both signs meet, and where a weight below 2^-37
+ *     of the largest, or of a score of -inf, meets one).
  *   - What pages hold past a sequence's end, and table entries there, are
  *     never used.  A length below 0 or above max_pages * page_size, or a page
  *     number outside 0..npages-1, makes that sequence's output NaN (of the
