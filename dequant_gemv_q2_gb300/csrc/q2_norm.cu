@@ -318,10 +318,7 @@ __global__ void __launch_bounds__(NT, norm_ctas<TPR, CH, VEC, NT>()) k_rmsnorm(c
 
 template <int TPR, int CH, bool VEC, int NT>
 int launch_rows(const NormArgs& a, int grid, int threads, void* stream) {
-  auto kernel = k_rmsnorm<TPR, CH, VEC, NT>;
-  const int smem = norm_smem<VEC>(a, TPR ? 256 / (TPR ? TPR : 1) : 1);
-  if (smem > 47 * 1024 && set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
-  return launch_pdl(kernel, a, grid, threads, smem, stream);
+  return launch_pdl(k_rmsnorm<TPR, CH, VEC, NT>, a, grid, threads, norm_smem<VEC>(a, TPR ? 256 / (TPR ? TPR : 1) : 1), stream);
 }
 
 template <bool VEC>
