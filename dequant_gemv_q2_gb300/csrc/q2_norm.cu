@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(NT, norm_ctas<TPR, CH, VEC, NT>()) k_rmsnorm(c
     if (CH > 2) me.load(a.w, wr);
     ss = row_reduce<TPR, false>(ss, psum[turn]);
     if (a.res_out) me.store(a.res_out + (size_t)row * a.C, h, hbuf);
-    const float k = rsqrtf(ss / (float)a.C + a.eps);
+    const float d = ss / (float)a.C + a.eps, k = d == 0.f ? 0.f : rsqrtf(d);   // eps = 0: zeros for a row of zeros
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float w[8];

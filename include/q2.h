@@ -323,8 +323,9 @@ int q2_rotate_split(int C, int* nh, int* nq);
  *   - Pointers need their element's alignment only (Q2_EALIGN); C, ldx and
  *     ldy multiples of 8 and pointers on 16-byte (y8: 8-byte) boundaries run
  *     on 16-byte loads and stores.
- *   - An all-zero row has scale8 = 0.  A row with an inf or NaN has a
- *     scale8 that is not finite, so y8 * scale8 is not finite either.
+ *   - An all-zero row gives zeros and scale8 = 0, also where eps = 0.  A row
+ *     with an inf or NaN has a scale8 that is not finite, so y8 * scale8 is
+ *     not finite either.
  *   - ntok == 0 does nothing.  Asynchronous on `stream`, launched like
  *     q2_gemv (all inputs are read after the previous kernel has finished). */
 #define Q2_NORM_MAX_C 32768
