@@ -443,26 +443,39 @@ __global__ void __launch_bounds__(kManyWarps * 32, STAGES == 4 ? 2 : many_ctas<N
     }
     __syncthreads();
   }
-  cg::cluster_group cluster = cg::this_cluster();
-  if (nsplit > 1) cluster_meet();
   const int row0 = (int)blockIdx.x / nsplit * kManyRows;
-  const int all = a.ntok * kManyRows, e0 = all * rank / nsplit, e1 = all * (rank + 1) / nsplit;
+  auto store = [&](int e, float v) {
+    const int t = e / kManyRows, r = e % kManyRows;
+    if (row0 + r < a.R) a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(X8 ? v * a.xs[t] : v);
+  };
+  const int all = a.ntok * kManyRows;
+  if (nsplit == 1) {
+    for (int e = threadIdx.x; e < all; e += kManyWarps * 32) store(e, out[e / kManyRows * kOutLd + e % kManyRows]);
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster_meet();
+  constexpr int PER = NTOK * kManyRows / 2 / (kManyWarps * 32);   // elements of a thread: two CTAs at least share them
+  const int e0 = all * rank / nsplit + threadIdx.x, e1 = all * (rank + 1) / nsplit;
   const float* peer[kManyMax];
 #pragma unroll
-  for (int k = 0; k < kManyMax; ++k) peer[k] = k < nsplit && nsplit > 1 ? cluster.map_shared_rank(out, k) : out;
-  for (int e = e0 + threadIdx.x; e < e1; e += kManyWarps * 32) {
-    const int t = e / kManyRows, r = e % kManyRows;
-    if (row0 + r >= a.R) continue;                          // (before its loads: see cluster_leave)
+  for (int k = 0; k < kManyMax; ++k) peer[k] = k < nsplit ? cluster.map_shared_rank(out, k) : out;
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i * (kManyWarps * 32), at = e / kManyRows * kOutLd + e % kManyRows;
     float p[kManyMax];
 #pragma unroll
-    for (int k = 0; k < kManyMax; ++k) p[k] = k < nsplit ? peer[k][t * kOutLd + r] : 0.f;
-    float v = p[0];
+    for (int k = 0; k < kManyMax; ++k) p[k] = k < nsplit && e < e1 ? peer[k][at] : 0.f;
+    v[i] = p[0];
 #pragma unroll
-    for (int k = 1; k < kManyMax; ++k) v += p[k];
-    if (X8) v *= a.xs[t];
-    a.y[(size_t)t * a.R + row0 + r] = __float2half_rn(v);
+    for (int k = 1; k < kManyMax; ++k) v[i] += p[k];
   }
-  if (nsplit > 1) cluster_leave();                          // every CTA's sums stay readable until all are done
+  cluster_arrive();                                         // this CTA has read the others' sums
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (e0 + i * (kManyWarps * 32) < e1) store(e0 + i * (kManyWarps * 32), v[i]);
+  cluster_wait();                                           // and they this one's
 }
 
 // ------------------------------------------------------- launch

@@ -157,20 +157,22 @@ __device__ __forceinline__ void add_group(float2& acc, float s, float z, float2 
   fma2(acc, make_float2(s, s), t);
 }
 
-// The cluster's barrier behind the last reads of other CTAs' shared memory,
-// each of whose values has gone into a store by then: nothing is handed over,
-// so what was written before need not be waited for, as a releasing arrival
-// would (4096 x 4096 at 8 tokens 4.4 -> 3.8 us).
-__device__ __forceinline__ void cluster_leave() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-}
-// The one in front: what each CTA has left in its shared memory is there.
-__device__ __forceinline__ void cluster_meet() {
+// The cluster's barriers, by converged warps.  The first: what each CTA has left
+// in its shared memory is there for the others.  The second, behind the last
+// reads of other CTAs' shared memory, in two halves: the arrival orders those
+// reads before it (a releasing one does, a relaxed one would not), and the
+// stores of what was read come behind it, so that it does not wait for them.
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own

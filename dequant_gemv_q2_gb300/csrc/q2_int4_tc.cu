@@ -516,32 +516,40 @@ __global__ void __launch_bounds__(tc_threads<X8>(), 1) k_int4_tc(const __grid_co
   cg::cluster_group cluster = cg::this_cluster();
   if (cs > 1) {
     cluster_meet();
-    // the tile that this run begins in the middle of, and the one it leaves
-    // unfinished: this CTA's share of the rows of each
+    // The tile that this run begins in the middle of, and the one it leaves
+    // unfinished: this CTA's share of the rows of each.  The sums of all CTAs
+    // are added up in the ring, which is free now, and stored when this CTA
+    // has said that it has read them.
     const int head = u0 / a.nblk, tail = (u0 + n - 1) / a.nblk;
+    auto each = [&](auto use) {
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const int tile = k ? tail : head, s = tile * a.nblk, e = s + a.nblk;
-      const bool open = k ? tail != head && e > u0 + n : s < u0 || e > u0 + n;
-      if (!open) continue;
-      auto rank_of = [&](int u) { return (int)((((long long)u + 1) * cs - 1) / T); };
-      const int r0 = rank_of(s), cnt = rank_of(e - 1) - r0 + 1, all = a.ntok * kRows;
-      const int e0 = all * (rank - r0) / cnt, e1 = all * (rank - r0 + 1) / cnt;
-      for (int x = e0 + threadIdx.x; x < e1; x += blockDim.x) {
-        const int t = x / kRows, r = x % kRows, row = (t0 + tile) * kRows + r;
-        if (row >= a.R) continue;                   // (before its loads: see cluster_leave)
-        float p[kMaxCluster];
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)       // the first CTA has the tile as its last, the others as their first
-          p[c] = c < cnt ? cluster.map_shared_rank(part, r0 + c)[(c ? 0 : N * kOutLd) + t * kOutLd + r] : 0.f;
-        float v = p[0];
-#pragma unroll
-        for (int c = 1; c < kMaxCluster; ++c) v += p[c];
-        if (X8) v *= a.xs[t];
-        a.y[(size_t)t * a.R + row] = __float2half_rn(v);
+      for (int k = 0; k < 2; ++k) {
+        const int tile = k ? tail : head, s = tile * a.nblk, e = s + a.nblk;
+        const bool open = k ? tail != head && e > u0 + n : s < u0 || e > u0 + n;
+        if (!open) continue;
+        auto rank_of = [&](int u) { return (int)((((long long)u + 1) * cs - 1) / T); };
+        const int r0 = rank_of(s), cnt = rank_of(e - 1) - r0 + 1, all = a.ntok * kRows;   // cnt >= 2
+        const int e0 = all * (rank - r0) / cnt, e1 = all * (rank - r0 + 1) / cnt;
+        float* sum = reinterpret_cast<float*>(B) + k * (N * kRows / 2);
+        for (int x = e0 + threadIdx.x; x < e1; x += blockDim.x)
+          use(sum[x - e0], r0, cnt, x / kRows, x % kRows, (t0 + tile) * kRows + x % kRows);
       }
-    }
-    cluster_leave();                                // every CTA's sums stay readable until all are done
+    };
+    each([&](float& sum, int r0, int cnt, int t, int r, int) {
+      float p[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)         // the first CTA has the tile as its last, the others as their first
+        p[c] = c < cnt ? cluster.map_shared_rank(part, r0 + c)[(c ? 0 : N * kOutLd) + t * kOutLd + r] : 0.f;
+      float v = p[0];
+#pragma unroll
+      for (int c = 1; c < kMaxCluster; ++c) v += p[c];
+      sum = v;
+    });
+    cluster_arrive();                               // this CTA has read the others' sums
+    each([&](float& sum, int, int, int t, int, int row) {
+      if (row < a.R) a.y[(size_t)t * a.R + row] = __float2half_rn(X8 ? sum * a.xs[t] : sum);
+    });
+    cluster_wait();                                 // and they this one's
   }
   tc_fence_before();
   __syncthreads();
