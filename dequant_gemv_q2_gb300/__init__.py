@@ -192,6 +192,18 @@ def _check_tensor(where: str, name: str, t, dtype, shape, strides=None) -> None:
         raise Q2Error(ESHAPE, f"{where}: {name} has strides {t.stride()}")
 
 
+def _check_rows(where: str, name: str, t, ntok: int, width: int) -> None:
+    """Refuse what the C call would not read (or write) as fp16 [ntok][width]: rows of another width, fewer of them,
+    another type or layout, or a tensor that is not on a GPU.  Rows behind the first ntok are left alone."""
+    import torch
+    if t.dtype is not torch.float16 or not t.is_cuda:
+        raise Q2Error(EINVAL, f"{where}: {name} is {t.dtype} on {t.device}, not {torch.float16} on a GPU")
+    if t.numel() != ntok * width and not (t.dim() == 2 and t.shape[0] >= ntok and t.shape[1] == width):
+        raise Q2Error(ESHAPE, f"{where}: {name} has shape {tuple(t.shape)}, not {(ntok, width)}")
+    if not t.is_contiguous():
+        raise Q2Error(ESHAPE, f"{where}: {name} has strides {t.stride()}")
+
+
 def device_errors() -> int:
     """The tensor-core and attention kernels' device error word (then cleared); 0 is normal."""
     v = ctypes.c_uint(0)
@@ -223,6 +235,7 @@ class Packed:
         f, R, C = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
         _check(L.q2_info(h, ctypes.byref(f), ctypes.byref(R), ctypes.byref(C)), "q2_info")
         self.fmt, self.R, self.C = f.value, R.value, C.value
+        self._fn, self._f16 = L.q2_gemv, torch.float16
         self.ws = None
         # the workspace of every call up to ntok_max tokens (the paths differ by token count)
         need = max(self.workspace_bytes(t) for t in range(1, int(ntok_max) + 1))
@@ -246,16 +259,26 @@ class Packed:
         return n.value
 
     def gemv(self, x, y=None, stream=None, fmt=None):
-        """y[ntok][R] = x[ntok][C] @ W^T through q2_gemv (asynchronous)."""
-        import torch
-        if x.dim() == 1:
+        """y[ntok][R] = x[ntok][C] @ W^T through q2_gemv (asynchronous).
+
+        x and y: fp16, contiguous, on the GPU; a token's C columns may be of any shape ([ntok][heads][dim]).
+        """
+        f16, C, R, shape = self._f16, self.C, self.R, x.shape
+        if len(shape) == 1:
             x = x.view(1, -1)
-        ntok = x.shape[0]
+            shape = x.shape
+        ntok = shape[0]
+        # what each tensor has to be is tested here at once, and put into words by the function called otherwise
+        if not (x.dtype is f16 and x.is_cuda and shape == (ntok, C) and x.is_contiguous()):
+            _check_rows("q2_gemv", "x", x, ntok, C)
         if y is None:
-            y = torch.empty((ntok, self.R), dtype=torch.float16, device=x.device)
-        st = load().q2_gemv(self.fmt if fmt is None else int(fmt), self.h, x.data_ptr(), y.data_ptr(), ntok,
-                            _stream_ptr(stream))
-        _check(st, "q2_gemv")
+            import torch
+            y = torch.empty((ntok, R), dtype=f16, device=x.device)
+        elif not (y.dtype is f16 and y.is_cuda and y.shape == (ntok, R) and y.is_contiguous()):
+            _check_rows("q2_gemv", "y", y, ntok, R)
+        st = self._fn(self.fmt if fmt is None else int(fmt), self.h, x.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_gemv")
         return y
 
     def gemv_x8(self, x8, xscale, y=None, stream=None):
@@ -318,6 +341,9 @@ class Chain:
         n = len(links)
         self.links = list(links)            # keeps the tensors alive
         self.ntok, self.lookahead = int(ntok), int(lookahead)
+        for i, (p, x, y) in enumerate(self.links):
+            _check_rows("q2_gemv_chain", f"x of link {i}", x, self.ntok, p.C)
+            _check_rows("q2_gemv_chain", f"y of link {i}", y, self.ntok, p.R)
         self._fmt = (ctypes.c_int * n)(*[p.fmt for p, _, _ in links])
         self._h = (ctypes.c_void_p * n)(*[p.h.value for p, _, _ in links])
         self._x = (ctypes.c_void_p * n)(*[x.data_ptr() for _, x, _ in links])
@@ -361,8 +387,11 @@ class Rotation:
         import torch
         if x.dim() == 1:
             x = x.view(1, -1)
+        _check_rows("q2_rotate", "x", x, x.shape[0], self.C)
         if out is None:
             out = torch.empty_like(x)
+        else:
+            _check_rows("q2_rotate", "out", out, x.shape[0], self.C)
         _check(q2_rotate(x, out, x.shape[0], self.C, self.nh, self.signs, self.q, stream), "q2_rotate")
         return out
 
