@@ -204,6 +204,15 @@ def _check_rows(where: str, name: str, t, ntok: int, width: int) -> None:
         raise Q2Error(ESHAPE, f"{where}: {name} has strides {t.stride()}")
 
 
+def _workspace_bytes(where: str, ws) -> int:
+    """The bytes of a workspace, which is one run of GPU memory."""
+    if not ws.is_cuda:
+        raise Q2Error(EINVAL, f"{where}: workspace on {ws.device}, not on a GPU")
+    if not ws.is_contiguous():
+        raise Q2Error(ESHAPE, f"{where}: workspace has strides {ws.stride()}")
+    return ws.numel() * ws.element_size()
+
+
 def device_errors() -> int:
     """The tensor-core and attention kernels' device error word (then cleared); 0 is normal."""
     v = ctypes.c_uint(0)
@@ -250,8 +259,9 @@ class Packed:
         return n.value
 
     def set_workspace(self, ws) -> None:
+        n = _workspace_bytes("q2_set_workspace", ws)
+        _check(load().q2_set_workspace(self.h, ctypes.c_void_p(ws.data_ptr()), n), "q2_set_workspace")
         self.ws = ws
-        _check(load().q2_set_workspace(self.h, ctypes.c_void_p(ws.data_ptr()), ws.numel()), "q2_set_workspace")
 
     def bytes_read(self, ntok: int = 1) -> int:
         n = ctypes.c_size_t(0)
@@ -520,9 +530,10 @@ class PagedKV:
                "q2_attend_workspace_bytes")
         if workspace is None:
             workspace = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
-        elif workspace.numel() < n.value:
-            raise Q2Error(EWORKSPACE, f"PagedKV: workspace of {workspace.numel()} bytes, {n.value} needed")
-        self.ws, self._ws, self._ws_bytes = workspace, workspace.data_ptr(), workspace.numel()
+        size = _workspace_bytes("PagedKV", workspace)
+        if size < n.value:
+            raise Q2Error(EWORKSPACE, f"PagedKV: workspace of {size} bytes, {n.value} needed")
+        self.ws, self._ws, self._ws_bytes = workspace, workspace.data_ptr(), size
 
     def attend(self, q, lens, new_k=None, new_v=None, scale=None, out=None, stream=None):
         """Attention of q [batch][q_heads][dim] over the first lens[b] (int32) tokens of each sequence.
