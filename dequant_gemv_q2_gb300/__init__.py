@@ -204,6 +204,24 @@ def _check_rows(where: str, name: str, t, ntok: int, width: int) -> None:
         raise Q2Error(ESHAPE, f"{where}: {name} has strides {t.stride()}")
 
 
+def _new(make, shape, dtype, device, stream):
+    """A tensor made on the stream that writes it: memory of another stream's might still be in that one's use."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _zero_workspace(n: int, device):
+    """A workspace of zeros, filled when this returns: its first call may come on any stream."""
+    import torch
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
 def _workspace_bytes(where: str, ws) -> int:
     """The bytes of a workspace, which is one run of GPU memory."""
     if not ws.is_cuda:
@@ -251,7 +269,7 @@ class Packed:
         if workspace is not None:
             self.set_workspace(workspace)
         elif need:
-            self.set_workspace(torch.zeros(need, dtype=torch.uint8, device=device))
+            self.set_workspace(_zero_workspace(need, device))
 
     def workspace_bytes(self, ntok: int) -> int:
         n = ctypes.c_size_t(0)
@@ -283,7 +301,7 @@ class Packed:
             _check_rows("q2_gemv", "x", x, ntok, C)
         if y is None:
             import torch
-            y = torch.empty((ntok, R), dtype=f16, device=x.device)
+            y = _new(torch.empty, (ntok, R), f16, x.device, stream)
         elif not (y.dtype is f16 and y.is_cuda and y.shape == (ntok, R) and y.is_contiguous()):
             _check_rows("q2_gemv", "y", y, ntok, R)
         st = self._fn(self.fmt if fmt is None else int(fmt), self.h, x.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream))
@@ -304,7 +322,7 @@ class Packed:
         if not (xscale.dtype is torch.float32 and xscale.is_cuda and xscale.shape == (ntok,) and xscale.is_contiguous()):
             _check_tensor("q2_gemv_x8", "xscale", xscale, torch.float32, (ntok,))
         if y is None:
-            y = torch.empty((ntok, self.R), dtype=torch.float16, device=x8.device)
+            y = _new(torch.empty, (ntok, self.R), torch.float16, x8.device, stream)
         elif not (y.dtype is torch.float16 and y.is_cuda and y.shape == (ntok, self.R) and y.is_contiguous()):
             _check_tensor("q2_gemv_x8", "y", y, torch.float16, (ntok, self.R))
         st = load().q2_gemv_x8(self.h, x8.data_ptr(), xscale.data_ptr(), y.data_ptr(), ntok, _stream_ptr(stream))
@@ -317,7 +335,7 @@ class Packed:
         import torch
         n = ctypes.c_size_t(0)
         _check(load().q2_decode_bytes(self.h, ctypes.byref(n)), "q2_decode_bytes")
-        out = torch.zeros(n.value, dtype=torch.uint8, device=self.dev.device)
+        out = _new(torch.zeros, n.value, torch.uint8, self.dev.device, stream)
         _check(load().q2_decode(self.h, ctypes.c_void_p(out.data_ptr()), _stream_ptr(stream)), "q2_decode")
         return out
 
@@ -399,7 +417,7 @@ class Rotation:
             x = x.view(1, -1)
         _check_rows("q2_rotate", "x", x, x.shape[0], self.C)
         if out is None:
-            out = torch.empty_like(x)
+            out = _new(torch.empty, x.shape, x.dtype, x.device, stream)
         else:
             _check_rows("q2_rotate", "out", out, x.shape[0], self.C)
         _check(q2_rotate(x, out, x.shape[0], self.C, self.nh, self.signs, self.q, stream), "q2_rotate")
@@ -456,7 +474,7 @@ class RmsNorm:
             y = out.data_ptr()
         elif out8 is None:
             import torch
-            out = torch.empty(shape, dtype=f16, device=x.device)
+            out = _new(torch.empty, shape, f16, x.device, stream)
             y = out.data_ptr()
         if residual is not None:
             if not (residual.dtype is f16 and residual.is_cuda and residual.shape == shape and residual.is_contiguous()):
@@ -529,7 +547,7 @@ class PagedKV:
         _check(load().q2_attend_workspace_bytes(self.batch, self.q_heads, self.kv_heads, self.dim, ctypes.byref(n)),
                "q2_attend_workspace_bytes")
         if workspace is None:
-            workspace = torch.zeros(n.value, dtype=torch.uint8, device=k.device)
+            workspace = _zero_workspace(n.value, k.device)
         size = _workspace_bytes("PagedKV", workspace)
         if size < n.value:
             raise Q2Error(EWORKSPACE, f"PagedKV: workspace of {size} bytes, {n.value} needed")
@@ -546,7 +564,7 @@ class PagedKV:
         # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
         if out is None:
             import torch
-            out = torch.empty(shape, dtype=f16, device=q.device)
+            out = _new(torch.empty, shape, f16, q.device, stream)
         ldq = ldo = self.q_heads * self.dim
         if not (q.dtype is f16 and q.is_cuda and q.shape == shape and q.is_contiguous()):
             ldq = _rows("q", q, shape)
