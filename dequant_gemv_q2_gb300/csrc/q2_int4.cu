@@ -5,16 +5,15 @@
 // for x in fp16, or in 8 bits with one fp32 scale per token.
 //
 // The inner sums run on the tensor cores, 16 rows x 16 columns of weights
-// against 8 tokens per instruction, fp32 accumulators.  The four bits are used
-// as they are: in the lowest bits of an fp16 number they are the subnormal
-// q * 2^-24 (shifted left by four: q * 2^-20), which the tensor cores multiply
-// exactly, so 8 weights cost 5 instructions.  The powers of two go into the
-// scales, and the zero point is taken off the group's sum,
-//   sum (q - z) x = 2^24 sum (q 2^-24) x - z sum x,
-// with the sums of x over each group from a product with ones.  Both terms are
-// fp32 sums of the group's products, at most 15 sum |x| each, so the
-// difference keeps the rounding of such a sum; nothing but y itself is rounded
-// to fp16.  For 8-bit x both are integers below 2^18 and thus exact.
+// against 8 tokens per instruction, fp32 accumulators.  The operands are q - z,
+// exact in fp16 (9 instructions per 8 weights, unpack_step), so a group's sum
+// is an fp32 sum of its exact products, for 8-bit x exact itself (integers
+// below 2^18); group sums are scaled and added in fp32, and nothing but y is
+// rounded to fp16.  The four bits as they are, as the fp16 subnormals q 2^-24,
+// with the zero point taken off through the sums of x, cost 5 instructions but
+// lost up to ten bits of the smaller terms beside a large one (the tensor cores
+// line products up without normalising a subnormal): an activation of 6e4 over
+// a zero weight put outputs off by their own size.
 //
 // Weights are stored in the order in which lanes use them: the unit is a
 // block of 16 rows x 128 columns, 1 KB as two 16-byte loads per lane, with
@@ -36,8 +35,7 @@ namespace {
 
 // ------------------------------------------------------- 1 and 2 tokens
 // At one token a block's 2048 weights have to pass in about 50 cycles per SM,
-// so instructions are what is scarce: k_int4_few computes the sums of x once
-// per CTA.
+// so instructions are what is scarce.
 //
 // A CTA's warps split the columns of a row tile (16 rows) and keep their
 // column range over all row tiles that the CTA takes (every gridDim.x-th): a
@@ -47,25 +45,23 @@ namespace {
 // end the warps leave their sums in one of two shared-memory buffers and the
 // first threads add them in warp order: one barrier per row tile, no atomics.
 //
-// 24576 x 4096 at one token, groups of 128 with zero points: 11.0 us on the
-// device, 4.7 TB/s (4096 x 4096: 3.6 us, of which 2 are the launch and the
-// first bytes' way).  Issue slots are 70% full and what remains is the ends:
-// the first loads, x and its sums before them, the last row tiles.  Steps:
-// register ring 19.1 us, shared-memory ring 14.3, the bits as subnormals and
-// sums of x once per CTA 11.2, sums added a pair of tokens at a time 11.0.
+// 24576 x 4096 at one token, groups of 128 with zero points: 11.3 us on the
+// device, 4.6 TB/s; two tokens 11.9; from 8-bit x, which becomes fp16 on its way
+// into shared memory, 11.3 (groups of 64).  4096 x 4096: 3.1 us, of which 2 are
+// the launch and the first bytes' way.  What remains is instructions and the
+// ends: the first loads, x before them, the last row tiles.
 constexpr int kFewWarps = 8, kFewTok = 2, kFewStages = 3, kFewCtas = 2;
 constexpr int kFewRed = 2 * kFewWarps * kFewTok * 16 * 4;
 
-// The buffers, then a ring of pairs of blocks per warp, x by blocks and tokens
-// (whole blocks, zeros past C), the sums of x.
-template <int GPB, bool X8>
+// The buffers, then a ring of pairs of blocks per warp, x in fp16 by blocks and
+// tokens (whole blocks, zeros past C).
 int few_smem(const Int4Args& a, int nwarp) {
-  return kFewRed + nwarp * kFewStages * 2 * a.item + a.nblk * (a.ntok * 128 * (X8 ? 1 : 2) + GPB * kFewTok * 4);
+  return kFewRed + nwarp * kFewStages * 2 * a.item + a.nblk * a.ntok * 256;
 }
 
 template <int GPB, bool Z, bool X8>
 __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __grid_constant__ Int4Args a) {
-  constexpr int esz = X8 ? 1 : 2, STEPS = 8 / GPB, XB = 128 * esz;      // bytes of x in a block
+  constexpr int STEPS = 8 / GPB, XB = 256;                              // bytes of a token's x in a block
   constexpr int ITEM = Q2_INT4_BLOCK_BYTES + GPB * (Z ? 48 : 32), STAGE = 2 * ITEM;
   extern __shared__ __align__(16) unsigned char q2_int4_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
@@ -75,7 +71,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   float* red = reinterpret_cast<float*>(q2_int4_smem);      // [2][kFewWarps][kFewTok][16]
   const uint32_t ring = saddr(q2_int4_smem) + kFewRed + warp * (kFewStages * STAGE);
   unsigned char* xs = q2_int4_smem + kFewRed + nwarp * (kFewStages * STAGE) + b0 * (a.ntok * XB);   // this warp's x
-  float* sums = reinterpret_cast<float*>(xs + (a.nblk - b0) * (a.ntok * XB)) + b0 * (GPB * kFewTok);
 
   // the stream: pairs of blocks (the last of a row tile may be one block)
   int left = mine, fb = 0;                                  // row tiles to load; block of the row tile at `src`
@@ -105,65 +100,48 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   pdl_wait();                                               // x may come from the previous kernel
   pdl_trigger();
   // x in the order of the products' operands: a lane's words of two steps are
-  // consecutive (16 bytes of fp16, 8 of 8-bit integers)
-  for (int e = lane; e < nb * a.ntok * (XB / 16); e += 32) {
-    const int p = e % (XB / 16), kt = e / (XB / 16), k = a.ntok == 2 ? kt >> 1 : kt, t = kt - k * a.ntok;
-    const int c = (b0 + k) * 128 + p * (16 / esz);
-    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + ((size_t)t * a.C + c) * esz);
+  // consecutive.  8-bit x becomes fp16 here, once (in the loop below it would
+  // be as many instructions again as half of the weights').
+  constexpr int PIECES = X8 ? 8 : 16, COLS = 128 / PIECES;  // 16-byte loads of a block, columns of each
+  for (int e = lane; e < nb * a.ntok * PIECES; e += 32) {
+    const int p = e % PIECES, kt = e / PIECES, k = a.ntok == 2 ? kt >> 1 : kt, t = kt - k * a.ntok;
+    const int c = (b0 + k) * 128 + p * COLS;
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.x) + ((size_t)t * a.C + c) * (16 / COLS));
     const uint4 v = c < a.C ? *from : make_uint4(0, 0, 0, 0);
-    uint32_t* to = reinterpret_cast<uint32_t*>(xs + kt * XB);
-    if constexpr (X8) {                                     // columns 16p ..: step p
-      to += (p >> 1) * 8 + (p & 1);
-      to[0] = __byte_perm(v.x, v.z, 0x5410);
-      to[2] = __byte_perm(v.x, v.z, 0x7632);
-      to[4] = __byte_perm(v.y, v.w, 0x5410);
-      to[6] = __byte_perm(v.y, v.w, 0x7632);
-    } else {                                                // columns 8p ..: half p % 2 of step p / 2
-      to += (p >> 2) * 16 + (p & 3);
-      to[0] = v.x;
-      to[4] = v.y;
-      to[8] = v.z;
-      to[12] = v.w;
+    auto put = [&](int half, const uint4& u) {              // columns 8 half ..: half % 2 of step half / 2
+      uint32_t* to = reinterpret_cast<uint32_t*>(xs + kt * XB) + (half >> 2) * 16 + (half & 3);
+      to[0] = u.x;
+      to[4] = u.y;
+      to[8] = u.z;
+      to[12] = u.w;
+    };
+    if constexpr (X8) {
+      uint4 u;
+      int8x4(v.x, u.x, u.y);
+      int8x4(v.y, u.z, u.w);
+      put(2 * p, u);
+      int8x4(v.z, u.x, u.y);
+      int8x4(v.w, u.z, u.w);
+      put(2 * p + 1, u);
+    } else {
+      put(p, v);
     }
   }
   __syncwarp();
   // A lane's columns of one token (token g, of two: the other columns of the
   // products repeat them and are not stored).
-  const uint32_t xl = saddr(xs) + (g & (a.ntok - 1)) * XB + j * (8 * esz);
+  const uint32_t xl = saddr(xs) + (g & (a.ntok - 1)) * XB + j * 16;
   const int xblk = a.ntok * XB;
   auto xload = [&](uint32_t(&b)[16], uint32_t from) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if constexpr (X8) {
-        const uint2 v = lds64(from + r * 32);
-        int8x4(v.x, b[4 * r], b[4 * r + 1]);
-        int8x4(v.y, b[4 * r + 2], b[4 * r + 3]);
-      } else {
-        const uint4 v = lds128(from + r * 64);
-        b[4 * r] = v.x;
-        b[4 * r + 1] = v.y;
-        b[4 * r + 2] = v.z;
-        b[4 * r + 3] = v.w;
-      }
+      const uint4 v = lds128(from + r * 64);
+      b[4 * r] = v.x;
+      b[4 * r + 1] = v.y;
+      b[4 * r + 2] = v.z;
+      b[4 * r + 3] = v.w;
     }
   };
-  for (int k = 0; k < nb; ++k) {
-    uint32_t b[16];
-    xload(b, xl + k * xblk);
-    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-#pragma unroll
-    for (int q = 0; q < GPB; ++q) {
-      float c[4];
-#pragma unroll
-      for (int t = 0; t < STEPS; ++t) {
-        const int st = q * STEPS + t;
-        if (t == 0) mma_first(c, one, b[2 * st], b[2 * st + 1]);
-        else mma(c, one, b[2 * st], b[2 * st + 1]);
-      }
-      if (lane == 0) *reinterpret_cast<float2*>(sums + (k * GPB + q) * kFewTok) = make_float2(c[0], c[1]);
-    }
-  }
-  __syncwarp();
   const float xsc0 = X8 ? a.xs[0] : 1.f, xsc1 = X8 && a.ntok > 1 ? a.xs[1] : 1.f;
 
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // rows g and g + 8, tokens 0 and 1
@@ -171,7 +149,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
   auto use = [&](auto kc, uint32_t from, int blk) {
     constexpr int K = decltype(kc)::value;
     const uint32_t xat = xl + blk * xblk;
-    const float* sat = sums + blk * (GPB * kFewTok);
     uint32_t b[K][16];
     uint4 w[K][2];
     Sides<GPB> sd[K];
@@ -185,25 +162,25 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 #pragma unroll
     for (int q = 0; q < GPB; ++q) {
       float c[K][4];
+      Zeros z[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) z[k] = zeros_of(Z ? sd[k].z[q >> 1] >> (16 * (q & 1)) : 0x0808u);
 #pragma unroll
       for (int t = 0; t < STEPS; ++t) {
         const int st = q * STEPS + t;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const uint32_t v = word(w[k][st >> 2], st & 3), v8 = v >> 8;
-          const uint32_t A[4] = {v & 0x000f000fu, v & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u};
+          uint32_t A[4];
+          unpack_step(word(w[k][st >> 2], st & 3), z[k], A[0], A[1], A[2], A[3]);
           if (t == 0) mma_first(c[k], A, b[k][2 * st], b[k][2 * st + 1]);
           else mma(c[k], A, b[k][2 * st], b[k][2 * st + 1]);
         }
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const float2 X = *reinterpret_cast<const float2*>(sat + (k * GPB + q) * kFewTok);
         const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[k].s[q]));
-        const uint32_t zz = sd[k].z[q >> 1] >> (16 * (q & 1));
-        const float z0 = Z ? (float)(zz & 0xffu) : 8.f, z1 = Z ? (float)((zz >> 8) & 0xffu) : 8.f;
-        add_group(acc[0], sc.x, z0, make_float2(c[k][0], c[k][1]), X, 16777216.f);
-        add_group(acc[1], sc.y, z1, make_float2(c[k][2], c[k][3]), X, 1048576.f);
+        fma2(acc[0], make_float2(sc.x, sc.x), make_float2(c[k][0], c[k][1]));
+        fma2(acc[1], make_float2(sc.y, sc.y), make_float2(c[k][2], c[k][3]));
       }
     }
   };
@@ -243,20 +220,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 // group's x of all tokens (a token's row is padded so that the lanes that load
 // together fall on different banks) and each warp's own weights come through a
 // ring of shared-memory stages by asynchronous 16-byte copies.  A block's
-// operands are unpacked once and used for all tokens; two row tiles and the
-// product with ones (per 8 tokens) give three chains of products in flight.
+// operands are unpacked once and used for all tokens.
 // When the column range is split over CTAs, they form a cluster and add their
 // fp32 sums through distributed shared memory in rank order.
 //
 // What bounds it at 8 tokens is instructions and uneven SMs (240 CTAs, two on
-// some and one on others: an even spread would save 20%), 3.3 TB/s at
-// 5120 x 17408 (8-bit x, groups of 64: 14.4 us) and 3.6 at 24576 x 4096 (14.5
-// us); at 16 tokens the products (an instruction takes the tensor cores 2
-// cycles of an SM whatever its operands are worth, 12.5 us of the 21.3 at
-// 24576 x 4096) and, with two CTAs per SM, the latencies between them.  More than
-// 16 tokens would cost another product with ones and 48 accumulators more per
-// thread: they go to the kernel in q2_int4_tc.cu
-// (24576 x 4096 at 32 tokens 25.1 us, twice the 16-token time here 43).
+// some and one on others: an even spread would save 20%), 3.2 TB/s at
+// 5120 x 17408 (8-bit x, groups of 64: 15.0 us) and 3.7 at 24576 x 4096 (14.3
+// us); at 16 tokens (20.8 us at 24576 x 4096) the products and, with two CTAs
+// per SM, the latencies between them.  More than 16 tokens would cost 32
+// accumulators more per thread: they go to the kernel in q2_int4_tc.cu
+// (24576 x 4096 at 32 tokens 25.7 us, twice the 16-token time here 42).
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>
@@ -378,45 +352,35 @@ __global__ void __launch_bounds__(kManyWarps * 32, STAGES == 4 ? 2 : many_ctas<N
       w[m][1] = lds128(at + 512 + lane * 16);
       load_sides(sd[m], at, a.zeros, g);
     }
-    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
     uint32_t b[NT][16];
 #pragma unroll
     for (int t = 0; t < NT; ++t) xload(b[t], t);
 #pragma unroll
     for (int q = 0; q < GPB; ++q) {
-      float c[MT][NT][4], X[NT][4];
+      float c[MT][NT][4];
+      Zeros z[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) z[m] = zeros_of(sd[m].z[q >> 1] >> (16 * (q & 1)));
 #pragma unroll
       for (int k = q * STEPS; k < (q + 1) * STEPS; ++k) {
         uint32_t A[MT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t v = word(w[m][k >> 2], k & 3), v8 = v >> 8;
-          A[m][0] = v & 0x000f000fu;
-          A[m][1] = v & 0x00f000f0u;
-          A[m][2] = v8 & 0x000f000fu;
-          A[m][3] = v8 & 0x00f000f0u;
-        }
+        for (int m = 0; m < MT; ++m) unpack_step(word(w[m][k >> 2], k & 3), z[m], A[m][0], A[m][1], A[m][2], A[m][3]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (k == q * STEPS) mma_first(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
-          else mma(X[t], one, b[t][2 * k], b[t][2 * k + 1]);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (k == q * STEPS) mma_first(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
             else mma(c[m][t], A[m], b[t][2 * k], b[t][2 * k + 1]);
           }
-        }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&sd[m].s[q]));
-        const uint32_t zz = sd[m].z[q >> 1] >> (16 * (q & 1));
-        const float z0 = (float)(zz & 0xffu), z1 = (float)((zz >> 8) & 0xffu);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float2 x2 = make_float2(X[t][0], X[t][1]);
-          add_group(acc[m][t][0], sc.x, z0, make_float2(c[m][t][0], c[m][t][1]), x2, 16777216.f);
-          add_group(acc[m][t][1], sc.y, z1, make_float2(c[m][t][2], c[m][t][3]), x2, 1048576.f);
+          fma2(acc[m][t][0], make_float2(sc.x, sc.x), make_float2(c[m][t][0], c[m][t][1]));
+          fma2(acc[m][t][1], make_float2(sc.y, sc.y), make_float2(c[m][t][2], c[m][t][3]));
         }
       }
     }
@@ -481,7 +445,7 @@ __global__ void __launch_bounds__(kManyWarps * 32, STAGES == 4 ? 2 : many_ctas<N
 // ------------------------------------------------------- launch
 template <int GPB, bool X8>
 int launch_few(const Int4Args& a, int slots, void* stream) {
-  const int nwarp = a.nblk < kFewWarps ? a.nblk : kFewWarps, smem = few_smem<GPB, X8>(a, nwarp);
+  const int nwarp = a.nblk < kFewWarps ? a.nblk : kFewWarps, smem = few_smem(a, nwarp);
   const int grid = a.ntile < slots ? a.ntile : slots;
   return a.zeros ? launch_pdl(k_int4_few<GPB, true, X8>, a, grid, nwarp * 32, smem, stream)
                  : launch_pdl(k_int4_few<GPB, false, X8>, a, grid, nwarp * 32, smem, stream);
@@ -531,12 +495,14 @@ template <int GPB, bool X8>
 int launch_tokens(const Int4Args& a, void* stream) {
   if (a.ntok <= kFewTok) {
     // k_int4_few keeps x in shared memory and hands out whole row tiles: it is
-    // taken where x fits, unless the last of several rounds is mostly empty
-    // (5120 x 17408 at one token, 1.05 rounds: 14.2 us, 12.3 with k_int4_many;
-    // 6144 x 4096, 1.26 rounds: 4.9 and 5.4; 24576 x 4096, 5.05: 11.1 and 13.4).
-    const int slots = std::min(kFewCtas, kSmemPerSm / (few_smem<GPB, X8>(a, kFewWarps) + 1024)) * dev_info().sms;
-    const int rounds = slots ? (a.ntile + slots - 1) / slots : 0;
-    if (rounds == 1 || (slots && 5ll * a.ntile >= 3ll * rounds * slots)) return launch_few<GPB, X8>(a, slots, stream);
+    // taken where two CTAs fit an SM with it (5120 x 17408 at two tokens, one
+    // CTA: 16.0 us, 12.6 with k_int4_many), unless the last of several rounds is
+    // mostly empty (5120 x 17408 at one token, 1.05 rounds: 13.1 us, 12.4 with
+    // k_int4_many; 6144 x 4096, 1.26 rounds: 4.7 and 5.4; 24576 x 4096, 5.05: 11.0
+    // and 13.5).
+    const int slots = kFewCtas * dev_info().sms, rounds = (a.ntile + slots - 1) / slots;
+    const bool fits = kFewCtas * (few_smem(a, kFewWarps) + 1024) <= kSmemPerSm;
+    if (fits && (rounds == 1 || 5ll * a.ntile >= 3ll * rounds * slots)) return launch_few<GPB, X8>(a, slots, stream);
   }
   if (a.ntok <= 8) return launch_many<1, GPB, X8>(a, stream);
   if (a.ntok <= 16) return launch_many<2, GPB, X8>(a, stream);

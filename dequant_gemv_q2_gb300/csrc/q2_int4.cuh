@@ -115,6 +115,8 @@ __device__ __forceinline__ Zeros zeros_of(uint32_t zz) {
 // One step's q - z (four columns of rows g and g + 8) as an operand fragment:
 // a0 and a2 of row g, a1 and a3 of row g + 8.  The word holds, from its lowest
 // four bits up, columns 0, 0, 2, 2, 1, 1, 3, 3, rows g and g + 8 in turn.
+// (Integers in the mantissa of 1024: Kim, Henry, Fahim and Awadalla, "Who Says
+// Elephants Can't Run", 2022.)
 __device__ __forceinline__ void unpack_step(uint32_t v, const Zeros& z, uint32_t& a0, uint32_t& a1, uint32_t& a2,
                                             uint32_t& a3) {
   const uint32_t v8 = v >> 8;
@@ -148,13 +150,6 @@ __device__ __forceinline__ void int8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
 __device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
   uint64_t& cc = reinterpret_cast<uint64_t&>(c);
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-}
-
-// A group's sums of two tokens onto the row's: acc += s (2^e c - z X).
-__device__ __forceinline__ void add_group(float2& acc, float s, float z, float2 c, float2 X, float two_e) {
-  float2 t = make_float2(-z * X.x, -z * X.y);
-  fma2(t, c, make_float2(two_e, two_e));
-  fma2(acc, make_float2(s, s), t);
 }
 
 // The cluster's barriers, by converged warps.  The first: what each CTA has left

@@ -193,10 +193,8 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* weight_bytes_read_per_call);
  * x in shared memory (where the rows fill its rounds), up to 16 one on the
  * warps' tensor instructions, 17..64 one on the 5th-generation tensor cores,
  * each one launch whose K splits are summed in split order (matrices of up to
- * 128 columns: a launch per 16 tokens).  There q * x is exact; up to 16
- * tokens the zero point is taken off a group's fp32 sum, so a group's error
- * is that of an fp32 sum of s * (q + z) * |x|, from 17 tokens on that of
- * s * |q - z| * |x|.  An inf or NaN in a token's x makes that token's outputs
+ * 128 columns: a launch per 16 tokens).  There (q - z) * x is exact, and a
+ * group's error is that of an fp32 sum of s * |q - z| * |x|.  An inf or NaN in a token's x makes that token's outputs
  * NaN, of Q2_INT4 not finite (the IEEE result is non-finite for every row;
  * the fixed-point sums carry a sticky flag for it).  Launches use programmatic dependent launch: weights are
  * fetched before the previous kernel on the stream has finished; x, y and
