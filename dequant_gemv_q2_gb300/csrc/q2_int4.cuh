@@ -3,6 +3,7 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
+#include <vector>
 
 #include "q2_common.cuh"
 
@@ -173,22 +174,23 @@ __device__ __forceinline__ void cluster_meet() {
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
 // How many clusters of cs CTAs of a kernel the device runs at once (a cluster
-// lives in one GPC, so this is not SMs / cs), each asked for once.
+// lives in one GPC, so this is not SMs / cs), each asked for once: kernels that
+// share a table differ in their registers.
 class ClusterCounts {
   struct Known {
+    const void* fn;
     int dev, cs, smem, n;
   };
   std::mutex mu;
-  Known known[64];
-  int nknown = 0;
+  std::vector<Known> known;
 
  public:
   int get(const void* fn, int cs, int threads, int smem) {
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lk(mu);
-    for (int i = 0; i < nknown; ++i)
-      if (known[i].dev == dev && known[i].cs == cs && known[i].smem == smem) return known[i].n;
+    for (const Known& k : known)
+      if (k.fn == fn && k.dev == dev && k.cs == cs && k.smem == smem) return k.n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cs);
     cfg.blockDim = dim3(threads);
@@ -205,7 +207,9 @@ class ClusterCounts {
       (void)cudaGetLastError();
       return 1;
     }
-    if (nknown < 64) known[nknown++] = {dev, cs, smem, n};
+    try {
+      known.push_back({fn, dev, cs, smem, n});
+    } catch (...) {}                                // no memory: asked for again
     return n;
   }
 };
