@@ -173,11 +173,14 @@ def q2_pack_noweights(R: int, C: int) -> np.ndarray:
 
 def _stream_ptr(stream):
     """The cudaStream_t of a torch stream, or of the current one (asked for without making a stream object: 0.15
-    instead of 3.2 us per call on the GB300's host cores)."""
+    instead of 3.2 us per call on the GB300's host cores; by the public call where torch has no such functions)."""
     if stream is not None:
         return stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _check_tensor(where: str, name: str, t, dtype, shape, strides=None) -> None:
