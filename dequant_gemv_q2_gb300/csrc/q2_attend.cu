@@ -38,12 +38,13 @@
 // query heads to a key-value head (eight of 256 columns) are taken 16 (eight)
 // at a time, each reading the tokens again.
 //
-// 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 319 us
-// on the device, 6.7 TB/s, the rate of a copy; one of 131072: 88 us, 6.1; 16
+// 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 318 us
+// on the device, 6.8 TB/s, the rate of a copy; one of 131072: 89 us, 6.0; 16
 // of 1 to 4096 with 40 query heads 30 us, 4.5 (each CTA's start, its ends of
 // sequences and the joins are 9 of them); one of 777 tokens 7.0 us: the
 // lengths, the first pages' numbers, the first rows and the join behind one
-// another.
+// another.  Heads of 256 have one CTA per SM, whose threads spill 164 bytes at
+// 255 registers: 64 of 4096 tokens 336 us, 6.4 TB/s, 16 of 2048 53, 5.0.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -136,8 +137,9 @@ struct Walk {
 constexpr int kEnd = 2;
 
 // CTAs per SM: what registers and the rings of three stages leave room for, but
-// no more than three (64 sequences of 8192 tokens, heads of 64: 163 us; with two
-// CTAs of six stages 199, with four of three 169).
+// no more than three (64 sequences of 8192 tokens, heads of 64, pages of 64
+// stored head by head: 161 us; with two CTAs of six stages 199, with four of
+// three 169; stored token by token 182).
 template <int D>
 __host__ __device__ constexpr int att_ctas() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 
@@ -612,8 +614,8 @@ size_t part_bytes(int sms) {
 
 // Query heads of a unit.  Sixteen where a key-value head has more than eight
 // and the registers hold them, so that its tokens are read once for sixteen:
-// there lo has its own products (55 us instead of 89 for 8 sequences of 8192
-// tokens, 128 query and 8 key-value heads of 128).
+// there lo has its own products (52 to 56 us by the pages' order, instead of
+// 89, for 8 sequences of 8192 tokens, 128 query and 8 key-value heads of 128).
 int unit_heads(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
 
 // Shared checks of the head counts; hu: heads of units.

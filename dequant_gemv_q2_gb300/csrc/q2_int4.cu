@@ -46,9 +46,10 @@ namespace {
 // first threads add them in warp order: one barrier per row tile, no atomics.
 //
 // 24576 x 4096 at one token, groups of 128 with zero points: 11.3 us on the
-// device, 4.6 TB/s; two tokens 11.9; from 8-bit x, which becomes fp16 on its way
-// into shared memory, 11.3 (groups of 64).  4096 x 4096: 3.1 us, of which 2 are
-// the launch and the first bytes' way.  What remains is instructions and the
+// device, 4.6 TB/s (without zero points 10.9); two tokens 11.9; from 8-bit x,
+// which becomes fp16 on its way into shared memory, 11.2 (groups of 64).  4096 x
+// 4096: 3.1 us, of which 2 are the launch and the first bytes' way.  What remains
+// is instructions (2.2 of 4 issue slots per cycle under the profiler) and the
 // ends: the first loads, x before them, the last row tiles.
 constexpr int kFewWarps = 8, kFewTok = 2, kFewStages = 3, kFewCtas = 2;
 constexpr int kFewRed = 2 * kFewWarps * kFewTok * 16 * 4;
@@ -226,11 +227,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_int4_few(const __g
 //
 // What bounds it at 8 tokens is instructions and uneven SMs (240 CTAs, two on
 // some and one on others: an even spread would save 20%), 3.2 TB/s at
-// 5120 x 17408 (8-bit x, groups of 64: 15.0 us) and 3.7 at 24576 x 4096 (14.3
-// us); at 16 tokens (20.8 us at 24576 x 4096) the products and, with two CTAs
+// 5120 x 17408 (8-bit x, groups of 64: 14.9 us) and 3.7 at 24576 x 4096 (14.3
+// us); at 16 tokens (20.7 us at 24576 x 4096) the products and, with two CTAs
 // per SM, the latencies between them.  More than 16 tokens would cost 32
 // accumulators more per thread: they go to the kernel in q2_int4_tc.cu
-// (24576 x 4096 at 32 tokens 25.7 us, twice the 16-token time here 42).
+// (24576 x 4096 at 32 tokens 25.7 us, twice the 16-token time here 42).  In
+// groups of 32 the variants of three stages spill 4 to 16 bytes.
 constexpr int kManyWarps = 8, kManyRows = 128, kManyMax = 8;
 
 template <bool X8>

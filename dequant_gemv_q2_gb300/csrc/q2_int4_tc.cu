@@ -29,7 +29,7 @@
 // end in distributed shared memory, after one barrier of the cluster, and are
 // added in column order.
 //
-// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 37.2 us on the
+// 34816 x 5120 at 64 tokens, groups of 128 with zero points: 36.9 us on the
 // device, 2.6 TB/s, 0.61 PFLOP/s (a block of 128 x 128 every 900 cycles of an
 // SM).  What bounds it is not one unit: the decoders (about 800 cycles per
 // block, their 9 instructions per 8 weights being half of the issue slots
@@ -40,7 +40,13 @@
 // without x 2%; 12 or 16 decoder warps and deeper rings of weights or x gain
 // nothing.  What waits cost shows in the steps: a barrier's address that the
 // compiler cannot show to be uniform costs 200 cycles and more at each wait
-// (58 -> 42 us at 24576 x 4096 in groups of 32).
+// (58 -> 42 us at 24576 x 4096 in groups of 32, 39.0 now).  Matrices of few rows
+// and many columns also pay for whole tiles: a cluster gets whole tiles and has
+// 1, 2, 4 or 8 CTAs, so the longest run of 5120 x 17408 is 51 blocks where an
+// even share of its 40 tiles of 136 is 36 (32 tokens 26.5 us, 64 29.3), and that
+// of 34816 x 5120 80 of 72.  8-bit x is turned to fp16 by every CTA for every
+// tile: 5120 x 17408 in groups of 64 at 32 tokens 36.5 us, at 64 43.2; 34816 x
+// 5120 49.5 and 58.3.  That variant with groups of 32 spills 20 bytes.
 //
 // Every wait is bounded: one that runs out sets the error word
 // (q2_device_errors) and a flag on which the other roles give up (the issuing

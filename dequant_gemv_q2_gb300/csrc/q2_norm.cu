@@ -6,8 +6,9 @@
 //   r' = fp16(h),  y16 = fp16(y),  s = max|y| / 127,  y8 = rint(y / s),
 //
 // all in fp32 from the fp16 inputs; h, y and s are each rounded once.  The sum
-// of squares is a tree over the row's threads in a fixed order (one up to as
-// many rows as SMs and one beyond), wherever the row lies.
+// of squares is a tree over the row's threads in an order that follows from the
+// width, from whether all rows lie on 16-byte boundaries, and there, up to 4096
+// columns, from whether there are more rows than SMs; nothing else changes it.
 //
 // A row is read once and stays in registers between the sum, the maximum and
 // the stores, so the bytes of the inputs and outputs are all that moves.  Rows
@@ -16,7 +17,7 @@
 // with the next row's loads in flight during the reductions of the one before.
 //
 // 16384 rows of 4096 with residual and both outputs: 107 us on the device, 5.6
-// of the 6.7 TB/s that a copy reaches (one row per block and no row ahead:
+// of the 6.8 TB/s that a copy reaches (one row per block and no row ahead:
 // 164).  One row of 4096: 1.6 us, which is a launch, one trip to memory and
 // one block reduction; 64 rows of 5120 to 8 bits 2.3.
 #include <cuda_fp16.h>
@@ -93,9 +94,12 @@ __device__ __forceinline__ uint32_t pack4(const float* r) {
 // may begin anywhere: a piece is cut out of two 16-byte loads, and written
 // through shared memory in pieces of 16 bytes as they lie in global memory;
 // the ends of a row go element by element (4096 rows of 5125 columns with
-// residual 50 us, 91 with every element by itself; 16 rows of 3001, where
-// only the latency counts, 4.3 and 2.7).  A thread's columns, and with them
-// the order of the sums, do not depend on where a row begins.
+// residual 50 us, with both outputs 69.5; 91 to fp16 with every element by
+// itself; 16 rows of 3001, where only the latency counts, 3.6 and 2.7).  A
+// thread's columns, and with them the order of the sums, do not depend on where
+// such a row begins.  A block's threads spill 64 bytes at their 32 registers,
+// beyond 8192 columns 204 at 64; on 16-byte boundaries 144 there (2048 rows of
+// 17408 with residual 72 us, 4.0 TB/s), nothing up to 8192.
 template <int TPR, int CH, bool VEC>
 struct Row {
   int tid, nt, C;
@@ -345,7 +349,7 @@ int launch_norm(const NormArgs& a, void* stream) {
   if (!VEC) return launch_rows<0, 4, false, 1024>(a, grid(threads(4)), threads(4), stream);
   // Few rows: more threads, for the latency (1 or 64 rows of 4096: 1.71 us,
   // 1.78 with two pieces per thread); many: two pieces in flight each (600
-  // rows 3.1 us, 3.9 with one).
+  // rows with residual 3.2 us, 3.9 with one).
   const bool few = a.rows <= dev_info().sms;
   if (few && pieces <= 512) return launch_rows<0, 1, true, 512>(a, (int)a.rows, threads(1), stream);
   if (pieces <= 512) return launch_rows<0, 2, true, 256>(a, grid(threads(2)), threads(2), stream);
