@@ -190,14 +190,16 @@ int q2_bytes(const q2_handle* h, int ntok, size_t* weight_bytes_read_per_call);
  * it; each term then carries an absolute rounding error of at most
  * 2^-(F+1), about 2e-8 per 256-column slice for weights of magnitude
  * 0.05.  Q2_INT4 needs no workspace: 1 and 2 tokens take a kernel that keeps
- * x in shared memory (where the rows fill its rounds), up to 16 one on the
- * warps' tensor instructions, 17..64 one on the 5th-generation tensor cores,
- * each one launch whose K splits are summed in split order (matrices of up to
- * 128 columns: a launch per 16 tokens).  There (q - z) * x is exact, and a
- * group's error is that of an fp32 sum of s * |q - z| * |x|.  An inf or NaN in a token's x makes that token's outputs
- * NaN, of Q2_INT4 not finite (the IEEE result is non-finite for every row;
- * the fixed-point sums carry a sticky flag for it).  Launches use programmatic dependent launch: weights are
- * fetched before the previous kernel on the stream has finished; x, y and
+ * x in shared memory (where that leaves room for two CTAs per SM and the rows
+ * fill its rounds), up to 16 one on the warps' tensor instructions, 17..64 one
+ * on the 5th-generation tensor cores, each one launch whose K splits are
+ * summed in split order (matrices of up to 128 columns: a launch per 16
+ * tokens).  There (q - z) * x is exact, and a group's error is that of an fp32
+ * sum of s * |q - z| * |x|.  An inf or NaN in a token's x makes that token's
+ * outputs NaN, of Q2_INT4 not finite (the IEEE result is non-finite for every
+ * row; the fixed-point sums carry a sticky flag for it).  Launches use
+ * programmatic dependent launch: weights are fetched before the previous
+ * kernel on the stream has finished; x, y and
  * the workspace are touched only after it has.  Returns Q2_ECUDA if a
  * launch fails. */
 int q2_gemv(q2_fmt fmt, const q2_handle* h, const void* x, void* y, int ntok, q2_stream stream);
