@@ -20,9 +20,15 @@ FMT_NAMES = {FP16: "fp16", BPDQ: "bpdq", TRELLIS: "trellis", LEECH: "leech", NOW
 EINVAL, ESHAPE, EALIGN, EWORKSPACE = -1, -2, -3, -7
 ERR_LENGTH, ERR_PAGE = 0x100, 0x200     # bits of device_errors()
 MAX_NTOK = 64
+BLOCK = 64                              # tokens of a block that has bounds and is selected as one
 INV_SQRT8_F32 = float(np.float32(1.0 / np.sqrt(8.0)))
 
 _lib = None
+
+_vp, _ll, _i32 = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int
+_APPEND = [_vp, _vp, _vp, _ll, _vp, _ll, _i32, _vp, _ll, _vp, _ll, _vp, _vp, _i32, _i32, _vp, _vp]
+_SELECT = [_vp, _vp, _vp, _ll, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]
+_READ = [_vp, _vp, _ll, _vp, _ll, _vp, _vp, _i32, _i32, _vp]
 
 
 class Q2Error(RuntimeError):
@@ -65,6 +71,14 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "q2_attend_workspace_bytes": [i32, i32, i32, i32, psz],
         "q2_attend": [vp, vp, ctypes.c_longlong, vp, vp, ctypes.c_longlong, vp, i32, i32, ctypes.c_float, vp,
                       ctypes.c_longlong, vp, sz, vp],
+        "q2_attend_blocks": [vp, vp, ctypes.c_longlong, vp, i32, i32, vp, i32, ctypes.c_float, vp, ctypes.c_longlong, vp, sz, vp],
+        "q2_attend4": [vp, vp, ctypes.c_longlong, vp, i32, i32, vp, i32, ctypes.c_float, vp, ctypes.c_longlong, vp, sz, vp],
+        "q2_select": _SELECT,
+        "q2_select4": _SELECT,
+        "q2_append": _APPEND,
+        "q2_append4": _APPEND,
+        "q2_read": _READ,
+        "q2_read4": _READ,
         "q2_decode_bytes": [vp, psz],
         "q2_decode": [vp, vp, vp],
         "q2_gemv_chain": [i32, vp, vp, vp, vp, i32, i32, vp],
@@ -89,7 +103,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
 EXPORTS = ["q2_pack_fp16", "q2_pack_bpdq", "q2_pack_trellis", "q2_pack_leech", "q2_pack_int4", "q2_pack_noweights",
            "q2_bind", "q2_unbind", "q2_workspace_bytes", "q2_set_workspace", "q2_info", "q2_bytes",
            "q2_gemv", "q2_gemv_chain", "q2_gemv_x8", "q2_rmsnorm",
-           "q2_attend", "q2_attend_workspace_bytes", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
+           "q2_attend", "q2_attend_workspace_bytes", "q2_append", "q2_append4", "q2_read", "q2_read4",
+           "q2_attend4", "q2_attend_blocks", "q2_select", "q2_select4", "q2_decode_bytes", "q2_decode", "q2_strerror", "q2_gemv_bpdq_noalloc",
            "q2_device_errors", "q2_debug_wait_limit", "q2_rotate", "q2_rotate_split"]
 
 
@@ -508,24 +523,204 @@ class _KV(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int)]
 
 
-def _rows(name: str, t, shape) -> int:
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+def _rows(name: str, t, shape, where: str = "q2_attend") -> int:
     """The leading dimension of fp16 rows [batch][heads][dim], each sequence's contiguous."""
     import torch
     stride = t.stride()
     if not (t.dtype is torch.float16 and t.is_cuda and t.shape == shape and stride[1] == shape[2] and stride[2] == 1):
-        _check_tensor("q2_attend", name, t, torch.float16, shape, (t.stride(0), shape[2], 1))
+        _check_tensor(where, name, t, torch.float16, shape, (t.stride(0) if t.dim() else 1, shape[2], 1))
     return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-class PagedKV:
+class Rope:
+    """The angles of positions that ``append`` turns queries and keys by.
+
+    ``table``: fp32 [positions][rot / 2][2] on the GPU, cos and sin (kept, not copied).  Pair i is columns i and
+    i + rot / 2 of a head, or 2i and 2i + 1 if ``interleaved``; columns from rot on are not turned.
+    """
+
+    def __init__(self, table, interleaved: bool = False):
+        import torch
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise Q2Error(ESHAPE, f"Rope: table has shape {tuple(table.shape)}, not [positions][rot / 2][2]")
+        _check_tensor("Rope", "table", table, torch.float32, table.shape)
+        self.table, self.interleaved = table, bool(interleaved)
+        self._rope = _Rope(table.data_ptr(), table.shape[0], 2 * table.shape[1], int(self.interleaved))
+        self._ref = ctypes.byref(self._rope)
+
+    @classmethod
+    def of(cls, rot: int, positions: int, base: float = 10000.0, interleaved: bool = False, device="cuda"):
+        """Pair i turns by base ** (-2 i / rot) per position (angles, cos and sin made in 64 bits)."""
+        import torch
+        turn = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+        angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * turn
+        return cls(torch.stack([angle.cos(), angle.sin()], dim=-1).float(), interleaved)
+
+
+class _Cache:
+    """What the caches in fp16 and in 4 bits share: tokens in (``append``) and out (``read``)."""
+
+    def _describe(self, pages: int, page: int, bounds, append, read, select) -> None:
+        import torch
+        self.batch = self.table.shape[0]
+        self.scale = self.dim ** -0.5
+        self._qshape = torch.Size((self.batch, self.q_heads, self.dim))
+        self._f16, self._i32, self._append, self._read, self._select = torch.float16, torch.int32, append, read, select
+        self.bounds, self._bounds = bounds, None
+        if bounds is not None:
+            if page % BLOCK and BLOCK % page:
+                raise Q2Error(ESHAPE, f"{self._name}: bounds with pages of {page} tokens, neither a multiple nor a divisor of {BLOCK}")
+            _check_tensor(self._name, "bounds", bounds, torch.float16, (pages, -(-page // BLOCK), self.kv_heads, 2, self.dim))
+            self._bounds = bounds.data_ptr()
+
+    def _workspace(self, workspace, bytes_of) -> None:
+        n = ctypes.c_size_t(0)
+        _check(bytes_of(self.batch, self.q_heads, self.kv_heads, self.dim, ctypes.byref(n)), "q2_attend_workspace_bytes")
+        if workspace is None:
+            workspace = _zero_workspace(n.value, self.k.device)
+        size = _workspace_bytes(self._name, workspace)
+        if size < n.value:
+            raise Q2Error(EWORKSPACE, f"{self._name}: workspace of {size} bytes, {n.value} needed")
+        self.ws, self._ws, self._ws_bytes = workspace, workspace.data_ptr(), size
+
+    def _tokens(self, where: str, lens, starts):
+        """The addresses of starts and lens."""
+        if not (lens.dtype is self._i32 and lens.is_cuda and lens.shape == (self.batch,) and lens.is_contiguous()):
+            _check_tensor(where, "lens", lens, self._i32, (self.batch,))
+        if starts is None:
+            return None, lens.data_ptr()
+        if not (starts.dtype is self._i32 and starts.is_cuda and starts.shape == (self.batch + 1,) and starts.is_contiguous()):
+            _check_tensor(where, "starts", starts, self._i32, (self.batch + 1,))
+        return starts.data_ptr(), lens.data_ptr()
+
+    def append(self, k, v, lens, starts=None, q=None, q_out=None, rope=None, stream=None):
+        """Store the new tokens' keys and values, keys and queries turned by their positions' angles (asynchronous).
+
+        ``k``, ``v`` fp16 [ntok][kv_heads][dim], ``q`` [ntok][q_heads][dim] (any token stride: slices of a projection's
+        output): rows starts[b] .. starts[b + 1] - 1 are the last tokens of sequence b, which has lens[b] with them;
+        without ``starts`` (int32 [batch + 1]) one token each.  ``q_out``: the turned queries, q itself if None.
+        ``rope``: a ``Rope``, or None to turn nothing.  Keeps up ``bounds`` where the cache has them.  Returns ``q_out``.
+        """
+        ntok, f16 = k.shape[0], self._f16
+        if starts is None and ntok != self.batch:
+            raise Q2Error(ESHAPE, f"q2_append: {ntok} tokens for {self.batch} sequences, and no starts")
+        st, ln = self._tokens("q2_append", lens, starts)
+        shape = (ntok, self.kv_heads, self.dim)
+        ldk, ldv = _rows("k", k, shape, "q2_append"), _rows("v", v, shape, "q2_append")
+        qp = qo = None
+        ldq = ldo = 0
+        if q is not None:
+            shape = (ntok, self.q_heads, self.dim)
+            ldq = ldo = _rows("q", q, shape, "q2_append")
+            qp = qo = q.data_ptr()
+            if q_out is None:
+                q_out = q
+            elif q_out is not q:
+                ldo, qo = _rows("q_out", q_out, shape, "q2_append"), q_out.data_ptr()
+        elif q_out is not None:
+            raise Q2Error(EINVAL, "q2_append: q_out without q")
+        st = self._append(self._ref, self._bounds, qp, ldq, qo, ldo, self.q_heads, k.data_ptr(), ldk, v.data_ptr(), ldv, st, ln,
+                          self.batch, ntok, None if rope is None else rope._ref, _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_append")
+        return q_out
+
+    def read(self, lens, starts=None, k_out=None, v_out=None, ntok=None, stream=None):
+        """The last tokens of every sequence as fp16 rows, keys and values (asynchronous).
+
+        Rows starts[b] .. starts[b + 1] - 1 become the last tokens of sequence b (as for ``append``); running sums of
+        all lengths give whole sequences.  ``k_out``, ``v_out`` [ntok][kv_heads][dim] (any token stride): made here,
+        with ``ntok`` rows of zeros, if both are None.  Returns (k_out, v_out).
+        """
+        st, ln = self._tokens("q2_read", lens, starts)
+        if k_out is None and v_out is None:
+            import torch
+            ntok = self.batch if starts is None and ntok is None else ntok
+            if ntok is None:
+                raise Q2Error(EINVAL, "q2_read: starts without k_out, v_out or ntok")
+            k_out, v_out = (_new(torch.zeros, (int(ntok), self.kv_heads, self.dim), self._f16, self.k.device, stream) for _ in range(2))
+        rows = (k_out if k_out is not None else v_out).shape[0]
+        if (ntok is not None and ntok != rows) or (starts is None and rows != self.batch):
+            raise Q2Error(ESHAPE, f"q2_read: outputs of {rows} rows")
+        shape = (rows, self.kv_heads, self.dim)
+        ldk, kp = (0, None) if k_out is None else (_rows("k_out", k_out, shape, "q2_read"), k_out.data_ptr())
+        ldv, vp = (0, None) if v_out is None else (_rows("v_out", v_out, shape, "q2_read"), v_out.data_ptr())
+        st = self._read(self._ref, kp, ldk, vp, ldv, st, ln, self.batch, rows, _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_read")
+        return k_out, v_out
+
+
+    def select(self, q, lens, blocks: int, first: int = 0, last: int = 1, out=None, stream=None):
+        """The ``blocks`` blocks of 64 tokens whose bounds promise the most to each key-value head's queries.
+
+        int32 [batch][kv_heads][blocks], ascending, -1 behind the last; the first ``first`` and the last ``last`` blocks of
+        a sequence are always among them.  q [batch][q_heads][dim] may have any batch stride (asynchronous).
+        """
+        if self._bounds is None:
+            raise Q2Error(EINVAL, f"q2_select: {self._name} without bounds")
+        shape = (self.batch, self.kv_heads, int(blocks))
+        if out is None:
+            import torch
+            if blocks < 1:
+                raise Q2Error(ESHAPE, f"q2_select: {blocks} blocks")
+            out = _new(torch.empty, shape, self._i32, q.device, stream)
+        else:
+            _check_tensor("q2_select", "out", out, self._i32, shape)
+        ldq = _rows("q", q, self._qshape, "q2_select")
+        _, ln = self._tokens("q2_select", lens, None)
+        st = self._select(self._ref, self._bounds, q.data_ptr(), ldq, ln, self.batch, self.q_heads, shape[2], int(first), int(last),
+                          out.data_ptr(), _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_select")
+        return out
+
+    def _attend_blocks(self, q, lens, blocks, scale, out, stream):
+        f16, shape = self._f16, self._qshape
+        # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
+        if out is None:
+            import torch
+            out = _new(torch.empty, shape, f16, q.device, stream)
+        ldq = ldo = self.q_heads * self.dim
+        if not (q.dtype is f16 and q.is_cuda and q.shape == shape and q.is_contiguous()):
+            ldq = _rows("q", q, shape)
+        if not (out.dtype is f16 and out.is_cuda and out.shape == shape and out.is_contiguous()):
+            ldo = _rows("out", out, shape)
+        if not (lens.dtype is self._i32 and lens.is_cuda and lens.shape == shape[:1] and lens.is_contiguous()):
+            _check_tensor("q2_attend", "lens", lens, self._i32, shape[:1])
+        sel, n = None, 0
+        if blocks is not None:
+            n = blocks.shape[2] if blocks.dim() == 3 else 0
+            if not (blocks.dtype is self._i32 and blocks.is_cuda and blocks.shape == (self.batch, self.kv_heads, n)
+                    and blocks.is_contiguous()):
+                _check_tensor("q2_attend", "blocks", blocks, self._i32, (self.batch, self.kv_heads, n))
+            if n < 1:
+                raise Q2Error(ESHAPE, f"q2_attend: blocks has shape {tuple(blocks.shape)}")
+            sel = blocks.data_ptr()
+        st = self._blocks(self._ref, q.data_ptr(), ldq, lens.data_ptr(), self.batch, self.q_heads, sel, n,
+                          self.scale if scale is None else scale, out.data_ptr(), ldo, self._ws, self._ws_bytes, _stream_ptr(stream))
+        if st:
+            raise Q2Error(st, "q2_attend")
+        return out
+
+
+class PagedKV(_Cache):
     """A paged key-value cache and attention of one new token per sequence over it (``q2_attend``).
 
     ``k``, ``v``: fp16 pools seen as [pages][page_size][kv_heads][dim], in any order of storage (dim contiguous; both
     alike).  ``table``: int32 [batch][max_pages] page numbers on the same GPU.  The tensors stay the caller's: pages,
     table and lengths may be changed between calls.  ``workspace``: uint8, zero when first used (made here if None).
+    ``bounds``: fp16 [pages][ceil(page_size / 64)][kv_heads][2][dim], the least and greatest keys of blocks of 64
+    tokens, which ``append`` keeps up.
     """
 
-    def __init__(self, k, v, table, q_heads: int, workspace=None):
+    _name = "PagedKV"
+
+    def __init__(self, k, v, table, q_heads: int, workspace=None, bounds=None):
         import torch
         if k.dim() != 4 or table.dim() != 2:
             raise Q2Error(ESHAPE, "PagedKV: k is not [pages][page_size][kv_heads][dim], or table not [batch][max_pages]")
@@ -538,31 +733,27 @@ class PagedKV:
         _check_tensor("PagedKV", "table", table, torch.int32, table.shape, (table.stride(0), 1))
         self.k, self.v, self.table, self.q_heads = k, v, table, int(q_heads)
         pages, page, self.kv_heads, self.dim = k.shape
-        self.batch = table.shape[0]
-        self.scale = self.dim ** -0.5
-        self._qshape = torch.Size((self.batch, self.q_heads, self.dim))
+        self._describe(pages, page, bounds, load().q2_append, load().q2_read, load().q2_select)
+        self._fn, self._blocks = load().q2_attend, load().q2_attend_blocks
         self._kvshape = torch.Size((self.batch, self.kv_heads, self.dim))
-        self._fn, self._f16, self._i32 = load().q2_attend, torch.float16, torch.int32
         self._kv = _KV(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), pages, page, self.kv_heads,
                        self.dim, table.data_ptr(), table.stride(0) if self.batch > 1 else table.shape[1], table.shape[1])
         self._ref = ctypes.byref(self._kv)
-        n = ctypes.c_size_t(0)
-        _check(load().q2_attend_workspace_bytes(self.batch, self.q_heads, self.kv_heads, self.dim, ctypes.byref(n)),
-               "q2_attend_workspace_bytes")
-        if workspace is None:
-            workspace = _zero_workspace(n.value, k.device)
-        size = _workspace_bytes("PagedKV", workspace)
-        if size < n.value:
-            raise Q2Error(EWORKSPACE, f"PagedKV: workspace of {size} bytes, {n.value} needed")
-        self.ws, self._ws, self._ws_bytes = workspace, workspace.data_ptr(), size
+        self._workspace(workspace, load().q2_attend_workspace_bytes)
 
-    def attend(self, q, lens, new_k=None, new_v=None, scale=None, out=None, stream=None):
+    def attend(self, q, lens, new_k=None, new_v=None, scale=None, out=None, stream=None, blocks=None):
         """Attention of q [batch][q_heads][dim] over the first lens[b] (int32) tokens of each sequence.
 
         ``new_k``, ``new_v`` [batch][kv_heads][dim]: the new token's, counted by ``lens``; they are stored as token
         lens[b] - 1.  q, new_k, new_v and ``out`` may have any batch stride (slices of a projection's output).
-        ``scale``: dim ** -0.5 if None.  Returns ``out`` (asynchronous).
+        ``scale``: dim ** -0.5 if None.  ``blocks``: what ``select`` returns, or any int32 [batch][kv_heads][n]: only the
+        tokens of these blocks of 64 (without new_k and new_v: ``append`` stores the new token before).  Returns ``out``
+        (asynchronous).
         """
+        if blocks is not None:
+            if new_k is not None or new_v is not None:
+                raise Q2Error(EINVAL, "q2_attend: blocks go without new_k and new_v")
+            return self._attend_blocks(q, lens, blocks, scale, out, stream)
         f16, shape = self._f16, self._qshape
         # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
         if out is None:
@@ -592,3 +783,69 @@ class PagedKV:
         if st:
             raise Q2Error(st, "q2_attend")
         return out
+
+
+class _KV4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("ks", ctypes.c_void_p),
+                ("vs", ctypes.c_void_p), ("s_page_stride", ctypes.c_longlong), ("s_token_stride", ctypes.c_longlong),
+                ("s_head_stride", ctypes.c_longlong), ("npages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("group", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int)]
+
+
+class PagedKV4(_Cache):
+    """A paged key-value cache in 4 bits and attention of one new token per sequence over it (``q2_attend4``).
+
+    ``k``, ``v``: uint8 pools of codes seen as [pages][page_size][kv_heads][dim / 2] (column 2j in the low four bits of
+    byte j), ``ks``, ``vs``: fp16 pools of steps and offsets [pages][page_size][kv_heads][dim / group][2], groups of 32
+    or 64 columns; a value is offset + step * code.  Any order of storage with a head's bytes (pairs) contiguous, k and v
+    alike, ks and vs alike; head by head ([pages][kv_heads][page_size][..], transposed) reads fastest.  ``append`` fills
+    the cache.  ``table``, ``workspace`` and ``bounds`` are as for ``PagedKV``.
+    """
+
+    _name = "PagedKV4"
+
+    def __init__(self, k, ks, v, vs, table, q_heads: int, workspace=None, bounds=None):
+        import torch
+        if k.dim() != 4 or ks.dim() != 5 or table.dim() != 2 or 0 in ks.shape[2:4]:
+            raise Q2Error(ESHAPE, "PagedKV4: k is not [pages][page_size][kv_heads][dim / 2], ks not "
+                          "[pages][page_size][kv_heads][dim / group][2], or table not [batch][max_pages]")
+        pages, page, self.kv_heads, half = k.shape
+        self.dim, groups = 2 * half, ks.shape[3]
+        for name, t, dtype, like, tail in (("k", k, torch.uint8, k, (1,)), ("v", v, torch.uint8, k, (1,)),
+                                           ("ks", ks, torch.float16, ks, (2, 1)), ("vs", vs, torch.float16, ks, (2, 1))):
+            shape = k.shape if like is k else (pages, page, self.kv_heads, groups, 2)
+            _check_tensor("PagedKV4", name, t, dtype, shape, like.stride()[:3] + tail)
+            if t.stride() != like.stride():
+                raise Q2Error(ESHAPE, f"PagedKV4: {name} has strides {t.stride()}, not {like.stride()}")
+        if any(s % 2 for s in ks.stride()[:3]):
+            raise Q2Error(EALIGN, f"PagedKV4: ks has strides {ks.stride()}")
+        _check_tensor("PagedKV4", "table", table, torch.int32, table.shape, (table.stride(0), 1))
+        self.k, self.ks, self.v, self.vs, self.table, self.q_heads = k, ks, v, vs, table, int(q_heads)
+        self._describe(pages, page, bounds, load().q2_append4, load().q2_read4, load().q2_select4)
+        self._blocks = load().q2_attend4
+        self._kv = _KV4(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), ks.data_ptr(), vs.data_ptr(),
+                        ks.stride(0) // 2, ks.stride(1) // 2, ks.stride(2) // 2, pages, page, self.kv_heads, self.dim,
+                        self.dim // groups if self.dim % groups == 0 else 0, table.data_ptr(),
+                        table.stride(0) if self.batch > 1 else table.shape[1], table.shape[1])
+        self._ref = ctypes.byref(self._kv)
+        self._workspace(workspace, load().q2_attend_workspace_bytes)
+
+    def attend(self, q, lens, scale=None, out=None, blocks=None, stream=None):
+        """Attention of q [batch][q_heads][dim] over the first lens[b] (int32) tokens of each sequence, or over selected blocks.
+
+        q and ``out`` may have any batch stride; ``scale``: dim ** -0.5 if None; ``blocks``: what ``select`` returns, or any
+        int32 [batch][kv_heads][n].  Returns ``out`` (asynchronous).
+        """
+        return self._attend_blocks(q, lens, blocks, scale, out, stream)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, dim: int, group: int, table, q_heads: int, bounds: bool = False):
+        """A cache whose pools are made here, stored head by head, without anything in them."""
+        import torch
+        new = lambda tail, dtype: torch.zeros((pages, kv_heads, page_size) + tail, dtype=dtype, device=table.device).transpose(1, 2)  # noqa: E731
+        k, v = (new((dim // 2,), torch.uint8) for _ in range(2))
+        ks, vs = (new((dim // group, 2), torch.float16) for _ in range(2))
+        kept = torch.zeros((pages, -(-page_size // BLOCK), kv_heads, 2, dim), dtype=torch.float16, device=table.device)
+        return cls(k, ks, v, vs, table, q_heads, bounds=kept if bounds else None)

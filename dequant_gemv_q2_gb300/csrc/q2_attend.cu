@@ -45,71 +45,26 @@
 // lengths, the first pages' numbers, the first rows and the join behind one
 // another.  Heads of 256 have one CTA per SM, whose threads spill 164 bytes at
 // 255 registers: 64 of 4096 tokens 336 us, 6.4 TB/s, 16 of 2048 53, 5.0.
-#include <cuda_fp16.h>
-
-#include <algorithm>
-
-#include "q2_common.cuh"
+#include "q2_attend.cuh"
 
 namespace q2 {
 namespace {
 
 __device__ unsigned int q2_attend_error;
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16, kUnit = kTile * kWarps;   // tokens of a warp's tile, of a unit
-constexpr int kMostHeads = 16;                      // query heads of a unit at most
-
-struct AttendArgs {
+struct AttendArgs : UnitArgs {
   __half* k;
   __half* v;
   long long page_stride, token_stride, head_stride;
   const int* table;
   long long table_stride;
-  const int* lens;
-  const __half* q;
   const __half* nk;           // new keys and values, or null
   const __half* nv;
-  __half* o;
-  long long ldq, ldn, ldo;
-  unsigned int* count;        // [batch][units' heads] arrivals, zero between calls
-  float* part;                // [2 * CTAs][H][D] numerators, H the query heads of a unit
-  float2* ml;                 // [2 * CTAs][H] maximum, denominator
-  int batch, npages, page, cap;   // cap: tokens that a table row can hold
-  int hu, nht, group;         // heads of units = kv_heads * nht; query heads of a key-value head
-  uint32_t page_mul, page_sh; // t / page = (high half of t * page_mul, + t) >> page_sh, t < 2^31
+  long long ldn;
+  int npages, page;
+  uint32_t page_mul, page_sh; // of page_of()
   int aligned;                // page % 16 == 0: a tile lies in one page
-  float sc2;                  // scale * log2(e)
 };
-
-// Division by an invariant with a multiplication (Granlund and Montgomery,
-// "Division by Invariant Integers using Multiplication", 1994).
-__device__ __forceinline__ int page_of(const AttendArgs& a, int t) {
-  return (int)((__umulhi((uint32_t)t, a.page_mul) + (uint32_t)t) >> a.page_sh);
-}
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
-}
-
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
-}
-
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // 2^15 p0 and 2^15 p1 (0 <= p <= 1) as pairs of fp16 numbers whose sums they
 // are, to 2^-20 of each or half of fp16's smallest, 2^-40 of the largest p.
@@ -125,23 +80,12 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// A place in the order of units.
-struct Walk {
-  int b, h, chunk, nch, len;
-};
-
-// What the end of a (sequence, head) costs a CTA, in units: the shares are cut
-// by units plus this, so that a CTA with many short sequences gets fewer units
-// (16 sequences of 1 to 4096 tokens, 40 query heads of 128: 31.6 us; 34.2 with
-// 0, 31.9 with 4).
-constexpr int kEnd = 2;
-
 // CTAs per SM: what registers and the rings of three stages leave room for, but
 // no more than three (64 sequences of 8192 tokens, heads of 64, pages of 64
 // stored head by head: 161 us; with two CTAs of six stages 199, with four of
 // three 169; stored token by token 182).
 template <int D>
-__host__ __device__ constexpr int att_ctas() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
+__host__ __device__ constexpr int ctas_of() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 
 template <int D, int H>
 struct Shape {
@@ -154,19 +98,9 @@ struct Shape {
   static int smem(int batch) { return fixed + 4 * (2 * batch + 1); }
 };
 
-constexpr int kJoin = 8;                            // parts whose loads are in flight together in a join
-
-// Counts a part in; before it what this CTA wrote becomes visible, and behind
-// it what the parts counted before wrote.
-__device__ __forceinline__ unsigned count_part(unsigned* count) {
-  unsigned before;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
-  return before;
-}
-
-// H: query heads of a unit, 8 or 16 (rows of the products)
-template <int D, int H>
-__global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid_constant__ AttendArgs a) {
+// H: query heads of a unit, 8 or 16 (rows of the products); SP: of selected blocks, see q2_attend_blocks
+template <int D, int H, bool SP>
+__global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_constant__ AttendArgs a) {
   using S = Shape<D, H>;
   constexpr int RH = H / 8;                         // rows g, g + 8 of a lane that are heads
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
@@ -180,89 +114,11 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
 
   pdl_wait();                                       // everything may come from the previous kernel
   pdl_trigger();
-  if (warp == 0) {                                  // the units before each sequence
-    int carry = 0, longest = 0, used = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int b = b0 + lane;
-      int len = b < a.batch ? a.lens[b] : 0;
-      if (len < 0 || len > a.cap) len = 0;
-      if (b < a.batch) lens[b] = len;
-      longest = max(longest, (len + kUnit - 1) / kUnit);
-      used += __popc(__ballot_sync(0xffffffffu, len > 0));
-      int v = len ? ((len + kUnit - 1) / kUnit + kEnd) * a.hu : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (b < a.batch) pre[b + 1] = carry + v;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) {
-      pre[0] = 0;
-      // How many CTAs.  Each part of a (sequence, head) costs its join about a
-      // quarter of what a unit costs its CTA, so n units are best cut into
-      // about 2 sqrt(n) parts; with few (sequence, head)s, a multiple of their
-      // number, so that sequences of one length are cut at their heads.
-      const int heads = used * a.hu, parts = max(1, (int)(2.f * sqrtf((float)longest)));
-      *nowed = heads * 4 > (int)gridDim.x ? (int)gridDim.x : heads * min(parts, (int)gridDim.x / max(heads, 1));
-    }
-  }
-  // sequences without a token give zeros, lengths that the table cannot hold NaN
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-    const int len = a.lens[b];
-    if (len > 0 && len <= a.cap) continue;
-    if (len != 0 && threadIdx.x == 0) atomicOr(&q2_attend_error, Q2_ERR_LENGTH);
-    const int n = a.hu / a.nht * a.group * D;
-    for (int e = threadIdx.x; e < n; e += kThreads)
-      a.o[b * a.ldo + e] = len ? __ushort_as_half(0x7e00) : __ushort_as_half(0);
-  }
-  __syncthreads();
-    // The order of units: each (sequence, head) has its units and kEnd places
-  // without one.  This CTA takes the units at places u0 .. u1 - 1.
-  const int total = pre[a.batch], ncta = min(*nowed, total);
-  if ((int)blockIdx.x >= ncta) return;
-  const int each = total / ncta, over = total - each * ncta;
-  auto first_of = [&](int cta) { return each * cta + over * cta / ncta; };   // total * cta / ncta in 32 bits
-  int u0 = first_of(blockIdx.x);
-  const int u1 = first_of(blockIdx.x + 1);
-
-  Walk c;                                           // the unit in use
-  {
-    int lo = 0, hi = a.batch - 1;                   // the sequence b with pre[b] <= u0 < pre[b + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid + 1] <= u0) lo = mid + 1;
-      else hi = mid;
-    }
-    c.b = lo;
-    c.len = lens[lo];
-    c.nch = (c.len + kUnit - 1) / kUnit;
-    const int r = u0 - pre[lo];
-    c.h = r / (c.nch + kEnd);
-    c.chunk = r - c.h * (c.nch + kEnd);
-  }
-  // to the next unit; how many places further it is
-  auto advance = [&](Walk& w) {
-    if (++w.chunk < w.nch) return 1;
-    const int skipped = w.nch + kEnd - w.chunk;
-    w.chunk = 0;
-    if (++w.h == a.hu) {
-      w.h = 0;
-      do ++w.b;
-      while (w.b < a.batch && pre[w.b + 1] == pre[w.b]);
-      if (w.b < a.batch) {
-        w.len = lens[w.b];
-        w.nch = (w.len + kUnit - 1) / kUnit;
-      }
-    }
-    return 1 + skipped;
-  };
-  if (c.chunk >= c.nch) {                           // the share begins behind the last unit of a (sequence, head)
-    --c.chunk;
-    u0 += advance(c) - 1;
-  }
+  const Share sh = share_out<D, SP>(a, nowed, pre, lens, &q2_attend_error);
+  int u0 = sh.u0;
+  const int u1 = sh.u1;
+  if (u0 >= u1) return;                             // no share
+  Walk c = walk_from<SP>(a, pre, lens, u0);         // the unit in use
   if (u0 >= u1) return;
 
   // ---- the warp's loads, STAGES - 1 units ahead of their use
@@ -273,16 +129,20 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   const int piece = lane % CPR, row0 = lane / CPR;
   const long long lrow = row0 * a.token_stride + piece * 8;            // this lane's place in a tile that lies in one page
   const uint32_t ldst = ring + row0 * (D * 2), lpiece = (uint32_t)((piece ^ row0) << 4);   // row0 < 8; ring and rows on 128 bytes
+  int pt0 = 0;                                      // the warp's first token in the unit to load
+  uint32_t haves = 0;                               // SP: a stage's tokens, a byte each
   auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
-    const int t = p.chunk * kUnit + warp * kTile + (a.aligned ? 0 : lane & 15);
+    pt0 = (SP ? block_of(a, p, pu < u1) : p.chunk) * kUnit + warp * kTile;
+    const int t = pt0 + (a.aligned ? 0 : lane & 15);
     ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
   };
   lookup();
   auto issue = [&]() {
     if (pu < u1) {
-      const int t0 = p.chunk * kUnit + warp * kTile;
+      const int t0 = pt0;
+      if (SP) haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)min(max(p.len - t0, 0), kTile) << (8 * pslot);
       if (t0 < p.len) {
-        const int have = p.len - t0 - (a.nk ? 1 : 0);                  // rows to copy: the new token does not come from the cache
+        const int have = p.len - t0 - (!SP && a.nk ? 1 : 0);                  // rows to copy: the new token does not come from the cache
         const int kvh = a.nht == 1 ? p.h : p.h / a.nht;
         const uint32_t dst = ldst + pslot * (2 * S::kTileBytes);
         bool bad;
@@ -323,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
         if (bad && lane == 0) atomicOr(&q2_attend_error, Q2_ERR_PAGE);
         badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
       }
-      pu += advance(p);
+      pu += advance<SP>(a, pre, lens, p);
       lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
     }
@@ -340,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
   for (int u = u0; u < u1;) {
     const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
     const int qh = kvh * a.group + ht * H;
-    const int t0 = c.chunk * kUnit + warp * kTile;
     if (fresh) {
       fresh = false;
       const __half* q = a.q + c.b * a.ldq + (long long)(qh + g) * D + 2 * j;
@@ -352,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
           qa[s][2 * y] = is ? *reinterpret_cast<const uint32_t*>(q + 8 * y * D + 16 * s) : 0u;
           qa[s][2 * y + 1] = is ? *reinterpret_cast<const uint32_t*>(q + 8 * y * D + 16 * s + 8) : 0u;
         }
-      if (a.nk && lane < CPR) {
+      if (!SP && a.nk && lane < CPR) {
         const long long e = c.b * a.ldn + kvh * D + lane * 8;
         newk = *reinterpret_cast<const uint4*>(a.nk + e);
         newv = *reinterpret_cast<const uint4*>(a.nv + e);
@@ -376,10 +235,11 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       --ahead;
       continue;
     }
-    if (t0 < c.len) {
+    // row of the last token, if below kTile; negative: none
+    const int fin = SP ? (int)(haves >> (8 * slot) & 255u) - 1 : c.len - 1 - (c.chunk * kUnit + warp * kTile);
+    if (fin >= 0) {
       const uint32_t kt = ring + slot * (2 * S::kTileBytes), vt = kt + S::kTileBytes;
-      const int fin = c.len - 1 - t0;               // row of the last token, if below kTile
-      if (a.nk && fin < kTile) {                    // the new token's row, and its place in the cache
+      if (!SP && a.nk && fin < kTile) {                    // the new token's row, and its place in the cache
         if (lane < CPR) {
           const uint32_t d = fin * (D * 2) + ((lane ^ (fin & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kt + d), "r"(newk.x), "r"(newk.y), "r"(newk.z),
@@ -471,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
     const Walk w = c;
-    u += advance(c);
+    u += advance<SP>(a, pre, lens, c);
     const bool ends = w.chunk + 1 == w.nch, all = u >= u1;
     if (ends || all) {                              // the end of this (sequence, head), or of this CTA's share of it
       // Every warp leaves its sums (the numerators in place of the keys it has
@@ -491,59 +351,10 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
       }
       __syncthreads();
       const bool whole = ends && seg == 0;
-      const int part = 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0);
-      constexpr int PPL = D / kWarps / 16;          // 16-byte pieces of a lane: row lane / 4, a quarter of the warp's columns
-#pragma unroll
-      for (int row = g; row < H; row += 8) {
-        float wt[kWarps], mm = -INFINITY, ll = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, wml[k * H + row].x);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float2 v = wml[k * H + row];
-          wt[k] = exp2f(v.x - ref);
-          ll += wt[k] * v.y;
-        }
-        if (row < rows) {
-          const float inv = 1.f / (kUp * ll);      // (the numerators are 2^15 too large)
-#pragma unroll
-          for (int q = 0; q < PPL; ++q) {
-            const int piece4 = (warp * 4 + j) * PPL + q;      // columns 4 * piece4 ..
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-              const float4 v = *reinterpret_cast<const float4*>(q2_att_smem + k * (STAGES * 2 * S::kTileBytes) + mine +
-                                                                row * (D * 4) + ((piece4 ^ g) << 4));
-              x.x += v.x * wt[k];
-              x.y += v.y * wt[k];
-              x.z += v.z * wt[k];
-              x.w += v.w * wt[k];
-            }
-            if (whole) {
-              __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
-              *reinterpret_cast<uint2*>(a.o + w.b * a.ldo + (long long)(qh + row) * D + piece4 * 4) = *reinterpret_cast<uint2*>(h);
-            } else {
-              *reinterpret_cast<float4*>(a.part + ((size_t)part * H + row) * D + piece4 * 4) = x;
-            }
-          }
-          if (!whole && warp == 0 && j == 0) a.ml[(size_t)part * H + row] = make_float2(mm, ll);
-        }
-      }
+      join_warps<D, H, SP>(a, q2_att_smem + mine, STAGES * 2 * S::kTileBytes, wml, whole,
+                           2 * (int)blockIdx.x + (seg == 0 ? 1 : 0), rows, w.b, qh, kUp);
       __syncthreads();                              // the stages may be filled again; the part is written
-      if (!whole) {
-        // The part that completes a (sequence, head) owes its join; a CTA has
-        // two parts at most (the one it begins with and the one it ends with)
-        // and joins at its end, so that nothing waits for the counter here.
-        if (threadIdx.x == 0) {
-          const unsigned before = count_part(a.count + (size_t)w.b * a.hu + w.h);
-          // the CTAs that hold parts of this (sequence, head): c0 (from its first unit) .. c1
-          const int s = pre[w.b] + w.h * (w.nch + kEnd);
-          auto cta_of = [&](int v) { return (int)((((long long)v + 1) * ncta - 1) / total); };
-          const int c0 = cta_of(s), c1 = cta_of(s + w.nch - 1);
-          if (before == (unsigned)(c1 - c0)) owe[owed++] = make_int4(w.b, w.h, c0, c1);
-        }
-      }
+      if (!whole && threadIdx.x == 0) owe_part(a, sh, pre, w, owe, owed);
       fresh = true;
       seg = 0;
     }
@@ -551,82 +362,50 @@ __global__ void __launch_bounds__(kThreads, att_ctas<D>()) k_attend(const __grid
 
   if (threadIdx.x == 0) *nowed = owed;
   __syncthreads();
-  for (int q = 0; q < *nowed; ++q) {
-    const int4 w = owe[q];
-    const int kvh = a.nht == 1 ? w.y : w.y / a.nht, ht = w.y - kvh * a.nht, rows = min(H, a.group - ht * H);
-    const int parts = w.w - w.z + 1;
-    if (threadIdx.x == 0) a.count[(size_t)w.x * a.hu + w.y] = 0;
-    for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
-      const int r = e / (D / 4), d4 = e % (D / 4);
-      float mj = -INFINITY, lj = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int k0 = 0; k0 < parts; k0 += kJoin) {       // kJoin parts' loads at a time
-        float2 v[kJoin];
-        float4 f[kJoin];
-#pragma unroll
-        for (int k = 0; k < kJoin; ++k) {
-          // the first CTA's second part, the others' first
-          const size_t at = (size_t)(2 * (w.z + min(k0 + k, parts - 1)) + (k0 + k == 0)) * H + r;
-          v[k] = __ldcg(&a.ml[at]);
-          f[k] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + d4);
-          if (k0 + k >= parts) v[k].x = -INFINITY;
-        }
-        float mn = mj;
-#pragma unroll
-        for (int k = 0; k < kJoin; ++k) mn = fmaxf(mn, v[k].x);
-        const float ref = mn == -INFINITY ? 0.f : mn, old = exp2f(mj - ref);
-        mj = mn;
-        lj *= old;
-        x.x *= old;
-        x.y *= old;
-        x.z *= old;
-        x.w *= old;
-#pragma unroll
-        for (int k = 0; k < kJoin; ++k) {
-          if (k0 + k < parts) {
-            const float wk = exp2f(v[k].x - ref);
-            lj += wk * v[k].y;
-            x.x += wk * f[k].x;
-            x.y += wk * f[k].y;
-            x.z += wk * f[k].z;
-            x.w += wk * f[k].w;
-          }
-        }
-      }
-      const float inv = 1.f / (kUp * lj);
-      __half2 h[2] = {__floats2half2_rn(x.x * inv, x.y * inv), __floats2half2_rn(x.z * inv, x.w * inv)};
-      *reinterpret_cast<uint2*>(a.o + w.x * a.ldo + (long long)(kvh * a.group + ht * H + r) * D + d4 * 4) =
-          *reinterpret_cast<uint2*>(h);
-    }
-  }
+  join_parts<D, H, SP>(a, owe, *nowed, kUp);
 }
 
-int most_ctas(int D, int sms) { return sms * (D == 64 ? att_ctas<64>() : D == 128 ? att_ctas<128>() : att_ctas<256>()); }
-
-// The workspace: the parts' sums, in a region that fits every head_dim (so the
-// counters behind it have one place for calls of all shapes), then counters.
-size_t part_bytes(int sms) {
-  size_t n = 0;
-  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D, sms) * kMostHeads * (D * 4 + 8));
-  return (n + 255) / 256 * 256;
-}
-
-// Query heads of a unit.  Sixteen where a key-value head has more than eight
-// and the registers hold them, so that its tokens are read once for sixteen:
-// there lo has its own products (52 to 56 us by the pages' order, instead of
-// 89, for 8 sequences of 8192 tokens, 128 query and 8 key-value heads of 128).
-int unit_heads(int group, int D) { return group > 8 && D <= 128 ? 16 : 8; }
-
-// Shared checks of the head counts; hu: heads of units.
-int check_heads(int batch, int q_heads, int kv_heads, int D, int* hu, int* nht) {
-  if (batch < 0 || batch > Q2_ATT_MAX_BATCH || kv_heads < 1 || kv_heads > 65536 || q_heads < 1 || q_heads % kv_heads)
-    return Q2_ESHAPE;
-  if (q_heads / kv_heads > Q2_ATT_MAX_GROUP || (D != 64 && D != 128 && D != 256)) return Q2_ESHAPE;
-  const int H = unit_heads(q_heads / kv_heads, D);
-  *nht = (q_heads / kv_heads + H - 1) / H;
-  *hu = kv_heads * *nht;
-  return Q2_OK;
+template <bool SP>
+int attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, const void* new_v, long long ldn,
+           const int* lens, int batch, int q_heads, const int* sel, int nsel, float scale, void* out, long long ldo, void* ws,
+           size_t ws_bytes, void* stream) {
+  if (!kv || (!new_k) != (!new_v)) return Q2_EINVAL;
+  AttendArgs a = {};
+  Pages pg;
+  CacheShape c;
+  UnitCall u = {q, ldq, lens, batch, q_heads, sel, nsel, scale, out, ldo, ws, ws_bytes};
+  int st = u.check(kv);
+  if (st) return st;
+  if (batch == 0) return Q2_OK;
+  if ((st = check_cache(kv, batch, pg, c)) || (st = u.fill(c, SP, a))) return st;
+  if (batch > 1 && new_k && ldn < (long long)kv->kv_heads * c.D) return Q2_ESHAPE;
+  if (misaligned(new_k, 16) || misaligned(new_v, 16) || (batch > 1 && new_k && ldn % 8)) return Q2_EALIGN;
+  a.k = static_cast<__half*>(kv->k);
+  a.v = static_cast<__half*>(kv->v);
+  a.page_stride = kv->page_stride;
+  a.token_stride = kv->token_stride;
+  a.head_stride = kv->head_stride;
+  a.table = kv->table;
+  a.table_stride = kv->table_stride;
+  a.nk = static_cast<const __half*>(new_k);
+  a.nv = static_cast<const __half*>(new_v);
+  a.ldn = ldn;
+  a.npages = kv->npages;
+  a.page = kv->page_size;
+  a.aligned = kv->page_size % kTile == 0;
+  a.page_mul = pg.page_mul;
+  a.page_sh = pg.page_sh;
+  const bool wide = unit_heads(a.group, c.D) == 16;
+  auto launch = [&](auto kernel, int ctas, int smem) {
+    return launch_pdl(kernel, a, (int)std::min(u.units, (long long)ctas * dev_info().sms), kThreads, smem, stream);
+  };
+  if (c.D == 64)
+    return wide ? launch(k_attend<64, 16, SP>, ctas_of<64>(), Shape<64, 16>::smem(batch))
+                : launch(k_attend<64, 8, SP>, ctas_of<64>(), Shape<64, 8>::smem(batch));
+  if (c.D == 128)
+    return wide ? launch(k_attend<128, 16, SP>, ctas_of<128>(), Shape<128, 16>::smem(batch))
+                : launch(k_attend<128, 8, SP>, ctas_of<128>(), Shape<128, 8>::smem(batch));
+  return launch(k_attend<256, 8, SP>, ctas_of<256>(), Shape<256, 8>::smem(batch));
 }
 
 }  // namespace
@@ -646,69 +425,14 @@ extern "C" int q2_attend_workspace_bytes(int batch, int q_heads, int kv_heads, i
 extern "C" int q2_attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, const void* new_v,
                          long long ldn, const int* lens, int batch, int q_heads, float scale, void* out, long long ldo,
                          void* ws, size_t ws_bytes, q2_stream stream) {
-  if (!kv || (!new_k) != (!new_v)) return Q2_EINVAL;
-  const int D = kv->head_dim;
-  int hu, nht;
-  int st = check_heads(batch, q_heads, kv->kv_heads, D, &hu, &nht);
-  if (st) return st;
-  if (kv->page_size < 1 || kv->npages < 0 || kv->max_pages < 0) return Q2_ESHAPE;
-  if (!(scale == scale) || scale - scale != 0.f) return Q2_EINVAL;
-  if (batch == 0) return Q2_OK;
-  if (!q || !lens || !out || !kv->k || !kv->v || !kv->table) return Q2_EINVAL;
-  const long long qw = (long long)q_heads * D, kw = (long long)kv->kv_heads * D;
-  if (batch > 1 && (ldq < qw || ldo < qw || (new_k && ldn < kw) || kv->table_stride < kv->max_pages)) return Q2_ESHAPE;
-  if (kv->page_stride < 0 || kv->token_stride < 0 || kv->head_stride < 0) return Q2_ESHAPE;
-  auto off = [](const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; };
-  if (off(q, 16) || off(out, 16) || off(new_k, 16) || off(new_v, 16) || off(kv->k, 16) || off(kv->v, 16) ||
-      off(kv->table, 4) || off(lens, 4) || kv->page_stride % 8 || kv->token_stride % 8 || kv->head_stride % 8 ||
-      (batch > 1 && (ldq % 8 || ldo % 8 || (new_k && ldn % 8))))
-    return Q2_EALIGN;
-  const int sms = dev_info().sms;
-  const size_t parts = part_bytes(sms), need = parts + (size_t)batch * hu * 4;
-  if (!ws || ws_bytes < need) return Q2_EWORKSPACE;
-  if (off(ws, 256)) return Q2_EALIGN;
-  // tokens of a table row, and of all units: both are counted in 32 bits on the device
-  const long long cap = (long long)kv->max_pages * kv->page_size;
-  const long long units = (cap / kUnit + 1 + kEnd) * hu * batch;
-  if (cap > 0x7fffff00ll || units > 0x7fffffffll) return Q2_ESHAPE;
-  AttendArgs a = {};
-  a.k = static_cast<__half*>(kv->k);
-  a.v = static_cast<__half*>(kv->v);
-  a.page_stride = kv->page_stride;
-  a.token_stride = kv->token_stride;
-  a.head_stride = kv->head_stride;
-  a.table = kv->table;
-  a.table_stride = kv->table_stride;
-  a.lens = lens;
-  a.q = static_cast<const __half*>(q);
-  a.nk = static_cast<const __half*>(new_k);
-  a.nv = static_cast<const __half*>(new_v);
-  a.o = static_cast<__half*>(out);
-  a.ldq = ldq;
-  a.ldn = ldn;
-  a.ldo = ldo;
-  const int most = most_ctas(D, sms);
-  a.part = static_cast<float*>(ws);
-  a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + parts);
-  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most * unit_heads(q_heads / kv->kv_heads, D) * D);
-  a.batch = batch;
-  a.npages = kv->npages;
-  a.page = kv->page_size;
-  a.aligned = kv->page_size % kTile == 0;
-  while ((1ll << a.page_sh) < a.page) ++a.page_sh;
-  a.page_mul = (uint32_t)(((1ull << 32) * ((1ull << a.page_sh) - a.page)) / a.page + 1);
-  a.cap = (int)cap;
-  a.hu = hu;
-  a.nht = nht;
-  a.group = q_heads / kv->kv_heads;
-  a.sc2 = (float)((double)scale * 1.4426950408889634);
-  const int grid = units < most ? (int)units : most;
-  auto launch = [&](auto kernel, int smem) { return launch_pdl(kernel, a, grid, kThreads, smem, stream); };
-  const bool wide = unit_heads(a.group, D) == 16;
-  if (D == 64) return wide ? launch(k_attend<64, 16>, Shape<64, 16>::smem(batch)) : launch(k_attend<64, 8>, Shape<64, 8>::smem(batch));
-  if (D == 128)
-    return wide ? launch(k_attend<128, 16>, Shape<128, 16>::smem(batch)) : launch(k_attend<128, 8>, Shape<128, 8>::smem(batch));
-  return launch(k_attend<256, 8>, Shape<256, 8>::smem(batch));
+  return attend<false>(kv, q, ldq, new_k, new_v, ldn, lens, batch, q_heads, nullptr, 0, scale, out, ldo, ws, ws_bytes, stream);
+}
+
+extern "C" int q2_attend_blocks(const q2_kv* kv, const void* q, long long ldq, const int* lens, int batch, int q_heads,
+                                const int* sel, int nsel, float scale, void* out, long long ldo, void* ws, size_t ws_bytes,
+                                q2_stream stream) {
+  if (nsel < 1) return Q2_ESHAPE;
+  return attend<true>(kv, q, ldq, nullptr, nullptr, 0, lens, batch, q_heads, sel, nsel, scale, out, ldo, ws, ws_bytes, stream);
 }
 
 // The error word of the attention kernels, then cleared (q2_device_errors).

@@ -205,10 +205,10 @@ __device__ __forceinline__ float fx_value(unsigned long long w, int n, float fin
 // may start while the previous kernel on the stream drains; it must call
 // pdl_wait() before reading anything that kernel writes.
 template <typename A>
-int launch_pdl(void (*kernel)(A), const A& args, int grid, int threads, int smem, void* stream) {
+int launch_pdl(void (*kernel)(A), const A& args, dim3 grid, int threads, int smem, void* stream) {
   if (set_smem(reinterpret_cast<const void*>(kernel), smem)) return Q2_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -218,6 +218,48 @@ int launch_pdl(void (*kernel)(A), const A& args, int grid, int threads, int smem
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return Q2_ECUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? Q2_OK : Q2_ECUDA;
+}
+
+// The cluster's barriers, by converged warps.  The first: what each CTA has left
+// in its shared memory is there for the others.  The second, behind the last
+// reads of other CTAs' shared memory, in two halves: the arrival orders those
+// reads before it (a releasing one does, a relaxed one would not), and the
+// stores of what was read come behind it, so that it does not wait for them.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  cluster_arrive();
+  cluster_wait();
+}
+
+// Launch in clusters of cs CTAs, programmatic stream serialization allowed.
+template <typename... A, typename... B>
+int launch_clusters(void (*kernel)(A...), int clusters, int cs, int threads, int smem, void* stream, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * cs);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return Q2_ECUDA;
   }

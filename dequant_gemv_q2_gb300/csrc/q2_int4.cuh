@@ -153,24 +153,6 @@ __device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(cc) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
 }
 
-// The cluster's barriers, by converged warps.  The first: what each CTA has left
-// in its shared memory is there for the others.  The second, behind the last
-// reads of other CTAs' shared memory, in two halves: the arrival orders those
-// reads before it (a releasing one does, a relaxed one would not), and the
-// stores of what was read come behind it, so that it does not wait for them.
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_meet() {
-  cluster_arrive();
-  cluster_wait();
-}
-
 constexpr int kSmemPerSm = 228 * 1024;              // a CTA takes 1 KB beside its own
 
 // How many clusters of cs CTAs of a kernel the device runs at once (a cluster
@@ -213,30 +195,6 @@ class ClusterCounts {
     return n;
   }
 };
-
-// Launch in clusters of cs CTAs, programmatic stream serialization allowed.
-template <typename... A, typename... B>
-int launch_clusters(void (*kernel)(A...), int clusters, int cs, int threads, int smem, void* stream, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * cs);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return Q2_ECUDA;
-  }
-  return cudaGetLastError() == cudaSuccess ? Q2_OK : Q2_ECUDA;
-}
 
 }  // namespace q2
 

@@ -1059,6 +1059,9 @@ extern "C" int q2_debug_wait_limit(long long polls) {
 
 extern "C" int q2_attend_errors(unsigned int* out);   // q2_attend.cu
 extern "C" int q2_int4_errors(unsigned int* out);     // q2_int4_tc.cu
+extern "C" int q2_cache_errors(unsigned int* out);    // q2_cache.cu
+extern "C" int q2_attend4_errors(unsigned int* out);  // q2_attend4.cu
+extern "C" int q2_select_errors(unsigned int* out);   // q2_select.cu
 
 // Device-side error word of the tensor-core and attention kernels since the last call
 // (then cleared): 0 in normal operation, else the code of a bounded wait
@@ -1068,8 +1071,10 @@ extern "C" int q2_device_errors(unsigned int* out) {
   unsigned int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, q2_tc_error, sizeof(v)) != cudaSuccess) return Q2_ECUDA;
   if (cudaMemcpyToSymbol(q2_tc_error, &z, sizeof(z)) != cudaSuccess) return Q2_ECUDA;
-  unsigned int att = 0, int4 = 0;
-  if (q2_attend_errors(&att) != Q2_OK || q2_int4_errors(&int4) != Q2_OK) return Q2_ECUDA;
-  *out = v | att | int4;
+  for (auto errors : {q2_attend_errors, q2_int4_errors, q2_cache_errors, q2_attend4_errors, q2_select_errors}) {
+    if (errors(&z) != Q2_OK) return Q2_ECUDA;
+    v |= z;
+  }
+  *out = v;
   return Q2_OK;
 }

@@ -401,8 +401,159 @@ int q2_attend(const q2_kv* kv, const void* q, long long ldq, const void* new_k, 
 #define Q2_ERR_LENGTH 0x100u    /* a sequence length outside its table row     */
 #define Q2_ERR_PAGE 0x200u      /* a page number outside the pools             */
 
-/* Device-side error word of the tensor-core (7..64 tokens; Q2_INT4 17..64) and
- * the attention kernels, then cleared: 0 in normal operation; Q2_ERR_LENGTH
+/* ------------------------------------------------------------- cache, 4 bits
+ * A paged key-value cache in 4 bits (no counterpart on the source pages).  A
+ * row's head of head_dim values is cut into groups of `group` columns (32 or
+ * 64); a group has an fp16 step s and an fp16 offset m, and a value is m + s c
+ * with a code c from 0 to 15.  Byte j of a head's head_dim / 2 code bytes holds
+ * column 2j in its low four bits and column 2j + 1 in its high four (as
+ * q2_pack_int4 takes them); its head_dim / group pairs (s, m) are fp16, in the
+ * order of the groups.  What is stored for x: m = fp16(min), s = fp16((max -
+ * min) / 15), c = rint((x - m) / s) held to 0..15 (ties to even, 0 where s is
+ * 0), all from fp32 values; a group with an inf or NaN, or an offset beyond
+ * fp16, gets m = NaN and s = 0.
+ *
+ * Codes of (page, slot, head) begin at page * page_stride + slot * token_stride
+ * + head * head_stride bytes, pairs at the same with the s_ strides, counted in
+ * pairs.  Stored head by head (slots of one head behind one another) the cache
+ * reads fastest.  Token l of sequence b is where q2_kv would have it. */
+typedef struct {
+  void* k;                      /* device uint8 pools of codes, 16-byte aligned */
+  void* v;
+  long long page_stride;        /* bytes, multiples of 16                      */
+  long long token_stride;
+  long long head_stride;
+  void* ks;                     /* device fp16 pools of (s, m), 16-byte aligned */
+  void* vs;
+  long long s_page_stride;      /* pairs, multiples of min(4, head_dim / group) */
+  long long s_token_stride;
+  long long s_head_stride;
+  int npages;
+  int page_size;
+  int kv_heads;
+  int head_dim;                 /* 64, 128 or 256                              */
+  int group;                    /* 32 or 64                                    */
+  const int* table;             /* device [batch][table_stride] page numbers   */
+  long long table_stride;
+  int max_pages;
+} q2_kv4;
+
+/* The angles of positions: cos and sin of pair i at position p are
+ * table[(p * rot / 2 + i) * 2] and the value behind it, fp32 on the device,
+ * 16-byte aligned.  The first rot columns of a head are turned (rot a multiple
+ * of 16, at most head_dim), the others are left as they are.  Pair i is columns
+ * i and i + rot / 2, or 2i and 2i + 1 where interleaved is not 0:
+ *   (a, b) becomes (a cos - b sin, b cos + a sin). */
+typedef struct {
+  const float* table;
+  int positions;
+  int rot;
+  int interleaved;
+} q2_rope;
+
+#define Q2_BLOCK 64             /* tokens of a block (bounds, q2_select)       */
+
+/* New tokens of a batch of sequences into the cache, their queries and keys
+ * turned on the way.  Rows starts[b] .. starts[b + 1] - 1 of q, k and v are the
+ * last tokens of sequence b, which has lens[b] tokens with them (so a row r has
+ * position lens[b] - (starts[b + 1] - r)); starts == NULL: one token each, row
+ * b, ntok == batch.
+ *   - k, v: device fp16, head h of row r at + r * ldk (ldv) + h * head_dim; q
+ *     and q_out the same with ldq, ldqo and q_heads heads, or both NULL (then
+ *     q_heads is not used).  q_out may be q with ldqo == ldq; no other overlap.
+ *   - rope: may be NULL (nothing is turned; q_out is a copy of q).
+ *   - Keys are turned in fp32 to the last bit (both products exact, one
+ *     rounding), then rounded to fp16 or to 4 bits; queries in fp32, then to
+ *     fp16.  Values are stored as they are, or in 4 bits.
+ *   - bounds: NULL, or device fp16 [npages][ceil(page_size / 64)][kv_heads][2]
+ *     [head_dim], 16-byte aligned: the least and the greatest value per column
+ *     of the turned keys, rounded to fp16, of every block of 64 tokens (tokens
+ *     64 i .. 64 i + 63 of a sequence).  A block's bounds lie at the page of its
+ *     first token; a block whose first token is stored by this call begins
+ *     anew.  page_size must be a multiple or a divisor of 64 (Q2_ESHAPE).  A NaN
+ *     among a column's keys makes its bounds NaN.
+ *   - starts: device int32 [batch + 1]; lens: device int32 [batch].  Rows
+ *     outside every sequence, and those of a sequence of length 0, are left as
+ *     they are.  No two tokens may be stored to the same place.
+ *   - A length below 0 or above max_pages * page_size, one that is neither 0
+ *     nor at least the sequence's rows, or one above rope->positions: nothing of
+ *     the sequence is stored, its rows of q_out become NaN, and Q2_ERR_LENGTH is
+ *     set; the same bit for starts that do not ascend within 0..ntok (nothing
+ *     is written then).  A page outside 0..npages-1: its tokens are not stored,
+ *     Q2_ERR_PAGE.
+ *   - Pointers 16-byte aligned, leading dimensions multiples of 8, strides as the
+ *     cache's structure says (Q2_EALIGN); batch <= Q2_ATT_MAX_BATCH, q_heads <=
+ *     65536 (Q2_ESHAPE).  ntok == 0 or batch == 0 does nothing.  One launch, launched
+ *     like q2_gemv (all inputs are read after the previous kernel finished). */
+int q2_append(const q2_kv* kv, void* bounds, const void* q, long long ldq, void* q_out, long long ldqo, int q_heads,
+              const void* k, long long ldk, const void* v, long long ldv, const int* starts, const int* lens, int batch,
+              int ntok, const q2_rope* rope, q2_stream stream);
+int q2_append4(const q2_kv4* kv, void* bounds, const void* q, long long ldq, void* q_out, long long ldqo, int q_heads,
+               const void* k, long long ldk, const void* v, long long ldv, const int* starts, const int* lens, int batch,
+               int ntok, const q2_rope* rope, q2_stream stream);
+
+/* The last tokens of every sequence out of the cache: row r of sequence b (as
+ * for q2_append, with which it shares starts, lens and their errors) is token
+ * lens[b] - (starts[b + 1] - r), so starts of all lengths' running sums give
+ * whole sequences.  k, v: device fp16, head h of row r at + r * ldk (ldv) + h *
+ * head_dim; either may be NULL.  4 bits: fp16(m + s c), the sum rounded to fp32
+ * before.  A token whose page does not exist, and rows of a sequence whose
+ * length is wrong, are NaN. */
+int q2_read(const q2_kv* kv, void* k, long long ldk, void* v, long long ldv, const int* starts, const int* lens,
+            int batch, int ntok, q2_stream stream);
+int q2_read4(const q2_kv4* kv, void* k, long long ldk, void* v, long long ldv, const int* starts, const int* lens,
+             int batch, int ntok, q2_stream stream);
+
+/* Attention of one new token per sequence over a cache in 4 bits: q2_attend on
+ * what the cache stands for, of tokens that q2_append4 has stored (the last one
+ * among them).  fp16 in and out, fp32 sums; no value is rounded on the way.
+ *   - q, out, lens, scale, their checks and the errors are as for q2_attend, and
+ *     so is the workspace (q2_attend_workspace_bytes), which calls on both kinds
+ *     of cache may share if they are ordered on one stream.
+ *   - sel: NULL (nsel 0), or the blocks to attend, as for q2_attend_blocks.
+ *   - A group whose offset is NaN makes its token's score NaN (keys) or its
+ *     columns of the output NaN (values). */
+int q2_attend4(const q2_kv4* kv, const void* q, long long ldq, const int* lens, int batch, int q_heads, const int* sel,
+               int nsel, float scale, void* out, long long ldo, void* ws, size_t ws_bytes, q2_stream stream);
+
+/* The blocks of 64 tokens that promise the most to a token's queries.  Block n
+ * of a key-value head can give query head h at most U_h(n) = sum_d max(q_hd
+ * lo_nd, q_hd hi_nd) with lo and hi its bounds (q2_append); the block's score is
+ * the largest fp32(U_h(n)) of the head's query heads.
+ *   - sel: device int32 [batch][kv_heads][nsel]; per (sequence, key-value head)
+ *     the nsel blocks of the highest score, in ascending order, -1 behind the
+ *     last where the sequence has fewer.  Equal scores: the lower block.  The
+ *     first `first` and the last `last` blocks are always among them (first,
+ *     last >= 0, first + last <= nsel).  A block with a U_h that is not a finite
+ *     number is above all others.
+ *   - U_h is summed to 2^-36 of the sum of its terms' magnitudes and rounded to
+ *     fp32, so the selection is that of the exact scores.
+ *   - kv: head_dim, kv_heads, npages, page_size, table and max_pages are used, the
+ *     pools are not read; bounds as for q2_append; q, ldq, q_heads, lens and
+ *     batch as for q2_attend.  A length that cannot be, or a page of a block's
+ *     first token that does not exist, sets Q2_ERR_LENGTH (all of sel -1) or
+ *     Q2_ERR_PAGE (the block scores as one with NaN, so that attending it shows
+ *     the page).  1 <= nsel <= Q2_MAX_BLOCKS; max_pages * page_size at most 64 *
+ *     Q2_MAX_BLOCKS tokens (Q2_ESHAPE).
+ *   - One launch, launched like q2_gemv; needs no workspace. */
+#define Q2_MAX_BLOCKS 32768
+int q2_select(const q2_kv* kv, const void* bounds, const void* q, long long ldq, const int* lens, int batch, int q_heads,
+              int nsel, int first, int last, int* sel, q2_stream stream);
+int q2_select4(const q2_kv4* kv, const void* bounds, const void* q, long long ldq, const int* lens, int batch,
+               int q_heads, int nsel, int first, int last, int* sel, q2_stream stream);
+
+/* q2_attend (without new keys and values) over selected blocks: key-value head k
+ * of sequence b attends the tokens below lens[b] of the blocks of 64 tokens that
+ * sel[(b * kv_heads + k) * nsel ..] names, of which the first min(nsel,
+ * ceil(lens[b] / 64)) entries are read, in any order.  An entry outside
+ * 0..ceil(lens[b] / 64) - 1 names none; a block named twice counts twice; where
+ * none is named the output is zero.  Pages of blocks that are not named are not
+ * looked up. */
+int q2_attend_blocks(const q2_kv* kv, const void* q, long long ldq, const int* lens, int batch, int q_heads, const int* sel,
+                     int nsel, float scale, void* out, long long ldo, void* ws, size_t ws_bytes, q2_stream stream);
+
+/* Device-side error word of the tensor-core (7..64 tokens; Q2_INT4 17..64), the
+ * attention and the cache's kernels, then cleared: 0 in normal operation; Q2_ERR_LENGTH
  * and Q2_ERR_PAGE as above; any other bit means a bounded wait on the tensor
  * core ran out and the kernel skipped its work (the rows of the tiles
  * concerned are NaN).  Before such a kernel's CTA exits it waits, with the
