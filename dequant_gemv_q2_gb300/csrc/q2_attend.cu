@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
 
   pdl_wait();                                       // everything may come from the previous kernel
   pdl_trigger();
-  const Share sh = share_out<D, SP>(a, nowed, pre, lens, &q2_attend_error);
+  const Share sh = share_out<D, SP, kUnit>(a, nowed, pre, lens, &q2_attend_error);
   int u0 = sh.u0;
   const int u1 = sh.u1;
   if (u0 >= u1) return;                             // no share
-  Walk c = walk_from<SP>(a, pre, lens, u0);         // the unit in use
+  Walk c = walk_from<SP, kUnit>(a, pre, lens, u0);         // the unit in use
   if (u0 >= u1) return;
 
   // ---- the warp's loads, STAGES - 1 units ahead of their use
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
   int pt0 = 0;                                      // the warp's first token in the unit to load
   uint32_t haves = 0;                               // SP: a stage's tokens, a byte each
   auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
-    pt0 = (SP ? block_of(a, p, pu < u1) : p.chunk) * kUnit + warp * kTile;
+    pt0 = first_token<SP, kUnit, kTile>(a, p, warp, pu < u1);
     const int t = pt0 + (a.aligned ? 0 : lane & 15);
     ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
   };
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
         if (bad && lane == 0) atomicOr(&q2_attend_error, Q2_ERR_PAGE);
         badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
       }
-      pu += advance<SP>(a, pre, lens, p);
+      pu += advance<SP, kUnit>(a, pre, lens, p);
       lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
     }
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
     const Walk w = c;
-    u += advance<SP>(a, pre, lens, c);
+    u += advance<SP, kUnit>(a, pre, lens, c);
     const bool ends = w.chunk + 1 == w.nch, all = u >= u1;
     if (ends || all) {                              // the end of this (sequence, head), or of this CTA's share of it
       // Every warp leaves its sums (the numerators in place of the keys it has

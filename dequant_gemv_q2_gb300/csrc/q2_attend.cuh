@@ -11,9 +11,8 @@
 namespace q2 {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16, kUnit = kTile * kWarps;   // tokens of a warp's tile, of a unit
+constexpr int kTile = 16, kUnit = kTile * kWarps;   // tokens of a warp's tile, of the fp16 cache's units
 constexpr int kMostHeads = 16;                      // query heads of a unit at most
-static_assert(kUnit == Q2_BLOCK, "a unit is a block that q2_select selects");
 
 // The part of a call's arguments that does not depend on how the cache is held.
 struct UnitArgs {
@@ -75,11 +74,13 @@ __device__ __forceinline__ unsigned count_part(unsigned* count) {
   return before;
 }
 
-// Units of a sequence, per head.  SP: only selected blocks are attended.
-template <bool SP>
+// Units of UNIT tokens of a sequence, per head.  SP: only selected blocks are
+// attended, UNIT / 64 list entries to a unit.
+template <bool SP, int UNIT>
 __device__ __forceinline__ int units_of(const UnitArgs& a, int len) {
-  const int n = (len + kUnit - 1) / kUnit;
-  return SP ? min(n, a.nsel) : n;
+  static_assert(UNIT % Q2_BLOCK == 0, "a unit is made of blocks that q2_select selects");
+  if (!SP) return (len + UNIT - 1) / UNIT;
+  return (min((len + Q2_BLOCK - 1) / Q2_BLOCK, a.nsel) + UNIT / Q2_BLOCK - 1) / (UNIT / Q2_BLOCK);
 }
 
 // The order of units: each (sequence, head) has its units and kEnd places
@@ -92,7 +93,7 @@ struct Share {
 // Shared memory behind a kernel's own: `nowed` (4 ints, at first how many CTAs
 // have work), pre [batch + 1] places before each sequence, lens [batch].  Writes
 // the outputs of sequences without a token, and of lengths that cannot be.
-template <int D, bool SP>
+template <int D, bool SP, int UNIT>
 __device__ __forceinline__ Share share_out(const UnitArgs& a, int* nowed, int* pre, int* lens, unsigned* error) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == 0) {                                  // the units before each sequence
@@ -102,7 +103,7 @@ __device__ __forceinline__ Share share_out(const UnitArgs& a, int* nowed, int* p
       int len = b < a.batch ? a.lens[b] : 0;
       if (len < 0 || len > a.cap) len = 0;
       if (b < a.batch) lens[b] = len;
-      const int n = units_of<SP>(a, len);
+      const int n = units_of<SP, UNIT>(a, len);
       longest = max(longest, n);
       used += __popc(__ballot_sync(0xffffffffu, len > 0));
       int v = len ? (n + kEnd) * a.hu : 0;
@@ -149,7 +150,7 @@ __device__ __forceinline__ Share share_out(const UnitArgs& a, int* nowed, int* p
 }
 
 // To the next unit; how many places further it is.
-template <bool SP>
+template <bool SP, int UNIT>
 __device__ __forceinline__ int advance(const UnitArgs& a, const int* pre, const int* lens, Walk& w) {
   if (++w.chunk < w.nch) return 1;
   const int skipped = w.nch + kEnd - w.chunk;
@@ -160,14 +161,14 @@ __device__ __forceinline__ int advance(const UnitArgs& a, const int* pre, const 
     while (w.b < a.batch && pre[w.b + 1] == pre[w.b]);
     if (w.b < a.batch) {
       w.len = lens[w.b];
-      w.nch = units_of<SP>(a, w.len);
+      w.nch = units_of<SP, UNIT>(a, w.len);
     }
   }
   return 1 + skipped;
 }
 
 // The unit at place u0, or the next one behind it (then u0 moves too).
-template <bool SP>
+template <bool SP, int UNIT>
 __device__ __forceinline__ Walk walk_from(const UnitArgs& a, const int* pre, const int* lens, int& u0) {
   Walk c;
   int lo = 0, hi = a.batch - 1;                     // the sequence b with pre[b] <= u0 < pre[b + 1]
@@ -178,13 +179,13 @@ __device__ __forceinline__ Walk walk_from(const UnitArgs& a, const int* pre, con
   }
   c.b = lo;
   c.len = lens[lo];
-  c.nch = units_of<SP>(a, c.len);
+  c.nch = units_of<SP, UNIT>(a, c.len);
   const int r = u0 - pre[lo];
   c.h = r / (c.nch + kEnd);
   c.chunk = r - c.h * (c.nch + kEnd);
   if (c.chunk >= c.nch) {                           // behind the last unit of a (sequence, head)
     --c.chunk;
-    u0 += advance<SP>(a, pre, lens, c) - 1;
+    u0 += advance<SP, UNIT>(a, pre, lens, c) - 1;
   }
   return c;
 }
@@ -310,12 +311,16 @@ __device__ __forceinline__ void join_parts(const UnitArgs& a, const int4* owe, i
   }
 }
 
-// SP: the block that a unit is of, one behind the sequence's last where the
-// list names none.
-__device__ __forceinline__ int block_of(const UnitArgs& a, const Walk& w, bool there) {
-  const int kvh = a.nht == 1 ? w.h : w.h / a.nht, n = (w.len + kUnit - 1) / kUnit;
-  const int i = there ? a.sel[((long long)w.b * (a.hu / a.nht) + kvh) * a.nsel + w.chunk] : n;
-  return (unsigned)i < (unsigned)n ? i : n;
+// The first token of the TW that a warp has of a unit; SP: behind the sequence's
+// last where the list names no block.
+template <bool SP, int UNIT, int TW>
+__device__ __forceinline__ int first_token(const UnitArgs& a, const Walk& w, int warp, bool there) {
+  if (!SP) return w.chunk * UNIT + warp * TW;
+  const int kvh = a.nht == 1 ? w.h : w.h / a.nht, n = (w.len + Q2_BLOCK - 1) / Q2_BLOCK;
+  const int i = w.chunk * (UNIT / Q2_BLOCK) + warp * TW / Q2_BLOCK;
+  int block = n;
+  if (there && i < min(n, a.nsel)) block = a.sel[((long long)w.b * (a.hu / a.nht) + kvh) * a.nsel + i];
+  return ((unsigned)block < (unsigned)n ? block : n) * Q2_BLOCK + warp * TW % Q2_BLOCK;
 }
 
 // ---------------------------------------------------------------- host side

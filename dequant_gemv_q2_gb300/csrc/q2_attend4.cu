@@ -43,18 +43,30 @@ namespace {
 __device__ unsigned int q2_attend4_error;
 
 struct Attend4Args : UnitArgs {
-  Pages pg;                     // codes
-  Pages sp;                     // steps and offsets
-  int aligned;                  // page % 16 == 0: a tile lies in one page
+  const unsigned char* k;       // codes; strides in 16 bytes
+  const unsigned char* ks;      // pairs; strides in pairs
+  long long v, vs;              // the values' pools, in bytes behind the keys'
+  uint32_t page_stride, token_stride, head_stride;
+  uint32_t s_page_stride, s_token_stride, s_head_stride;
+  const int* table;
+  long long table_stride;
+  int npages, page;
+  uint32_t page_mul, page_sh;   // of page_of()
+  int aligned;                  // a step's tokens of a warp lie in one page
 };
+
+// Tokens of a warp's step: two tiles where registers allow it, which share the
+// copies' addresses, the maximum and the rescaling.
+template <int D>
+__host__ __device__ constexpr int step_of() { return D == 256 ? 16 : 32; }
 
 template <int D>
 __host__ __device__ constexpr int ctas_of() { return D == 256 ? 1 : D == 128 ? 2 : 3; }
 
 template <int D, int G, int H>
 struct Shape {
-  static constexpr int STAGES = 4;
-  static constexpr int kCodes = kTile * D / 2, kPairs = kTile * G * 4;   // bytes of a tile, keys or values
+  static constexpr int STAGES = 3, TW = step_of<D>();
+  static constexpr int kCodes = TW * D / 2, kPairs = TW * G * 4;         // bytes of a step, keys or values
   static constexpr int kStage = 2 * (kCodes + kPairs);
   static constexpr int kRing = kWarps * STAGES * kStage;
   static constexpr int kSums = H * D * 4;                                // a warp's numerators
@@ -64,32 +76,63 @@ struct Shape {
   static int smem(int batch) { return fixed + 4 * (2 * batch + 1); }
 };
 
+// N bytes, or zeros
 template <int N>
-__device__ __forceinline__ void cp_pairs(uint32_t dst, const void* src, bool live) {
-  if constexpr (N == 32) {
-    cp16(dst, src, live);
-    cp16(dst + 16, static_cast<const char*>(src) + 16, live);
-  } else if constexpr (N == 16) {
-    cp16(dst, src, live);
+__device__ __forceinline__ void cp_pairs(uint32_t dst, const unsigned char* src, bool live) {
+  if constexpr (N >= 16) {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) cp16(dst + i, src + i, live);
   } else {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(live ? N : 0) : "memory");
   }
 }
 
-// The (step, offset) of group g of tokens t and t + 1 of a tile.
+__device__ __forceinline__ void cp16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ float2 halves(uint32_t r) { return __half22float2(*reinterpret_cast<const __half2*>(&r)); }
+
+// The pairs (step, offset) of tokens t, t + 1 of a step, all groups.
 template <int G>
-__device__ __forceinline__ void pairs_of(const unsigned char* tile, int t, int g, float2& a, float2& b) {
-  const __half2* h = reinterpret_cast<const __half2*>(tile) + t * G + g;
-  a = __half22float2(h[0]);
-  b = __half22float2(h[G]);
+__device__ __forceinline__ void load_pairs(const unsigned char* pairs, int t, uint32_t (&r)[2][G]) {
+  const unsigned char* at = pairs + t * (4 * G);
+  if constexpr (G == 1) {
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    r[0][0] = x.x;
+    r[1][0] = x.y;
+  } else if constexpr (G == 2) {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    r[0][0] = x.x;
+    r[0][1] = x.y;
+    r[1][0] = x.z;
+    r[1][1] = x.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < G; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + u * (4 * G) + 4 * i);
+        r[u][i] = x.x;
+        r[u][i + 1] = x.y;
+        r[u][i + 2] = x.z;
+        r[u][i + 3] = x.w;
+      }
+  }
+}
+
+// 2^x to 2 units in the last place; what is below the normal numbers is zero
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // w0, w1 >= 0 as pairs of fp16 numbers whose sums they are, to 2^-22.
 __device__ __forceinline__ void split2(float w0, float w1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(w0, w1);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(w0 - f.x, w1 - f.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __half2 l = __floats2half2_rn(fma_h(lo16(hi), 0xbc00, w0), fma_h(hi16(hi), 0xbc00, w1));   // (0xbc00 is -1)
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -106,6 +149,7 @@ template <int D, int G, int H, bool SP>
 __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid_constant__ Attend4Args a) {
   using S = Shape<D, G, H>;
   constexpr int RH = H / 8, STAGES = S::STAGES, NB = D / 32;   // NB: 16-byte pieces of a row, 32 columns each
+  constexpr int TW = S::TW, NTL = TW / kTile, UNIT = kWarps * TW;
   constexpr int RPI = 32 / NB, NT = D / 8, BPG = NB / G;       // BPG: pieces of a group
   extern __shared__ __align__(128) unsigned char q2_att4_smem[];
   unsigned char* sums = q2_att4_smem + S::kRing;
@@ -118,11 +162,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
 
   pdl_wait();
   pdl_trigger();
-  const Share sh = share_out<D, SP>(a, nowed, pre, lens, &q2_attend4_error);
+  const Share sh = share_out<D, SP, UNIT>(a, nowed, pre, lens, &q2_attend4_error);
   int u0 = sh.u0;
   const int u1 = sh.u1;
   if (u0 >= u1) return;
-  Walk c = walk_from<SP>(a, pre, lens, u0);         // the unit in use
+  Walk c = walk_from<SP, UNIT>(a, pre, lens, u0);   // the unit in use
   if (u0 >= u1) return;
 
   // ---- the warp's loads, STAGES - 1 units ahead of their use
@@ -130,63 +174,75 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   const uint32_t ring = saddr(myring);
   Walk p = c;
   int pu = u0, pslot = 0, ppage = -1, pt0 = 0;      // place of the unit to load, its stage, page of this lane's row, first token
-  uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; a stage's tokens, 5 bits each
-  const int piece = lane % NB, row0 = lane / NB;
+  uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; a stage's tokens, 8 bits each
+  const int piece = lane % NB, row0 = lane / NB, prow = lane % TW;
   // the pieces of a row are exchanged so that eight rows of one piece lie in different banks
   auto place = [&](int row, int pc) { return row * (D / 2) + ((pc ^ (row / (8 / NB) & (NB - 1))) << 4); };
-  auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
-    pt0 = (SP ? block_of(a, p, pu < u1) : p.chunk) * kUnit + warp * kTile;
-    const int t = pt0 + (a.aligned ? 0 : lane & 15);
-    ppage = pu < u1 && t < p.len ? a.pg.table[p.b * a.pg.table_stride + page_of(a.pg, t)] : -1;
+  auto lookup = [&]() {                             // tokens in one page: its page; else that of this lane's row
+    pt0 = first_token<SP, UNIT, TW>(a, p, warp, pu < u1);
+    const int t = pt0 + (a.aligned ? 0 : prow);
+    ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
   };
   lookup();
   auto issue = [&]() {
     if (pu < u1) {
-      const int have = min(max(p.len - pt0, 0), kTile);
-      haves = (haves & ~(31u << (5 * pslot))) | (uint32_t)have << (5 * pslot);
+      const int have = min(max(p.len - pt0, 0), TW);
+      haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)have << (8 * pslot);
       if (have) {
-        const int kvh = a.nht == 1 ? p.h : p.h / a.nht;
+        const uint32_t kvh = a.nht == 1 ? p.h : p.h / a.nht;
         const uint32_t dst = ring + pslot * S::kStage;
-        // codes: this lane's piece of rows row0, row0 + RPI, ..; pairs: row lane % 16 of the keys, above lane 16 of the values
-        const int t = pt0 + (a.aligned ? 0 : lane & 15), pi = page_of(a.pg, t);
-        const bool there = (unsigned)ppage < (unsigned)a.pg.npages;
+        const int t = pt0 + (a.aligned ? 0 : prow);
+        const bool there = (unsigned)ppage < (unsigned)a.npages;
         const bool bad = __any_sync(0xffffffffu, t < p.len && !there);
-        const int at = t - pi * a.pg.page;          // the place in the page of the tile's first token, or of this lane's row
-        const int prow = lane & 15;
-        const unsigned char* ps = (lane < 16 ? a.sp.k : a.sp.v);
-        if (there)
-          ps += ppage * a.sp.page_stride + (at + (a.aligned ? prow : 0)) * a.sp.token_stride + kvh * a.sp.head_stride;
-        cp_pairs<4 * G>(dst + 2 * S::kCodes + (lane < 16 ? 0 : S::kPairs) + prow * (4 * G), ps, there && prow < have);
-        if (a.aligned) {
-          const long long off = there ? ppage * a.pg.page_stride + (at + row0) * a.pg.token_stride + kvh * a.pg.head_stride : 0;
-          const unsigned char* k = a.pg.k + off + piece * 16;
-          const unsigned char* v = a.pg.v + off + piece * 16;
+        // the place of the tokens' first (else of this lane's row) in the pools
+        const uint32_t at = t - page_of(a, t) * a.page, page = there ? ppage : 0;
+        const unsigned long long off = (unsigned long long)page * a.page_stride + (at * a.token_stride + kvh * a.head_stride);
+        const unsigned long long soff = (unsigned long long)page * a.s_page_stride +
+                                        ((at + (a.aligned ? prow : 0)) * a.s_token_stride + kvh * a.s_head_stride);
+        const uint32_t pd = dst + 2 * S::kCodes + prow * (4 * G);
+        const unsigned char* ps = a.ks + soff * 4;
+        if (a.aligned && have == TW && !bad) {      // the usual step: all rows, one behind another
+          if constexpr (TW == 32) {
+            cp_pairs<4 * G>(pd, ps, true);
+            cp_pairs<4 * G>(pd + S::kPairs, ps + a.vs, true);
+          } else {
+            cp_pairs<4 * G>(pd + (lane < 16 ? 0 : S::kPairs), ps + (lane < 16 ? 0 : a.vs), true);
+          }
+          const unsigned char* k = a.k + (off + (uint32_t)row0 * a.token_stride + piece) * 16;
+          const unsigned long long step = (unsigned long long)a.token_stride * (RPI * 16);
 #pragma unroll
-          for (int i = 0; i < kTile / RPI; ++i) {
-            const bool live = there && row0 + i * RPI < have;
+          for (int i = 0; i < TW / RPI; ++i) {
             const uint32_t d = dst + place(row0 + i * RPI, piece);
-            const long long step = live ? i * RPI * a.pg.token_stride : 0;
-            cp16(d, k + step, live);
-            cp16(d + S::kCodes, v + step, live);
+            cp16_all(d, k);
+            cp16_all(d + S::kCodes, k + a.v);
+            k += step;
           }
         } else {
-          const long long off =
-              there ? ppage * a.pg.page_stride + at * a.pg.token_stride + kvh * a.pg.head_stride : -1;
-#pragma unroll
-          for (int i = 0; i < kTile / RPI; ++i) {
+          const bool plive = there && prow < have;
+          if (!plive) ps = a.ks;
+          if constexpr (TW == 32) {
+            cp_pairs<4 * G>(pd, ps, plive);
+            cp_pairs<4 * G>(pd + S::kPairs, ps + a.vs, plive);
+          } else {
+            cp_pairs<4 * G>(pd + (lane < 16 ? 0 : S::kPairs), ps + (lane < 16 ? 0 : a.vs), plive);
+          }
+          const unsigned long long mine = there ? off : ~0ull;
+#pragma unroll 2
+          for (int i = 0; i < TW / RPI; ++i) {
             const int row = row0 + i * RPI;
-            const long long o = __shfl_sync(0xffffffffu, off, row);
-            const bool live = o >= 0 && row < have;
-            const long long e = (live ? o : 0) + piece * 16;
+            unsigned long long o = a.aligned ? mine : __shfl_sync(0xffffffffu, mine, row);
+            const bool live = o != ~0ull && row < have;
+            if (a.aligned) o += (uint32_t)row * a.token_stride;
+            const unsigned char* k = a.k + (live ? o + piece : 0) * 16;
             const uint32_t d = dst + place(row, piece);
-            cp16(d, a.pg.k + e, live);
-            cp16(d + S::kCodes, a.pg.v + e, live);
+            cp16(d, k, live);
+            cp16(d + S::kCodes, k + a.v, live);
           }
         }
         if (bad && lane == 0) atomicOr(&q2_attend4_error, Q2_ERR_PAGE);
         badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
       }
-      pu += advance<SP>(a, pre, lens, p);
+      pu += advance<SP, UNIT>(a, pre, lens, p);
       lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
     }
@@ -194,8 +250,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   };
 
   // ---- sums of the current (sequence, head)
-  uint32_t qa[NB][RH][4];                           // the queries of 32 columns: codes 0 and 2, then 1 and 3 of the words 2j, 2j + 1
-  float qs[RH][G];                                  // their sums over the groups
+  // The queries of 32 columns, for codes 0 and 2, then 1 and 3 of the words 2j,
+  // 2j + 1: times a power of two that brings a head's largest to 2^10 .. 2^11,
+  // those of codes 1 and 3 (which come 16 times too large) a sixteenth of that.
+  uint32_t qa[NB][RH][4];
+  float qs[RH][G], qf[RH];                          // their sums over the groups (in the units of the products); what a score is to be multiplied by
   float o[NT][4], om[RH][G], m[RH], l[RH];          // numerators of codes and of offsets, maximum, denominator
   uint32_t top_s = 1;                               // exponent field of the largest step so far, 1 at least
   bool fresh = true;
@@ -211,27 +270,51 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
       const __half* q = a.q + c.b * a.ldq + (long long)(qh + g) * D + 8 * j;
 #pragma unroll
       for (int y = 0; y < RH; ++y) {
+        uint4 r[NB];
+        uint32_t top = 0;                           // the largest exponent field
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          r[b] = g + 8 * y < rows ? *reinterpret_cast<const uint4*>(q + 8 * y * D + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {r[b].x, r[b].y, r[b].z, r[b].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = halves(w[i]);
+            top = max(top, max(__float_as_uint(f.x) >> 23 & 255u, __float_as_uint(f.y) >> 23 & 255u));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = min(max(top, 90u), 142u);             // (a head of zeros; an infinite or NaN column, which stays one)
+        const float up = __uint_as_float((127u + 10u + 127u - top) << 23);           // 2^10 over the largest's power of two
+        qf[y] = a.sc2 * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);      // (a code is c 2^-22)
 #pragma unroll
         for (int i = 0; i < G; ++i) qs[y][i] = om[y][i] = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint4 r = g + 8 * y < rows ? *reinterpret_cast<const uint4*>(q + 8 * y * D + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
-          // columns 8j .. 8j + 7 are r.x = (0, 1), r.y = (2, 3), r.z = (4, 5), r.w = (6, 7); words 2j and 2j + 1 are 0..3 and 4..7
-          qa[b][y][0] = __byte_perm(r.x, r.z, 0x5410);          // (0, 4): code 0
-          qa[b][y][1] = __byte_perm(r.y, r.w, 0x5410);          // (2, 6): code 2
-          qa[b][y][2] = __byte_perm(r.x, r.z, 0x7632);          // (1, 5): code 1
-          qa[b][y][3] = __byte_perm(r.y, r.w, 0x7632);          // (3, 7): code 3
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+          const uint32_t w[4] = {r[b].x, r[b].y, r[b].z, r[b].w};
+          float f[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            qs[y][b / BPG] += f.x + f.y;
+            const float2 x = halves(w[i]);
+            f[2 * i] = x.x * up;
+            f[2 * i + 1] = x.y * up;
+            qs[y][b / BPG] += f[2 * i] + f[2 * i + 1];
           }
+          auto pack = [](float x, float y, float s) {
+            const __half2 h = __floats2half2_rn(x * s, y * s);
+            return *reinterpret_cast<const uint32_t*>(&h);
+          };
+          // words 2j and 2j + 1 are columns 0..3 and 4..7 of these eight
+          qa[b][y][0] = pack(f[0], f[4], 1.f);
+          qa[b][y][1] = pack(f[2], f[6], 1.f);
+          qa[b][y][2] = pack(f[1], f[5], 0.0625f);
+          qa[b][y][3] = pack(f[3], f[7], 0.0625f);
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           qs[y][i] += __shfl_xor_sync(0xffffffffu, qs[y][i], 1);
           qs[y][i] += __shfl_xor_sync(0xffffffffu, qs[y][i], 2);
+          qs[y][i] *= 1.f / 4194304.f;              // 2^-22
         }
         m[y] = -INFINITY;
         l[y] = 0.f;
@@ -250,88 +333,94 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
       --ahead;
       continue;
     }
-    const int fin = (int)(haves >> (5 * slot) & 31u) - 1;      // row of the last token; negative: none
+    const int fin = (int)(haves >> (8 * slot) & 255u) - 1;     // row of the last token; negative: none
     if (fin >= 0) {
-      const unsigned char* stage = myring + slot * S::kStage;
-      const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
-      const unsigned char* ks = stage + 2 * S::kCodes;
+      const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes;
       const unsigned char* vs = ks + S::kPairs;
-      // ---- scores of 16 tokens: x[y] of row g + 8 y, tokens 2j, 2j + 1, 2j + 8, 2j + 9
-      float x[RH][4], al[RH];
-#pragma unroll
-      for (int y = 0; y < RH; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[y][e] = 0.f;
+      const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
+      // ---- scores: x[n][y] of row g + 8 y, tokens 8 n + 2j, 8 n + 2j + 1
+      float x[2 * NTL][RH][2], al[RH];
       const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
-      float lowc[2][4], highc[2][4];                // sums of codes 0 and 2, of codes 1 and 3, per 8 tokens
 #pragma unroll
-      for (int b = 0; b < NB; b += 2) {
-        uint32_t r[4];                              // pieces b, b + 1 of tokens 0..7, then of 8..15
-        ldsm4(r, kt + place(krow, b + kpiece));
+      for (int i = 0; i < NTL; ++i) {
+        uint32_t sm[2][2][G];
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          if ((b + bb) % BPG == 0) {
+        for (int n = 0; n < 2; ++n) load_pairs<G>(ks, 16 * i + 8 * n + 2 * j, sm[n]);
+        float acc[2][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+        for (int b = 0; b < NB; b += 2) {
+          uint32_t r[4];                            // pieces b, b + 1 of tokens 0..7, then of 8..15
+          ldsm4(r, kt + i * (kTile * D / 2) + place(krow, b + kpiece));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) lowc[n][e] = highc[n][e] = 0.f;
-          }
-          const auto& q = qa[b + bb];
+          for (int bb = 0; bb < 2; ++bb) {
+            if ((b + bb) % BPG == 0) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t w = r[2 * n + bb], up = w << 2, dn = w >> 6;      // codes 0, 1 and 2, 3 in bits 2..5, 6..9
-            mma(lowc[n], q[0][0], RH == 2 ? q[RH - 1][0] : 0u, q[0][1], RH == 2 ? q[RH - 1][1] : 0u, up & 0x003c003cu,
-                dn & 0x003c003cu);
-            mma(highc[n], q[0][2], RH == 2 ? q[RH - 1][2] : 0u, q[0][3], RH == 2 ? q[RH - 1][3] : 0u, up & 0x03c003c0u,
-                dn & 0x03c003c0u);
-          }
-          if ((b + bb) % BPG == BPG - 1) {
-            constexpr float kLow = 4194304.f, kHigh = 262144.f;            // 2^22, 2^18
-            const int gi = (b + bb) / BPG;
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+            }
+            const auto& q = qa[b + bb];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              float2 s0, s1;
-              pairs_of<G>(ks, 8 * n + 2 * j, gi, s0, s1);
+              const uint32_t w = r[2 * n + bb], lw = w << 2, hw = w >> 6;    // codes 0, 1 and 2, 3 in bits 2..5, 6..9
+              mma(acc[n], q[0][0], RH == 2 ? q[RH - 1][0] : 0u, q[0][1], RH == 2 ? q[RH - 1][1] : 0u, lw & 0x003c003cu,
+                  hw & 0x003c003cu);
+              mma(acc[n], q[0][2], RH == 2 ? q[RH - 1][2] : 0u, q[0][3], RH == 2 ? q[RH - 1][3] : 0u, lw & 0x03c003c0u,
+                  hw & 0x03c003c0u);
+            }
+            if ((b + bb) % BPG == BPG - 1) {
+              const int gi = (b + bb) / BPG;
 #pragma unroll
-              for (int y = 0; y < RH; ++y) {
-                const float t0 = fmaf(highc[n][2 * y], kHigh, lowc[n][2 * y] * kLow);
-                const float t1 = fmaf(highc[n][2 * y + 1], kHigh, lowc[n][2 * y + 1] * kLow);
-                x[y][2 * n] = fmaf(s0.x, t0, fmaf(s0.y, qs[y][gi], x[y][2 * n]));
-                x[y][2 * n + 1] = fmaf(s1.x, t1, fmaf(s1.y, qs[y][gi], x[y][2 * n + 1]));
-              }
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float2 s = halves(sm[n][e][gi]);
+#pragma unroll
+                  for (int y = 0; y < RH; ++y) {
+                    float& z = x[2 * i + n][y][e];
+                    z = fmaf(s.x, acc[n][2 * y + e], gi ? fmaf(s.y, qs[y][gi], z) : s.y * qs[y][0]);
+                  }
+                }
             }
           }
         }
       }
       // ---- probabilities
-      uint32_t most = 0;                            // the largest step of the tile's values
+      uint32_t vp[2 * NTL][2][G];                   // the values' pairs
+      __half2 most = __float2half2_rn(0.f);
 #pragma unroll
-      for (int i = 0; i < G; ++i)
+      for (int n = 0; n < 2 * NTL; ++n) {
+        load_pairs<G>(vs, 8 * n + 2 * j, vp[n]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          most = max(most, (uint32_t)reinterpret_cast<const unsigned short*>(vs)[2 * ((2 * j + (e & 1) + (e >> 1) * 8) * G + i)]);
-      most = __reduce_max_sync(0xffffffffu, most & 0x7fffu) >> 10;
-      bool rise = most > top_s;
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][e][i]));
+      }
+      const uint32_t most_s = __reduce_max_sync(0xffffffffu, (uint32_t)__half_as_ushort(__low2half(most))) >> 10;
+      bool rise = most_s > top_s;
       const uint32_t before_s = top_s;
-      top_s = max(top_s, most);
+      top_s = max(top_s, most_s);
 #pragma unroll
       for (int y = 0; y < RH; ++y) {
+        float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[y][e] *= a.sc2;
-        if (fin < kTile - 1) {
+        for (int n = 0; n < 2 * NTL; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (2 * j + (e & 1) + (e >> 1) * 8 > fin) x[y][e] = -INFINITY;
-        }
-        float top = fmaxf(fmaxf(x[y][0], x[y][1]), fmaxf(x[y][2], x[y][3]));
+          for (int e = 0; e < 2; ++e) {
+            x[n][y][e] *= qf[y];
+            if (fin < TW - 1 && 8 * n + 2 * j + e > fin) x[n][y][e] = -INFINITY;
+            top = fmaxf(top, x[n][y][e]);
+          }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float mn = fmaxf(m[y], top), ref = mn == -INFINITY ? 0.f : mn;
         rise = rise || mn > m[y];
-        al[y] = exp2f(m[y] - ref);
+        al[y] = ex2(m[y] - ref);
         m[y] = mn;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[y][e] = exp2f(x[y][e] - ref);
+        for (int n = 0; n < 2 * NTL; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[n][y][e] = ex2(x[n][y][e] - ref);
       }
       if (__any_sync(0xffffffffu, rise)) {          // a new maximum somewhere, or a new scale: scale what there is
         const float fall = __uint_as_float((127u - (top_s - before_s)) << 23);
@@ -350,44 +439,55 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
           o[t][3] *= al[RH - 1];
         }
       }
-#pragma unroll
-      for (int y = 0; y < RH; ++y) {
-        l[y] += (x[y][0] + x[y][1]) + (x[y][2] + x[y][3]);
-        if ((badslots >> slot) & 1u) l[y] = __int_as_float(0x7fc00000);
-      }
+      if ((badslots >> slot) & 1u) l[0] = l[RH - 1] = __int_as_float(0x7fc00000);
       // ---- numerators: p s scaled so that it stays below 2^15
       const float scale = __uint_as_float((127u + 29u - top_s) << 23);
-      uint32_t hi[RH][2], lo[RH][2];
       const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
 #pragma unroll
-      for (int b = 0; b < NB; b += 2) {
-        uint32_t r[4];                              // tokens 0..7 and 8..15 of piece b, then of b + 1
-        ldsm4t(r, vt + place(vrow, b + vpiece));
+      for (int i = 0; i < NTL; ++i) {
+        float xs[RH][4];
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          if ((b + bb) % BPG == 0) {
-            const int gi = (b + bb) / BPG;
-            float2 s[4];
-            pairs_of<G>(vs, 2 * j, gi, s[0], s[1]);
-            pairs_of<G>(vs, 2 * j + 8, gi, s[2], s[3]);
+        for (int y = 0; y < RH; ++y)
 #pragma unroll
-            for (int y = 0; y < RH; ++y) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) om[y][gi] = fmaf(x[y][e], fmaf(8.f, s[e].x, s[e].y), om[y][gi]);
-              split2(x[y][0] * (s[0].x * scale), x[y][1] * (s[1].x * scale), hi[y][0], lo[y][0]);
-              split2(x[y][2] * (s[2].x * scale), x[y][3] * (s[3].x * scale), hi[y][1], lo[y][1]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float pr = x[2 * i + e / 2][y][e % 2];
+            l[y] += pr;
+            xs[y][e] = pr * scale;
           }
+        uint32_t hi[RH][2], lo[RH][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {             // code i of the words: columns 32 (b + bb) + 4 word + i
-            const uint32_t b0 = centred(i < 2 ? r[2 * bb] : r[2 * bb] >> 8, i % 2);
-            const uint32_t b1 = centred(i < 2 ? r[2 * bb + 1] : r[2 * bb + 1] >> 8, i % 2);
-            float(&t)[4] = o[4 * (b + bb) + i];
-            if constexpr (RH == 1) {                // hi in rows 0..7, lo in rows 8..15
-              mma(t, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
-            } else {
-              mma(t, hi[0][0], hi[RH - 1][0], hi[0][1], hi[RH - 1][1], b0, b1);
-              mma(t, lo[0][0], lo[RH - 1][0], lo[0][1], lo[RH - 1][1], b0, b1);
+        for (int b = 0; b < NB; b += 2) {
+          uint32_t r[4];                            // tokens 0..7 and 8..15 of piece b, then of b + 1
+          ldsm4t(r, vt + i * (kTile * D / 2) + place(vrow, b + vpiece));
+#pragma unroll
+          for (int bb = 0; bb < 2; ++bb) {
+            if ((b + bb) % BPG == 0) {
+              const int gi = (b + bb) / BPG;
+              float2 s[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[e] = halves(vp[2 * i + e / 2][e % 2][gi]);
+                s[e].y = fmaf(8.f, s[e].x, s[e].y);
+              }
+#pragma unroll
+              for (int y = 0; y < RH; ++y) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) om[y][gi] = fmaf(x[2 * i + e / 2][y][e % 2], s[e].y, om[y][gi]);
+                split2(xs[y][0] * s[0].x, xs[y][1] * s[1].x, hi[y][0], lo[y][0]);
+                split2(xs[y][2] * s[2].x, xs[y][3] * s[3].x, hi[y][1], lo[y][1]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {           // code k of the words: columns 32 (b + bb) + 4 word + k
+              const uint32_t b0 = centred(k < 2 ? r[2 * bb] : r[2 * bb] >> 8, k % 2);
+              const uint32_t b1 = centred(k < 2 ? r[2 * bb + 1] : r[2 * bb + 1] >> 8, k % 2);
+              float(&t)[4] = o[4 * (b + bb) + k];
+              if constexpr (RH == 1) {              // hi in rows 0..7, lo in rows 8..15
+                mma(t, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+              } else {
+                mma(t, hi[0][0], hi[RH - 1][0], hi[0][1], hi[RH - 1][1], b0, b1);
+                mma(t, lo[0][0], lo[RH - 1][0], lo[0][1], lo[RH - 1][1], b0, b1);
+              }
             }
           }
         }
@@ -396,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
     const Walk w = c;
-    u += advance<SP>(a, pre, lens, c);
+    u += advance<SP, UNIT>(a, pre, lens, c);
     const bool ends = w.chunk + 1 == w.nch, all = u >= u1;
     if (ends || all) {                              // the end of this (sequence, head), or of this CTA's share of it
       // Every warp leaves its sums, then joins a quarter of the columns of all
@@ -470,13 +570,38 @@ extern "C" int q2_attend4(const q2_kv4* kv, const void* q, long long ldq, const 
   if (!kv) return Q2_EINVAL;
   if (sel ? nsel < 1 : nsel != 0) return Q2_ESHAPE;
   Attend4Args a = {};
+  Pages pg, sp;
   CacheShape c;
   UnitCall u = {q, ldq, lens, batch, q_heads, sel, nsel, scale, out, ldo, ws, ws_bytes};
   int st = u.check(kv);
   if (st) return st;
   if (batch == 0) return Q2_OK;
-  if ((st = check_cache4(kv, batch, a.pg, a.sp, c)) || (st = u.fill(c, sel != nullptr, a))) return st;
-  a.aligned = kv->page_size % kTile == 0;
+  if ((st = check_cache4(kv, batch, pg, sp, c)) || (st = u.fill(c, sel != nullptr, a))) return st;
+  // strides, and places within a page, are counted in 32 bits (of 16 bytes, of pairs)
+  auto within = [&](long long page, long long token, long long head) {
+    return page <= 0xffffffffll && token * (c.page - 1) + head * (c.kv_heads - 1) <= 0xffffffffll && token <= 0xffffffffll &&
+           head <= 0xffffffffll;
+  };
+  if (!within(kv->page_stride / 16, kv->token_stride / 16, kv->head_stride / 16) ||
+      !within(kv->s_page_stride, kv->s_token_stride, kv->s_head_stride))
+    return Q2_ESHAPE;
+  a.k = pg.k;
+  a.ks = sp.k;
+  a.v = pg.v - pg.k;
+  a.vs = sp.v - sp.k;
+  a.page_stride = (uint32_t)(kv->page_stride / 16);
+  a.token_stride = (uint32_t)(kv->token_stride / 16);
+  a.head_stride = (uint32_t)(kv->head_stride / 16);
+  a.s_page_stride = (uint32_t)kv->s_page_stride;
+  a.s_token_stride = (uint32_t)kv->s_token_stride;
+  a.s_head_stride = (uint32_t)kv->s_head_stride;
+  a.table = kv->table;
+  a.table_stride = kv->table_stride;
+  a.npages = kv->npages;
+  a.page = kv->page_size;
+  a.page_mul = pg.page_mul;
+  a.page_sh = pg.page_sh;
+  a.aligned = kv->page_size % (c.D == 256 ? step_of<256>() : step_of<128>()) == 0;
   return sel ? attend4<true>(kv, a, c, u.units, stream) : attend4<false>(kv, a, c, u.units, stream);
 }
 
