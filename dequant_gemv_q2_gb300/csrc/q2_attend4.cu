@@ -61,7 +61,7 @@ template <int D>
 __host__ __device__ constexpr int step_of() { return D == 256 ? 16 : 32; }
 
 template <int D>
-__host__ __device__ constexpr int ctas_of() { return D == 256 ? 1 : D == 128 ? 2 : 3; }
+__host__ __device__ constexpr int ctas_of(int H) { return D == 256 || (D == 128 && H == 16) ? 2 : 3; }
 
 template <int D, int G, int H>
 struct Shape {
@@ -93,31 +93,24 @@ __device__ __forceinline__ void cp16_all(uint32_t dst, const void* src) {
 
 __device__ __forceinline__ float2 halves(uint32_t r) { return __half22float2(*reinterpret_cast<const __half2*>(&r)); }
 
-// The pairs (step, offset) of tokens t, t + 1 of a step, all groups.
+// The pairs (step, offset) of a token, all groups.
 template <int G>
-__device__ __forceinline__ void load_pairs(const unsigned char* pairs, int t, uint32_t (&r)[2][G]) {
-  const unsigned char* at = pairs + t * (4 * G);
+__device__ __forceinline__ void load_pairs(const unsigned char* at, uint32_t (&r)[G]) {
   if constexpr (G == 1) {
-    const uint2 x = *reinterpret_cast<const uint2*>(at);
-    r[0][0] = x.x;
-    r[1][0] = x.y;
+    r[0] = *reinterpret_cast<const uint32_t*>(at);
   } else if constexpr (G == 2) {
-    const uint4 x = *reinterpret_cast<const uint4*>(at);
-    r[0][0] = x.x;
-    r[0][1] = x.y;
-    r[1][0] = x.z;
-    r[1][1] = x.w;
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    r[0] = x.x;
+    r[1] = x.y;
   } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < G; i += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(at + u * (4 * G) + 4 * i);
-        r[u][i] = x.x;
-        r[u][i + 1] = x.y;
-        r[u][i + 2] = x.z;
-        r[u][i + 3] = x.w;
-      }
+    for (int i = 0; i < G; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(at + 4 * i);
+      r[i] = x.x;
+      r[i + 1] = x.y;
+      r[i + 2] = x.z;
+      r[i + 3] = x.w;
+    }
   }
 }
 
@@ -144,13 +137,22 @@ __device__ __forceinline__ uint32_t centred(uint32_t w, bool high) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// H: query heads of a unit, 8 or 16 (rows of the products); G: groups of a row
-template <int D, int G, int H, bool SP>
-__global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid_constant__ Attend4Args a) {
+// 8 x 8 numbers of 16 bits, transposed
+__device__ __forceinline__ uint32_t transpose(uint32_t r) {
+  uint32_t t;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(r));
+  return t;
+}
+
+// H: query heads of a unit, 8 or 16 (columns of the products); FOLD: four at
+// most; G: groups of a row
+template <int D, int G, int H, bool FOLD, bool SP>
+__global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __grid_constant__ Attend4Args a) {
   using S = Shape<D, G, H>;
-  constexpr int RH = H / 8, STAGES = S::STAGES, NB = D / 32;   // NB: 16-byte pieces of a row, 32 columns each
+  constexpr int NH = H / 8, STAGES = S::STAGES, NB = D / 32;   // NB: 16-byte pieces of a row, 32 columns each
   constexpr int TW = S::TW, NTL = TW / kTile, UNIT = kWarps * TW;
-  constexpr int RPI = 32 / NB, NT = D / 8, BPG = NB / G;       // BPG: pieces of a group
+  constexpr int RPI = 32 / NB, BPG = NB / G;                   // rows of a copy instruction; pieces of a group
+  static_assert(!FOLD || H == 8, "");
   extern __shared__ __align__(128) unsigned char q2_att4_smem[];
   unsigned char* sums = q2_att4_smem + S::kRing;
   float2* wml = reinterpret_cast<float2*>(sums + kWarps * S::kSums);     // [kWarps][H] maximum, denominator
@@ -173,33 +175,42 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   unsigned char* const myring = q2_att4_smem + warp * (STAGES * S::kStage);
   const uint32_t ring = saddr(myring);
   Walk p = c;
-  int pu = u0, pslot = 0, ppage = -1, pt0 = 0;      // place of the unit to load, its stage, page of this lane's row, first token
+  int pu = u0, pslot = 0, ppage = -1, pt0 = 0, pat = 0;   // place of the unit to load, its stage; page, first token, place in the page (of this lane's row where not aligned)
   uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; a stage's tokens, 8 bits each
   const int piece = lane % NB, row0 = lane / NB, prow = lane % TW;
   // the pieces of a row are exchanged so that eight rows of one piece lie in different banks
-  auto place = [&](int row, int pc) { return row * (D / 2) + ((pc ^ (row / (8 / NB) & (NB - 1))) << 4); };
+  auto place = [](int row, int pc) { return row * (D / 2) + ((pc ^ (row / (8 / NB) & (NB - 1))) << 4); };
+  const uint32_t cdst = ring + place(row0, piece);  // (rows RPI apart have their pieces alike, of eight pieces the fifth for the first)
+  const uint32_t pdst = ring + 2 * S::kCodes + prow * (4 * G);
+  const int* trow = nullptr;                        // of p's (sequence, head): the table's row, the head's place
+  uint32_t phead = 0, pshead = 0;
+  auto enter = [&]() {
+    if (p.b >= a.batch) return;
+    const uint32_t kvh = a.nht == 1 ? p.h : p.h / a.nht;
+    trow = a.table + p.b * a.table_stride;
+    phead = kvh * a.head_stride;
+    pshead = kvh * a.s_head_stride;
+  };
   auto lookup = [&]() {                             // tokens in one page: its page; else that of this lane's row
     pt0 = first_token<SP, UNIT, TW>(a, p, warp, pu < u1);
-    const int t = pt0 + (a.aligned ? 0 : prow);
-    ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
+    const int t = pt0 + (a.aligned ? 0 : prow), pi = page_of(a, t);
+    pat = t - pi * a.page;
+    ppage = pu < u1 && t < p.len ? trow[pi] : -1;
   };
+  enter();
   lookup();
   auto issue = [&]() {
     if (pu < u1) {
       const int have = min(max(p.len - pt0, 0), TW);
       haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)have << (8 * pslot);
       if (have) {
-        const uint32_t kvh = a.nht == 1 ? p.h : p.h / a.nht;
-        const uint32_t dst = ring + pslot * S::kStage;
-        const int t = pt0 + (a.aligned ? 0 : prow);
         const bool there = (unsigned)ppage < (unsigned)a.npages;
-        const bool bad = __any_sync(0xffffffffu, t < p.len && !there);
-        // the place of the tokens' first (else of this lane's row) in the pools
-        const uint32_t at = t - page_of(a, t) * a.page, page = there ? ppage : 0;
-        const unsigned long long off = (unsigned long long)page * a.page_stride + (at * a.token_stride + kvh * a.head_stride);
+        const bool bad = __any_sync(0xffffffffu, (a.aligned || prow < have) && !there);
+        const uint32_t page = there ? ppage : 0;
+        const unsigned long long off = (unsigned long long)page * a.page_stride + (pat * a.token_stride + phead);
         const unsigned long long soff = (unsigned long long)page * a.s_page_stride +
-                                        ((at + (a.aligned ? prow : 0)) * a.s_token_stride + kvh * a.s_head_stride);
-        const uint32_t pd = dst + 2 * S::kCodes + prow * (4 * G);
+                                        ((pat + (a.aligned ? prow : 0)) * a.s_token_stride + pshead);
+        const uint32_t cd = cdst + pslot * S::kStage, pd = pdst + pslot * S::kStage;
         const unsigned char* ps = a.ks + soff * 4;
         if (a.aligned && have == TW && !bad) {      // the usual step: all rows, one behind another
           if constexpr (TW == 32) {
@@ -208,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
           } else {
             cp_pairs<4 * G>(pd + (lane < 16 ? 0 : S::kPairs), ps + (lane < 16 ? 0 : a.vs), true);
           }
-          const unsigned char* k = a.k + (off + (uint32_t)row0 * a.token_stride + piece) * 16;
+          const unsigned char* k = a.k + (off + ((uint32_t)row0 * a.token_stride + piece)) * 16;
           const unsigned long long step = (unsigned long long)a.token_stride * (RPI * 16);
 #pragma unroll
           for (int i = 0; i < TW / RPI; ++i) {
-            const uint32_t d = dst + place(row0 + i * RPI, piece);
+            const uint32_t d = (NB == 8 && i % 2 ? cd ^ 64u : cd) + i * (RPI * D / 2);
             cp16_all(d, k);
             cp16_all(d + S::kCodes, k + a.v);
             k += step;
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
             const bool live = o != ~0ull && row < have;
             if (a.aligned) o += (uint32_t)row * a.token_stride;
             const unsigned char* k = a.k + (live ? o + piece : 0) * 16;
-            const uint32_t d = dst + place(row, piece);
+            const uint32_t d = (NB == 8 && i % 2 ? cd ^ 64u : cd) + i * (RPI * D / 2);
             cp16(d, k, live);
             cp16(d + S::kCodes, k + a.v, live);
           }
@@ -243,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
         badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
       }
       pu += advance<SP, UNIT>(a, pre, lens, p);
+      if (p.chunk == 0) enter();
       lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
     }
@@ -250,31 +262,33 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   };
 
   // ---- sums of the current (sequence, head)
-  // The queries of 32 columns, for codes 0 and 2, then 1 and 3 of the words 2j,
-  // 2j + 1: times a power of two that brings a head's largest to 2^10 .. 2^11,
-  // those of codes 1 and 3 (which come 16 times too large) a sixteenth of that.
-  uint32_t qa[NB][RH][4];
-  float qs[RH][G], qf[RH];                          // their sums over the groups (in the units of the products); what a score is to be multiplied by
-  float o[NT][4], om[RH][G], m[RH], l[RH];          // numerators of codes and of offsets, maximum, denominator
+  // The queries of 32 columns of head g (+ 8), for codes 0 and 2, then 1 and 3 of
+  // the words 2j, 2j + 1: times a power of two that brings a head's largest to
+  // 2^10 .. 2^11, those of codes 1 and 3 (which come 16 times too large) a
+  // sixteenth of that.  The rest is of the heads 2j, 2j + 1 (+ 8).
+  uint32_t qa[NB][NH][4];
+  float qs[NH][2][G], qf[NH][2];                    // sums over the groups, in the units of the products; what a score is to be multiplied by
+  float o[NB][NH][2][4];                            // numerators: columns 32 b + 4 g + 2 k, + 1, each of two heads
+  float om[NH][2][G], m[NH][2], ref[NH][2], l[NH][2];   // of the offsets; maximum, and 0 for -inf; denominator (these over the lane's tokens)
   uint32_t top_s = 1;                               // exponent field of the largest step so far, 1 at least
   bool fresh = true;
   int seg = c.chunk, slot = 0;
   int ahead = STAGES - 1;
   int owed = 0;
   for (int u = u0; u < u1;) {
-    const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
-    const int qh = kvh * a.group + ht * H;
     if (fresh) {
       fresh = false;
       top_s = 1;
-      const __half* q = a.q + c.b * a.ldq + (long long)(qh + g) * D + 8 * j;
+      const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
+      const int row = FOLD ? g & 3 : g;
+      const __half* q = a.q + c.b * a.ldq + (long long)(kvh * a.group + ht * H + row) * D + 8 * j;
 #pragma unroll
-      for (int y = 0; y < RH; ++y) {
+      for (int y = 0; y < NH; ++y) {
         uint4 r[NB];
         uint32_t top = 0;                           // the largest exponent field
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          r[b] = g + 8 * y < rows ? *reinterpret_cast<const uint4*>(q + 8 * y * D + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
+          r[b] = row + 8 * y < rows ? *reinterpret_cast<const uint4*>(q + 8 * y * D + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w[4] = {r[b].x, r[b].y, r[b].z, r[b].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -286,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = min(max(top, 90u), 142u);             // (a head of zeros; an infinite or NaN column, which stays one)
         const float up = __uint_as_float((127u + 10u + 127u - top) << 23);           // 2^10 over the largest's power of two
-        qf[y] = a.sc2 * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);      // (a code is c 2^-22)
+        const float down = a.sc2 * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);   // (a code is c 2^-22)
+        float sum[G];
 #pragma unroll
-        for (int i = 0; i < G; ++i) qs[y][i] = om[y][i] = 0.f;
+        for (int i = 0; i < G; ++i) sum[i] = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t w[4] = {r[b].x, r[b].y, r[b].z, r[b].w};
@@ -298,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
             const float2 x = halves(w[i]);
             f[2 * i] = x.x * up;
             f[2 * i + 1] = x.y * up;
-            qs[y][b / BPG] += f[2 * i] + f[2 * i + 1];
+            sum[b / BPG] += f[2 * i] + f[2 * i + 1];
           }
           auto pack = [](float x, float y, float s) {
             const __half2 h = __floats2half2_rn(x * s, y * s);
@@ -312,17 +327,28 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          qs[y][i] += __shfl_xor_sync(0xffffffffu, qs[y][i], 1);
-          qs[y][i] += __shfl_xor_sync(0xffffffffu, qs[y][i], 2);
-          qs[y][i] *= 1.f / 4194304.f;              // 2^-22
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+          sum[i] *= 1.f / 4194304.f;                // 2^-22
         }
-        m[y] = -INFINITY;
-        l[y] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {               // from head g's lanes to those that have its scores
+          qf[y][e] = __shfl_sync(0xffffffffu, down, (2 * j + e) * 4);
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            qs[y][e][i] = __shfl_sync(0xffffffffu, sum[i], (2 * j + e) * 4);
+            om[y][e][i] = 0.f;
+          }
+          m[y][e] = -INFINITY;
+          ref[y][e] = l[y][e] = 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[b][y][k][e] = 0.f;
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[t][x] = 0.f;
     }
     if (!ahead) {                                   // this unit has arrived for all lanes, the one before is done with
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -335,18 +361,18 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
     }
     const int fin = (int)(haves >> (8 * slot) & 255u) - 1;     // row of the last token; negative: none
     if (fin >= 0) {
-      const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes;
+      const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes + g * (4 * G);   // the pairs of token g
       const unsigned char* vs = ks + S::kPairs;
       const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
-      // ---- scores: x[n][y] of row g + 8 y, tokens 8 n + 2j, 8 n + 2j + 1
-      float x[2 * NTL][RH][2], al[RH];
+      // ---- scores: x[n][y][e] of token 8 n + g, head 8 y + 2j + e
+      float x[2 * NTL][NH][2];
       const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
 #pragma unroll
       for (int i = 0; i < NTL; ++i) {
-        uint32_t sm[2][2][G];
+        uint32_t sm[2][G];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) load_pairs<G>(ks, 16 * i + 8 * n + 2 * j, sm[n]);
-        float acc[2][4];
+        for (int n = 0; n < 2; ++n) load_pairs<G>(ks + (16 * i + 8 * n) * (4 * G), sm[n]);
+        float acc[NH][4];
 #pragma unroll
         for (int b = 0; b < NB; b += 2) {
           uint32_t r[4];                            // pieces b, b + 1 of tokens 0..7, then of 8..15
@@ -355,106 +381,101 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
           for (int bb = 0; bb < 2; ++bb) {
             if ((b + bb) % BPG == 0) {
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+              for (int y = 0; y < NH; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
             }
-            const auto& q = qa[b + bb];
+            // codes 0, 1 and 2, 3 in bits 2..5, 6..9
+            const uint32_t l0 = r[bb] << 2, l1 = r[2 + bb] << 2, h0 = r[bb] >> 6, h1 = r[2 + bb] >> 6;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t w = r[2 * n + bb], lw = w << 2, hw = w >> 6;    // codes 0, 1 and 2, 3 in bits 2..5, 6..9
-              mma(acc[n], q[0][0], RH == 2 ? q[RH - 1][0] : 0u, q[0][1], RH == 2 ? q[RH - 1][1] : 0u, lw & 0x003c003cu,
-                  hw & 0x003c003cu);
-              mma(acc[n], q[0][2], RH == 2 ? q[RH - 1][2] : 0u, q[0][3], RH == 2 ? q[RH - 1][3] : 0u, lw & 0x03c003c0u,
-                  hw & 0x03c003c0u);
+            for (int y = 0; y < NH; ++y) {
+              const auto& q = qa[b + bb][y];
+              mma(acc[y], l0 & 0x003c003cu, l1 & 0x003c003cu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
+              mma(acc[y], l0 & 0x03c003c0u, l1 & 0x03c003c0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
             }
             if ((b + bb) % BPG == BPG - 1) {
               const int gi = (b + bb) / BPG;
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+              for (int n = 0; n < 2; ++n) {
+                const float2 s = halves(sm[n][gi]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float2 s = halves(sm[n][e][gi]);
+                for (int y = 0; y < NH; ++y)
 #pragma unroll
-                  for (int y = 0; y < RH; ++y) {
+                  for (int e = 0; e < 2; ++e) {
                     float& z = x[2 * i + n][y][e];
-                    z = fmaf(s.x, acc[n][2 * y + e], gi ? fmaf(s.y, qs[y][gi], z) : s.y * qs[y][0]);
+                    z = fmaf(s.x, acc[y][2 * n + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
                   }
-                }
+              }
             }
           }
         }
       }
       // ---- probabilities
-      uint32_t vp[2 * NTL][2][G];                   // the values' pairs
+      uint32_t vp[2 * NTL][G];                      // the pairs of the values of token 8 n + g
       __half2 most = __float2half2_rn(0.f);
 #pragma unroll
       for (int n = 0; n < 2 * NTL; ++n) {
-        load_pairs<G>(vs, 8 * n + 2 * j, vp[n]);
+        load_pairs<G>(vs + 8 * n * (4 * G), vp[n]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][e][i]));
+        for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][i]));
       }
-      const uint32_t most_s = __reduce_max_sync(0xffffffffu, (uint32_t)__half_as_ushort(__low2half(most))) >> 10;
+      const uint32_t most_s = (uint32_t)__half_as_ushort(__low2half(most)) >> 10;
       bool rise = most_s > top_s;
-      const uint32_t before_s = top_s;
-      top_s = max(top_s, most_s);
 #pragma unroll
-      for (int y = 0; y < RH; ++y) {
-        float top = -INFINITY;
+      for (int n = 0; n < 2 * NTL; ++n)
 #pragma unroll
-        for (int n = 0; n < 2 * NTL; ++n)
+        for (int y = 0; y < NH; ++y)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[n][y][e] *= qf[y];
-            if (fin < TW - 1 && 8 * n + 2 * j + e > fin) x[n][y][e] = -INFINITY;
-            top = fmaxf(top, x[n][y][e]);
+            x[n][y][e] *= qf[y][e];
+            if (fin < TW - 1 && 8 * n + g > fin) x[n][y][e] = -INFINITY;
+            rise = rise || x[n][y][e] > m[y][e];
           }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m[y], top), ref = mn == -INFINITY ? 0.f : mn;
-        rise = rise || mn > m[y];
-        al[y] = ex2(m[y] - ref);
-        m[y] = mn;
+      if (__any_sync(0xffffffffu, rise)) {          // a new maximum somewhere, or a larger step: scale what there is
+        const uint32_t now_s = max(top_s, __reduce_max_sync(0xffffffffu, most_s));
+        const float fall = __uint_as_float((127u - (now_s - top_s)) << 23);
+        top_s = now_s;
 #pragma unroll
-        for (int n = 0; n < 2 * NTL; ++n)
+        for (int y = 0; y < NH; ++y)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[n][y][e] = ex2(x[n][y][e] - ref);
+          for (int e = 0; e < 2; ++e) {
+            float top = m[y][e];
+#pragma unroll
+            for (int n = 0; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            ref[y][e] = top == -INFINITY ? 0.f : top;
+            const float al = ex2(m[y][e] - ref[y][e]), alf = al * fall;
+            m[y][e] = top;
+            l[y][e] *= al;
+#pragma unroll
+            for (int i = 0; i < G; ++i) om[y][e][i] *= al;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                o[b][y][k][e] *= alf;
+                o[b][y][k][2 + e] *= alf;
+              }
+          }
       }
-      if (__any_sync(0xffffffffu, rise)) {          // a new maximum somewhere, or a new scale: scale what there is
-        const float fall = __uint_as_float((127u - (top_s - before_s)) << 23);
 #pragma unroll
-        for (int y = 0; y < RH; ++y) {
-          l[y] *= al[y];
+      for (int y = 0; y < NH; ++y)
 #pragma unroll
-          for (int i = 0; i < G; ++i) om[y][i] *= al[y];
-          al[y] *= fall;
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int n = 0; n < 2 * NTL; ++n) {
+            x[n][y][e] = ex2(x[n][y][e] - ref[y][e]);
+            l[y][e] += x[n][y][e];
+          }
+          if ((badslots >> slot) & 1u) l[y][e] = __int_as_float(0x7fc00000);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {              // of 8 heads rows 0..7 and 8..15 are halves of the same head
-          o[t][0] *= al[0];
-          o[t][1] *= al[0];
-          o[t][2] *= al[RH - 1];
-          o[t][3] *= al[RH - 1];
-        }
-      }
-      if ((badslots >> slot) & 1u) l[0] = l[RH - 1] = __int_as_float(0x7fc00000);
       // ---- numerators: p s scaled so that it stays below 2^15
       const float scale = __uint_as_float((127u + 29u - top_s) << 23);
       const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
 #pragma unroll
       for (int i = 0; i < NTL; ++i) {
-        float xs[RH][4];
-#pragma unroll
-        for (int y = 0; y < RH; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float pr = x[2 * i + e / 2][y][e % 2];
-            l[y] += pr;
-            xs[y][e] = pr * scale;
-          }
-        uint32_t hi[RH][2], lo[RH][2];
+        uint32_t hi[NH][2], lo[NH][2];              // p s of 8 tokens each: tokens 2j, 2j + 1, head g
 #pragma unroll
         for (int b = 0; b < NB; b += 2) {
           uint32_t r[4];                            // tokens 0..7 and 8..15 of piece b, then of b + 1
@@ -463,30 +484,35 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
           for (int bb = 0; bb < 2; ++bb) {
             if ((b + bb) % BPG == 0) {
               const int gi = (b + bb) / BPG;
-              float2 s[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s[e] = halves(vp[2 * i + e / 2][e % 2][gi]);
-                s[e].y = fmaf(8.f, s[e].x, s[e].y);
-              }
+              for (int n = 0; n < 2; ++n) {
+                float2 s = halves(vp[2 * i + n][gi]);
+                s.y = fmaf(8.f, s.x, s.y);
+                s.x *= scale;
 #pragma unroll
-              for (int y = 0; y < RH; ++y) {
+                for (int y = 0; y < NH; ++y) {
+                  const float(&w)[2] = x[2 * i + n][y];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) om[y][gi] = fmaf(x[2 * i + e / 2][y][e % 2], s[e].y, om[y][gi]);
-                split2(xs[y][0] * s[0].x, xs[y][1] * s[1].x, hi[y][0], lo[y][0]);
-                split2(xs[y][2] * s[2].x, xs[y][3] * s[3].x, hi[y][1], lo[y][1]);
+                  for (int e = 0; e < 2; ++e) om[y][e][gi] = fmaf(w[e], s.y, om[y][e][gi]);
+                  uint32_t h, t;
+                  split2(w[0] * s.x, w[1] * s.x, h, t);
+                  if (FOLD) {                       // lanes of columns 4..7 have heads 0..3 again: theirs is the lower part
+                    hi[y][n] = transpose(j < 2 ? h : t);
+                  } else {
+                    hi[y][n] = transpose(h);
+                    lo[y][n] = transpose(t);
+                  }
+                }
               }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {           // code k of the words: columns 32 (b + bb) + 4 word + k
-              const uint32_t b0 = centred(k < 2 ? r[2 * bb] : r[2 * bb] >> 8, k % 2);
-              const uint32_t b1 = centred(k < 2 ? r[2 * bb + 1] : r[2 * bb + 1] >> 8, k % 2);
-              float(&t)[4] = o[4 * (b + bb) + k];
-              if constexpr (RH == 1) {              // hi in rows 0..7, lo in rows 8..15
-                mma(t, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
-              } else {
-                mma(t, hi[0][0], hi[RH - 1][0], hi[0][1], hi[RH - 1][1], b0, b1);
-                mma(t, lo[0][0], lo[RH - 1][0], lo[0][1], lo[RH - 1][1], b0, b1);
+            for (int k = 0; k < 2; ++k) {           // codes 2k, 2k + 1 of the words: columns 32 (b + bb) + 4 word + 2k, + 1
+              const uint32_t w0 = k ? r[2 * bb] >> 8 : r[2 * bb], w1 = k ? r[2 * bb + 1] >> 8 : r[2 * bb + 1];
+              const uint32_t a0 = centred(w0, false), a1 = centred(w0, true), a2 = centred(w1, false), a3 = centred(w1, true);
+#pragma unroll
+              for (int y = 0; y < NH; ++y) {
+                mma(o[b + bb][y][k], a0, a1, a2, a3, hi[y][0], hi[y][1]);
+                if (!FOLD) mma(o[b + bb][y][k], a0, a1, a2, a3, lo[y][0], lo[y][1]);
               }
             }
           }
@@ -497,39 +523,40 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
 
     const Walk w = c;
     u += advance<SP, UNIT>(a, pre, lens, c);
-    const bool ends = w.chunk + 1 == w.nch, all = u >= u1;
-    if (ends || all) {                              // the end of this (sequence, head), or of this CTA's share of it
+    const bool ends = w.chunk + 1 == w.nch;
+    if (ends || u >= u1) {                          // the end of this (sequence, head), or of this CTA's share of it
       // Every warp leaves its sums, then joins a quarter of the columns of all
       // warps.  (p s was scaled by 2^(29 - top_s).)
       const float unit = __uint_as_float((127u - 29u + top_s) << 23);
 #pragma unroll
-      for (int y = 0; y < RH; ++y) {
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-        if (j == 0) wml[warp * H + g + 8 * y] = make_float2(m[y], l[y]);
+      for (int y = 0; y < NH; ++y)
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          om[y][i] += __shfl_xor_sync(0xffffffffu, om[y][i], 1);
-          om[y][i] += __shfl_xor_sync(0xffffffffu, om[y][i], 2);
-        }
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+          for (int s = 4; s < 32; s <<= 1) {
+            l[y][e] += __shfl_xor_sync(0xffffffffu, l[y][e], s);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {    // words 2j and 2j + 1
-            float f[4];
+            for (int i = 0; i < G; ++i) om[y][e][i] += __shfl_xor_sync(0xffffffffu, om[y][e][i], s);
+          }
+          const int head = 8 * y + 2 * j + e;
+          if (g == 0) wml[warp * H + head] = make_float2(m[y][e], l[y][e]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float(&t)[4] = o[4 * b + i];
-              const float v = RH == 1 ? t[half] + t[2 + half] : t[2 * y + half];
-              f[i] = fmaf(v, unit, om[y][b / BPG]);
+          for (int b = 0; b < NB; ++b) {
+            float f[4] = {o[b][y][0][e], o[b][y][0][2 + e], o[b][y][1][e], o[b][y][1][2 + e]};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (FOLD) f[k] += __shfl_xor_sync(0xffffffffu, f[k], 2);
+              f[k] = fmaf(f[k], unit, om[y][e][b / BPG]);
             }
-            *reinterpret_cast<float4*>(sums + warp * S::kSums + (g + 8 * y) * (D * 4) + (((8 * b + 2 * j + half) ^ g) << 4)) =
+            *reinterpret_cast<float4*>(sums + warp * S::kSums + head * (D * 4) + (((8 * b + g) ^ (head & 7)) << 4)) =
                 make_float4(f[0], f[1], f[2], f[3]);
           }
-      }
+        }
       __syncthreads();
       const bool whole = ends && seg == 0;
-      join_warps<D, H, SP>(a, sums, S::kSums, wml, whole, 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0), rows, w.b, qh, 1.f);
+      const int kvh = a.nht == 1 ? w.h : w.h / a.nht, ht = w.h - kvh * a.nht;
+      join_warps<D, H, SP>(a, sums, S::kSums, wml, whole, 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0), min(H, a.group - ht * H), w.b,
+                           kvh * a.group + ht * H, 1.f);
       __syncthreads();                              // the sums may be written again; the part is written
       if (!whole && threadIdx.x == 0) owe_part(a, sh, pre, w, owe, owed);
       fresh = true;
@@ -550,11 +577,14 @@ int attend4(const q2_kv4* kv, const Attend4Args& a, const CacheShape& c, long lo
       return (int)Q2_ESHAPE;                        // (an fp16 cache, which check_cache4 does not give)
     } else {
       constexpr int G = D / group;
-      const int most = (int)std::min(units, (long long)ctas_of<D>() * dev_info().sms);
+      auto launch = [&](auto kernel, int H, int smem) {
+        return launch_pdl(kernel, a, (int)std::min(units, (long long)ctas_of<D>(H) * dev_info().sms), kThreads, smem, stream);
+      };
       if constexpr (D <= 128)
         if (unit_heads(a.group, D) == 16)
-          return launch_pdl(k_attend4<D, G, 16, SP>, a, most, kThreads, Shape<D, G, 16>::smem(a.batch), stream);
-      return launch_pdl(k_attend4<D, G, 8, SP>, a, most, kThreads, Shape<D, G, 8>::smem(a.batch), stream);
+          return launch(k_attend4<D, G, 16, false, SP>, 16, Shape<D, G, 16>::smem(a.batch));
+      const int smem = Shape<D, G, 8>::smem(a.batch);
+      return a.group <= 4 ? launch(k_attend4<D, G, 8, true, SP>, 8, smem) : launch(k_attend4<D, G, 8, false, SP>, 8, smem);
     }
   });
 }
