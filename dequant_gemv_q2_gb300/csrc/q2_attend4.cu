@@ -121,12 +121,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// w0, w1 >= 0 as pairs of fp16 numbers whose sums they are, to 2^-22.
-__device__ __forceinline__ void split2(float w0, float w1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(w0, w1);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  const __half2 l = __floats2half2_rn(fma_h(lo16(hi), 0xbc00, w0), fma_h(hi16(hi), 0xbc00, w1));   // (0xbc00 is -1)
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Codes in bits 0..3 (high: 4..7) of both halves as c - 8 in fp16: 1024 + c (1024 + 16 c), then what is too much.
@@ -160,50 +157,55 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
   int* nowed = reinterpret_cast<int*>(owe + 2);
   int* pre = nowed + 4;
   int* lens = pre + a.batch + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);      // (known to be the warp's)
 
   pdl_wait();
   pdl_trigger();
   const Share sh = share_out<D, SP, UNIT>(a, nowed, pre, lens, &q2_attend4_error);
-  int u0 = sh.u0;
+  int u = sh.u0;
   const int u1 = sh.u1;
-  if (u0 >= u1) return;
-  Walk c = walk_from<SP, UNIT>(a, pre, lens, u0);   // the unit in use
-  if (u0 >= u1) return;
+  if (u >= u1) return;
+  Walk c = walk_from<SP, UNIT>(a, pre, lens, u);    // the unit in use, at place u
+  if (u >= u1) return;
+  // units of w's (sequence, head) from w on that are this CTA's, w at place v
+  auto run_of = [&](const Walk& w, int v) { return min(w.nch - w.chunk, u1 - v); };
 
   // ---- the warp's loads, STAGES - 1 units ahead of their use
   unsigned char* const myring = q2_att4_smem + warp * (STAGES * S::kStage);
   const uint32_t ring = saddr(myring);
-  Walk p = c;
-  int pu = u0, pslot = 0, ppage = -1, pt0 = 0, pat = 0;   // place of the unit to load, its stage; page, first token, place in the page (of this lane's row where not aligned)
-  uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; a stage's tokens, 8 bits each
+  Walk p = c;                                       // the unit to load, at place pu
+  int pu = u, prun = run_of(p, u), pleft = prun, pslot = 0;    // units of its (sequence, head) in all and still to be loaded, its stage
+  int ppage = -1, pt0 = 0, pat = 0;                 // page, first token, place in the page (of this lane's row where not aligned)
+  uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; SP: a stage's tokens, 8 bits each
   const int piece = lane % NB, row0 = lane / NB, prow = lane % TW;
   // the pieces of a row are exchanged so that eight rows of one piece lie in different banks
   auto place = [](int row, int pc) { return row * (D / 2) + ((pc ^ (row / (8 / NB) & (NB - 1))) << 4); };
   const uint32_t cdst = ring + place(row0, piece);  // (rows RPI apart have their pieces alike, of eight pieces the fifth for the first)
   const uint32_t pdst = ring + 2 * S::kCodes + prow * (4 * G);
+  const uint32_t lrow = (uint32_t)row0 * a.token_stride + piece, step = a.token_stride * 16;
   const int* trow = nullptr;                        // of p's (sequence, head): the table's row, the head's place
   uint32_t phead = 0, pshead = 0;
   auto enter = [&]() {
-    if (p.b >= a.batch) return;
     const uint32_t kvh = a.nht == 1 ? p.h : p.h / a.nht;
     trow = a.table + p.b * a.table_stride;
     phead = kvh * a.head_stride;
     pshead = kvh * a.s_head_stride;
+    pt0 = p.chunk * UNIT + warp * TW;
   };
   auto lookup = [&]() {                             // tokens in one page: its page; else that of this lane's row
-    pt0 = first_token<SP, UNIT, TW>(a, p, warp, pu < u1);
+    if (SP) pt0 = first_token<SP, UNIT, TW>(a, p, warp, pleft > 0);
     const int t = pt0 + (a.aligned ? 0 : prow), pi = page_of(a, t);
     pat = t - pi * a.page;
-    ppage = pu < u1 && t < p.len ? trow[pi] : -1;
+    ppage = pleft > 0 && t < p.len ? trow[pi] : -1;
   };
   enter();
   lookup();
   auto issue = [&]() {
-    if (pu < u1) {
-      const int have = min(max(p.len - pt0, 0), TW);
-      haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)have << (8 * pslot);
-      if (have) {
+    if (pleft > 0) {
+      const int have = SP ? min(max(p.len - pt0, 0), TW) : p.len - pt0;       // tokens; negative: none
+      if (SP) haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)have << (8 * pslot);
+      if (have > 0) {
         const bool there = (unsigned)ppage < (unsigned)a.npages;
         const bool bad = __any_sync(0xffffffffu, (a.aligned || prow < have) && !there);
         const uint32_t page = there ? ppage : 0;
@@ -212,21 +214,21 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
                                         ((pat + (a.aligned ? prow : 0)) * a.s_token_stride + pshead);
         const uint32_t cd = cdst + pslot * S::kStage, pd = pdst + pslot * S::kStage;
         const unsigned char* ps = a.ks + soff * 4;
-        if (a.aligned && have == TW && !bad) {      // the usual step: all rows, one behind another
+        if (a.aligned && have >= TW && !bad) {      // the usual step: all rows, one behind another
           if constexpr (TW == 32) {
             cp_pairs<4 * G>(pd, ps, true);
             cp_pairs<4 * G>(pd + S::kPairs, ps + a.vs, true);
           } else {
             cp_pairs<4 * G>(pd + (lane < 16 ? 0 : S::kPairs), ps + (lane < 16 ? 0 : a.vs), true);
           }
-          const unsigned char* k = a.k + (off + ((uint32_t)row0 * a.token_stride + piece)) * 16;
-          const unsigned long long step = (unsigned long long)a.token_stride * (RPI * 16);
+          const unsigned char* k = a.k + (off + lrow) * 16;
+          const unsigned char* v = k + a.v;
 #pragma unroll
           for (int i = 0; i < TW / RPI; ++i) {
             const uint32_t d = (NB == 8 && i % 2 ? cd ^ 64u : cd) + i * (RPI * D / 2);
-            cp16_all(d, k);
-            cp16_all(d + S::kCodes, k + a.v);
-            k += step;
+            const unsigned long long at = (unsigned long long)(i * RPI) * step;
+            cp16_all(d, k + at);
+            cp16_all(d + S::kCodes, v + at);
           }
         } else {
           const bool plive = there && prow < have;
@@ -250,13 +252,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
             cp16(d + S::kCodes, k + a.v, live);
           }
         }
-        if (bad && lane == 0) atomicOr(&q2_attend4_error, Q2_ERR_PAGE);
-        badslots = (badslots & ~(1u << pslot)) | (bad ? 1u << pslot : 0u);
+        if (bad) {
+          if (lane == 0) atomicOr(&q2_attend4_error, Q2_ERR_PAGE);
+          badslots |= 1u << pslot;
+        }
       }
-      pu += advance<SP, UNIT>(a, pre, lens, p);
-      if (p.chunk == 0) enter();
-      lookup();
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
+      pt0 += UNIT;
+      if (SP) ++p.chunk;
+      if (--pleft == 0) {                           // on to the next (sequence, head)
+        p.chunk += SP ? -1 : prun - 1;
+        pu += prun - 1 + advance<SP, UNIT>(a, pre, lens, p);
+        if (pu < u1) {
+          pleft = prun = run_of(p, pu);
+          enter();
+        }
+      }
+      lookup();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -269,17 +281,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
   uint32_t qa[NB][NH][4];
   float qs[NH][2][G], qf[NH][2];                    // sums over the groups, in the units of the products; what a score is to be multiplied by
   float o[NB][NH][2][4];                            // numerators: columns 32 b + 4 g + 2 k, + 1, each of two heads
-  float om[NH][2][G], m[NH][2], ref[NH][2], l[NH][2];   // of the offsets; maximum, and 0 for -inf; denominator (these over the lane's tokens)
-  uint32_t top_s = 1;                               // exponent field of the largest step so far, 1 at least
-  bool fresh = true;
-  int seg = c.chunk, slot = 0;
-  int ahead = STAGES - 1;
-  int owed = 0;
-  for (int u = u0; u < u1;) {
-    if (fresh) {
-      fresh = false;
-      top_s = 1;
-      const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
+  float om[NH][2][G], m[NH][2], ref[NH][2], l[NH][2];   // of the offsets; largest sum, its score (0 for none); denominator (this and om over the lane's tokens)
+  const unsigned short less = !FOLD || j >= 2 ? 0xbc00 : 0;     // -1 or 0
+  uint32_t top_s;                                   // exponent field of the largest step so far, 1 at least
+  int slot = 0;
+  int ahead = STAGES - 1;                           // units still to be requested before the first is used
+  int owed = 0;                                     // parts of this CTA that were the last of their (sequence, head)
+  while (u < u1) {                                  // a (sequence, head), or what is this CTA's of it
+    const int run = run_of(c, u), seg = c.chunk;
+    const int kvh = a.nht == 1 ? c.h : c.h / a.nht, ht = c.h - kvh * a.nht, rows = min(H, a.group - ht * H);
+    {
       const int row = FOLD ? g & 3 : g;
       const __half* q = a.q + c.b * a.ldq + (long long)(kvh * a.group + ht * H + row) * D + 8 * j;
 #pragma unroll
@@ -299,8 +310,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = min(max(top, 90u), 142u);             // (a head of zeros; an infinite or NaN column, which stays one)
-        const float up = __uint_as_float((127u + 10u + 127u - top) << 23);           // 2^10 over the largest's power of two
-        const float down = a.sc2 * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);   // (a code is c 2^-22)
+        // 2^10 over the largest's power of two, of the scale's sign: the largest score is the largest sum
+        const float up = copysignf(__uint_as_float((127u + 10u + 127u - top) << 23), a.sc2);
+        const float down = fabsf(a.sc2) * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);   // (a code is c 2^-22)
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) sum[i] = 0.f;
@@ -315,15 +327,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
             f[2 * i + 1] = x.y * up;
             sum[b / BPG] += f[2 * i] + f[2 * i + 1];
           }
-          auto pack = [](float x, float y, float s) {
-            const __half2 h = __floats2half2_rn(x * s, y * s);
-            return *reinterpret_cast<const uint32_t*>(&h);
-          };
           // words 2j and 2j + 1 are columns 0..3 and 4..7 of these eight
-          qa[b][y][0] = pack(f[0], f[4], 1.f);
-          qa[b][y][1] = pack(f[2], f[6], 1.f);
-          qa[b][y][2] = pack(f[1], f[5], 0.0625f);
-          qa[b][y][3] = pack(f[3], f[7], 0.0625f);
+          qa[b][y][0] = pack2(f[0], f[4]);
+          qa[b][y][1] = pack2(f[2], f[6]);
+          qa[b][y][2] = pack2(f[1] * 0.0625f, f[5] * 0.0625f);
+          qa[b][y][3] = pack2(f[3] * 0.0625f, f[7] * 0.0625f);
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -350,6 +358,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
             for (int e = 0; e < 4; ++e) o[b][y][k][e] = 0.f;
       }
     }
+    top_s = 1;
+    int t0 = seg * UNIT + warp * TW;
+#pragma unroll 1
+    for (int left = run; left;) {
     if (!ahead) {                                   // this unit has arrived for all lanes, the one before is done with
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       __syncwarp();
@@ -359,53 +371,54 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
       --ahead;
       continue;
     }
-    const int fin = (int)(haves >> (8 * slot) & 255u) - 1;     // row of the last token; negative: none
+    // row of the last token, if below TW; negative: none
+    const int fin = SP ? (int)(haves >> (8 * slot) & 255u) - 1 : c.len - 1 - t0;
     if (fin >= 0) {
       const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes + g * (4 * G);   // the pairs of token g
       const unsigned char* vs = ks + S::kPairs;
       const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
-      // ---- scores: x[n][y][e] of token 8 n + g, head 8 y + 2j + e
+      // ---- scores: x[n][y][e] of token 8 n + g, head 8 y + 2j + e, still to be multiplied by qf
       float x[2 * NTL][NH][2];
       const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
+      uint32_t sm[2 * NTL][G];
 #pragma unroll
-      for (int i = 0; i < NTL; ++i) {
-        uint32_t sm[2][G];
+      for (int n = 0; n < 2 * NTL; ++n) load_pairs<G>(ks + 8 * n * (4 * G), sm[n]);
+      float acc[NTL][NH][2][4];                     // (two chains of products to a tile)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) load_pairs<G>(ks + (16 * i + 8 * n) * (4 * G), sm[n]);
-        float acc[NH][4];
+      for (int b = 0; b < NB; b += 2) {
+        uint32_t r[NTL][4];                         // pieces b, b + 1 of tokens 0..7, then of 8..15
 #pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-          uint32_t r[4];                            // pieces b, b + 1 of tokens 0..7, then of 8..15
-          ldsm4(r, kt + i * (kTile * D / 2) + place(krow, b + kpiece));
+        for (int i = 0; i < NTL; ++i) ldsm4(r[i], kt + i * (kTile * D / 2) + place(krow, b + kpiece));
 #pragma unroll
-          for (int bb = 0; bb < 2; ++bb) {
-            if ((b + bb) % BPG == 0) {
+        for (int bb = 0; bb < 2; ++bb) {
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) {
+            // codes 0, 1 and 2, 3 in bits 2..5, 6..9
+            const uint32_t l0 = r[i][bb] << 2, l1 = r[i][2 + bb] << 2, h0 = r[i][bb] >> 6, h1 = r[i][2 + bb] >> 6;
+#pragma unroll
+            for (int y = 0; y < NH; ++y) {
+              if ((b + bb) % BPG == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][y][0][e] = acc[i][y][1][e] = 0.f;
+              }
+              const auto& q = qa[b + bb][y];
+              mma(acc[i][y][0], l0 & 0x003c003cu, l1 & 0x003c003cu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
+              mma(acc[i][y][1], l0 & 0x03c003c0u, l1 & 0x03c003c0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
+            }
+          }
+          if ((b + bb) % BPG == BPG - 1) {
+            const int gi = (b + bb) / BPG;
+#pragma unroll
+            for (int n = 0; n < 2 * NTL; ++n) {
+              const float2 s = halves(sm[n][gi]);
 #pragma unroll
               for (int y = 0; y < NH; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
-            }
-            // codes 0, 1 and 2, 3 in bits 2..5, 6..9
-            const uint32_t l0 = r[bb] << 2, l1 = r[2 + bb] << 2, h0 = r[bb] >> 6, h1 = r[2 + bb] >> 6;
-#pragma unroll
-            for (int y = 0; y < NH; ++y) {
-              const auto& q = qa[b + bb][y];
-              mma(acc[y], l0 & 0x003c003cu, l1 & 0x003c003cu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
-              mma(acc[y], l0 & 0x03c003c0u, l1 & 0x03c003c0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
-            }
-            if ((b + bb) % BPG == BPG - 1) {
-              const int gi = (b + bb) / BPG;
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                const float2 s = halves(sm[n][gi]);
-#pragma unroll
-                for (int y = 0; y < NH; ++y)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    float& z = x[2 * i + n][y][e];
-                    z = fmaf(s.x, acc[y][2 * n + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
-                  }
-              }
+                for (int e = 0; e < 2; ++e) {
+                  float& z = x[n][y][e];
+                  const auto& t = acc[n / 2][y];
+                  z = fmaf(s.x, t[0][2 * (n % 2) + e] + t[1][2 * (n % 2) + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
+                }
             }
           }
         }
@@ -420,20 +433,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
         for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][i]));
       }
       const uint32_t most_s = (uint32_t)__half_as_ushort(__low2half(most)) >> 10;
-      bool rise = most_s > top_s;
+      bool rise = most_s > top_s || fin < TW - 1 || badslots;
 #pragma unroll
-      for (int n = 0; n < 2 * NTL; ++n)
+      for (int y = 0; y < NH; ++y)
 #pragma unroll
-        for (int y = 0; y < NH; ++y)
+        for (int e = 0; e < 2; ++e) {
+          float top = x[0][y][e];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[n][y][e] *= qf[y][e];
-            if (fin < TW - 1 && 8 * n + g > fin) x[n][y][e] = -INFINITY;
-            rise = rise || x[n][y][e] > m[y][e];
-          }
-      if (__any_sync(0xffffffffu, rise)) {          // a new maximum somewhere, or a larger step: scale what there is
+          for (int n = 1; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
+          rise = rise || top > m[y][e];
+        }
+      // A new maximum somewhere, or a larger step: scale what there is.  (Also a
+      // step that is not whole, or has a page that does not exist.)
+      if (__any_sync(0xffffffffu, rise)) {
         const uint32_t now_s = max(top_s, __reduce_max_sync(0xffffffffu, most_s));
         const float fall = __uint_as_float((127u - (now_s - top_s)) << 23);
+        const bool bad = (badslots >> slot) & 1u;
+        badslots &= ~(1u << slot);
         top_s = now_s;
 #pragma unroll
         for (int y = 0; y < NH; ++y)
@@ -441,13 +457,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
           for (int e = 0; e < 2; ++e) {
             float top = m[y][e];
 #pragma unroll
-            for (int n = 0; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
+            for (int n = 0; n < 2 * NTL; ++n) {
+              if (8 * n + g > fin) x[n][y][e] = -INFINITY;
+              top = fmaxf(top, x[n][y][e]);
+            }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            ref[y][e] = top == -INFINITY ? 0.f : top;
-            const float al = ex2(m[y][e] - ref[y][e]), alf = al * fall;
+            ref[y][e] = top == -INFINITY ? 0.f : top * qf[y][e];
+            const float al = m[y][e] == -INFINITY ? 0.f : ex2(fmaf(m[y][e], qf[y][e], -ref[y][e])), alf = al * fall;
             m[y][e] = top;
-            l[y][e] *= al;
+            l[y][e] = bad ? __int_as_float(0x7fc00000) : l[y][e] * al;
 #pragma unroll
             for (int i = 0; i < G; ++i) om[y][e][i] *= al;
 #pragma unroll
@@ -462,14 +481,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
 #pragma unroll
       for (int y = 0; y < NH; ++y)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int n = 0; n < 2 * NTL; ++n) {
-            x[n][y][e] = ex2(x[n][y][e] - ref[y][e]);
+            x[n][y][e] = ex2(fmaf(x[n][y][e], qf[y][e], -ref[y][e]));
             l[y][e] += x[n][y][e];
           }
-          if ((badslots >> slot) & 1u) l[y][e] = __int_as_float(0x7fc00000);
-        }
       // ---- numerators: p s scaled so that it stays below 2^15
       const float scale = __uint_as_float((127u + 29u - top_s) << 23);
       const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
@@ -494,14 +511,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
                   const float(&w)[2] = x[2 * i + n][y];
 #pragma unroll
                   for (int e = 0; e < 2; ++e) om[y][e][gi] = fmaf(w[e], s.y, om[y][e][gi]);
-                  uint32_t h, t;
-                  split2(w[0] * s.x, w[1] * s.x, h, t);
-                  if (FOLD) {                       // lanes of columns 4..7 have heads 0..3 again: theirs is the lower part
-                    hi[y][n] = transpose(j < 2 ? h : t);
-                  } else {
-                    hi[y][n] = transpose(h);
-                    lo[y][n] = transpose(t);
-                  }
+                  const float w0 = w[0] * s.x, w1 = w[1] * s.x;
+                  const uint32_t h = pack2(w0, w1);
+                  // FOLD: lanes of columns 4..7 have heads 0..3 again, theirs is the lower part
+                  const uint32_t t = pack2(fma_h(lo16(h), less, w0), fma_h(hi16(h), less, w1));
+                  hi[y][n] = transpose(FOLD ? t : h);
+                  if (!FOLD) lo[y][n] = transpose(t);
                 }
               }
             }
@@ -520,11 +535,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
       }
     }
     slot = slot + 1 == STAGES ? 0 : slot + 1;
+    t0 += UNIT;
+    --left;
+    }
 
-    const Walk w = c;
-    u += advance<SP, UNIT>(a, pre, lens, c);
-    const bool ends = w.chunk + 1 == w.nch;
-    if (ends || u >= u1) {                          // the end of this (sequence, head), or of this CTA's share of it
+    {
       // Every warp leaves its sums, then joins a quarter of the columns of all
       // warps.  (p s was scaled by 2^(29 - top_s).)
       const float unit = __uint_as_float((127u - 29u + top_s) << 23);
@@ -539,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
             for (int i = 0; i < G; ++i) om[y][e][i] += __shfl_xor_sync(0xffffffffu, om[y][e][i], s);
           }
           const int head = 8 * y + 2 * j + e;
-          if (g == 0) wml[warp * H + head] = make_float2(m[y][e], l[y][e]);
+          if (g == 0) wml[warp * H + head] = make_float2(m[y][e] == -INFINITY ? -INFINITY : ref[y][e], l[y][e]);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             float f[4] = {o[b][y][0][e], o[b][y][0][2 + e], o[b][y][1][e], o[b][y][1][2 + e]};
@@ -553,15 +568,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
           }
         }
       __syncthreads();
-      const bool whole = ends && seg == 0;
-      const int kvh = a.nht == 1 ? w.h : w.h / a.nht, ht = w.h - kvh * a.nht;
-      join_warps<D, H, SP>(a, sums, S::kSums, wml, whole, 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0), min(H, a.group - ht * H), w.b,
+      const bool whole = seg == 0 && run == c.nch;
+      join_warps<D, H, SP>(a, sums, S::kSums, wml, whole, 2 * (int)blockIdx.x + (seg == 0 ? 1 : 0), rows, c.b,
                            kvh * a.group + ht * H, 1.f);
       __syncthreads();                              // the sums may be written again; the part is written
-      if (!whole && threadIdx.x == 0) owe_part(a, sh, pre, w, owe, owed);
-      fresh = true;
-      seg = 0;
+      if (!whole && threadIdx.x == 0) owe_part(a, sh, pre, c, owe, owed);
     }
+    c.chunk += run - 1;
+    u += run - 1 + advance<SP, UNIT>(a, pre, lens, c);
   }
 
   if (threadIdx.x == 0) *nowed = owed;
@@ -612,6 +626,7 @@ extern "C" int q2_attend4(const q2_kv4* kv, const void* q, long long ldq, const 
     return page <= 0xffffffffll && token * (c.page - 1) + head * (c.kv_heads - 1) <= 0xffffffffll && token <= 0xffffffffll &&
            head <= 0xffffffffll;
   };
+  if (kv->token_stride > 0xffffffffll) return Q2_ESHAPE;
   if (!within(kv->page_stride / 16, kv->token_stride / 16, kv->head_stride / 16) ||
       !within(kv->s_page_stride, kv->s_token_stride, kv->s_head_stride))
     return Q2_ESHAPE;
