@@ -21,11 +21,12 @@
 // operand of the tensor instruction.  The columns' order inside the sums is that
 // of the words; the queries, and the places of the outputs, follow it.
 //
-// Keys: four bits masked out of an fp16 number are one below the normal ones, c
-// 2^-22 in bits 2..5 and c 2^-18 in bits 6..9: three instructions for two
+// Keys: four bits masked out of the lower ten of an fp16 number are one below the
+// normal ones, c 2^-24 times the place of the bits: a word in place has two codes
+// there, shifted down by six the other two, so five instructions make four
 // registers of operands.  (The tensor cores align such products as if they were
-// 2^-14 and cut them off: an error of 2^-16 of a step times the largest q column
-// there.  Bits 0..3 and 4..7 would save one shift in six and lose two bits more.)
+// 2^-14 and cut them off, an error of 2^-13 of a step times the largest q column
+// at most, of 2^-17 for two codes of four.)
 //
 // Values: c - 8, by 1024 + c and a subtraction, two instructions for a register.
 // With c itself both terms of the numerator are some eight steps times the
@@ -139,6 +140,18 @@ __device__ __forceinline__ uint32_t transpose(uint32_t r) {
   uint32_t t;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(r));
   return t;
+}
+
+// mma(), or the product alone
+__device__ __forceinline__ void mma_from(bool zero, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (!zero) {
+    mma(c, a0, a1, a2, a3, b0, b1);
+    return;
+  }
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // H: query heads of a unit, 8 or 16 (columns of the products); FOLD: four at
@@ -276,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
   // ---- sums of the current (sequence, head)
   // The queries of 32 columns of head g (+ 8), for codes 0 and 2, then 1 and 3 of
   // the words 2j, 2j + 1: times a power of two that brings a head's largest to
-  // 2^10 .. 2^11, those of codes 1 and 3 (which come 16 times too large) a
-  // sixteenth of that.  The rest is of the heads 2j, 2j + 1 (+ 8).
+  // 2^10 .. 2^11, and over the 16, 4 and 64 that codes 1, 2 and 3 come too large.
+  // The rest is of the heads 2j, 2j + 1 (+ 8).
   uint32_t qa[NB][NH][4];
   float qs[NH][2][G], qf[NH][2];                    // sums over the groups, in the units of the products; what a score is to be multiplied by
   float o[NB][NH][2][4];                            // numerators: columns 32 b + 4 g + 2 k, + 1, each of two heads
@@ -312,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
         top = min(max(top, 90u), 142u);             // (a head of zeros; an infinite or NaN column, which stays one)
         // 2^10 over the largest's power of two, of the scale's sign: the largest score is the largest sum
         const float up = copysignf(__uint_as_float((127u + 10u + 127u - top) << 23), a.sc2);
-        const float down = fabsf(a.sc2) * __uint_as_float((127u + 22u - 10u - 127u + top) << 23);   // (a code is c 2^-22)
+        const float down = fabsf(a.sc2) * __uint_as_float((127u + 24u - 10u - 127u + top) << 23);   // (a code is c 2^-24)
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) sum[i] = 0.f;
@@ -329,15 +342,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
           }
           // words 2j and 2j + 1 are columns 0..3 and 4..7 of these eight
           qa[b][y][0] = pack2(f[0], f[4]);
-          qa[b][y][1] = pack2(f[2], f[6]);
+          qa[b][y][1] = pack2(f[2] * 0.25f, f[6] * 0.25f);
           qa[b][y][2] = pack2(f[1] * 0.0625f, f[5] * 0.0625f);
-          qa[b][y][3] = pack2(f[3] * 0.0625f, f[7] * 0.0625f);
+          qa[b][y][3] = pack2(f[3] * 0.015625f, f[7] * 0.015625f);
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
           sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-          sum[i] *= 1.f / 4194304.f;                // 2^-22
+          sum[i] *= 1.f / 16777216.f;               // 2^-24
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {               // from head g's lanes to those that have its scores
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
       uint32_t sm[2 * NTL][G];
 #pragma unroll
       for (int n = 0; n < 2 * NTL; ++n) load_pairs<G>(ks + 8 * n * (4 * G), sm[n]);
-      float acc[NTL][NH][2][4];                     // (two chains of products to a tile)
+      float acc[NTL][NH][4];
 #pragma unroll
       for (int b = 0; b < NB; b += 2) {
         uint32_t r[NTL][4];                         // pieces b, b + 1 of tokens 0..7, then of 8..15
@@ -393,17 +406,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
         for (int bb = 0; bb < 2; ++bb) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i) {
-            // codes 0, 1 and 2, 3 in bits 2..5, 6..9
-            const uint32_t l0 = r[i][bb] << 2, l1 = r[i][2 + bb] << 2, h0 = r[i][bb] >> 6, h1 = r[i][2 + bb] >> 6;
+            // codes 0, 1 in bits 0..3, 4..7 of w0 and w1, codes 2, 3 in bits 2..5, 6..9 of h0 and h1
+            const uint32_t w0 = r[i][bb], w1 = r[i][2 + bb], h0 = w0 >> 6, h1 = w1 >> 6;
 #pragma unroll
             for (int y = 0; y < NH; ++y) {
-              if ((b + bb) % BPG == 0) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][y][0][e] = acc[i][y][1][e] = 0.f;
-              }
+              const bool first = (b + bb) % BPG == 0;
               const auto& q = qa[b + bb][y];
-              mma(acc[i][y][0], l0 & 0x003c003cu, l1 & 0x003c003cu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
-              mma(acc[i][y][1], l0 & 0x03c003c0u, l1 & 0x03c003c0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
+              mma_from(first, acc[i][y], w0 & 0x000f000fu, w1 & 0x000f000fu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
+              mma(acc[i][y], w0 & 0x00f000f0u, w1 & 0x00f000f0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
             }
           }
           if ((b + bb) % BPG == BPG - 1) {
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __gri
                 for (int e = 0; e < 2; ++e) {
                   float& z = x[n][y][e];
                   const auto& t = acc[n / 2][y];
-                  z = fmaf(s.x, t[0][2 * (n % 2) + e] + t[1][2 * (n % 2) + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
+                  z = fmaf(s.x, t[2 * (n % 2) + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
                 }
             }
           }

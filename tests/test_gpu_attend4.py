@@ -3,11 +3,13 @@
 A score of the 4-bit cache is a sum over groups of s sum(q c) + m sum(q).  The
 tensor cores take codes as numbers below fp16's normal ones, which they align as
 if they were 2^-14: a product is cut off at most 2^-23 2^-14 max|q| below, where
-a code's unit is 2^-22 (two columns of four) or 2^-18: 2^-15 or 2^-19 max|q| of a
-code each, 16 of them per instruction, and one instruction of each kind per 32
-columns: (2^-11 + 2^-15) s max|q| per 32 columns.  The sums in fp32 add at most
-(D + 8) 2^-23 of the magnitudes M = sum |q| (s c + |m|).  So a scaled score is
-off by d = scale (sum over 32 columns 2^-10 s max|q| + (D + 8) 2^-23 M), and a
+a code's unit is 2^-24 (columns 0 and 2 of four, q over 1 and 4) or, of columns 1
+and 3, 2^-20 with q over 16 and 64: 2^-13 or 2^-17 max|q| of a code each, 16 of
+them per instruction, and one instruction of each kind per 32 columns: (2^-9 +
+2^-13) s max|q| per 32 columns.  q over 64 is exact but below 2^-24 of the
+largest 2^10: another 2^-28.  The sums in fp32 add at most (D + 8) 2^-23 of the
+magnitudes M = sum |q| (s c + |m|).  So a scaled score is off by d = scale (sum
+over 32 columns 2^-8 s max|q| + (D + 8) 2^-23 M), and a
 probability, with exp2 and the joins, by e = 2 d + 2^-20 + 2^-19 relative.
 The numerators add terms of p s = hi + lo (2^-22) times c - 8, exact, and of p (m
 + 8 s), one step of at most 2^-23 of the sum of magnitudes N = sum p (8 s + |m +
@@ -118,7 +120,7 @@ class Case:
                     e = 2 * (self.D + 8) * 2.0 ** -23 * self.scale * M + 2.0 ** -21 + 2.0 ** -19
                 else:
                     per = np.abs(q).reshape(self.G, -1, 32).max(2) @ ks[:, ::32].T            # [G][n]
-                    d = self.scale * (2.0 ** -10 * per.max(1) + (self.D + 8) * 2.0 ** -23 * M)
+                    d = self.scale * (2.0 ** -8 * per.max(1) + (self.D + 8) * 2.0 ** -23 * M)
                     e = 2 * d + 2.0 ** -20 + 2.0 ** -19
                 N = p @ vmag / l
                 tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2 * (e[:, None] + len(tokens) / 16 * 2.0 ** -23) * N
