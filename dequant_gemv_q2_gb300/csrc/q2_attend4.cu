@@ -62,7 +62,7 @@ template <int D>
 __host__ __device__ constexpr int step_of() { return D == 256 ? 16 : 32; }
 
 template <int D>
-__host__ __device__ constexpr int ctas_of(int H) { return D == 256 || (D == 128 && H == 16) ? 2 : 3; }
+__host__ __device__ constexpr int ctas_of() { return D == 64 ? 3 : 2; }
 
 template <int D, int G, int H>
 struct Shape {
@@ -157,7 +157,7 @@ __device__ __forceinline__ void mma_from(bool zero, float (&c)[4], uint32_t a0, 
 // H: query heads of a unit, 8 or 16 (columns of the products); FOLD: four at
 // most; G: groups of a row
 template <int D, int G, int H, bool FOLD, bool SP>
-__global__ void __launch_bounds__(kThreads, ctas_of<D>(H)) k_attend4(const __grid_constant__ Attend4Args a) {
+__global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid_constant__ Attend4Args a) {
   using S = Shape<D, G, H>;
   constexpr int NH = H / 8, STAGES = S::STAGES, NB = D / 32;   // NB: 16-byte pieces of a row, 32 columns each
   constexpr int TW = S::TW, NTL = TW / kTile, UNIT = kWarps * TW;
@@ -601,14 +601,14 @@ int attend4(const q2_kv4* kv, const Attend4Args& a, const CacheShape& c, long lo
       return (int)Q2_ESHAPE;                        // (an fp16 cache, which check_cache4 does not give)
     } else {
       constexpr int G = D / group;
-      auto launch = [&](auto kernel, int H, int smem) {
-        return launch_pdl(kernel, a, (int)std::min(units, (long long)ctas_of<D>(H) * dev_info().sms), kThreads, smem, stream);
+      auto launch = [&](auto kernel, int smem) {
+        return launch_pdl(kernel, a, (int)std::min(units, (long long)ctas_of<D>() * dev_info().sms), kThreads, smem, stream);
       };
       if constexpr (D <= 128)
         if (unit_heads(a.group, D) == 16)
-          return launch(k_attend4<D, G, 16, false, SP>, 16, Shape<D, G, 16>::smem(a.batch));
+          return launch(k_attend4<D, G, 16, false, SP>, Shape<D, G, 16>::smem(a.batch));
       const int smem = Shape<D, G, 8>::smem(a.batch);
-      return a.group <= 4 ? launch(k_attend4<D, G, 8, true, SP>, 8, smem) : launch(k_attend4<D, G, 8, false, SP>, 8, smem);
+      return a.group <= 4 ? launch(k_attend4<D, G, 8, true, SP>, smem) : launch(k_attend4<D, G, 8, false, SP>, smem);
     }
   });
 }
