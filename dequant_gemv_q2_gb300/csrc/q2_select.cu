@@ -11,20 +11,24 @@
 //
 // One cluster per (sequence, key-value head).  Its CTAs share out the blocks,
 // score them and leave the scores in the shared memory of the first, which
-// finds the nsel-th largest by its digits (three histograms) and writes the
-// selection in order.
+// finds the nsel-th largest and writes the selection in order.
 //
-// Which of two blocks is selected must not depend on the order of a sum, so U
-// is summed exactly enough to be the exact value's rounding to fp32.  Products
-// of fp16 numbers are exact in fp32.  A lane adds its columns to a number M
-// above 2^log2(columns) times any of them, so that every sum s = fl(s' + p) has
-// the same exponent: s - s' and p - (s - s') are exact, the first parts add up
-// without error in s, the second in a sum of their own.  Lanes join pairs of
-// sums with the error of the larger added to the smaller (Knuth, "The Art of
-// Computer Programming" 2, 4.2.2, theorem B).
+// The scores are first taken on the tensor cores, with q+ = max(q, 0) on hi and
+// q- = min(q, 0) on lo as one product of 2 D columns: eight blocks and eight
+// heads to an instruction, every lane on the bounds that it has copied itself,
+// a few steps ahead.
+//
+// Which of two blocks is selected must not depend on the order of a sum.  So the
+// sums of the terms' magnitudes are taken beside: an instruction of 16 products
+// and the sum so far drops at most 17 2^-23 of that, 2 D / 16 of them at most e
+// = 17 D 2^-26.  Blocks that are further than 2 e from the nsel-th largest sum
+// are in or out; the others, mostly the nsel-th itself and one more or none, are
+// decided by sums that are exact enough to be the exact value's rounding to
+// fp32: products of fp16 numbers are exact in fp32, and their sums keep each
+// addition's error (Knuth, "The Art of Computer Programming" 2, 4.2.2, theorem B).
 #include <cooperative_groups.h>
 
-#include "q2_page.cuh"
+#include "q2_attend.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -33,9 +37,10 @@ namespace {
 
 __device__ unsigned int q2_select_error;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kAtOnce = 4;                          // blocks of a warp's step
-constexpr int kBins = 2048;                         // of a histogram: 11, 11 and 10 bits of a key
+constexpr int kAtOnce = 8;                          // blocks of a warp's step
+constexpr int kBins = 2048;
+constexpr int kMostSmem = 226 * 1024;
+constexpr uint32_t kAlways = 0xffffffffu, kOdd = 0xfffffffeu;    // keys of first and last blocks, of scores that are not finite
 
 struct SelectArgs {
   const int* table;
@@ -46,8 +51,19 @@ struct SelectArgs {
   const __half* q;
   long long ldq;
   const int* lens;
-  int cap, kv_heads, group, nsel, first, last, cs;
+  int cap, kv_heads, group, nsel, first, last, cs, stages;
   int* sel;
+};
+
+// Shared memory behind the queries' fragments, of a CTA of T threads.
+template <int T>
+struct SelectShared {
+  static constexpr int kWarps = T / 32;
+  uint32_t hist[kBins];
+  uint32_t wsum[2][kWarps];
+  float4 warps[8 * kWarps];                         // of each warp of the cluster: largest sum of magnitudes; least and greatest key, keys kOdd
+  uint32_t found[4];
+  uint32_t list[T];
 };
 
 // (h, e) + (h2, e2), h and e the sum's fp32 value and what it lacks
@@ -57,53 +73,160 @@ __device__ __forceinline__ void join(float& h, float& e, float h2, float e2) {
   h = t;
 }
 
-template <int N>
-__device__ __forceinline__ void halves(const __half* p, float (&x)[N]) {
-  if constexpr (N == 2) {
-    const __half2 r = *reinterpret_cast<const __half2*>(p);
-    const float2 f = __half22float2(r);
-    x[0] = f.x;
-    x[1] = f.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint2 r = *reinterpret_cast<const uint2*>(p + i);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.x)), g = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-      x[i + 2] = g.x;
-      x[i + 3] = g.y;
-    }
-  }
-}
-
-// The exponent field of a bound above every |x| (of 2^-25 at least, 2^16 at most)
-template <int N>
-__device__ __forceinline__ uint32_t exponent(const float (&x)[N], uint32_t least) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) least = max(least, __float_as_uint(x[i]) >> 23 & 255u);
-  return min(least, 143u);
-}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }
 
 // Larger keys for larger scores; what is not a finite number above them all.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (!(fabsf(x) <= 3.4028235e38f)) return 0xfffffffeu;
+  if (!finite(x)) return kOdd;
   const uint32_t b = __float_as_uint(x + 0.f);      // (-0 as 0)
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) k_select(const __grid_constant__ SelectArgs a) {
-  constexpr int CPL = D / 32;                       // columns of a lane
-  constexpr uint32_t kBits = CPL == 2 ? 1 : CPL == 4 ? 2 : 3;
-  extern __shared__ __align__(16) unsigned char q2_sel_smem[];
-  float* qs = reinterpret_cast<float*>(q2_sel_smem);                        // [group][32][CPL]
-  uint32_t* qe = reinterpret_cast<uint32_t*>(qs + a.group * D);             // [group][32] exponents
-  uint32_t* hist = qe + a.group * 32;                                       // [kBins]
-  uint32_t* keys = hist + kBins;                                            // [blocks] of the first CTA
-  __shared__ uint32_t wsum[2][kWarps];
-  __shared__ uint32_t found[2];                     // digits so far, how many more are above
+// An exclusive sum over the CTA's threads of a and b; `total` of them (all threads get them).
+template <int T>
+__device__ __forceinline__ uint2 scan(SelectShared<T>& s, uint32_t a, uint32_t b, uint2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = a, y = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    s.wsum[0][warp] = x;
+    s.wsum[1][warp] = y;
+  }
+  __syncthreads();
+  const uint32_t u = lane < (T / 32) ? s.wsum[0][lane] : 0u, v = lane < (T / 32) ? s.wsum[1][lane] : 0u;
+  total.x = __reduce_add_sync(0xffffffffu, u);
+  total.y = __reduce_add_sync(0xffffffffu, v);
+  const uint32_t p = __reduce_add_sync(0xffffffffu, lane < warp ? u : 0u), q = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u);
+  return make_uint2(x - a + p, y - b + q);
+}
+
+// The need-th largest of n keys, `always` of them kAlways, `odds` kOdd and the
+// others from lo to hi; `need` becomes how many of those equal to it count among
+// the largest (1 <= need <= n).
+template <int T>
+__device__ uint32_t largest(SelectShared<T>& s, const uint32_t* keys, int n, uint32_t always, uint32_t odds, uint32_t lo,
+                            uint32_t hi, uint32_t& need) {
+  if (need <= always) return kAlways;
+  need -= always;
+  if (need <= odds) return kOdd;
+  need -= odds;
+  // Histograms of even steps over a range that holds the key sought, until few
+  // are left in its bin.
+  uint32_t left = n - always - odds;                // keys in lo .. hi
+  while (left > T && lo < hi) {
+    const uint32_t span = hi - lo;
+    const int shift = max(0, 32 - __clz(span) - 11);                          // (span >> shift) < kBins
+    for (int i = threadIdx.x; i < kBins; i += T) s.hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += T) {
+      const uint32_t k = keys[i];
+      if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
+    }
+    __syncthreads();
+    // from the highest bin down, kBins / T to a thread
+    constexpr int each = kBins / T;
+    uint32_t c[each], sum = 0;
+#pragma unroll
+    for (int k = 0; k < each; ++k) sum += c[k] = s.hist[kBins - 1 - (threadIdx.x * each + k)];
+    uint2 total;
+    uint32_t before = scan(s, sum, 0u, total).x;
+    if (before < need && before + sum >= need) {    // in one thread
+#pragma unroll
+      for (int k = 0; k < each; ++k) {
+        if (before < need && before + c[k] >= need) {
+          s.found[0] = kBins - 1 - (threadIdx.x * each + k);
+          s.found[1] = need - before;
+          s.found[2] = c[k];
+        }
+        before += c[k];
+      }
+    }
+    __syncthreads();
+    const uint32_t bin = s.found[0];
+    need = s.found[1];
+    left = s.found[2];
+    lo += bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    __syncthreads();
+  }
+  if (lo == hi) return lo;
+  // few are left: each counts those above it
+  if (threadIdx.x == 0) s.found[3] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += T) {
+    const uint32_t k = keys[i];
+    if (k >= lo && k <= hi) s.list[atomicAdd(&s.found[3], 1u)] = k;
+  }
+  __syncthreads();
+  if (threadIdx.x < left) {
+    const uint32_t k = s.list[threadIdx.x];
+    uint32_t above = 0, equal = 0;
+    for (uint32_t i = 0; i < left; ++i) {
+      above += s.list[i] > k;
+      equal += s.list[i] == k;
+    }
+    if (above < need && need <= above + equal) {    // (all that are equal write the same)
+      s.found[0] = k;
+      s.found[1] = need - above;
+    }
+  }
+  __syncthreads();
+  need = s.found[1];
+  const uint32_t k = s.found[0];
+  __syncthreads();
+  return k;
+}
+
+// The exact score of a block, to the rounding to fp32.  By a warp.
+template <int D>
+__device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, const __half* p, const __half* q) {
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  float lo[CPL], hi[CPL], best = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) {
+    lo[k] = __half2float(p[lane + 32 * k]);
+    hi[k] = __half2float(p[D + lane + 32 * k]);
+  }
+#pragma unroll 4
+  for (int h = 0; h < a.group; ++h) {
+    float x = 0.f, e = 0.f;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+      const float y = __half2float(q[h * D + lane + 32 * k]);
+      join(x, e, y * (y >= 0.f ? hi[k] : lo[k]), 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) join(x, e, __shfl_xor_sync(0xffffffffu, x, o), __shfl_xor_sync(0xffffffffu, e, o));
+    best = fmaxf(best, x + e);
+  }
+  return key_of(best);
+}
+
+// STAGED: bounds by way of shared memory, a.stages - 1 steps ahead
+template <int D, int T, bool STAGED>
+__global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ SelectArgs a) {
+  constexpr int NB = D / 32, W = T / 32;            // 32 columns each
+  constexpr int kStage = kAtOnce * 4 * D;           // bytes of a warp's step
+  extern __shared__ __align__(16) unsigned char q2_sel_smem[];
+  // q+ and q- in 16-byte pieces: [head tile][32 columns][q+, q-][lane]
+  uint4* frag = reinterpret_cast<uint4*>(q2_sel_smem);
+  const int tiles = (a.group + 7) / 8;
+  SelectShared<T>& s = *reinterpret_cast<SelectShared<T>*>(frag + tiles * NB * 64);
+  unsigned char* ring = reinterpret_cast<unsigned char*>(&s + 1);           // [warp][stage][32 columns][lo, hi][lane] of 16 bytes
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ring + (STAGED ? W * a.stages * kStage : 0));   // [blocks]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = a.cs == 1 ? 0 : (int)cluster.block_rank();
   const int id = blockIdx.x / a.cs, b = id / a.kv_heads, kvh = id - b * a.kv_heads;
@@ -119,118 +242,140 @@ __global__ void __launch_bounds__(kThreads) k_select(const __grid_constant__ Sel
   int* sel = a.sel + (long long)id * a.nsel;
   if (n <= a.nsel) {                                // all there are
     if (rank == 0)
-      for (int i = threadIdx.x; i < a.nsel; i += kThreads) sel[i] = i < n ? i : -1;
+      for (int i = threadIdx.x; i < a.nsel; i += T) sel[i] = i < n ? i : -1;
     return;
   }
   if (a.cs > 1) cluster_arrive();
-  for (int i = threadIdx.x; i < a.group * 32; i += kThreads) {
-    float x[CPL];
-    halves<CPL>(a.q + b * a.ldq + (long long)kvh * a.group * D + i * CPL, x);
+  const int* trow = a.table + b * a.table_stride;
+  const __half* qrows = a.q + b * a.ldq + (long long)kvh * a.group * D;
+  auto page_at = [&](int i) {                       // the page of a block's first token; -1 behind the last block
+    return i < n ? trow[page_of(a, i * Q2_BLOCK)] : -1;
+  };
+  auto bounds_of = [&](int i, int page) {
+    const int t = i * Q2_BLOCK;
+    return a.bounds + (((long long)page * a.sub + (t - page_of(a, t) * a.page) / Q2_BLOCK) * a.kv_heads + kvh) * (2 * D);
+  };
+  const int stride = a.cs * W * kAtOnce;
+  const int first = (rank * W + warp) * kAtOnce;
+  // Each lane copies the pieces that it will use: columns 32 c + 8 j .. of block g.
+  const uint32_t mine = saddr(ring) + warp * (a.stages * kStage) + lane * 16;
+  int m0 = first, mslot = 0, page = page_at(first + g);             // the step to be copied
+  uint32_t odds = 0;                                // bit `stage`: block g of it has no page
+  auto copy = [&]() {
+    if (m0 < n) {
+      const bool there = (unsigned)page < (unsigned)a.npages;
+      if (m0 + g < n && !there && j == 0) atomicOr(&q2_select_error, Q2_ERR_PAGE);
+      odds = (odds & ~(1u << mslot)) | (there ? 0u : 1u << mslot);
+      const __half* p = there ? bounds_of(m0 + g, page) + 8 * j : a.bounds;
+      const uint32_t d = mine + mslot * kStage;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) qs[i * CPL + k] = x[k];
-    qe[i] = exponent<CPL>(x, 102u);
+      for (int c = 0; c < NB; ++c) {
+        cp16(d + c * 1024, p + 32 * c, there);
+        cp16(d + c * 1024 + 512, p + D + 32 * c, there);
+      }
+      m0 += stride;
+      page = page_at(m0 + g);
+      mslot = mslot + 1 == a.stages ? 0 : mslot + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (STAGED)
+    for (int k = 1; k < a.stages; ++k) copy();
+  for (int i = threadIdx.x; i < tiles * NB * 32; i += T) {
+    const int l = i & 31, head = i / (NB * 32) * 8 + (l >> 2), c = i / 32 % NB;
+    uint4 r = make_uint4(0u, 0u, 0u, 0u), up, dn;
+    if (head < a.group) r = *reinterpret_cast<const uint4*>(qrows + (long long)head * D + 32 * c + 8 * (l & 3));
+    const __half2 zero = __float2half2_rn(0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 x = reinterpret_cast<const __half2*>(&r)[k];
+      reinterpret_cast<__half2*>(&up)[k] = __hmax2_nan(x, zero);
+      reinterpret_cast<__half2*>(&dn)[k] = __hmin2_nan(x, zero);
+    }
+    frag[i / 32 * 64 + l] = up;
+    frag[i / 32 * 64 + 32 + l] = dn;
   }
   __syncthreads();
   if (a.cs > 1) cluster_wait();                     // the first CTA is there
   uint32_t* to = a.cs > 1 ? cluster.map_shared_rank(keys, 0) : keys;
+  float4* warps_to = a.cs > 1 ? cluster.map_shared_rank(s.warps, 0) : s.warps;
 
-  const int* trow = a.table + b * a.table_stride;
-  const int step = a.cs * kWarps * kAtOnce;
-  for (int n0 = (rank * kWarps + warp) * kAtOnce; n0 < n; n0 += step) {
-    // lanes 0..3: the places of the blocks' bounds
-    int place = -1;
-    if (lane < kAtOnce && n0 + lane < n) {
-      const int t = (n0 + lane) * Q2_BLOCK, pi = page_of(a, t), page = trow[pi];
-      if ((unsigned)page < (unsigned)a.npages) place = page * a.sub + (t - pi * a.page) / Q2_BLOCK;
-      else atomicOr(&q2_select_error, Q2_ERR_PAGE);
+  float most = 0.f;                                 // the largest sum of magnitudes
+  uint32_t kmin = 0xffffffffu, kmax = 0, kodd = 0;  // keys of this lane's blocks
+  int slot = 0;
+  for (int n0 = first; n0 < n; n0 += stride) {
+    const uint4* held = nullptr;
+    const __half* p = nullptr;
+    bool there = true;
+    if (STAGED) {
+      copy();
+      if (a.stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (a.stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      held = reinterpret_cast<const uint4*>(ring + (warp * a.stages + slot) * kStage) + lane;
+      there = !(odds >> slot & 1u);
+    } else {
+      there = (unsigned)page < (unsigned)a.npages;
+      if (n0 + g < n && !there && j == 0) atomicOr(&q2_select_error, Q2_ERR_PAGE);
+      p = there ? bounds_of(n0 + g, page) + 8 * j : nullptr;
+      page = page_at(n0 + stride + g);
     }
-    float lo[kAtOnce][CPL], hi[kAtOnce][CPL];
-    uint32_t be[kAtOnce];
-    bool there[kAtOnce];
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int at = __shfl_sync(0xffffffffu, place, u);
-      there[u] = at >= 0;
-      const __half* p = a.bounds + ((long long)max(at, 0) * a.kv_heads + kvh) * (2 * D) + lane * CPL;
-      if (there[u]) {
-        halves<CPL>(p, lo[u]);
-        halves<CPL>(p + D, hi[u]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) lo[u][k] = hi[u][k] = 0.f;
+    auto piece = [&](int c, int w) {
+      return STAGED ? held[c * 64 + w * 32]
+             : p    ? *reinterpret_cast<const uint4*>(p + w * D + 32 * c)
+                    : make_uint4(0u, 0u, 0u, 0u);
+    };
+    const uint32_t odd = __ballot_sync(0xffffffffu, !there);       // (lane 4 g + j: block n0 + g)
+    float best[2] = {-INFINITY, -INFINITY};         // of blocks n0 + 2j, + 1
+    for (int ht = 0; ht < tiles; ++ht) {
+      float u[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll (NB < 8 ? NB : 2)
+      for (int c = 0; c < NB; ++c) {
+        const uint4* f = frag + (ht * NB + c) * 64 + lane;
+        const uint4 up = f[0], dn = f[32], y = piece(c, 0), x = piece(c, 1);
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        mma(u, up.x, 0u, up.y, 0u, x.x, x.y);
+        mma(w, up.x, 0u, up.y, 0u, x.x & kAbs, x.y & kAbs);
+        mma(u, up.z, 0u, up.w, 0u, x.z, x.w);
+        mma(w, up.z, 0u, up.w, 0u, x.z & kAbs, x.w & kAbs);
+        mma(u, dn.x, 0u, dn.y, 0u, y.x, y.y);
+        mma(w, dn.x & kAbs, 0u, dn.y & kAbs, 0u, y.x & kAbs, y.y & kAbs);
+        mma(u, dn.z, 0u, dn.w, 0u, y.z, y.w);
+        mma(w, dn.z & kAbs, 0u, dn.w & kAbs, 0u, y.z & kAbs, y.w & kAbs);
       }
-    }
+      if (ht * 8 + g < a.group) {                   // rows are heads
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) be[u] = exponent<CPL>(lo[u], exponent<CPL>(hi[u], 102u));
-
-    float best = -INFINITY;
-    bool odd = false;                               // a score that is not a finite number
-    for (int h = 0; h < a.group; ++h) {
-      float q[CPL];
-      const float* qp = qs + (h * 32 + lane) * CPL;
-      if constexpr (CPL == 2) {
-        const float2 f = *reinterpret_cast<const float2*>(qp);
-        q[0] = f.x;
-        q[1] = f.y;
-      } else {
-#pragma unroll
-        for (int k = 0; k < CPL; k += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(qp + k);
-          q[k] = f.x;
-          q[k + 1] = f.y;
-          q[k + 2] = f.z;
-          q[k + 3] = f.w;
+        for (int e = 0; e < 2; ++e) {
+          best[e] = fmaxf(best[e], finite(u[e]) ? u[e] : INFINITY);
+          if (finite(w[e])) most = fmaxf(most, w[e]);
         }
       }
-      const uint32_t me = qe[h * 32 + lane];
-      float s[kAtOnce], e[kAtOnce];
+    }
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const float M = __uint_as_float((me + be[u] - 124u + kBits) << 23 | 0x400000u);
-        float acc = M;
-        e[u] = 0.f;
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-          const float y = q[k] >= 0.f ? hi[u][k] : lo[u][k];
-          const float t = fmaf(q[k], y, acc), z = t - acc;
-          e[u] += fmaf(q[k], y, -z);
-          acc = t;
-        }
-        s[u] = acc - M;
-      }
-      // lanes' sums joined, four blocks at a time: two exchanges leave a lane one block, three more its sum
-#pragma unroll
-      for (int o = 16, w = kAtOnce / 2; w > 0; o >>= 1, w >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int u = 0; u < w; ++u) {
-          const float hs = __shfl_xor_sync(0xffffffffu, up ? s[u] : s[u + w], o);
-          const float es = __shfl_xor_sync(0xffffffffu, up ? e[u] : e[u + w], o);
-          if (up) {
-            s[u] = s[u + w];
-            e[u] = e[u + w];
-          }
-          join(s[u], e[u], hs, es);
+      for (int o = 4; o < 32; o <<= 1) best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], o));
+      const int k = n0 + 2 * j + e;
+      if (g == 0 && k < n) {
+        const uint32_t key = odd >> (8 * j + 4 * e) & 1u ? kOdd : key_of(best[e]);
+        const bool always = k < a.first || k >= n - a.last;
+        to[k] = always ? kAlways : key;
+        kodd += !always && key == kOdd;
+        if (!always && key != kOdd) {
+          kmin = min(kmin, key);
+          kmax = max(kmax, key);
         }
       }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        const float hs = __shfl_xor_sync(0xffffffffu, s[0], o), es = __shfl_xor_sync(0xffffffffu, e[0], o);
-        join(s[0], e[0], hs, es);
-      }
-      const float v = s[0] + e[0];
-      odd = odd || !(fabsf(v) <= 3.4028235e38f);
-      best = fmaxf(best, v);
     }
-    // lane 8 u holds block u in the order of the exchanges: bit 4 took the upper two, bit 3 the upper one
-    const int u = lane >> 3, i = n0 + u;
-    if ((lane & 7) == 0 && i < n) {
-      bool mine = false;
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) mine = k == u ? there[k] : mine;
-      to[i] = i < a.first || i >= n - a.last ? 0xffffffffu : odd || !mine ? 0xfffffffeu : key_of(best);
-    }
+    slot = slot + 1 == a.stages ? 0 : slot + 1;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  kodd = __reduce_add_sync(0xffffffffu, kodd);
+  if (lane == 0)
+    warps_to[rank * W + warp] = make_float4(most, __uint_as_float(kmin), __uint_as_float(kmax), __uint_as_float(kodd));
   if (a.cs > 1) {
     cluster_meet();
     if (rank) return;
@@ -238,80 +383,98 @@ __global__ void __launch_bounds__(kThreads) k_select(const __grid_constant__ Sel
     __syncthreads();
   }
 
-  // the nsel-th largest key, digit by digit
-  uint32_t prefix = 0, need = a.nsel;               // keys with the digits so far: how many of them are to be taken
-  for (int shift = 21; ; shift = shift == 21 ? 10 : 0) {
-    const int bits = shift == 0 ? 10 : 11, bins = 1 << bits;
-    for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const uint32_t k = keys[i];
-      if (shift == 21 || (k >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
-    }
-    __syncthreads();
-    // counts from the highest bin down: thread t has bins [t * each, (t + 1) * each) of that order
-    const int each = bins / kThreads;
-    uint32_t sum = 0;
-    for (int k = 0; k < each; ++k) sum += hist[bins - 1 - (threadIdx.x * each + k)];
-    uint32_t run = sum;
+  // of all warps
+  most = 0.f;
+  kmin = 0xffffffffu;
+  kmax = kodd = 0;
+  for (int i = lane; i < a.cs * W; i += 32) {
+    const float4 f = s.warps[i];
+    most = fmaxf(most, f.x);
+    kmin = min(kmin, __float_as_uint(f.y));
+    kmax = max(kmax, __float_as_uint(f.z));
+    kodd += __float_as_uint(f.w);
+  }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += x;
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  kodd = __reduce_add_sync(0xffffffffu, kodd);
+
+  // threads have consecutive blocks from here on
+  const int each = (n + T - 1) / T, i0 = min(n, (int)threadIdx.x * each), i1 = min(n, i0 + each);
+  uint32_t need = a.nsel, key = largest(s, keys, n, a.first + a.last, kodd, kmin, kmax, need);
+  if (key < kOdd) {
+    // blocks whose sums lie within the error of the nsel-th
+    const float err = 2.f * (17.f * D / 67108864.f) * 1.01f * most, t = score_of(key), top = t + err, bottom = t - err;
+    auto near = [&](uint32_t k) { return k < kOdd && score_of(k) <= top && score_of(k) >= bottom; };
+    uint32_t in = 0, open = 0;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = keys[i];
+      const bool is = near(k);
+      open += is;
+      in += !is && k > key;
     }
-    if (lane == 31) wsum[0][warp] = run;
+    uint2 total;
+    uint32_t at = scan(s, in, open, total).y;
+    need = a.nsel - total.x;                        // of the open ones
+    const bool all = total.y == need, few = total.y <= T;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = keys[i];
+      const bool is = near(k);
+      if (is && !all && few) s.list[at++] = i;
+      keys[i] = is ? 1u : k > key ? kAlways : 0u;
+    }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) run += wsum[0][w];
-    uint32_t before = run - sum;
-    if (before < need && run >= need) {             // in one thread
-      for (int k = 0; k < each; ++k) {
-        const uint32_t d = bins - 1 - (threadIdx.x * each + k), c = hist[d];
-        if (before + c >= need) {
-          found[0] = prefix | d << shift;
-          found[1] = need - before;
-          break;
-        }
-        before += c;
+    key = 1;
+    if (!all && few) {
+      for (uint32_t k = warp; k < total.y; k += W) {
+        const int i = s.list[k];
+        const uint32_t x = exact_key<D>(a, bounds_of(i, page_at(i)), qrows);
+        if (lane == 0) s.hist[k] = x;
       }
+      __syncthreads();
+      if (threadIdx.x < total.y) {                  // (the list is in the order of the blocks)
+        const uint32_t k = s.hist[threadIdx.x];
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < total.y; ++i) before += s.hist[i] > k || (s.hist[i] == k && i < threadIdx.x);
+        keys[s.list[threadIdx.x]] = before < need ? kAlways : 0u;
+      }
+      __syncthreads();
+    } else if (!all) {
+      uint32_t greatest = 0;
+      for (int k = warp * 32; k < n; k += T) {
+        uint32_t todo = __ballot_sync(0xffffffffu, k + lane < n && keys[k + lane] == 1u);
+        while (todo) {
+          const int i = k + __ffs(todo) - 1;
+          todo &= todo - 1;
+          const uint32_t x = exact_key<D>(a, bounds_of(i, page_at(i)), qrows);
+          greatest = max(greatest, x);
+          __syncwarp();
+          if (lane == 0) keys[i] = x;               // (above 1)
+        }
+      }
+      if (lane == 0) s.wsum[1][warp] = greatest;
+      __syncthreads();
+      greatest = __reduce_max_sync(0xffffffffu, lane < W ? s.wsum[1][lane] : 0u);
+      __syncthreads();
+      need = a.nsel;
+      key = largest(s, keys, n, total.x, 0u, 0u, greatest, need);
     }
-    __syncthreads();
-    prefix = found[0];
-    need = found[1];
-    if (shift == 0) break;
   }
 
   // in order: all above the key, and the first `need` of those that have it
-  const int each = (n + kThreads - 1) / kThreads, i0 = min(n, (int)threadIdx.x * each), i1 = min(n, i0 + each);
   uint32_t above = 0, equal = 0;
   for (int i = i0; i < i1; ++i) {
-    above += keys[i] > prefix;
-    equal += keys[i] == prefix;
+    above += keys[i] > key;
+    equal += keys[i] == key;
   }
-  uint32_t ra = above, re = equal;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, ra, o), y = __shfl_up_sync(0xffffffffu, re, o);
-    if (lane >= o) {
-      ra += x;
-      re += y;
-    }
-  }
-  if (lane == 31) {
-    wsum[0][warp] = ra;
-    wsum[1][warp] = re;
-  }
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    ra += wsum[0][w];
-    re += wsum[1][w];
-  }
-  ra -= above;
-  re -= equal;
+  uint2 total;
+  uint2 run = scan(s, above, equal, total);
   for (int i = i0; i < i1; ++i) {
     const uint32_t k = keys[i];
-    if (k > prefix || (k == prefix && re < need)) sel[ra + min(re, need)] = i;
-    ra += k > prefix;
-    re += k == prefix;
+    if (k > key || (k == key && run.y < need)) sel[run.x + min(run.y, need)] = i;
+    run.x += k > key;
+    run.y += k == key;
   }
 }
 
@@ -346,16 +509,31 @@ int select(const Pages& pg, const CacheShape& c, const void* bounds, const void*
   a.first = first;
   a.last = last;
   a.sel = sel;
-  // CTAs of a cluster: two per SM in all, while each has a step for its warps
+  // Up to eight CTAs of 512 threads to a cluster where the clusters leave SMs
+  // idle and there are steps for their warps; with many clusters two of 256 per SM.
   const int blocks = (int)((c.cap + Q2_BLOCK - 1) / Q2_BLOCK), clusters = batch * c.kv_heads;
-  a.cs = 1;
-  while (a.cs < 8 && (long long)clusters * a.cs * 2 <= 2 * dev_info().sms && blocks >= 2 * a.cs * kWarps * kAtOnce) a.cs *= 2;
-  const int smem = a.group * (c.D + 32) * 4 + (kBins + blocks) * 4;
-  auto launch = [&](auto kernel) {
-    if (set_smem(reinterpret_cast<const void*>(kernel), smem)) return (int)Q2_ECUDA;
-    return launch_clusters(kernel, clusters, a.cs, kThreads, smem, stream, a);
+  auto launch = [&](auto kernel, int T, int D, int shared, bool staged) {
+    a.cs = 1;
+    while (a.cs < 8 && (long long)clusters * a.cs * 2 * T <= 512ll * dev_info().sms && blocks >= 2 * a.cs * (T / 32) * kAtOnce) a.cs *= 2;
+    const int smem = (a.group + 7) / 8 * (D / 32) * 1024 + shared + blocks * 4;
+    const int stage = T / 32 * kAtOnce * 4 * D, room = (T == 512 ? kMostSmem : kMostSmem / 2) - smem;
+    a.stages = staged ? std::max(1, std::min(3, room / stage)) : 0;
+    const int bytes = smem + a.stages * stage;
+    if (staged && bytes > kMostSmem) return (int)Q2_ESIZE;         // (for the form that holds no stages)
+    if (set_smem(reinterpret_cast<const void*>(kernel), bytes)) return (int)Q2_ECUDA;
+    return launch_clusters(kernel, clusters, a.cs, T, bytes, stream, a);
   };
-  return c.D == 64 ? launch(k_select<64>) : c.D == 128 ? launch(k_select<128>) : launch(k_select<256>);
+  auto with = [&](auto Dc) {
+    constexpr int D = Dc();
+    int st = Q2_ESIZE;
+    if constexpr (D <= 128)
+      if (clusters <= dev_info().sms) st = launch(k_select<D, 512, true>, 512, D, sizeof(SelectShared<512>), true);
+    if (st == Q2_ESIZE) st = launch(k_select<D, 256, true>, 256, D, sizeof(SelectShared<256>), true);
+    return st == Q2_ESIZE ? launch(k_select<D, 256, false>, 256, D, sizeof(SelectShared<256>), false) : st;
+  };
+  return c.D == 64    ? with(std::integral_constant<int, 64>())
+         : c.D == 128 ? with(std::integral_constant<int, 128>())
+                      : with(std::integral_constant<int, 256>());
 }
 
 }  // namespace

@@ -524,8 +524,8 @@ int q2_attend4(const q2_kv4* kv, const void* q, long long ldq, const int* lens, 
  *     the nsel blocks of the highest score, in ascending order, -1 behind the
  *     last where the sequence has fewer.  Equal scores: the lower block.  The
  *     first `first` and the last `last` blocks are always among them (first,
- *     last >= 0, first + last <= nsel).  A block with a U_h that is not a finite
- *     number is above all others.
+ *     last >= 0, first + last <= nsel).  A block whose bounds hold an inf or
+ *     NaN is above all others (all blocks are alike where the queries do).
  *   - U_h is summed to 2^-36 of the sum of its terms' magnitudes and rounded to
  *     fp32, so the selection is that of the exact scores.
  *   - kv: head_dim, kv_heads, npages, page_size, table and max_pages are used, the
