@@ -30,10 +30,6 @@ struct UnitArgs {
   float sc2;                  // scale * log2(e)
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -121,8 +117,12 @@ __device__ __forceinline__ Share share_out(const UnitArgs& a, int* nowed, int* p
       // How many CTAs.  Each part of a (sequence, head) costs its join about a
       // quarter of what a unit costs its CTA, so n units are best cut into
       // about 2 sqrt(n) parts; with few (sequence, head)s, a multiple of their
-      // number, so that sequences of one length are cut at their heads.
-      const int heads = used * a.hu, parts = max(1, (int)(2.f * sqrtf((float)longest)));
+      // number, so that sequences of one length are cut at their heads.  (Units
+      // of the 4-bit cache and of selected blocks wait longer for their first
+      // rows than they take: twice and one and a half times as many parts.  One
+      // sequence of 777 tokens in 4 bits 8.0 -> 7.1 us.)
+      constexpr float kParts = UNIT > kUnit ? 4.f : SP ? 3.f : 2.f;
+      const int heads = used * a.hu, parts = max(1, (int)(kParts * sqrtf((float)longest)));
       *nowed = heads * 4 > (int)gridDim.x ? (int)gridDim.x : heads * min(parts, (int)gridDim.x / max(heads, 1));
     }
   }

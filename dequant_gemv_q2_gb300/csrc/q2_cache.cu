@@ -101,7 +101,7 @@ struct AppendArgs {
   long long ldq, ldqo, ldk, ldv;
   __half* bounds;
   const float* angles;
-  int q_heads, kv_heads, chunk;         // chunk: heads of a CTA
+  int q_heads, kv_heads, chunk, cq, ck; // chunk: heads of a CTA; cq, ck: CTAs of a tile's queries, keys
   int rot, interleaved, sub;            // sub: bounds of a page
 };
 
@@ -158,10 +158,14 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
   return c;
 }
 
+constexpr int kBatch = 4;                           // rows of a slot whose loads are in flight together
+
 // GRP: columns of a group of the 4-bit cache, 0 for an fp16 cache
 template <int D, int GRP>
-__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
+  extern __shared__ __align__(16) float4 q2_append_smem[];                   // angles of the tile's tokens, [token][rot / 4]
+  __shared__ long long places[2][Q2_BLOCK];         // of its tokens in the pools, and in those of the pairs; -1: none
   __shared__ uint4 red[SLOTS][2][LPR];
   __shared__ int pre[Q2_ATT_MAX_BATCH + 1];         // tiles before each sequence
   __shared__ int wsum[kThreads / 32];
@@ -209,10 +213,20 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
     total = pre[rw.batch];
   }
 
-  const int qk = a.q_heads + a.kv_heads, heads = qk + a.kv_heads;
-  const int h0 = blockIdx.y * a.chunk, h1 = min(h0 + a.chunk, heads);
+  // This CTA's heads, all of one kind.
+  enum { QUERY, KEY, VALUE };
+  const int y = blockIdx.y, kind = y < a.cq ? QUERY : y < a.cq + a.ck ? KEY : VALUE;
+  const int h0 = (kind == QUERY ? y : kind == KEY ? y - a.cq : y - a.cq - a.ck) * a.chunk;
+  const int nh = min(a.chunk, (kind == QUERY ? a.q_heads : a.kv_heads) - h0);
+  const __half* src = kind == QUERY ? a.q : kind == KEY ? a.k : a.v;
+  const long long ld = kind == QUERY ? a.ldq : kind == KEY ? a.ldk : a.ldv;
+  src += (long long)h0 * D + piece * 8;
+  const bool turns = a.angles && kind != VALUE, bounded = a.bounds && kind == KEY;
   const int RP = a.rot / 8;                         // pieces of a head that are turned
-  const bool turned = a.angles && piece < RP;
+  const bool turned = turns && piece < RP, first_half = piece < RP / 2;
+  // this lane's first four angles of a token, in 16-byte pieces
+  const int apiece = a.interleaved ? piece * 2 : (first_half ? piece : piece - RP / 2) * 4;
+  const int partner = lane - piece + (!turned ? piece : first_half ? piece + RP / 2 : piece - RP / 2);
 
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     int b = tile, j = 0;
@@ -228,183 +242,171 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
     }
     const Seq s = seq_of(rw, b);
     if (!rw.starts) {
-      if (!s.ok && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
+      if (!s.ok && y == 0 && threadIdx.x == 0) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
       if (!s.n) continue;
     }
     const int past = s.len - s.n, block = past / Q2_BLOCK + j;
     const int p0 = s.ok ? max(past, block * Q2_BLOCK) : 0;
     const int n = s.ok ? min(s.len, (block + 1) * Q2_BLOCK) - p0 : min(Q2_BLOCK, s.n - j * Q2_BLOCK);
     const int row0 = s.row0 + (s.ok ? p0 - past : j * Q2_BLOCK);
-    int T = 1;                                      // tokens side by side
-    while (T < n && T < SLOTS) T <<= 1;
-    const int tk = slot & (T - 1), part = slot / T, HS = SLOTS / T;
     const int* trow = a.pg.table + b * a.pg.table_stride;
 
-    float cs[8], sn[8];                             // this lane's angles; of a first half's columns the sine is negated
-    // row t of the tile: where it goes
-    bool live = false, there = false;
-    int row = 0;
-    long long at = 0, sat = 0;                      // the token's place in the pools, and in those of the pairs
-    auto token = [&](int t) {
-      live = t < n;
-      row = row0 + t;
-      const int pos = p0 + t;
-      there = false;
-      if (live && s.ok) {
-        if (h1 > a.q_heads) {
-          const int pi = page_of(a.pg, pos), page = trow[pi];
-          there = (unsigned)page < (unsigned)a.pg.npages;
-          if (!there && piece == 0) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
-          if (there) {
-            at = page * a.pg.page_stride + (pos - pi * a.pg.page) * a.pg.token_stride;
-            if constexpr (GRP > 0) sat = page * a.sp.page_stride + (pos - pi * a.pg.page) * a.sp.token_stride;
-          }
-        }
-        if (turned && h0 < qk) {
-          const float* base = a.angles + (long long)pos * a.rot;
-          if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float4 f = __ldg(reinterpret_cast<const float4*>(base + piece * 8) + i);
-              cs[2 * i] = f.x;
-              sn[2 * i] = f.y;
-              cs[2 * i + 1] = f.z;
-              sn[2 * i + 1] = f.w;
-            }
-          } else {
-            const bool first = piece < RP / 2;
-            const float4* at4 = reinterpret_cast<const float4*>(base + (first ? piece : piece - RP / 2) * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = __ldg(at4 + i);
-              cs[2 * i] = f.x;
-              sn[2 * i] = first ? -f.y : f.y;
-              cs[2 * i + 1] = f.z;
-              sn[2 * i + 1] = first ? -f.w : f.w;
-            }
-          }
-        }
-      }
-    };
-    auto load = [&](int h) {
-      uint4 r = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h < h1) {
-        const __half* src = h < a.q_heads ? a.q + row * a.ldq + (long long)h * D
-                            : h < qk      ? a.k + row * a.ldk + (long long)(h - a.q_heads) * D
-                                          : a.v + row * a.ldv + (long long)(h - qk) * D;
-        r = *reinterpret_cast<const uint4*>(src + piece * 8);
-      }
-      return r;
-    };
-    // turns and stores the row's head h; returns it in fp16.  All lanes of the warp call it.
-    auto put = [&](int h, const uint4& raw) {
-      float x[8], y[8];
-      unpack8(raw, x);
-      const bool key = h >= a.q_heads;              // keys (and values, which are not turned)
-      if (a.angles && h0 < qk) {
-        uint4 other = raw;
-        if (!a.interleaved) {                       // the other half's columns
-          const int from = lane - piece + (piece < RP / 2 ? piece + RP / 2 : piece < RP ? piece - RP / 2 : piece);
-          other.x = __shfl_sync(0xffffffffu, raw.x, from);
-          other.y = __shfl_sync(0xffffffffu, raw.y, from);
-          other.z = __shfl_sync(0xffffffffu, raw.z, from);
-          other.w = __shfl_sync(0xffffffffu, raw.w, from);
-        }
-        if (turned && h < qk) {
-          float o[8];
-          unpack8(other, o);
-          if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float u = x[2 * i], w = x[2 * i + 1];
-              y[2 * i] = key ? turn_exact(u, cs[i], w, -sn[i]) : fmaf(u, cs[i], -w * sn[i]);
-              y[2 * i + 1] = key ? turn_exact(w, cs[i], u, sn[i]) : fmaf(w, cs[i], u * sn[i]);
-            }
-          } else if (key) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = turn_exact(x[i], cs[i], o[i], sn[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], cs[i], o[i] * sn[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = y[i];
-        }
-      }
-      uint4 h8 = pack8(x);
-      const bool mine = live && h < h1;
-      if (!key) {
-        if (!s.ok) h8 = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
-        if (mine) *reinterpret_cast<uint4*>(a.qo + row * a.ldqo + (long long)h * D + piece * 8) = h8;
-      }
-      const bool val = h >= qk;
-      const int hk = h - (val ? qk : a.q_heads);
-      unsigned char* to = (val ? a.pg.v : a.pg.k) + at + hk * a.pg.head_stride;
-      if constexpr (GRP == 0) {
-        if (key && mine && there) *reinterpret_cast<uint4*>(to + piece * 16) = h8;
-      } else {
-        if (__any_sync(0xffffffffu, key)) {
-          __half2 pair;
-          const uint32_t code = quantise<GRP>(x, pair);
-          if (key && mine && there) {
-            *reinterpret_cast<uint32_t*>(to + piece * 4) = code;
-            if (piece % (GRP / 8) == 0)
-              *reinterpret_cast<__half2*>((val ? a.sp.v : a.sp.k) + sat + hk * a.sp.head_stride + piece / (GRP / 8) * 4) = pair;
-          }
-        }
-      }
-      return h8;
-    };
+    // The slots take T tokens side by side and SLOTS / T heads; keys with bounds
+    // all heads, so that a slot's rows are of one head.
+    int T = SLOTS;
+    if (bounded)
+      while (T > 1 && SLOTS / T < nh) T >>= 1;
+    while (T > 1 && T / 2 >= n) T >>= 1;
+    const int tk = slot & (T - 1), part = slot / T, HS = SLOTS / T;
+    const int steps = (nh + HS - 1) / HS, items = (n + T - 1) / T * steps;   // a slot's rows: tokens in turn, and the heads of each
 
-    // keys whose bounds are kept are taken below, head by head
-    const int k0 = a.bounds ? max(h0, a.q_heads) : h1, k1 = a.bounds ? min(h1, qk) : h1;
-    if (k0 > h0 || k1 < h1 || !a.bounds) {
-      for (int t0 = 0; t0 < n; t0 += T) {
-        token(t0 + tk);
-        for (int e0 = h0; e0 < h1; e0 += HS) {
-          if (a.bounds && e0 >= k0 && e0 + HS <= k1) continue;
-          const int h = e0 + part;
-          const bool skip = a.bounds && h >= k0 && h < k1;
-          const uint4 raw = skip ? make_uint4(0u, 0u, 0u, 0u) : load(h);
-          put(skip ? h1 : h, raw);
+    // what is to be read from memory goes out first: the first rows, the angles, the pages
+    auto load = [&](int t, int e) {
+      return t < n && e < nh ? *reinterpret_cast<const uint4*>(src + (row0 + t) * ld + (long long)e * D) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 raw[kBatch];
+    int lt = tk, le = part;                         // the row to be loaded: token, head
+    auto fetch = [&]() {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        raw[u] = load(lt, le);
+        le += HS;
+        if (le - part >= steps * HS) {
+          le = part;
+          lt += T;
+        }
+      }
+    };
+    fetch();
+    if (turns && s.ok) {
+      const float4* from = reinterpret_cast<const float4*>(a.angles + (long long)p0 * a.rot);
+      for (int i = threadIdx.x; i < n * (a.rot / 4); i += kThreads)          // (exchanged by the lane that reads them, for the banks)
+        cp16(saddr(q2_append_smem + (i ^ (i >> 2 & 3))), from + i, true);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if (kind != QUERY && threadIdx.x < n) {
+      const int pos = p0 + threadIdx.x, pi = s.ok ? page_of(a.pg, pos) : 0, page = s.ok ? trow[pi] : -1;
+      const bool there = (unsigned)page < (unsigned)a.pg.npages;
+      if (s.ok && !there) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
+      const int at = pos - pi * a.pg.page;
+      places[0][threadIdx.x] = there ? page * a.pg.page_stride + at * a.pg.token_stride : -1;
+      if (GRP) places[1][threadIdx.x] = there ? page * a.sp.page_stride + at * a.sp.token_stride : -1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+
+    uint4 lo = make_uint4(0x7c007c00u, 0x7c007c00u, 0x7c007c00u, 0x7c007c00u);       // bounds of a slot's keys
+    uint4 hi = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+    float cs[8], sn[8];                             // this lane's angles; of a first half's columns the sine is negated
+    int t = tk, e = part;
+    for (int k0 = 0; k0 < items; k0 += kBatch) {
+      uint4 now[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) now[u] = raw[u];
+      if (k0 + kBatch < items) fetch();
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (k0 + u < items) {                       // (the same for all)
+          const bool live = t < n && e < nh;
+          uint4 h8 = now[u];
+          float x[8];
+          if (turns || GRP) unpack8(h8, x);
+          if (turns) {
+            if (turned && e == part) {              // another token
+              const int f = min(t, n - 1) * (a.rot / 4) + apiece;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i < 2 || !a.interleaved) {
+                  const float4 v = q2_append_smem[(f + i) ^ ((f + i) >> 2 & 3)];
+                  const float sign = a.interleaved || !first_half ? 1.f : -1.f;
+                  cs[2 * i] = v.x;
+                  sn[2 * i] = v.y * sign;
+                  cs[2 * i + 1] = v.z;
+                  sn[2 * i + 1] = v.w * sign;
+                }
+              }
+            }
+            if (a.interleaved) {
+              if (turned) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float v = x[2 * i], w = x[2 * i + 1];
+                  x[2 * i] = kind == KEY ? turn_exact(v, cs[i], w, -sn[i]) : fmaf(v, cs[i], -w * sn[i]);
+                  x[2 * i + 1] = kind == KEY ? turn_exact(w, cs[i], v, sn[i]) : fmaf(w, cs[i], v * sn[i]);
+                }
+              }
+            } else {
+              uint4 other;                          // the other half's columns
+              other.x = __shfl_sync(0xffffffffu, h8.x, partner);
+              other.y = __shfl_sync(0xffffffffu, h8.y, partner);
+              other.z = __shfl_sync(0xffffffffu, h8.z, partner);
+              other.w = __shfl_sync(0xffffffffu, h8.w, partner);
+              if (turned) {
+                float o[8];
+                unpack8(other, o);
+                if (kind == KEY) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] = turn_exact(x[i], cs[i], o[i], sn[i]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], o[i] * sn[i]);
+                }
+              }
+            }
+            h8 = pack8(x);
+          }
+          if (kind == QUERY) {
+            if (!s.ok) h8 = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+            if (live) *reinterpret_cast<uint4*>(a.qo + (row0 + t) * a.ldqo + (long long)(h0 + e) * D + piece * 8) = h8;
+          } else {
+            const long long at = live ? places[0][t] : -1;
+            unsigned char* to = (kind == VALUE ? a.pg.v : a.pg.k) + at + (h0 + e) * a.pg.head_stride;
+            if constexpr (GRP == 0) {
+              if (at >= 0) *reinterpret_cast<uint4*>(to + piece * 16) = h8;
+            } else {
+              __half2 pair;
+              const uint32_t code = quantise<GRP>(x, pair);
+              if (at >= 0) {
+                *reinterpret_cast<uint32_t*>(to + piece * 4) = code;
+                if (piece % (GRP / 8) == 0)
+                  *reinterpret_cast<__half2*>((kind == VALUE ? a.sp.v : a.sp.k) + places[1][t] + (h0 + e) * a.sp.head_stride +
+                                              piece / (GRP / 8) * 4) = pair;
+              }
+            }
+            if (bounded && live) {
+              lo = hmin8(lo, h8);
+              hi = hmax8(hi, h8);
+            }
+          }
+          e += HS;
+          if (e - part >= steps * HS) {
+            e = part;
+            t += T;
+          }
         }
       }
     }
-    if (a.bounds && k0 < k1) {
-      const int first = s.ok ? block * Q2_BLOCK : 0, pi = page_of(a.pg, first);
+    if (bounded) {                                  // (a slot's keys are of head `part`)
+      const int begin = s.ok ? block * Q2_BLOCK : 0, pi = page_of(a.pg, begin);
       const int page = s.ok ? trow[pi] : -1;
       const bool kept = (unsigned)page < (unsigned)a.pg.npages;
-      const int place = (first - pi * a.pg.page) / Q2_BLOCK;
-      for (int e0 = k0; e0 < k1; e0 += HS) {
-        const int h = e0 + part;
-        uint4 lo = make_uint4(0x7c007c00u, 0x7c007c00u, 0x7c007c00u, 0x7c007c00u);
-        uint4 hi = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
-        for (int t0 = 0; t0 < n; t0 += T) {
-          token(t0 + tk);
-          const bool mine = h < k1;
-          const uint4 y = put(mine ? h : h1, mine ? load(h) : make_uint4(0u, 0u, 0u, 0u));
-          if (live && mine) {
-            lo = hmin8(lo, y);
-            hi = hmax8(hi, y);
-          }
+      red[slot][0][piece] = lo;
+      red[slot][1][piece] = hi;
+      __syncthreads();
+      for (int i = threadIdx.x; i < nh * 2 * LPR; i += kThreads) {
+        const int h = i / (2 * LPR), w = i / LPR % 2, pc = i % LPR;
+        if (kept) {
+          uint4 x = red[h * T][w][pc];
+          for (int k = 1; k < T; ++k) x = w ? hmax8(x, red[h * T + k][w][pc]) : hmin8(x, red[h * T + k][w][pc]);
+          uint4* to = reinterpret_cast<uint4*>(
+              a.bounds +
+              ((((long long)page * a.sub + (begin - pi * a.pg.page) / Q2_BLOCK) * a.kv_heads + h0 + h) * 2 + w) * D + pc * 8);
+          if (p0 > begin) x = w ? hmax8(x, *to) : hmin8(x, *to);              // the block goes on
+          *to = x;
         }
-        red[slot][0][piece] = lo;
-        red[slot][1][piece] = hi;
-        __syncthreads();
-        for (int i = threadIdx.x; i < HS * 2 * LPR; i += kThreads) {
-          const int hh = i / (2 * LPR), w = i / LPR % 2, pc = i % LPR;
-          if (kept && e0 + hh < k1) {
-            uint4 x = red[hh * T][w][pc];
-            for (int t = 1; t < T; ++t) x = w ? hmax8(x, red[hh * T + t][w][pc]) : hmin8(x, red[hh * T + t][w][pc]);
-            uint4* to = reinterpret_cast<uint4*>(
-                a.bounds + ((((long long)page * a.sub + place) * a.kv_heads + (e0 + hh - a.q_heads)) * 2 + w) * D + pc * 8);
-            if (p0 > first) x = w ? hmax8(x, *to) : hmin8(x, *to);      // the block goes on
-            *to = x;
-          }
-        }
-        __syncthreads();
       }
     }
+    __syncthreads();                                // angles, places and bounds are another tile's from here on
   }
 }
 
@@ -533,20 +535,23 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   a.kv_heads = c.kv_heads;
   a.sub = (c.page + Q2_BLOCK - 1) / Q2_BLOCK;
   // Heads per CTA: as many as its row slots take side by side at the usual
-  // number of tokens, more where the tiles alone fill the SMs six times over.
-  const int heads = q_heads + 2 * c.kv_heads, slots = kThreads * 8 / c.D;
+  // number of tokens, more where there would be more than four CTAs per SM; keys
+  // whose bounds are kept no more than the slots.
+  const int slots = kThreads * 8 / c.D;
   const long long tiles = starts ? (long long)ntok / Q2_BLOCK + 2ll * std::min(batch, ntok) : batch;
   const int usual = std::min(Q2_BLOCK, (ntok + batch - 1) / batch);
   int side = slots;
   for (int t = 1; t < usual && side > 1; t <<= 1) side >>= 1;
-  const long long fill = (heads * tiles + 6 * dev_info().sms - 1) / (6 * dev_info().sms);
-  a.chunk = std::max(side, (int)std::min(16ll, fill));
-  dim3 grid((unsigned)std::min(tiles, 65535ll), (heads + a.chunk - 1) / a.chunk);
-  while (grid.y > 65535u) {
-    a.chunk *= 2;
-    grid.y = (heads + a.chunk - 1) / a.chunk;
-  }
-  return by_shape(c, [&](auto D, auto G) { return launch_pdl(k_append<D(), G()>, a, grid, kThreads, 0, stream); });
+  const long long heads = q_heads + 2ll * c.kv_heads;
+  a.chunk = std::max(side, (int)std::min((long long)std::min(16, slots), heads * tiles / (4 * dev_info().sms)));
+  auto ctas = [&](int h) { return (h + a.chunk - 1) / a.chunk; };
+  while (ctas(q_heads) + 2 * ctas(c.kv_heads) > 65535) a.chunk *= 2;
+  if (bounds) a.chunk = std::min(a.chunk, slots);
+  a.cq = ctas(q_heads);
+  a.ck = ctas(c.kv_heads);
+  const dim3 grid((unsigned)std::min(tiles, 65535ll), a.cq + 2 * a.ck);
+  const int smem = rope ? (starts ? Q2_BLOCK : 1) * a.rot * 4 : 0;
+  return by_shape(c, [&](auto D, auto G) { return launch_pdl(k_append<D(), G()>, a, grid, kThreads, smem, stream); });
 }
 
 int read(const Pages& pg, const Pages& sp, const CacheShape& c, void* k, long long ldk, void* v, long long ldv,

@@ -31,6 +31,11 @@ __device__ __forceinline__ int page_of(const A& a, int t) {
   return (int)((__umulhi((uint32_t)t, a.page_mul) + (uint32_t)t) >> a.page_sh);
 }
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
 struct CacheShape {
   int D, group, kv_heads, page;   // group: columns of a group in 4 bits, 0 in fp16
   long long cap;                  // tokens that a table row can hold
