@@ -160,14 +160,16 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
 
 constexpr int kBatch = 4;                           // rows of a slot whose loads are in flight together
 
-// GRP: columns of a group of the 4-bit cache, 0 for an fp16 cache
-template <int D, int GRP>
+// GRP: columns of a group of the 4-bit cache, 0 for an fp16 cache.  ONE: one
+// token per sequence (no starts): every lane reads its angles and the page, and
+// nothing is waited for.
+template <int D, int GRP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
   extern __shared__ __align__(16) float4 q2_append_smem[];                   // angles of the tile's tokens, [token][rot / 4]
-  __shared__ long long places[2][Q2_BLOCK];         // of its tokens in the pools, and in those of the pairs; -1: none
+  __shared__ long long places[2][ONE ? 1 : Q2_BLOCK];         // of its tokens in the pools, and in those of the pairs; -1: none
   __shared__ uint4 red[SLOTS][2][LPR];
-  __shared__ int pre[Q2_ATT_MAX_BATCH + 1];         // tiles before each sequence
+  __shared__ int pre[ONE ? 1 : Q2_ATT_MAX_BATCH + 1];         // tiles before each sequence
   __shared__ int wsum[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = threadIdx.x / LPR, piece = threadIdx.x % LPR;
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
   pdl_trigger();
   const RowArgs& rw = a.rows;
   int total = rw.batch;
-  if (rw.starts) {                                  // four sequences per thread, then a scan of the threads' sums
+  if constexpr (!ONE) {                             // four sequences per thread, then a scan of the threads' sums
     constexpr int EACH = Q2_ATT_MAX_BATCH / kThreads;
     int n[EACH], sum = 0;
     bool bad = false;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
 
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     int b = tile, j = 0;
-    if (rw.starts) {                                // the sequence with pre[b] <= tile < pre[b + 1]
+    if constexpr (!ONE) {                           // the sequence with pre[b] <= tile < pre[b + 1]
       int lo = 0, hi = rw.batch - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -241,20 +243,20 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
       j = tile - pre[lo];
     }
     const Seq s = seq_of(rw, b);
-    if (!rw.starts) {
+    if (ONE) {
       if (!s.ok && y == 0 && threadIdx.x == 0) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
       if (!s.n) continue;
     }
     const int past = s.len - s.n, block = past / Q2_BLOCK + j;
     const int p0 = s.ok ? max(past, block * Q2_BLOCK) : 0;
-    const int n = s.ok ? min(s.len, (block + 1) * Q2_BLOCK) - p0 : min(Q2_BLOCK, s.n - j * Q2_BLOCK);
+    const int n = ONE ? 1 : s.ok ? min(s.len, (block + 1) * Q2_BLOCK) - p0 : min(Q2_BLOCK, s.n - j * Q2_BLOCK);
     const int row0 = s.row0 + (s.ok ? p0 - past : j * Q2_BLOCK);
     const int* trow = a.pg.table + b * a.pg.table_stride;
 
     // The slots take T tokens side by side and SLOTS / T heads; keys with bounds
     // all heads, so that a slot's rows are of one head.
-    int T = SLOTS;
-    if (bounded)
+    int T = ONE ? 1 : SLOTS;
+    if (!ONE && bounded)
       while (T > 1 && SLOTS / T < nh) T >>= 1;
     while (T > 1 && T / 2 >= n) T >>= 1;
     const int tk = slot & (T - 1), part = slot / T, HS = SLOTS / T;
@@ -278,22 +280,32 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
       }
     };
     fetch();
-    if (turns && s.ok) {
+    long long place = -1, pair_place = -1;          // of the token in the pools, and in those of the pairs
+    auto place_of = [&](int pos) {
+      const int pi = s.ok ? page_of(a.pg, pos) : 0, page = s.ok ? trow[pi] : -1;
+      const bool there = (unsigned)page < (unsigned)a.pg.npages;
+      if (s.ok && !there) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
+      const int at = pos - pi * a.pg.page;
+      place = there ? page * a.pg.page_stride + at * a.pg.token_stride : -1;
+      if (GRP) pair_place = there ? page * a.sp.page_stride + at * a.sp.token_stride : -1;
+    };
+    if (!ONE && turns && s.ok) {
       const float4* from = reinterpret_cast<const float4*>(a.angles + (long long)p0 * a.rot);
       for (int i = threadIdx.x; i < n * (a.rot / 4); i += kThreads)          // (exchanged by the lane that reads them, for the banks)
         cp16(saddr(q2_append_smem + (i ^ (i >> 2 & 3))), from + i, true);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    if (kind != QUERY && threadIdx.x < n) {
-      const int pos = p0 + threadIdx.x, pi = s.ok ? page_of(a.pg, pos) : 0, page = s.ok ? trow[pi] : -1;
-      const bool there = (unsigned)page < (unsigned)a.pg.npages;
-      if (s.ok && !there) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
-      const int at = pos - pi * a.pg.page;
-      places[0][threadIdx.x] = there ? page * a.pg.page_stride + at * a.pg.token_stride : -1;
-      if (GRP) places[1][threadIdx.x] = there ? page * a.sp.page_stride + at * a.sp.token_stride : -1;
+    if (kind != QUERY && (ONE || threadIdx.x < n)) {
+      place_of(p0 + (ONE ? 0 : threadIdx.x));
+      if (!ONE) {
+        places[0][threadIdx.x] = place;
+        places[1][threadIdx.x] = pair_place;
+      }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    if (!ONE) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+    }
 
     uint4 lo = make_uint4(0x7c007c00u, 0x7c007c00u, 0x7c007c00u, 0x7c007c00u);       // bounds of a slot's keys
     uint4 hi = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
@@ -314,10 +326,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
           if (turns) {
             if (turned && e == part) {              // another token
               const int f = min(t, n - 1) * (a.rot / 4) + apiece;
+              const float4* one = reinterpret_cast<const float4*>(a.angles + (long long)p0 * a.rot) + apiece;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (i < 2 || !a.interleaved) {
-                  const float4 v = q2_append_smem[(f + i) ^ ((f + i) >> 2 & 3)];
+                  const float4 v = !ONE ? q2_append_smem[(f + i) ^ ((f + i) >> 2 & 3)] : s.ok ? __ldg(one + i) : make_float4(0.f, 0.f, 0.f, 0.f);
                   const float sign = a.interleaved || !first_half ? 1.f : -1.f;
                   cs[2 * i] = v.x;
                   sn[2 * i] = v.y * sign;
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
             if (!s.ok) h8 = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
             if (live) *reinterpret_cast<uint4*>(a.qo + (row0 + t) * a.ldqo + (long long)(h0 + e) * D + piece * 8) = h8;
           } else {
-            const long long at = live ? places[0][t] : -1;
+            const long long at = !live ? -1 : ONE ? place : places[0][t];
             unsigned char* to = (kind == VALUE ? a.pg.v : a.pg.k) + at + (h0 + e) * a.pg.head_stride;
             if constexpr (GRP == 0) {
               if (at >= 0) *reinterpret_cast<uint4*>(to + piece * 16) = h8;
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
               if (at >= 0) {
                 *reinterpret_cast<uint32_t*>(to + piece * 4) = code;
                 if (piece % (GRP / 8) == 0)
-                  *reinterpret_cast<__half2*>((kind == VALUE ? a.sp.v : a.sp.k) + places[1][t] + (h0 + e) * a.sp.head_stride +
+                  *reinterpret_cast<__half2*>((kind == VALUE ? a.sp.v : a.sp.k) + (ONE ? pair_place : places[1][t]) + (h0 + e) * a.sp.head_stride +
                                               piece / (GRP / 8) * 4) = pair;
               }
             }
@@ -406,35 +419,49 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
         }
       }
     }
-    __syncthreads();                                // angles, places and bounds are another tile's from here on
+    if (!ONE || bounded) __syncthreads();           // angles, places and bounds are another tile's from here on
   }
 }
 
 struct ReadArgs {
   RowArgs rows;
   Pages pg, sp;
-  __half* k;
-  __half* v;
-  long long ldk, ldv;
-  int kv_heads;
+  __half* out[2];               // keys and values; where there is one, `both` is 0 and it comes first
+  const unsigned char* pool[2];
+  const unsigned char* pairs[2];
+  long long ld[2];
+  long long items;              // of 8 columns, of all rows
+  int kv_heads, both;
 };
 
-// One row (all heads, keys then values) per step of a CTA; 8 columns per thread
-// and step.
-template <int D, int GRP>
+// kReads: pieces of 8 columns that a thread has in flight
+template <int D, int GRP, int kReads>
 __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ ReadArgs a) {
   constexpr int LPR = D / 8;
   __shared__ int starts[Q2_ATT_MAX_BATCH + 1];
   pdl_wait();
   pdl_trigger();
   const RowArgs& rw = a.rows;
-  if (rw.starts)
+  if (rw.starts) {
     for (int i = threadIdx.x; i <= rw.batch; i += kThreads) starts[i] = rw.starts[i];
+    __syncthreads();
+  }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < rw.batch; b += kThreads)
       if (!seq_of(rw, b).ok) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
-  __syncthreads();
-  for (int row = blockIdx.x; row < rw.ntok; row += gridDim.x) {
+  const uint32_t per = a.kv_heads * LPR, each = per << a.both;               // pieces of a row's keys or values; of a row
+  const long long first = (long long)blockIdx.x * (kThreads * kReads) + threadIdx.x;
+  __half* to[kReads];
+  const unsigned char* from[kReads];
+  const unsigned char* pair[kReads];
+#pragma unroll
+  for (int u = 0; u < kReads; ++u) {
+    const long long i = first + u * kThreads;
+    to[u] = nullptr;
+    from[u] = pair[u] = nullptr;
+    if (i >= a.items) continue;
+    const int row = (int)(i / each);
+    const uint32_t r = (uint32_t)(i - (long long)row * each), w = r >= per, h = (r - w * per) / LPR, piece = r % LPR;
     int b = row;
     if (rw.starts) {                                // the last sequence that begins at or before the row
       int lo = 0, hi = rw.batch;
@@ -448,33 +475,42 @@ __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ ReadA
     }
     const Seq s = seq_of(rw, b);
     if (s.n == 0 || row < s.row0 || row >= s.row0 + s.n) continue;
-    const int pos = s.len - s.n + (row - s.row0);
-    const int pi = s.ok ? page_of(a.pg, pos) : 0, page = s.ok ? a.pg.table[b * a.pg.table_stride + pi] : -1;
-    const bool there = (unsigned)page < (unsigned)a.pg.npages;
-    if (s.ok && !there && threadIdx.x == 0) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
-    const long long e = there ? page * a.pg.page_stride + (pos - pi * a.pg.page) * a.pg.token_stride : 0;
-    const long long f = there && GRP ? page * a.sp.page_stride + (pos - pi * a.pg.page) * a.sp.token_stride : 0;
-    for (int i = threadIdx.x; i < 2 * a.kv_heads * LPR; i += kThreads) {
-      const int w = i >= a.kv_heads * LPR, h = (i - w * a.kv_heads * LPR) / LPR, piece = i % LPR;
-      __half* to = w ? a.v : a.k;
-      if (!to) continue;
-      uint4 r = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
-      if (there) {
-        const unsigned char* src = (w ? a.pg.v : a.pg.k) + e + h * a.pg.head_stride;
-        if constexpr (GRP == 0) {
-          r = *reinterpret_cast<const uint4*>(src + piece * 16);
-        } else {
-          const uint32_t c = *reinterpret_cast<const uint32_t*>(src + piece * 4);
-          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>((w ? a.sp.v : a.sp.k) + f + h * a.sp.head_stride +
-                                                                             piece / (GRP / 8) * 4));
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((c >> (4 * k)) & 15u), sm.x, sm.y);
-          r = pack8(x);
-        }
-      }
-      *reinterpret_cast<uint4*>(to + row * (w ? a.ldv : a.ldk) + (long long)h * D + piece * 8) = r;
+    to[u] = a.out[w] + row * a.ld[w] + (long long)h * D + piece * 8;
+    if (!s.ok) continue;
+    const int pos = s.len - s.n + (row - s.row0), pi = page_of(a.pg, pos), page = a.pg.table[b * a.pg.table_stride + pi];
+    if ((unsigned)page >= (unsigned)a.pg.npages) {
+      if (r == 0) atomicOr(&q2_cache_error, Q2_ERR_PAGE);
+      continue;
     }
+    const int at = pos - pi * a.pg.page;
+    from[u] = a.pool[w] + page * a.pg.page_stride + at * a.pg.token_stride + h * a.pg.head_stride + piece * (GRP ? 4 : 16);
+    if (GRP)
+      pair[u] = a.pairs[w] + page * a.sp.page_stride + at * a.sp.token_stride + h * a.sp.head_stride + piece / (GRP ? GRP / 8 : 1) * 4;
+  }
+  uint4 raw[kReads];
+  __half2 sm[kReads];
+#pragma unroll
+  for (int u = 0; u < kReads; ++u) {
+    raw[u] = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+    if (from[u]) {
+      if constexpr (GRP == 0) {
+        raw[u] = *reinterpret_cast<const uint4*>(from[u]);
+      } else {
+        raw[u].x = *reinterpret_cast<const uint32_t*>(from[u]);
+        sm[u] = *reinterpret_cast<const __half2*>(pair[u]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kReads; ++u) {
+    if (GRP && from[u]) {
+      const float2 f = __half22float2(sm[u]);
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((raw[u].x >> (4 * k)) & 15u), f.x, f.y);
+      raw[u] = pack8(x);
+    }
+    if (to[u]) *reinterpret_cast<uint4*>(to[u]) = raw[u];
   }
 }
 
@@ -550,8 +586,11 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   a.cq = ctas(q_heads);
   a.ck = ctas(c.kv_heads);
   const dim3 grid((unsigned)std::min(tiles, 65535ll), a.cq + 2 * a.ck);
-  const int smem = rope ? (starts ? Q2_BLOCK : 1) * a.rot * 4 : 0;
-  return by_shape(c, [&](auto D, auto G) { return launch_pdl(k_append<D(), G()>, a, grid, kThreads, smem, stream); });
+  const int smem = rope && starts ? Q2_BLOCK * a.rot * 4 : 0;
+  return by_shape(c, [&](auto D, auto G) {
+    return starts ? launch_pdl(k_append<D(), G(), false>, a, grid, kThreads, smem, stream)
+                  : launch_pdl(k_append<D(), G(), true>, a, grid, kThreads, 0, stream);
+  });
 }
 
 int read(const Pages& pg, const Pages& sp, const CacheShape& c, void* k, long long ldk, void* v, long long ldv,
@@ -564,13 +603,27 @@ int read(const Pages& pg, const Pages& sp, const CacheShape& c, void* k, long lo
   if ((k && (st = check_ld(k, ldk, kw, ntok))) || (v && (st = check_ld(v, ldv, kw, ntok)))) return st;
   a.pg = pg;
   a.sp = sp;
-  a.k = static_cast<__half*>(k);
-  a.v = static_cast<__half*>(v);
-  a.ldk = ldk;
-  a.ldv = ldv;
+  a.both = k && v;
+  int w = 0;
+  auto add = [&](void* out, long long ld, const unsigned char* pool, const unsigned char* pairs) {
+    if (!out) return;
+    a.out[w] = static_cast<__half*>(out);
+    a.ld[w] = ld;
+    a.pool[w] = pool;
+    a.pairs[w++] = pairs;
+  };
+  add(k, ldk, pg.k, sp.k);
+  add(v, ldv, pg.v, sp.v);
   a.kv_heads = c.kv_heads;
-  const int grid = std::min(ntok, dev_info().sms * 8);
-  return by_shape(c, [&](auto D, auto G) { return launch_pdl(k_read<D(), G()>, a, grid, kThreads, 0, stream); });
+  a.items = ((long long)ntok * c.kv_heads * (c.D / 8)) << a.both;
+  // four pieces to a thread where that leaves four CTAs per SM
+  const int reads = a.items >= 4ll * kThreads * 4 * dev_info().sms ? 4 : 1;
+  const long long ctas = (a.items + kThreads * reads - 1) / (kThreads * reads);
+  if (ctas > 0x7fffffffll) return Q2_ESHAPE;
+  return by_shape(c, [&](auto D, auto G) {
+    return reads == 4 ? launch_pdl(k_read<D(), G(), 4>, a, (int)ctas, kThreads, 0, stream)
+                      : launch_pdl(k_read<D(), G(), 1>, a, (int)ctas, kThreads, 0, stream);
+  });
 }
 
 }  // namespace
