@@ -151,14 +151,18 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
   }
   pair = __halves2half2(sh, mh);
   if (s == 0.f) return 0;
+  // (y - m) / s rounded to nearest: from the rounded reciprocal one correction by
+  // the remainder gives it (Markstein, "Computation of elementary functions on
+  // the IBM RISC System/6000 processor", 1990, theorem 4.1)
+  const float r = __frcp_rn(s);
   uint32_t c = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    c |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(y[e] - m, s)), 0.f), 15.f) << (4 * e);
+  for (int e = 0; e < 8; ++e) {
+    const float d = y[e] - m, q = d * r;
+    c |= (uint32_t)fminf(fmaxf(rintf(fmaf(fmaf(-q, s, d), r, q)), 0.f), 15.f) << (4 * e);
+  }
   return c;
 }
-
-constexpr int kBatch = 4;                           // rows of a slot whose loads are in flight together
 
 // GRP: columns of a group of the 4-bit cache, 0 for an fp16 cache.  ONE: one
 // token per sequence (no starts): every lane reads its angles and the page, and
@@ -166,6 +170,7 @@ constexpr int kBatch = 4;                           // rows of a slot whose load
 template <int D, int GRP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
+  constexpr int kBatch = ONE ? 1 : GRP ? 2 : 4;     // rows of a slot whose loads are in flight together (long code costs fetches)
   extern __shared__ __align__(16) float4 q2_append_smem[];                   // angles of the tile's tokens, [token][rot / 4]
   __shared__ long long places[2][ONE ? 1 : Q2_BLOCK];         // of its tokens in the pools, and in those of the pairs; -1: none
   __shared__ uint4 red[SLOTS][2][LPR];
@@ -571,7 +576,7 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   a.kv_heads = c.kv_heads;
   a.sub = (c.page + Q2_BLOCK - 1) / Q2_BLOCK;
   // Heads per CTA: as many as its row slots take side by side at the usual
-  // number of tokens, more where there would be more than four CTAs per SM; keys
+  // number of tokens, more where there would be more CTAs than run at once; keys
   // whose bounds are kept no more than the slots.
   const int slots = kThreads * 8 / c.D;
   const long long tiles = starts ? (long long)ntok / Q2_BLOCK + 2ll * std::min(batch, ntok) : batch;
@@ -579,7 +584,8 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   int side = slots;
   for (int t = 1; t < usual && side > 1; t <<= 1) side >>= 1;
   const long long heads = q_heads + 2ll * c.kv_heads;
-  a.chunk = std::max(side, (int)std::min((long long)std::min(16, slots), heads * tiles / (4 * dev_info().sms)));
+  const long long at_once = 3ll * dev_info().sms;
+  a.chunk = std::max(side, (int)std::min((long long)std::min(16, slots), (heads * tiles + at_once - 1) / at_once));
   auto ctas = [&](int h) { return (h + a.chunk - 1) / a.chunk; };
   while (ctas(q_heads) + 2 * ctas(c.kv_heads) > 65535) a.chunk *= 2;
   if (bounds) a.chunk = std::min(a.chunk, slots);
