@@ -155,11 +155,16 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
   // the remainder gives it (Markstein, "Computation of elementary functions on
   // the IBM RISC System/6000 processor", 1990, theorem 4.1)
   const float r = __frcp_rn(s);
-  uint32_t c = 0;
+  // Added to 1.5 2^23 a number of 0..15 is rounded to a whole one, ties to even,
+  // in the sum's last bits; the codes are the sums' bits, 4 e up, less what
+  // 1.5 2^23 adds to that.
+  constexpr float kWhole = 12582912.f;
+  constexpr uint32_t kBits = 0x4b400000u, kAll = kBits * 0x11111111u;
+  uint32_t c = 0u - kAll;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float d = y[e] - m, q = d * r;
-    c |= (uint32_t)fminf(fmaxf(rintf(fmaf(fmaf(-q, s, d), r, q)), 0.f), 15.f) << (4 * e);
+    const float d = y[e] - m, q = d * r, f = fminf(fmaxf(fmaf(fmaf(-q, s, d), r, q), 0.f), 15.f);
+    c += __float_as_uint(f + kWhole) << (4 * e);
   }
   return c;
 }
@@ -170,7 +175,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
 template <int D, int GRP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
-  constexpr int kBatch = ONE ? 1 : GRP ? 2 : 4;     // rows of a slot whose loads are in flight together (long code costs fetches)
+  constexpr int kBatch = ONE ? 1 : GRP ? 2 : 3;     // rows of a slot whose loads are in flight together (long code costs fetches)
   extern __shared__ __align__(16) float4 q2_append_smem[];                   // angles of the tile's tokens, [token][rot / 4]
   __shared__ long long places[2][ONE ? 1 : Q2_BLOCK];         // of its tokens in the pools, and in those of the pairs; -1: none
   __shared__ uint4 red[SLOTS][2][LPR];
@@ -435,8 +440,8 @@ struct ReadArgs {
   const unsigned char* pool[2];
   const unsigned char* pairs[2];
   long long ld[2];
-  long long items;              // of 8 columns, of all rows
   int kv_heads, both;
+  uint32_t each_mul, each_sh;   // of a division by the pieces of a row
 };
 
 // kReads: pieces of 8 columns that a thread has in flight
@@ -455,18 +460,20 @@ __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ ReadA
     for (int b = threadIdx.x; b < rw.batch; b += kThreads)
       if (!seq_of(rw, b).ok) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
   const uint32_t per = a.kv_heads * LPR, each = per << a.both;               // pieces of a row's keys or values; of a row
-  const long long first = (long long)blockIdx.x * (kThreads * kReads) + threadIdx.x;
+  const long long first = (long long)blockIdx.x * (kThreads * kReads);
+  const int row0 = (int)(first / each);
+  const uint32_t skip = (uint32_t)(first - (long long)row0 * each) + threadIdx.x;
   __half* to[kReads];
   const unsigned char* from[kReads];
   const unsigned char* pair[kReads];
 #pragma unroll
   for (int u = 0; u < kReads; ++u) {
-    const long long i = first + u * kThreads;
+    const uint32_t i = skip + u * kThreads, rows = (__umulhi(i, a.each_mul) + i) >> a.each_sh;      // (below 2^31: page_of()'s division)
+    const int row = row0 + (int)rows;
     to[u] = nullptr;
     from[u] = pair[u] = nullptr;
-    if (i >= a.items) continue;
-    const int row = (int)(i / each);
-    const uint32_t r = (uint32_t)(i - (long long)row * each), w = r >= per, h = (r - w * per) / LPR, piece = r % LPR;
+    if (row >= rw.ntok) continue;
+    const uint32_t r = i - rows * each, w = r >= per, h = (r - w * per) / LPR, piece = r % LPR;
     int b = row;
     if (rw.starts) {                                // the last sequence that begins at or before the row
       int lo = 0, hi = rw.batch;
@@ -512,7 +519,8 @@ __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ ReadA
       const float2 f = __half22float2(sm[u]);
       float x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((raw[u].x >> (4 * k)) & 15u), f.x, f.y);
+      for (int k = 0; k < 8; ++k)                   // (2^23 + the code, less 2^23)
+        x[k] = fmaf(__uint_as_float(0x4b000000u | (raw[u].x >> (4 * k) & 15u)) - 8388608.f, f.x, f.y);
       raw[u] = pack8(x);
     }
     if (to[u]) *reinterpret_cast<uint4*>(to[u]) = raw[u];
@@ -621,10 +629,12 @@ int read(const Pages& pg, const Pages& sp, const CacheShape& c, void* k, long lo
   add(k, ldk, pg.k, sp.k);
   add(v, ldv, pg.v, sp.v);
   a.kv_heads = c.kv_heads;
-  a.items = ((long long)ntok * c.kv_heads * (c.D / 8)) << a.both;
+  const long long each = (long long)c.kv_heads * (c.D / 8) << a.both, items = each * ntok;
+  if (each > 0x3fffffffll) return Q2_ESHAPE;
+  set_page((int)each, a.each_mul, a.each_sh);
   // four pieces to a thread where that leaves four CTAs per SM
-  const int reads = a.items >= 4ll * kThreads * 4 * dev_info().sms ? 4 : 1;
-  const long long ctas = (a.items + kThreads * reads - 1) / (kThreads * reads);
+  const int reads = items >= 4ll * kThreads * 4 * dev_info().sms ? 4 : 1;
+  const long long ctas = (items + kThreads * reads - 1) / (kThreads * reads);
   if (ctas > 0x7fffffffll) return Q2_ESHAPE;
   return by_shape(c, [&](auto D, auto G) {
     return reads == 4 ? launch_pdl(k_read<D(), G(), 4>, a, (int)ctas, kThreads, 0, stream)
