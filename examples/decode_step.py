@@ -1,12 +1,13 @@
 """A decoder layer's decode step out of the library's operators, with random weights.
 
 Per layer: the residual's addition and the norm (``RmsNorm``), the qkv projection in 2 bits (BPDQ), the norm of every
-query and key head in place, rotary positions, attention over the paged cache with the new token stored on the way
-(``PagedKV``), the output projection in 4 bits, the second norm straight to 8-bit activations, the gate and up
-projections in 4 bits from those, and the down projection in 2 bits.  Sequences of different lengths decode together;
-a step is captured once as a CUDA graph and replayed.
+query and key head in place, the new token into the paged cache with queries and keys turned on the way (``append``),
+attention over the cache (``PagedKV``, or ``PagedKV4`` in 4 bits; with ``--blocks`` only over the blocks of 64 tokens
+that promise the most to the queries), the output projection in 4 bits, the second norm straight to 8-bit activations,
+the gate and up projections in 4 bits from those, and the down projection in 2 bits.  Sequences of different lengths
+decode together; a step is captured once as a CUDA graph and replayed.
 
-    python examples/decode_step.py --layers 4 --batch 8 --steps 64
+    python examples/decode_step.py --layers 4 --batch 8 --steps 64 --cache-bits 4
 """
 import argparse
 import os
@@ -44,7 +45,7 @@ class Layer:
         self.x, self.x8, self.s8 = new(hidden), new(hidden, torch.int8), torch.empty(batch, dtype=torch.float32, device="cuda")
         self.heads, self.att, self.gu = new((q_heads + 2 * kv_heads) * dim), new(q_heads * dim), new(2 * ffn)
 
-    def step(self, h, delta, cache, lens, cos, sin):
+    def step(self, h, delta, cache, lens, rope, blocks=None):
         """h += delta (h the residual stream, in place), then the layer; returns its last projection, not yet added."""
         D, Hq, Hk = self.D, self.Hq, self.Hk
         self.norm1.apply(delta, residual=h, out=self.x)
@@ -52,9 +53,9 @@ class Layer:
         q, k, v = (t.unflatten(1, (-1, D)) for t in self.heads.split([Hq * D, Hk * D, Hk * D], dim=1))
         self.norm_q.apply(q, out=q)
         self.norm_k.apply(k, out=k)
-        for t in (q, k):
-            t.copy_(rotary(t, cos, sin))
-        cache.attend(q, lens, new_k=k, new_v=v, out=self.att.unflatten(1, (Hq, D)))
+        cache.append(k, v, lens, q=q, rope=rope)
+        sel = None if blocks is None else cache.select(q, lens, blocks)
+        cache.attend(q, lens, out=self.att.unflatten(1, (Hq, D)), blocks=sel)
         delta = self.o.gemv(self.att)
         self.norm2.apply(delta, residual=h, out8=self.x8, scale8=self.s8)
         self.gate_up.gemv_x8(self.x8, self.s8, self.gu)
@@ -62,35 +63,38 @@ class Layer:
         return self.down.gemv(torch.nn.functional.silu(gate) * up)
 
 
-def rotary(t, cos, sin):
-    """The two halves of every head turned by the position's angles (cos, sin: fp32 [batch][1][dim / 2])."""
-    a, b = t.float().chunk(2, dim=-1)
-    return torch.cat([a * cos - b * sin, b * cos + a * sin], dim=-1)
-
-
 class Decoder:
-    """Layers, their caches and the state of a batch of sequences: page table, lengths, residual stream."""
+    """Layers, their caches and the state of a batch of sequences: page table, lengths, residual stream.
 
-    def __init__(self, layers, hidden, q_heads, kv_heads, dim, ffn, batch, room, page=16, seed=0):
+    ``bits``: of the cache, 16 or 4 (groups of 64 columns); ``blocks``: how many blocks of 64 tokens a key-value head
+    attends, all if None.
+    """
+
+    def __init__(self, layers, hidden, q_heads, kv_heads, dim, ffn, batch, room, page=16, seed=0, bits=16, blocks=None):
         self.layers = [Layer(hidden, q_heads, kv_heads, dim, ffn, batch, seed + 10 * i) for i in range(layers)]
         per, g = -(-room // page), torch.Generator(device="cuda").manual_seed(seed)
         pages = torch.randperm(batch * per, device="cuda", generator=g).to(torch.int32)
         self.table, self.dim = pages.view(batch, per), dim
-        pool = lambda: torch.empty((batch * per, page, kv_heads, dim), dtype=torch.float16, device="cuda")
-        self.caches = [q2.PagedKV(pool(), pool(), self.table, q_heads) for _ in range(layers)]
+        pool = lambda *tail: torch.zeros((batch * per, *tail), dtype=torch.float16, device="cuda")
+        kept = lambda: None if blocks is None else pool(-(-page // q2.BLOCK), kv_heads, 2, dim)
+        if bits == 16:
+            self.caches = [q2.PagedKV(pool(page, kv_heads, dim), pool(page, kv_heads, dim), self.table, q_heads, bounds=kept())
+                           for _ in range(layers)]
+        else:
+            self.caches = [q2.PagedKV4.empty(batch * per, page, kv_heads, dim, 64, self.table, q_heads, bounds=blocks is not None)
+                           for _ in range(layers)]
+        self.blocks = blocks
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.h = torch.zeros((batch, hidden), dtype=torch.float16, device="cuda")
         self.last = torch.zeros((batch, hidden), dtype=torch.float16, device="cuda")   # what is still to be added to h
-        self.freq = 10000.0 ** (-torch.arange(0, dim, 2, device="cuda").float() / dim)
+        self.rope = q2.Rope.of(dim, per * page)
 
     def step(self):
         """One more token per sequence: ``h`` holds its embedding on entry; afterwards ``h + last`` is the hidden state."""
-        angle = self.lens.float()[:, None, None] * self.freq
-        cos, sin = angle.cos(), angle.sin()
         self.lens += 1
         delta = torch.zeros_like(self.h)
         for layer, cache in zip(self.layers, self.caches):
-            delta = layer.step(self.h, delta, cache, self.lens, cos, sin)
+            delta = layer.step(self.h, delta, cache, self.lens, self.rope, self.blocks)
         self.last.copy_(delta)
 
     def capture(self):
@@ -112,14 +116,19 @@ def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in (("layers", 2), ("hidden", 4096), ("q-heads", 32), ("kv-heads", 8), ("dim", 128), ("ffn", 12288), ("batch", 4), ("steps", 64)):
         p.add_argument("--" + name, type=int, default=value)
+    p.add_argument("--cache-bits", type=int, default=16, choices=(16, 4))
+    p.add_argument("--blocks", type=int, help="blocks of 64 tokens that a key-value head attends (all)")
+    p.add_argument("--past", type=int, default=256, help="tokens that sequences have already, at most")
     a = p.parse_args()
     q2.load(build_if_missing=True)
-    d = Decoder(a.layers, a.hidden, a.q_heads, a.kv_heads, a.dim, a.ffn, a.batch, room=a.steps + 300)
-    # sequences that have 0, 37, 74, .. tokens already (random keys and values)
-    d.lens.copy_(torch.arange(a.batch, device="cuda") * 37 % 256)
+    d = Decoder(a.layers, a.hidden, a.q_heads, a.kv_heads, a.dim, a.ffn, a.batch, room=a.steps + a.past + 44, bits=a.cache_bits, blocks=a.blocks)
+    # sequences that have 0, 37, 74, .. tokens already: prompts of random keys and values
+    past = torch.arange(a.batch, dtype=torch.int32, device="cuda") * 37 % a.past
+    starts = torch.nn.functional.pad(past.cumsum(0), (1, 0)).to(torch.int32)
+    rows = lambda: torch.randn(int(starts[-1]), a.kv_heads, a.dim, device="cuda").half()
     for cache in d.caches:
-        cache.k.normal_()
-        cache.v.normal_()
+        cache.append(rows(), rows(), past, starts=starts, rope=d.rope)
+    d.lens.copy_(past)
     graph = d.capture()
     torch.cuda.synchronize()
     t = time.perf_counter()
