@@ -129,17 +129,17 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
   const int piece = lane % CPR, row0 = lane / CPR;
   const long long lrow = row0 * a.token_stride + piece * 8;            // this lane's place in a tile that lies in one page
   const uint32_t ldst = ring + row0 * (D * 2), lpiece = (uint32_t)((piece ^ row0) << 4);   // row0 < 8; ring and rows on 128 bytes
-  int pt0 = 0;                                      // the warp's first token in the unit to load
+  int pt0 = 0;                                      // SP: the warp's first token in the unit to load
   uint32_t haves = 0;                               // SP: a stage's tokens, a byte each
   auto lookup = [&]() {                             // a tile in one page: its page; else lanes l and l + 16: that of row l
-    pt0 = first_token<SP, kUnit, kTile>(a, p, warp, pu < u1);
-    const int t = pt0 + (a.aligned ? 0 : lane & 15);
+    if (SP) pt0 = first_token<SP, kUnit, kTile>(a, p, warp, pu < u1);
+    const int t = (SP ? pt0 : p.chunk * kUnit + warp * kTile) + (a.aligned ? 0 : lane & 15);
     ppage = pu < u1 && t < p.len ? a.table[p.b * a.table_stride + page_of(a, t)] : -1;
   };
   lookup();
   auto issue = [&]() {
     if (pu < u1) {
-      const int t0 = pt0;
+      const int t0 = SP ? pt0 : p.chunk * kUnit + warp * kTile;
       if (SP) haves = (haves & ~(255u << (8 * pslot))) | (uint32_t)min(max(p.len - t0, 0), kTile) << (8 * pslot);
       if (t0 < p.len) {
         const int have = p.len - t0 - (!SP && a.nk ? 1 : 0);                  // rows to copy: the new token does not come from the cache
