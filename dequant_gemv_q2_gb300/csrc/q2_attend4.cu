@@ -115,6 +115,12 @@ __device__ __forceinline__ void load_pairs(const unsigned char* at, uint32_t (&r
   }
 }
 
+// How far, in powers of two, a score may rise above the maximum before all is
+// scaled anew: p is at most 2^kSlack.  (With 0 a third of the steps of 2048 tokens
+// scaled: 45.0 us for 64 sequences, 43.4 with 4.  Of 20 bits that the smallest p
+// have between 2^-29 and 2^-15 of the largest, four are lost.)
+constexpr uint32_t kSlack = 4;
+
 // 2^x to 2 units in the last place; what is below the normal numbers is zero
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -295,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   float qs[NH][2][G], qf[NH][2];                    // sums over the groups, in the units of the products; what a score is to be multiplied by
   float o[NB][NH][2][4];                            // numerators: columns 32 b + 4 g + 2 k, + 1, each of two heads
   float om[NH][2][G], m[NH][2], ref[NH][2], l[NH][2];   // of the offsets; largest sum, its score (0 for none); denominator (this and om over the lane's tokens)
+  float bar[NH][2];                                 // the sum above which the maximum is taken anew
   const unsigned short less = !FOLD || j >= 2 ? 0xbc00 : 0;     // -1 or 0
   uint32_t top_s;                                   // exponent field of the largest step so far, 1 at least
   int slot = 0;
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
             qs[y][e][i] = __shfl_sync(0xffffffffu, sum[i], (2 * j + e) * 4);
             om[y][e][i] = 0.f;
           }
-          m[y][e] = -INFINITY;
+          m[y][e] = bar[y][e] = -INFINITY;
           ref[y][e] = l[y][e] = 0.f;
         }
 #pragma unroll
@@ -451,10 +458,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
           float top = x[0][y][e];
 #pragma unroll
           for (int n = 1; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
-          rise = rise || top > m[y][e];
+          rise = rise || top > bar[y][e];
         }
-      // A new maximum somewhere, or a larger step: scale what there is.  (Also a
-      // step that is not whole, or has a page that does not exist.)
+      // A maximum far enough above the last, or a larger step: scale what there
+      // is.  (Also a step that is not whole, or has a page that does not exist.)
       if (__any_sync(0xffffffffu, rise)) {
         const uint32_t now_s = max(top_s, __reduce_max_sync(0xffffffffu, most_s));
         const float fall = __uint_as_float((127u - (now_s - top_s)) << 23);
@@ -476,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
             ref[y][e] = top == -INFINITY ? 0.f : top * qf[y][e];
             const float al = m[y][e] == -INFINITY ? 0.f : ex2(fmaf(m[y][e], qf[y][e], -ref[y][e])), alf = al * fall;
             m[y][e] = top;
+            bar[y][e] = top + (float)kSlack / qf[y][e];
             l[y][e] = bad ? __int_as_float(0x7fc00000) : l[y][e] * al;
 #pragma unroll
             for (int i = 0; i < G; ++i) om[y][e][i] *= al;
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
             l[y][e] += x[n][y][e];
           }
       // ---- numerators: p s scaled so that it stays below 2^15
-      const float scale = __uint_as_float((127u + 29u - top_s) << 23);
+      const float scale = __uint_as_float((127u + 29u - kSlack - top_s) << 23);
       const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
 #pragma unroll
       for (int i = 0; i < NTL; ++i) {
@@ -551,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
 
     {
       // Every warp leaves its sums, then joins a quarter of the columns of all
-      // warps.  (p s was scaled by 2^(29 - top_s).)
-      const float unit = __uint_as_float((127u - 29u + top_s) << 23);
+      // warps.  (p s was scaled by 2^(29 - kSlack - top_s).)
+      const float unit = __uint_as_float((127u - 29u + kSlack + top_s) << 23);
 #pragma unroll
       for (int y = 0; y < NH; ++y)
 #pragma unroll
