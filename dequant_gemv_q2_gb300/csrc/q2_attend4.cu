@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   const uint32_t ring = saddr(myring);
   Walk p = c;                                       // the unit to load, at place pu
   int pu = u, prun = run_of(p, u), pleft = prun, pslot = 0;    // units of its (sequence, head) in all and still to be loaded, its stage
-  int ppage = -1, pt0 = 0, pat = 0;                 // page, first token, place in the page (of this lane's row where not aligned)
+  int pt0 = 0, ppage = -1;                          // its first token, its page (of this lane's row where not aligned)
+  int pstep = 0, nt0 = 0, npage = -1;               // SP: its number of them; first token and page of the next
   uint32_t badslots = 0, haves = 0;                 // stages with a row whose page does not exist; SP: a stage's tokens, 8 bits each
   const int piece = lane % NB, row0 = lane / NB, prow = lane % TW;
   // the pieces of a row are exchanged so that eight rows of one piece lie in different banks
@@ -205,21 +206,39 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
   const uint32_t lrow = (uint32_t)row0 * a.token_stride + piece, step = a.token_stride * 16;
   const int* trow = nullptr;                        // of p's (sequence, head): the table's row, the head's place
   uint32_t phead = 0, pshead = 0;
+  // SP: where a list says which blocks, two looks are behind one another, into the
+  // list and into the table: 32 units' at a time, and those a unit further ahead
+  // (32 sequences of up to 32768 tokens, 64 blocks of each: 50.4 -> 48.4 us).
+  int found = 0, fpage = -1;                        // first token and page of unit 32 n + lane
+  auto find = [&](int i, int& t0, int& pg) {        // unit i of p's: first token; page, if all its tokens are in one, or of this lane's row
+    if (i % 32 == 0) {
+      Walk w = p;
+      w.chunk += i + lane;
+      found = i + lane < prun ? first_token<SP, UNIT, TW>(a, w, warp, true) : p.len;
+      if (a.aligned) fpage = found < p.len ? trow[page_of(a, found)] : -1;
+    }
+    t0 = __shfl_sync(0xffffffffu, found, i % 32);
+    if (a.aligned) pg = __shfl_sync(0xffffffffu, fpage, i % 32);
+    else pg = t0 + prow < p.len ? trow[page_of(a, t0 + prow)] : -1;
+  };
   auto enter = [&]() {
     const uint32_t kvh = a.nht == 1 ? p.h : p.h / a.nht;
     trow = a.table + p.b * a.table_stride;
     phead = kvh * a.head_stride;
     pshead = kvh * a.s_head_stride;
-    pt0 = p.chunk * UNIT + warp * TW;
+    if (SP) {
+      find(0, pt0, ppage);
+      find(1, nt0, npage);
+    } else {
+      pt0 = p.chunk * UNIT + warp * TW;
+    }
   };
-  auto lookup = [&]() {                             // tokens in one page: its page; else that of this lane's row
-    if (SP) pt0 = first_token<SP, UNIT, TW>(a, p, warp, pleft > 0);
-    const int t = pt0 + (a.aligned ? 0 : prow), pi = page_of(a, t);
-    pat = t - pi * a.page;
-    ppage = pleft > 0 && t < p.len ? trow[pi] : -1;
+  auto lookup = [&]() {
+    const int t = pt0 + (a.aligned ? 0 : prow);
+    ppage = pleft > 0 && t < p.len ? trow[page_of(a, t)] : -1;
   };
   enter();
-  lookup();
+  if (!SP) lookup();
   auto issue = [&]() {
     if (pleft > 0) {
       const int have = SP ? min(max(p.len - pt0, 0), TW) : p.len - pt0;       // tokens; negative: none
@@ -228,6 +247,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
         const bool there = (unsigned)ppage < (unsigned)a.npages;
         const bool bad = __any_sync(0xffffffffu, (a.aligned || prow < have) && !there);
         const uint32_t page = there ? ppage : 0;
+        const int t = pt0 + (a.aligned ? 0 : prow);
+        const uint32_t pat = t - page_of(a, t) * a.page;       // place in the page
         const unsigned long long off = (unsigned long long)page * a.page_stride + (pat * a.token_stride + phead);
         const unsigned long long soff = (unsigned long long)page * a.s_page_stride +
                                         ((pat + (a.aligned ? prow : 0)) * a.s_token_stride + pshead);
@@ -278,16 +299,20 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
       }
       pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
       pt0 += UNIT;
-      if (SP) ++p.chunk;
       if (--pleft == 0) {                           // on to the next (sequence, head)
-        p.chunk += SP ? -1 : prun - 1;
+        p.chunk += prun - 1;
         pu += prun - 1 + advance<SP, UNIT>(a, pre, lens, p);
         if (pu < u1) {
           pleft = prun = run_of(p, pu);
+          pstep = 0;
           enter();
         }
+      } else if (SP) {
+        pt0 = nt0;
+        ppage = npage;
+        find(++pstep + 1, nt0, npage);
       }
-      lookup();
+      if (!SP) lookup();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
