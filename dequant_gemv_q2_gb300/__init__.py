@@ -605,26 +605,47 @@ class _Cache:
         without ``starts`` (int32 [batch + 1]) one token each.  ``q_out``: the turned queries, q itself if None.
         ``rope``: a ``Rope``, or None to turn nothing.  Keeps up ``bounds`` where the cache has them.  Returns ``q_out``.
         """
-        ntok, f16 = k.shape[0], self._f16
-        if starts is None and ntok != self.batch:
-            raise Q2Error(ESHAPE, f"q2_append: {ntok} tokens for {self.batch} sequences, and no starts")
-        st, ln = self._tokens("q2_append", lens, starts)
-        shape = (ntok, self.kv_heads, self.dim)
-        ldk, ldv = _rows("k", k, shape, "q2_append"), _rows("v", v, shape, "q2_append")
+        f16, D, batch, shape = self._f16, self.dim, self.batch, k.shape
+        ntok = shape[0]
+        if starts is None and ntok != batch:
+            raise Q2Error(ESHAPE, f"q2_append: {ntok} tokens for {batch} sequences, and no starts")
+        # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
+        st = None
+        if starts is None and lens.dtype is self._i32 and lens.is_cuda and lens.shape == (batch,) and lens.is_contiguous():
+            ln = lens.data_ptr()
+        else:
+            st, ln = self._tokens("q2_append", lens, starts)
+        stride = k.stride()
+        if k.dtype is f16 and k.is_cuda and shape == (ntok, self.kv_heads, D) and stride[1] == D and stride[2] == 1:
+            ldk = stride[0] if ntok > 1 else self.kv_heads * D
+        else:
+            ldk = _rows("k", k, (ntok, self.kv_heads, D), "q2_append")
+        if v.dtype is f16 and v.is_cuda and v.shape == shape and v.stride() == stride:
+            ldv = ldk
+        else:
+            ldv = _rows("v", v, (ntok, self.kv_heads, D), "q2_append")
         qp = qo = None
         ldq = ldo = 0
         if q is not None:
-            shape = (ntok, self.q_heads, self.dim)
-            ldq = ldo = _rows("q", q, shape, "q2_append")
+            heads, stride = self.q_heads, q.stride()
+            if q.dtype is f16 and q.is_cuda and q.shape == (ntok, heads, D) and stride[1] == D and stride[2] == 1:
+                ldq = stride[0] if ntok > 1 else heads * D
+            else:
+                ldq = _rows("q", q, (ntok, heads, D), "q2_append")
             qp = qo = q.data_ptr()
+            ldo = ldq
             if q_out is None:
                 q_out = q
             elif q_out is not q:
-                ldo, qo = _rows("q_out", q_out, shape, "q2_append"), q_out.data_ptr()
+                qo = q_out.data_ptr()
+                if q_out.dtype is f16 and q_out.is_cuda and q_out.shape == (ntok, heads, D) and q_out.is_contiguous():
+                    ldo = heads * D
+                else:
+                    ldo = _rows("q_out", q_out, (ntok, heads, D), "q2_append")
         elif q_out is not None:
             raise Q2Error(EINVAL, "q2_append: q_out without q")
         st = self._append(self._ref, self._bounds, qp, ldq, qo, ldo, self.q_heads, k.data_ptr(), ldk, v.data_ptr(), ldv, st, ln,
-                          self.batch, ntok, None if rope is None else rope._ref, _stream_ptr(stream))
+                          batch, ntok, None if rope is None else rope._ref, _stream_ptr(stream))
         if st:
             raise Q2Error(st, "q2_append")
         return q_out
@@ -646,9 +667,17 @@ class _Cache:
         rows = (k_out if k_out is not None else v_out).shape[0]
         if (ntok is not None and ntok != rows) or (starts is None and rows != self.batch):
             raise Q2Error(ESHAPE, f"q2_read: outputs of {rows} rows")
-        shape = (rows, self.kv_heads, self.dim)
-        ldk, kp = (0, None) if k_out is None else (_rows("k_out", k_out, shape, "q2_read"), k_out.data_ptr())
-        ldv, vp = (0, None) if v_out is None else (_rows("v_out", v_out, shape, "q2_read"), v_out.data_ptr())
+        shape, f16 = (rows, self.kv_heads, self.dim), self._f16
+        ldk = ldv = self.kv_heads * self.dim
+        kp = vp = None
+        if k_out is not None:
+            kp = k_out.data_ptr()
+            if not (k_out.dtype is f16 and k_out.is_cuda and k_out.shape == shape and k_out.is_contiguous()):
+                ldk = _rows("k_out", k_out, shape, "q2_read")
+        if v_out is not None:
+            vp = v_out.data_ptr()
+            if not (v_out.dtype is f16 and v_out.is_cuda and v_out.shape == shape and v_out.is_contiguous()):
+                ldv = _rows("v_out", v_out, shape, "q2_read")
         st = self._read(self._ref, kp, ldk, vp, ldv, st, ln, self.batch, rows, _stream_ptr(stream))
         if st:
             raise Q2Error(st, "q2_read")
@@ -663,18 +692,24 @@ class _Cache:
         """
         if self._bounds is None:
             raise Q2Error(EINVAL, f"q2_select: {self._name} without bounds")
-        shape = (self.batch, self.kv_heads, int(blocks))
+        i32, batch, shape = self._i32, self.batch, (self.batch, self.kv_heads, int(blocks))
+        # what each tensor has to be is tested here at once, and put into words by the functions called otherwise
         if out is None:
             import torch
             if blocks < 1:
                 raise Q2Error(ESHAPE, f"q2_select: {blocks} blocks")
-            out = _new(torch.empty, shape, self._i32, q.device, stream)
+            out = _new(torch.empty, shape, i32, q.device, stream)
+        elif not (out.dtype is i32 and out.is_cuda and out.shape == shape and out.is_contiguous()):
+            _check_tensor("q2_select", "out", out, i32, shape)
+        stride = q.stride()
+        if q.dtype is self._f16 and q.is_cuda and q.shape == self._qshape and stride[1] == self.dim and stride[2] == 1:
+            ldq = stride[0] if batch > 1 else self.q_heads * self.dim
         else:
-            _check_tensor("q2_select", "out", out, self._i32, shape)
-        ldq = _rows("q", q, self._qshape, "q2_select")
-        _, ln = self._tokens("q2_select", lens, None)
-        st = self._select(self._ref, self._bounds, q.data_ptr(), ldq, ln, self.batch, self.q_heads, shape[2], int(first), int(last),
-                          out.data_ptr(), _stream_ptr(stream))
+            ldq = _rows("q", q, self._qshape, "q2_select")
+        if not (lens.dtype is i32 and lens.is_cuda and lens.shape == (batch,) and lens.is_contiguous()):
+            _check_tensor("q2_select", "lens", lens, i32, (batch,))
+        st = self._select(self._ref, self._bounds, q.data_ptr(), ldq, lens.data_ptr(), batch, self.q_heads, shape[2], int(first),
+                          int(last), out.data_ptr(), _stream_ptr(stream))
         if st:
             raise Q2Error(st, "q2_select")
         return out
@@ -690,8 +725,8 @@ class _Cache:
             ldq = _rows("q", q, shape)
         if not (out.dtype is f16 and out.is_cuda and out.shape == shape and out.is_contiguous()):
             ldo = _rows("out", out, shape)
-        if not (lens.dtype is self._i32 and lens.is_cuda and lens.shape == shape[:1] and lens.is_contiguous()):
-            _check_tensor("q2_attend", "lens", lens, self._i32, shape[:1])
+        if not (lens.dtype is self._i32 and lens.is_cuda and lens.shape == (self.batch,) and lens.is_contiguous()):
+            _check_tensor("q2_attend", "lens", lens, self._i32, (self.batch,))
         sel, n = None, 0
         if blocks is not None:
             n = blocks.shape[2] if blocks.dim() == 3 else 0
