@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_
 
   if (threadIdx.x == 0) *nowed = owed;
   __syncthreads();
-  join_parts<D, H, SP>(a, owe, *nowed, kUp);
+  join_parts<D, H, SP, 8>(a, owe, *nowed, kUp);
 }
 
 template <bool SP>

@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
 
   if (threadIdx.x == 0) *nowed = owed;
   __syncthreads();
-  join_parts<D, H, SP>(a, owe, *nowed, 1.f);
+  join_parts<D, H, SP, 12>(a, owe, *nowed, 1.f);
 }
 
 template <bool SP>
