@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
         top = min(max(top, 90u), 142u);             // (a head of zeros; an infinite or NaN column, which stays one)
         // 2^10 over the largest's power of two, of the scale's sign: the largest score is the largest sum
         const float up = copysignf(__uint_as_float((127u + 10u + 127u - top) << 23), a.sc2);
-        const float down = fabsf(a.sc2) * __uint_as_float((127u + 24u - 10u - 127u + top) << 23);   // (a code is c 2^-24)
+        // (a code is c 2^-24; never zero, with which a masked sum of minus infinity were NaN: 2^-100 of a sum is none)
+        const float down = fmaxf(fabsf(a.sc2) * __uint_as_float((127u + 24u - 10u - 127u + top) << 23), 0x1p-100f);
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) sum[i] = 0.f;

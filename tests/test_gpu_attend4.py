@@ -116,11 +116,12 @@ class Case:
                 p = np.exp(s - s.max(1, keepdims=True))
                 ref, l = p @ v / p.sum(1, keepdims=True), p.sum(1, keepdims=True)
                 M = (np.abs(q) @ kmag.T).max(1)
+                size = abs(self.scale)                  # a score's error is |scale| times that of its product q.k
                 if self.bits == 16:
-                    e = 2 * (self.D + 8) * 2.0 ** -23 * self.scale * M + 2.0 ** -21 + 2.0 ** -19
+                    e = 2 * (self.D + 8) * 2.0 ** -23 * size * M + 2.0 ** -21 + 2.0 ** -19
                 else:
                     per = np.abs(q).reshape(self.G, -1, 32).max(2) @ ks[:, ::32].T            # [G][n]
-                    d = self.scale * (2.0 ** -8 * per.max(1) + (self.D + 8) * 2.0 ** -23 * M)
+                    d = size * (2.0 ** -8 * per.max(1) + (self.D + 8) * 2.0 ** -23 * M)
                     e = 2 * d + 2.0 ** -20 + 2.0 ** -19
                 N = p @ vmag / l
                 tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 2 * (e[:, None] + len(tokens) / 16 * 2.0 ** -23) * N
