@@ -683,7 +683,6 @@ class _Cache:
             raise Q2Error(st, "q2_read")
         return k_out, v_out
 
-
     def select(self, q, lens, blocks: int, first: int = 0, last: int = 1, out=None, stream=None):
         """The ``blocks`` blocks of 64 tokens whose bounds promise the most to each key-value head's queries.
 
@@ -750,7 +749,7 @@ class PagedKV(_Cache):
     alike).  ``table``: int32 [batch][max_pages] page numbers on the same GPU.  The tensors stay the caller's: pages,
     table and lengths may be changed between calls.  ``workspace``: uint8, zero when first used (made here if None).
     ``bounds``: fp16 [pages][ceil(page_size / 64)][kv_heads][2][dim], the least and greatest keys of blocks of 64
-    tokens, which ``append`` keeps up.
+    tokens, which ``append`` keeps up (sequences with new tokens in a block must not share the page of its first token).
     """
 
     _name = "PagedKV"
@@ -780,8 +779,8 @@ class PagedKV(_Cache):
         """Attention of q [batch][q_heads][dim] over the first lens[b] (int32) tokens of each sequence.
 
         ``new_k``, ``new_v`` [batch][kv_heads][dim]: the new token's, counted by ``lens``; they are stored as token
-        lens[b] - 1.  q, new_k, new_v and ``out`` may have any batch stride (slices of a projection's output).
-        ``scale``: dim ** -0.5 if None.  ``blocks``: what ``select`` returns, or any int32 [batch][kv_heads][n]: only the
+        lens[b] - 1 (not in a cache with ``bounds``, which ``append`` keeps up).  q, new_k, new_v and ``out`` may have any
+        batch stride (slices of a projection's output).  ``scale``: dim ** -0.5 if None.  ``blocks``: what ``select`` returns, or any int32 [batch][kv_heads][n]: only the
         tokens of these blocks of 64 (without new_k and new_v: ``append`` stores the new token before).  Returns ``out``
         (asynchronous).
         """
@@ -804,6 +803,8 @@ class PagedKV(_Cache):
         nk = nv = None
         ldn = 0
         if new_k is not None and new_v is not None:
+            if self._bounds is not None:
+                raise Q2Error(EINVAL, "q2_attend: a cache with bounds takes new tokens by append alone")
             shape = self._kvshape
             ldn = _rows("new_k", new_k, shape)
             if not (new_v.dtype is f16 and new_v.is_cuda and new_v.shape == shape and new_v.stride() == new_k.stride()):
@@ -848,6 +849,8 @@ class PagedKV4(_Cache):
                           "[pages][page_size][kv_heads][dim / group][2], or table not [batch][max_pages]")
         pages, page, self.kv_heads, half = k.shape
         self.dim, groups = 2 * half, ks.shape[3]
+        if self.dim not in (32 * groups, 64 * groups):
+            raise Q2Error(ESHAPE, f"PagedKV4: {groups} groups of {self.dim} columns, not of 32 or 64")
         for name, t, dtype, like, tail in (("k", k, torch.uint8, k, (1,)), ("v", v, torch.uint8, k, (1,)),
                                            ("ks", ks, torch.float16, ks, (2, 1)), ("vs", vs, torch.float16, ks, (2, 1))):
             shape = k.shape if like is k else (pages, page, self.kv_heads, groups, 2)
@@ -862,7 +865,7 @@ class PagedKV4(_Cache):
         self._blocks = load().q2_attend4
         self._kv = _KV4(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), ks.data_ptr(), vs.data_ptr(),
                         ks.stride(0) // 2, ks.stride(1) // 2, ks.stride(2) // 2, pages, page, self.kv_heads, self.dim,
-                        self.dim // groups if self.dim % groups == 0 else 0, table.data_ptr(),
+                        self.dim // groups, table.data_ptr(),
                         table.stride(0) if self.batch > 1 else table.shape[1], table.shape[1])
         self._ref = ctypes.byref(self._kv)
         self._workspace(workspace, load().q2_attend_workspace_bytes)

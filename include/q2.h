@@ -470,8 +470,11 @@ typedef struct {
  *     of the turned keys, rounded to fp16, of every block of 64 tokens (tokens
  *     64 i .. 64 i + 63 of a sequence).  A block's bounds lie at the page of its
  *     first token; a block whose first token is stored by this call begins
- *     anew.  page_size must be a multiple or a divisor of 64 (Q2_ESHAPE).  A NaN
- *     among a column's keys makes its bounds NaN.
+ *     anew, in others what they hold is widened (so tokens that a shorter length
+ *     took back stay in).  Two sequences with new tokens in a block must not
+ *     share the page of its first token.  page_size must be a multiple or a
+ *     divisor of 64 (Q2_ESHAPE).  A NaN among a column's keys makes its bounds
+ *     NaN.
  *   - starts: device int32 [batch + 1]; lens: device int32 [batch].  Rows
  *     outside every sequence, and those of a sequence of length 0, are left as
  *     they are.  No two tokens may be stored to the same place.
@@ -535,6 +538,8 @@ int q2_attend4(const q2_kv4* kv, const void* q, long long ldq, const int* lens, 
  *     Q2_ERR_PAGE (the block scores as one with NaN, so that attending it shows
  *     the page).  1 <= nsel <= Q2_MAX_BLOCKS; max_pages * page_size at most 64 *
  *     Q2_MAX_BLOCKS tokens (Q2_ESHAPE).
+ *     Where a sequence has no more than nsel blocks, all of them are selected and
+ *     neither bounds nor pages are looked at.
  *   - One launch, launched like q2_gemv; needs no workspace. */
 #define Q2_MAX_BLOCKS 32768
 int q2_select(const q2_kv* kv, const void* bounds, const void* q, long long ldq, const int* lens, int batch, int q_heads,

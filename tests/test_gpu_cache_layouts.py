@@ -160,3 +160,77 @@ def test_several_calls_in_a_row_without_waiting(q2):
     for n, (o, s, k) in zip(lens, outs):                # the same again, now that all is there
         assert torch.equal(o, cache.attend(q, n)) and torch.equal(k, cache.read(n)[0])
     assert torch.equal(outs[-1][1], cache.select(q, lens[-1], 2)) and q2.device_errors() == 0
+
+
+def test_what_the_caches_refuse(q2):
+    c = Append([20, 30], [1, 1], bits=16, page=16, seed=36, starts=False, bounds=True)
+    cache, q = c.cache(q2), torch.zeros((2, c.HQ, c.D), dtype=torch.float16, device="cuda")
+    with pytest.raises(q2.Q2Error):                     # the new tokens would not be in the bounds
+        cache.attend(q, c.dlens, c.dk, c.dv)
+    cache.attend(q, c.dlens)
+    c = Append([20, 30], [1, 1], bits=4, page=16, seed=37, starts=False)
+    d = c.dev
+    for n in (1, 3, 8, 16):                             # 128 columns in 1, 3, 8, 16 groups
+        bad = [torch.zeros(d["k"].shape[:3] + (n, 2), dtype=torch.float16, device="cuda") for _ in range(2)]
+        with pytest.raises(q2.Q2Error):
+            q2.PagedKV4(d["k"], bad[0], d["v"], bad[1], c.dtable, c.HQ)
+    assert q2.device_errors() == 0
+
+
+def _held_block(nbytes):
+    """Give back a block that the current stream will still write, some 20 ms from now."""
+    block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(40_000_000)
+    block.fill_(0x5A)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("which", ["attend", "blocks", "select", "read"])
+def test_outputs_made_by_calls_on_another_stream(q2, bits, which):
+    """They do not lie in memory that the current stream may still write."""
+    c = Append([200, 90], [200, 90], bits=bits, group=64, page=64, bounds=True, seed=38)
+    cache = c.cache(q2)
+    c.run(q2, cache=cache)
+    q, lens = torch.randn((2, c.HQ, c.D), device="cuda").half(), c.dlens
+    sel = cache.select(q, lens, 2)
+    call = {"attend": lambda s: (cache.attend(q, lens, stream=s),), "blocks": lambda s: (cache.attend(q, lens, blocks=sel, stream=s),),
+            "select": lambda s: (cache.select(q, lens, 2, stream=s),),
+            "read": lambda s: cache.read(lens, starts=c.dstarts, ntok=c.ntok, stream=s)}[which]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        for t in want:
+            _held_block(t.numel() * t.element_size())
+        got = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_two_captured_graphs_on_one_workspace(q2, bits):
+    """A step of a long sequence and one of a few short ones, replayed by turns."""
+    long, short = (Attention(lens, 2, 4, 128, 64, 16, 40 + i, bits=bits) for i, lens in enumerate(([9000], [70, 1, 300])))
+    caches = [c.cache(q2) for c in (long, short)]
+    ws = max((k.ws for k in caches), key=lambda w: w.numel())
+    caches = [type(k)(*(getattr(k, n) for n in (("k", "v") if bits == 16 else ("k", "ks", "v", "vs"))), k.table, k.q_heads, workspace=ws)
+              for k in caches]
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    for c, k in zip((long, short), caches):
+        out = torch.zeros((len(c.lens), 8, 128), dtype=torch.float16, device="cuda")
+        k.attend(c.dq, c.dlens, scale=c.scale, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            k.attend(c.dq, c.dlens, scale=c.scale, out=out)
+        graphs.append(graph)
+        outs.append(out)
+    for out in outs:
+        out.zero_()
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for c, out in zip((long, short), outs):
+        c.check(out)
+    assert q2.device_errors() == 0
