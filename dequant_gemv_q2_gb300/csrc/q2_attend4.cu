@@ -33,6 +33,11 @@
 // denominator and nearly cancel, and the fp32 sums' roundings showed in a long
 // sequence's output (one of 131072 tokens: 4.1e-4 off, 2.1e-4 of it fp16's own).
 //
+// A warp's step of 32 tokens is some 700 instructions, two warps to a scheduler: of
+// 134 us for 64 sequences of 8192 tokens (8 key-value heads of 128, groups of 64,
+// four query heads each; 605 MB, 4.5 TB/s of the 6.8 of a copy) the loads alone
+// take 97, the instructions alone 117, 2.2 of them per cycle and SM.
+//
 // p s is split into two fp16 numbers, in the two halves of the rows as p is for
 // the fp16 cache.  It is scaled by a power of two above the largest s so far
 // (of the warp's tiles), which changes as rarely as the maximum does.
@@ -408,179 +413,179 @@ __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid
     int t0 = seg * UNIT + warp * TW;
 #pragma unroll 1
     for (int left = run; left;) {
-    if (!ahead) {                                   // this unit has arrived for all lanes, the one before is done with
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-      __syncwarp();
-    }
-    issue();
-    if (ahead) {
-      --ahead;
-      continue;
-    }
-    // row of the last token, if below TW; negative: none
-    const int fin = SP ? (int)(haves >> (8 * slot) & 255u) - 1 : c.len - 1 - t0;
-    if (fin >= 0) {
-      const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes + g * (4 * G);   // the pairs of token g
-      const unsigned char* vs = ks + S::kPairs;
-      const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
-      // ---- scores: x[n][y][e] of token 8 n + g, head 8 y + 2j + e, still to be multiplied by qf
-      float x[2 * NTL][NH][2];
-      const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
-      uint32_t sm[2 * NTL][G];
+      if (!ahead) {                                   // this unit has arrived for all lanes, the one before is done with
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();
+      }
+      issue();
+      if (ahead) {
+        --ahead;
+        continue;
+      }
+      // row of the last token, if below TW; negative: none
+      const int fin = SP ? (int)(haves >> (8 * slot) & 255u) - 1 : c.len - 1 - t0;
+      if (fin >= 0) {
+        const unsigned char* ks = myring + slot * S::kStage + 2 * S::kCodes + g * (4 * G);   // the pairs of token g
+        const unsigned char* vs = ks + S::kPairs;
+        const uint32_t kt = ring + slot * S::kStage, vt = kt + S::kCodes;
+        // ---- scores: x[n][y][e] of token 8 n + g, head 8 y + 2j + e, still to be multiplied by qf
+        float x[2 * NTL][NH][2];
+        const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;
+        uint32_t sm[2 * NTL][G];
 #pragma unroll
-      for (int n = 0; n < 2 * NTL; ++n) load_pairs<G>(ks + 8 * n * (4 * G), sm[n]);
-      float acc[NTL][NH][4];
+        for (int n = 0; n < 2 * NTL; ++n) load_pairs<G>(ks + 8 * n * (4 * G), sm[n]);
+        float acc[NTL][NH][4];
 #pragma unroll
-      for (int b = 0; b < NB; b += 2) {
-        uint32_t r[NTL][4];                         // pieces b, b + 1 of tokens 0..7, then of 8..15
+        for (int b = 0; b < NB; b += 2) {
+          uint32_t r[NTL][4];                         // pieces b, b + 1 of tokens 0..7, then of 8..15
 #pragma unroll
-        for (int i = 0; i < NTL; ++i) ldsm4(r[i], kt + i * (kTile * D / 2) + place(krow, b + kpiece));
+          for (int i = 0; i < NTL; ++i) ldsm4(r[i], kt + i * (kTile * D / 2) + place(krow, b + kpiece));
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
+          for (int bb = 0; bb < 2; ++bb) {
 #pragma unroll
-          for (int i = 0; i < NTL; ++i) {
-            // codes 0, 1 in bits 0..3, 4..7 of w0 and w1, codes 2, 3 in bits 2..5, 6..9 of h0 and h1
-            const uint32_t w0 = r[i][bb], w1 = r[i][2 + bb], h0 = w0 >> 6, h1 = w1 >> 6;
+            for (int i = 0; i < NTL; ++i) {
+              // codes 0, 1 in bits 0..3, 4..7 of w0 and w1, codes 2, 3 in bits 2..5, 6..9 of h0 and h1
+              const uint32_t w0 = r[i][bb], w1 = r[i][2 + bb], h0 = w0 >> 6, h1 = w1 >> 6;
 #pragma unroll
-            for (int y = 0; y < NH; ++y) {
-              const bool first = (b + bb) % BPG == 0;
-              const auto& q = qa[b + bb][y];
-              mma_from(first, acc[i][y], w0 & 0x000f000fu, w1 & 0x000f000fu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
-              mma(acc[i][y], w0 & 0x00f000f0u, w1 & 0x00f000f0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
+              for (int y = 0; y < NH; ++y) {
+                const bool first = (b + bb) % BPG == 0;
+                const auto& q = qa[b + bb][y];
+                mma_from(first, acc[i][y], w0 & 0x000f000fu, w1 & 0x000f000fu, h0 & 0x003c003cu, h1 & 0x003c003cu, q[0], q[1]);
+                mma(acc[i][y], w0 & 0x00f000f0u, w1 & 0x00f000f0u, h0 & 0x03c003c0u, h1 & 0x03c003c0u, q[2], q[3]);
+              }
             }
-          }
-          if ((b + bb) % BPG == BPG - 1) {
-            const int gi = (b + bb) / BPG;
+            if ((b + bb) % BPG == BPG - 1) {
+              const int gi = (b + bb) / BPG;
 #pragma unroll
-            for (int n = 0; n < 2 * NTL; ++n) {
-              const float2 s = halves(sm[n][gi]);
+              for (int n = 0; n < 2 * NTL; ++n) {
+                const float2 s = halves(sm[n][gi]);
 #pragma unroll
-              for (int y = 0; y < NH; ++y)
+                for (int y = 0; y < NH; ++y)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float& z = x[n][y][e];
-                  const auto& t = acc[n / 2][y];
-                  z = fmaf(s.x, t[2 * (n % 2) + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
-                }
+                  for (int e = 0; e < 2; ++e) {
+                    float& z = x[n][y][e];
+                    const auto& t = acc[n / 2][y];
+                    z = fmaf(s.x, t[2 * (n % 2) + e], gi ? fmaf(s.y, qs[y][e][gi], z) : s.y * qs[y][e][0]);
+                  }
+              }
             }
           }
         }
-      }
-      // ---- probabilities
-      uint32_t vp[2 * NTL][G];                      // the pairs of the values of token 8 n + g
-      __half2 most = __float2half2_rn(0.f);
+        // ---- probabilities
+        uint32_t vp[2 * NTL][G];                      // the pairs of the values of token 8 n + g
+        __half2 most = __float2half2_rn(0.f);
 #pragma unroll
-      for (int n = 0; n < 2 * NTL; ++n) {
-        load_pairs<G>(vs + 8 * n * (4 * G), vp[n]);
+        for (int n = 0; n < 2 * NTL; ++n) {
+          load_pairs<G>(vs + 8 * n * (4 * G), vp[n]);
 #pragma unroll
-        for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][i]));
-      }
-      const uint32_t most_s = (uint32_t)__half_as_ushort(__low2half(most)) >> 10;
-      bool rise = most_s > top_s || fin < TW - 1 || badslots;
-#pragma unroll
-      for (int y = 0; y < NH; ++y)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = x[0][y][e];
-#pragma unroll
-          for (int n = 1; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
-          rise = rise || top > bar[y][e];
+          for (int i = 0; i < G; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&vp[n][i]));
         }
-      // A maximum far enough above the last, or a larger step: scale what there
-      // is.  (Also a step that is not whole, or has a page that does not exist.)
-      if (__any_sync(0xffffffffu, rise)) {
-        const uint32_t now_s = max(top_s, __reduce_max_sync(0xffffffffu, most_s));
-        const float fall = __uint_as_float((127u - (now_s - top_s)) << 23);
-        const bool bad = (badslots >> slot) & 1u;
-        badslots &= ~(1u << slot);
-        top_s = now_s;
+        const uint32_t most_s = (uint32_t)__half_as_ushort(__low2half(most)) >> 10;
+        bool rise = most_s > top_s || fin < TW - 1 || badslots;
 #pragma unroll
         for (int y = 0; y < NH; ++y)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = m[y][e];
+            float top = x[0][y][e];
+#pragma unroll
+            for (int n = 1; n < 2 * NTL; ++n) top = fmaxf(top, x[n][y][e]);
+            rise = rise || top > bar[y][e];
+          }
+        // A maximum far enough above the last, or a larger step: scale what there
+        // is.  (Also a step that is not whole, or has a page that does not exist.)
+        if (__any_sync(0xffffffffu, rise)) {
+          const uint32_t now_s = max(top_s, __reduce_max_sync(0xffffffffu, most_s));
+          const float fall = __uint_as_float((127u - (now_s - top_s)) << 23);
+          const bool bad = (badslots >> slot) & 1u;
+          badslots &= ~(1u << slot);
+          top_s = now_s;
+#pragma unroll
+          for (int y = 0; y < NH; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = m[y][e];
+#pragma unroll
+              for (int n = 0; n < 2 * NTL; ++n) {
+                if (8 * n + g > fin) x[n][y][e] = -INFINITY;
+                top = fmaxf(top, x[n][y][e]);
+              }
+#pragma unroll
+              for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+              ref[y][e] = top == -INFINITY ? 0.f : top * qf[y][e];
+              const float al = m[y][e] == -INFINITY ? 0.f : ex2(fmaf(m[y][e], qf[y][e], -ref[y][e])), alf = al * fall;
+              m[y][e] = top;
+              bar[y][e] = top + (float)kSlack / qf[y][e];
+              l[y][e] = bad ? __int_as_float(0x7fc00000) : l[y][e] * al;
+#pragma unroll
+              for (int i = 0; i < G; ++i) om[y][e][i] *= al;
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  o[b][y][k][e] *= alf;
+                  o[b][y][k][2 + e] *= alf;
+                }
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < NH; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int n = 0; n < 2 * NTL; ++n) {
-              if (8 * n + g > fin) x[n][y][e] = -INFINITY;
-              top = fmaxf(top, x[n][y][e]);
+              x[n][y][e] = ex2(fmaf(x[n][y][e], qf[y][e], -ref[y][e]));
+              l[y][e] += x[n][y][e];
             }
+        // ---- numerators: p s scaled so that it stays below 2^15
+        const float scale = __uint_as_float((127u + 29u - kSlack - top_s) << 23);
+        const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            ref[y][e] = top == -INFINITY ? 0.f : top * qf[y][e];
-            const float al = m[y][e] == -INFINITY ? 0.f : ex2(fmaf(m[y][e], qf[y][e], -ref[y][e])), alf = al * fall;
-            m[y][e] = top;
-            bar[y][e] = top + (float)kSlack / qf[y][e];
-            l[y][e] = bad ? __int_as_float(0x7fc00000) : l[y][e] * al;
+        for (int i = 0; i < NTL; ++i) {
+          uint32_t hi[NH][2], lo[NH][2];              // p s of 8 tokens each: tokens 2j, 2j + 1, head g
 #pragma unroll
-            for (int i = 0; i < G; ++i) om[y][e][i] *= al;
+          for (int b = 0; b < NB; b += 2) {
+            uint32_t r[4];                            // tokens 0..7 and 8..15 of piece b, then of b + 1
+            ldsm4t(r, vt + i * (kTile * D / 2) + place(vrow, b + vpiece));
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int bb = 0; bb < 2; ++bb) {
+              if ((b + bb) % BPG == 0) {
+                const int gi = (b + bb) / BPG;
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                o[b][y][k][e] *= alf;
-                o[b][y][k][2 + e] *= alf;
-              }
-          }
-      }
+                for (int n = 0; n < 2; ++n) {
+                  float2 s = halves(vp[2 * i + n][gi]);
+                  s.y = fmaf(8.f, s.x, s.y);
+                  s.x *= scale;
 #pragma unroll
-      for (int y = 0; y < NH; ++y)
+                  for (int y = 0; y < NH; ++y) {
+                    const float(&w)[2] = x[2 * i + n][y];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int n = 0; n < 2 * NTL; ++n) {
-            x[n][y][e] = ex2(fmaf(x[n][y][e], qf[y][e], -ref[y][e]));
-            l[y][e] += x[n][y][e];
-          }
-      // ---- numerators: p s scaled so that it stays below 2^15
-      const float scale = __uint_as_float((127u + 29u - kSlack - top_s) << 23);
-      const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vpiece = lane >> 4;
-#pragma unroll
-      for (int i = 0; i < NTL; ++i) {
-        uint32_t hi[NH][2], lo[NH][2];              // p s of 8 tokens each: tokens 2j, 2j + 1, head g
-#pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-          uint32_t r[4];                            // tokens 0..7 and 8..15 of piece b, then of b + 1
-          ldsm4t(r, vt + i * (kTile * D / 2) + place(vrow, b + vpiece));
-#pragma unroll
-          for (int bb = 0; bb < 2; ++bb) {
-            if ((b + bb) % BPG == 0) {
-              const int gi = (b + bb) / BPG;
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                float2 s = halves(vp[2 * i + n][gi]);
-                s.y = fmaf(8.f, s.x, s.y);
-                s.x *= scale;
-#pragma unroll
-                for (int y = 0; y < NH; ++y) {
-                  const float(&w)[2] = x[2 * i + n][y];
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) om[y][e][gi] = fmaf(w[e], s.y, om[y][e][gi]);
-                  const float w0 = w[0] * s.x, w1 = w[1] * s.x;
-                  const uint32_t h = pack2(w0, w1);
-                  // FOLD: lanes of columns 4..7 have heads 0..3 again, theirs is the lower part
-                  const uint32_t t = pack2(fma_h(lo16(h), less, w0), fma_h(hi16(h), less, w1));
-                  hi[y][n] = transpose(FOLD ? t : h);
-                  if (!FOLD) lo[y][n] = transpose(t);
+                    for (int e = 0; e < 2; ++e) om[y][e][gi] = fmaf(w[e], s.y, om[y][e][gi]);
+                    const float w0 = w[0] * s.x, w1 = w[1] * s.x;
+                    const uint32_t h = pack2(w0, w1);
+                    // FOLD: lanes of columns 4..7 have heads 0..3 again, theirs is the lower part
+                    const uint32_t t = pack2(fma_h(lo16(h), less, w0), fma_h(hi16(h), less, w1));
+                    hi[y][n] = transpose(FOLD ? t : h);
+                    if (!FOLD) lo[y][n] = transpose(t);
+                  }
                 }
               }
-            }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {           // codes 2k, 2k + 1 of the words: columns 32 (b + bb) + 4 word + 2k, + 1
-              const uint32_t w0 = k ? r[2 * bb] >> 8 : r[2 * bb], w1 = k ? r[2 * bb + 1] >> 8 : r[2 * bb + 1];
-              const uint32_t a0 = centred(w0, false), a1 = centred(w0, true), a2 = centred(w1, false), a3 = centred(w1, true);
+              for (int k = 0; k < 2; ++k) {           // codes 2k, 2k + 1 of the words: columns 32 (b + bb) + 4 word + 2k, + 1
+                const uint32_t w0 = k ? r[2 * bb] >> 8 : r[2 * bb], w1 = k ? r[2 * bb + 1] >> 8 : r[2 * bb + 1];
+                const uint32_t a0 = centred(w0, false), a1 = centred(w0, true), a2 = centred(w1, false), a3 = centred(w1, true);
 #pragma unroll
-              for (int y = 0; y < NH; ++y) {
-                mma(o[b + bb][y][k], a0, a1, a2, a3, hi[y][0], hi[y][1]);
-                if (!FOLD) mma(o[b + bb][y][k], a0, a1, a2, a3, lo[y][0], lo[y][1]);
+                for (int y = 0; y < NH; ++y) {
+                  mma(o[b + bb][y][k], a0, a1, a2, a3, hi[y][0], hi[y][1]);
+                  if (!FOLD) mma(o[b + bb][y][k], a0, a1, a2, a3, lo[y][0], lo[y][1]);
+                }
               }
             }
           }
         }
       }
-    }
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
-    t0 += UNIT;
-    --left;
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      t0 += UNIT;
+      --left;
     }
 
     {
