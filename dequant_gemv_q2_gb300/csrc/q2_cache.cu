@@ -181,8 +181,8 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], __half2& pair)
 
 // GRP: columns of a group of the 4-bit cache, 0 for an fp16 cache.  ONE: one
 // token per sequence (no starts): every lane reads its angles and the page, and
-// nothing is waited for (64 sequences into 4 bits and out again 7.1 -> 6.5 us; as
-// a branch of the general kernel it gained nothing).
+// nothing is waited for (64 sequences into 4 bits 0.6 us less; as a branch of the
+// general kernel it gained nothing).
 template <int D, int GRP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
