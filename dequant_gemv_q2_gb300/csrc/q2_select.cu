@@ -18,21 +18,27 @@
 // heads to an instruction, every lane on the bounds that it has copied itself,
 // a few steps ahead.
 //
-// Which of two blocks is selected must not depend on the order of a sum.  So the
-// sums of the terms' magnitudes are taken beside: an instruction of 16 products
-// and the sum so far drops at most 17 2^-23 of that, 2 D / 16 of them at most e
-// = 17 D 2^-26.  Blocks that are further than 2 e from the nsel-th largest sum
+// Which of two blocks is selected must not depend on the order of a sum.  An
+// instruction of 16 products and the sum so far drops at most 17 2^-23 of the sum
+// of the terms' magnitudes M, D / 16 of them for either of q+ hi and q- lo, and
+// one addition 2^-24 of it: less than e = 17 D 2^-26 M.  M is taken once per warp,
+// of the queries on the largest magnitudes of its blocks' bounds: one instruction
+// for two packed numbers in place of a second product for each block (22.4 ->
+// 21.1 us for the second case below; 0.2 us more where a warp has one step).
+// Blocks that are further than 2 e from the nsel-th largest sum
 // are in or out; the others, mostly the nsel-th itself and one more or none, are
 // decided by sums that are exact enough to be the exact value's rounding to
 // fp32: products of fp16 numbers are exact in fp32, and their sums keep each
 // addition's error (Knuth, "The Art of Computer Programming" 2, 4.2.2, theorem B).
 //
 // Measured (GB300, 8 key-value heads of 128): one sequence of 131072 tokens, 64 of
-// 2048 blocks per head, 12.5 us, of them 7.8 scoring 8.4 MB, 1.5 the threshold and
+// 2048 blocks per head, 12.2 us, of them 7.6 scoring 8.4 MB, 1.5 the threshold and
 // 3 the exact sums and the writing; 32 sequences of up to 32768 tokens, 64 blocks,
-// 22.4 us, of them 18.5 scoring 33.6 MB.  Latency bounds the first (one CTA of
+// 21.1 us, of them 17.4 scoring 33.6 MB (14.7 without the products, 9.7 without
+// the loads, 5.2 with neither).  Latency bounds the first (one CTA of
 // each cluster works behind the scores), the clusters of the longest sequences
-// the second.  Larger clusters were slower in both, four chains of sums spilled.
+// the second.  Larger clusters were slower in both; the table looked up four steps
+// at a time gained nothing.
 #include <cooperative_groups.h>
 
 #include "q2_attend.cuh"
@@ -307,7 +313,9 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
   uint32_t* to = a.cs > 1 ? cluster.map_shared_rank(keys, 0) : keys;
   float4* warps_to = a.cs > 1 ? cluster.map_shared_rank(s.warps, 0) : s.warps;
 
-  float most = 0.f;                                 // the largest sum of magnitudes
+  __half2 size[4];                                  // the largest magnitudes of the blocks n0 + g: of columns 8 j .. of any 32
+#pragma unroll
+  for (int k = 0; k < 4; ++k) size[k] = __float2half2_rn(0.f);
   uint32_t kmin = 0xffffffffu, kmax = 0, kodd = 0;  // keys of this lane's blocks
   int slot = 0;
   for (int n0 = first; n0 < n; n0 += stride) {
@@ -335,27 +343,27 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
     const uint32_t odd = __ballot_sync(0xffffffffu, !there);       // (lane 4 g + j: block n0 + g)
     float best[2] = {-INFINITY, -INFINITY};         // of blocks n0 + 2j, + 1
     for (int ht = 0; ht < tiles; ++ht) {
-      float u[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+      float u[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};          // on greatest keys, on least
 #pragma unroll (NB < 8 ? NB : 2)
       for (int c = 0; c < NB; ++c) {
         const uint4* f = frag + (ht * NB + c) * 64 + lane;
         const uint4 up = f[0], dn = f[32], y = piece(c, 0), x = piece(c, 1);
-        constexpr uint32_t kAbs = 0x7fff7fffu;
         mma(u, up.x, 0u, up.y, 0u, x.x, x.y);
-        mma(w, up.x, 0u, up.y, 0u, x.x & kAbs, x.y & kAbs);
+        mma(w, dn.x, 0u, dn.y, 0u, y.x, y.y);
         mma(u, up.z, 0u, up.w, 0u, x.z, x.w);
-        mma(w, up.z, 0u, up.w, 0u, x.z & kAbs, x.w & kAbs);
-        mma(u, dn.x, 0u, dn.y, 0u, y.x, y.y);
-        mma(w, dn.x & kAbs, 0u, dn.y & kAbs, 0u, y.x & kAbs, y.y & kAbs);
-        mma(u, dn.z, 0u, dn.w, 0u, y.z, y.w);
-        mma(w, dn.z & kAbs, 0u, dn.w & kAbs, 0u, y.z & kAbs, y.w & kAbs);
+        mma(w, dn.z, 0u, dn.w, 0u, y.z, y.w);
+        if (ht == 0) {
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            size[k] = __hmax2(size[k], __habs2(*reinterpret_cast<const __half2*>(&xs[k])));
+            size[k] = __hmax2(size[k], __habs2(*reinterpret_cast<const __half2*>(&ys[k])));
+          }
+        }
       }
       if (ht * 8 + g < a.group) {                   // rows are heads
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          best[e] = fmaxf(best[e], finite(u[e]) ? u[e] : INFINITY);
-          if (finite(w[e])) most = fmaxf(most, w[e]);
-        }
+        for (int e = 0; e < 2; ++e) best[e] = fmaxf(best[e], finite(u[e] + w[e]) ? u[e] + w[e] : INFINITY);
       }
     }
 #pragma unroll
@@ -375,6 +383,29 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
       }
     }
     slot = slot + 1 == a.stages ? 0 : slot + 1;
+  }
+  // What no sum of magnitudes is above: that of the queries' on the largest ones of
+  // these blocks (finite ones: a block with others is not decided by its sum).
+  uint32_t big[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 z = __hmin2(size[k], __float2half2_rn(65504.f));
+    big[k] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  float most = 0.f;
+  for (int ht = 0; ht < tiles; ++ht) {
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+      const uint4* f = frag + (ht * NB + c) * 64 + lane;
+      const uint4 up = f[0], dn = f[32];            // (one of the two is zero, or both are NaN)
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      mma(w, (up.x | dn.x) & kAbs, 0u, (up.y | dn.y) & kAbs, 0u, big[0], big[1]);
+      mma(w, (up.z | dn.z) & kAbs, 0u, (up.w | dn.w) & kAbs, 0u, big[2], big[3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (finite(w[e])) most = fmaxf(most, w[e]);   // (else no block is decided by its sum)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));

@@ -234,3 +234,17 @@ def test_two_captured_graphs_on_one_workspace(q2, bits):
     for c, out in zip((long, short), outs):
         c.check(out)
     assert q2.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,q_group,lens", [(128, 4, [64 * 2000]), (64, 3, [64 * 1500, 64 * 700]), (256, 12, [64 * 900, 5000])])
+def test_one_block_far_above_the_rest(q2, D, q_group, lens):
+    """Its magnitudes say that any of the others' sums may be off by more than they are apart: all are taken exactly."""
+    c = Selection(lens, 2, q_group, D, 64, D + 1)
+    pages = c.table[0]
+    c.bounds[pages[100], 0, 0] = [[-65504.0], [65504.0]]
+    c.bounds[pages[200], 0, 1, 1, 7] = np.inf
+    c.check(q2, 40, 1, 1)
+    c.check(q2, 1, 0, 0)
+    c.q[:, :, :3] *= 1000                               # and some columns of the queries far above the others
+    c.check(q2, 40, 0, 1)
+    assert q2.device_errors() == 0
