@@ -25,11 +25,11 @@
 // of the queries on the largest magnitudes of its blocks' bounds: one instruction
 // for two packed numbers in place of a second product for each block (22.4 ->
 // 21.1 us for the second case below; 0.2 us more where a warp has one step).
-// Blocks that are further than 2 e from the nsel-th largest sum
-// are in or out; the others, mostly the nsel-th itself and one more or none, are
-// decided by sums that are exact enough to be the exact value's rounding to
-// fp32: products of fp16 numbers are exact in fp32, and their sums keep each
-// addition's error (Knuth, "The Art of Computer Programming" 2, 4.2.2, theorem B).
+// Blocks that are further than 2 e from the nsel-th largest sum are in or out; the
+// others, mostly the nsel-th itself and a few more or none, are decided by sums that
+// are exact enough to be the exact value's rounding to fp32: products of fp16
+// numbers are exact in fp32, and their sums keep each addition's error (Knuth, "The
+// Art of Computer Programming" 2, 4.2.2, theorem B).
 //
 // Measured (GB300, 8 key-value heads of 128): one sequence of 131072 tokens, 64 of
 // 2048 blocks per head, 12.2 us, of them 7.6 scoring 8.4 MB, 1.5 the threshold and
@@ -52,6 +52,7 @@ __device__ unsigned int q2_select_error;
 
 constexpr int kAtOnce = 8;                          // blocks of a warp's step
 constexpr int kBins = 2048;
+constexpr int kFew = 64;                            // keys that are ranked by comparing all (some 35 cycles each; a histogram is a microsecond)
 constexpr int kMostSmem = 226 * 1024;
 constexpr uint32_t kAlways = 0xffffffffu, kOdd = 0xfffffffeu;    // keys of first and last blocks, of scores that are not finite
 
@@ -137,7 +138,7 @@ __device__ uint32_t largest(SelectShared<T>& s, const uint32_t* keys, int n, uin
   // Histograms of even steps over a range that holds the key sought, until few
   // are left in its bin.
   uint32_t left = n - always - odds;                // keys in lo .. hi
-  while (left > T && lo < hi) {
+  while (left > kFew && lo < hi) {
     const uint32_t span = hi - lo;
     const int shift = max(0, 32 - __clz(span) - 11);                          // (span >> shift) < kBins
     for (int i = threadIdx.x; i < kBins; i += T) s.hist[i] = 0;
@@ -438,8 +439,9 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   kodd = __reduce_add_sync(0xffffffffu, kodd);
 
-  // threads have consecutive blocks from here on
-  const int each = (n + T - 1) / T, i0 = min(n, (int)threadIdx.x * each), i1 = min(n, i0 + each);
+  // threads have consecutive blocks from here on; of many an odd number, for the
+  // banks (2^20 tokens 82 -> 49 us; with 4 of 2048 it cost 0.4)
+  const int some = (n + T - 1) / T, each = some > 8 ? some | 1 : some, i0 = min(n, (int)threadIdx.x * each), i1 = min(n, i0 + each);
   uint32_t need = a.nsel, key = largest(s, keys, n, a.first + a.last, kodd, kmin, kmax, need);
   if (key < kOdd) {
     // blocks whose sums lie within the error of the nsel-th
@@ -547,12 +549,18 @@ int select(const Pages& pg, const CacheShape& c, const void* bounds, const void*
   a.first = first;
   a.last = last;
   a.sel = sel;
-  // Up to eight CTAs of 512 threads to a cluster where the clusters leave SMs
-  // idle and there are steps for their warps; with many clusters two of 256 per SM.
+  // Up to eight CTAs to a cluster where the clusters leave SMs idle and there are
+  // steps for their warps.  With few clusters and some blocks CTAs of 512 threads,
+  // one per SM (4 sequences of 65536 tokens and 8 heads: 12.3 us, 15.2 of 256
+  // threads; 8 of 32768: 11.9 and 11.5; one of 4096: 6.6 and 6.0).  Eight to a
+  // cluster only where they leave half of the SMs: all may not find room at once
+  // (2 sequences of 131072: 18.2 us, 16.7 with four).
   const int blocks = (int)((c.cap + Q2_BLOCK - 1) / Q2_BLOCK), clusters = batch * c.kv_heads;
   auto launch = [&](auto kernel, int T, int D, int shared, bool staged) {
     a.cs = 1;
-    while (a.cs < 8 && (long long)clusters * a.cs * 2 * T <= 512ll * dev_info().sms && blocks >= 2 * a.cs * (T / 32) * kAtOnce) a.cs *= 2;
+    while (a.cs < 8 && (long long)clusters * a.cs * 2 * T <= (a.cs == 4 ? 256ll : 512ll) * dev_info().sms &&
+           blocks >= 2 * a.cs * (T / 32) * kAtOnce)
+      a.cs *= 2;
     const int smem = (a.group + 7) / 8 * (D / 32) * 1024 + shared + blocks * 4;
     const int stage = T / 32 * kAtOnce * 4 * D, room = (T == 512 ? kMostSmem : kMostSmem / 2) - smem;
     a.stages = staged ? std::max(1, std::min(3, room / stage)) : 0;
@@ -565,7 +573,7 @@ int select(const Pages& pg, const CacheShape& c, const void* bounds, const void*
     constexpr int D = Dc();
     int st = Q2_ESIZE;
     if constexpr (D <= 128)
-      if (clusters <= dev_info().sms) st = launch(k_select<D, 512, true>, 512, D, sizeof(SelectShared<512>), true);
+      if (clusters * 4 <= dev_info().sms && blocks > 256) st = launch(k_select<D, 512, true>, 512, D, sizeof(SelectShared<512>), true);
     if (st == Q2_ESIZE) st = launch(k_select<D, 256, true>, 256, D, sizeof(SelectShared<256>), true);
     return st == Q2_ESIZE ? launch(k_select<D, 256, false>, 256, D, sizeof(SelectShared<256>), false) : st;
   };
