@@ -11,8 +11,8 @@
 // 32 lanes (a slot); the partner of a column is in another lane of the same row (a
 // shuffle) or in the next register.
 //
-// Work is cut into tiles: the new tokens of one block of 64 positions of one
-// sequence, times a few heads of one kind (queries, keys or values).  The slots of
+// Work is cut into tiles: the new tokens of one block of 64 positions (where no
+// bounds are kept, of 8 at least) of one sequence, times a few heads of one kind (queries, keys or values).  The slots of
 // a CTA take tokens side by side as far as there are any, and heads with the rest;
 // where bounds are kept, all heads first, so that a slot's keys are of one head.
 // Tiles are cut at blocks so that a block's bounds (least and greatest key per
@@ -113,6 +113,7 @@ struct AppendArgs {
   const float* angles;
   int q_heads, kv_heads, chunk, cq, ck; // chunk: heads of a CTA; cq, ck: CTAs of a tile's queries, keys
   int rot, interleaved, sub;            // sub: bounds of a page
+  int tile;                             // 2^tile positions to a tile
 };
 
 __device__ __forceinline__ uint4 hmin8(const uint4& a, const uint4& b) {
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
       if (b < rw.batch) {
         const Seq s = seq_of(rw, b);
         bad = bad || !s.ok;
-        if (s.n) n[i] = s.ok ? (s.len - 1) / Q2_BLOCK - (s.len - s.n) / Q2_BLOCK + 1 : (s.n + Q2_BLOCK - 1) / Q2_BLOCK;
+        if (s.n) n[i] = s.ok ? ((s.len - 1) >> a.tile) - ((s.len - s.n) >> a.tile) + 1 : ((s.n - 1) >> a.tile) + 1;
       }
       sum += n[i];
     }
@@ -268,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
       if (!s.ok && y == 0 && threadIdx.x == 0) atomicOr(&q2_cache_error, Q2_ERR_LENGTH);
       if (!s.n) continue;
     }
-    const int past = s.len - s.n, block = past / Q2_BLOCK + j;
-    const int p0 = s.ok ? max(past, block * Q2_BLOCK) : 0;
-    const int n = ONE ? 1 : s.ok ? min(s.len, (block + 1) * Q2_BLOCK) - p0 : min(Q2_BLOCK, s.n - j * Q2_BLOCK);
-    const int row0 = s.row0 + (s.ok ? p0 - past : j * Q2_BLOCK);
+    const int past = s.len - s.n, block = ONE ? past / Q2_BLOCK : (past >> a.tile) + j;
+    const int p0 = !s.ok ? 0 : ONE ? past : max(past, block << a.tile);
+    const int n = ONE ? 1 : s.ok ? min(s.len, (block + 1) << a.tile) - p0 : min(1 << a.tile, s.n - (j << a.tile));
+    const int row0 = s.row0 + (s.ok ? p0 - past : j << a.tile);
     const int* trow = a.pg.table + b * a.pg.table_stride;
 
     // The slots take T tokens side by side and SLOTS / T heads; keys with bounds
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
         }
       }
     }
-    if (bounded) {                                  // (a slot's keys are of head `part`)
+    if (bounded) {                                  // (a slot's keys are of head `part`; a tile is a block)
       const int begin = s.ok ? block * Q2_BLOCK : 0, pi = page_of(a.pg, begin);
       const int page = s.ok ? trow[pi] : -1;
       const bool kept = (unsigned)page < (unsigned)a.pg.npages;
@@ -599,8 +600,13 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   // number of tokens, more where there would be more CTAs than run at once; keys
   // whose bounds are kept no more than the slots.
   const int slots = kThreads * 8 / c.D;
-  const long long tiles = starts ? (long long)ntok / Q2_BLOCK + 2ll * std::min(batch, ntok) : batch;
+  // Blocks of 64 positions are tiles where bounds are kept; else, with few tokens
+  // to a sequence, fewer: a prompt among them were the end of all (238 tokens of
+  // 126 sequences, 32 heads of 256: 36.2 -> 9.8 us).
   const int usual = std::min(Q2_BLOCK, (ntok + batch - 1) / batch);
+  a.tile = 6;
+  while (!bounds && a.tile > 3 && (1 << (a.tile - 1)) >= 2 * usual) --a.tile;
+  const long long tiles = starts ? ((long long)ntok >> a.tile) + 2ll * std::min(batch, ntok) : batch;
   int side = slots;
   for (int t = 1; t < usual && side > 1; t <<= 1) side >>= 1;
   const long long heads = q_heads + 2ll * c.kv_heads;
@@ -612,7 +618,7 @@ int append(const Pages& pg, const Pages& sp, const CacheShape& c, void* bounds, 
   a.cq = ctas(q_heads);
   a.ck = ctas(c.kv_heads);
   const dim3 grid((unsigned)std::min(tiles, 65535ll), a.cq + 2 * a.ck);
-  const int smem = rope && starts ? Q2_BLOCK * a.rot * 4 : 0;
+  const int smem = rope && starts ? a.rot * 4 << a.tile : 0;
   return by_shape(c, [&](auto D, auto G) {
     return starts ? launch_pdl(k_append<D(), G(), false>, a, grid, kThreads, smem, stream)
                   : launch_pdl(k_append<D(), G(), true>, a, grid, kThreads, 0, stream);

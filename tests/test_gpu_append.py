@@ -408,3 +408,15 @@ def test_binding_refuses_what_it_would_misread(q2):
         cache.read(c.dlens, starts=starts)
     with pytest.raises(q2.Q2Error):
         cache.read(c.dlens, k_out=c.dk[:1])
+
+
+@pytest.mark.parametrize("bits,group", FORMS)
+@pytest.mark.parametrize("bounds", [False, True])
+def test_a_prompt_among_sequences_of_few_tokens(q2, bits, group, bounds):
+    """Tiles of 8 to 64 positions: what one call stores does not depend on how many tokens the others have."""
+    for counts in ([1] * 20 + [70] + [2] * 9, [3, 4, 5, 150, 2, 1], [9] * 12, [0, 1, 17, 0, 33, 2]):
+        lens = [n + 13 * (b % 5) if n else 0 for b, n in enumerate(counts)]
+        c = Case(lens, counts, bits=bits, group=group, page=32, rot=64, bounds=bounds, seed=len(counts))
+        c.check_q(c.run(q2))
+        c.check_pools()
+    assert q2.device_errors() == 0
