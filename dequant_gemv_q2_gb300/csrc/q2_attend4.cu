@@ -34,7 +34,7 @@
 // sequence's output (one of 131072 tokens: 4.1e-4 off, 2.1e-4 of it fp16's own).
 //
 // A warp's step of 32 tokens is some 700 instructions, two warps to a scheduler: of
-// 134 us for 64 sequences of 8192 tokens (8 key-value heads of 128, groups of 64,
+// 135 us for 64 sequences of 8192 tokens (8 key-value heads of 128, groups of 64,
 // four query heads each; 605 MB, 4.5 TB/s of the 6.8 of a copy) the loads alone
 // take 97, the instructions alone 117, 2.2 of them per cycle and SM.
 //

@@ -11,10 +11,11 @@
 // 32 lanes (a slot); the partner of a column is in another lane of the same row (a
 // shuffle) or in the next register.
 //
-// Work is cut into tiles: the new tokens of one block of 64 positions (where no
-// bounds are kept, of 8 at least) of one sequence, times a few heads of one kind (queries, keys or values).  The slots of
-// a CTA take tokens side by side as far as there are any, and heads with the rest;
-// where bounds are kept, all heads first, so that a slot's keys are of one head.
+// Work is cut into tiles: the new tokens of one block of 64 positions (of 8 at
+// least where no bounds are kept) of one sequence, times a few heads of one kind
+// (queries, keys or values).  The slots of a CTA take tokens side by side as far as
+// there are any, and heads with the rest; where bounds are kept, all heads first,
+// so that a slot's keys are of one head.
 // Tiles are cut at blocks so that a block's bounds (least and greatest key per
 // column) are one CTA's: no atomics, and what a block held before is read only
 // where it goes on.
