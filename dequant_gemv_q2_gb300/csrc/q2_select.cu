@@ -386,11 +386,13 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
     slot = slot + 1 == a.stages ? 0 : slot + 1;
   }
   // What no sum of magnitudes is above: that of the queries' on the largest ones of
-  // these blocks (finite ones: a block with others is not decided by its sum).
+  // these blocks (finite ones: a block with others is not decided by its sum), none
+  // of the magnitudes below 2^-14.
+  const __half2 least = __float2half2_rn(0x1p-14f);
   uint32_t big[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const __half2 z = __hmin2(size[k], __float2half2_rn(65504.f));
+    const __half2 z = __hmin2(__hmax2(size[k], least), __float2half2_rn(65504.f));
     big[k] = *reinterpret_cast<const uint32_t*>(&z);
   }
   float most = 0.f;
@@ -400,9 +402,13 @@ __global__ void __launch_bounds__(T, 512 / T) k_select(const __grid_constant__ S
     for (int c = 0; c < NB; ++c) {
       const uint4* f = frag + (ht * NB + c) * 64 + lane;
       const uint4 up = f[0], dn = f[32];            // (one of the two is zero, or both are NaN)
-      constexpr uint32_t kAbs = 0x7fff7fffu;
-      mma(w, (up.x | dn.x) & kAbs, 0u, (up.y | dn.y) & kAbs, 0u, big[0], big[1]);
-      mma(w, (up.z | dn.z) & kAbs, 0u, (up.w | dn.w) & kAbs, 0u, big[2], big[3]);
+      auto size_of = [&](uint32_t x, uint32_t y) {
+        const uint32_t z = (x | y) & 0x7fff7fffu;
+        const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&z), least);
+        return *reinterpret_cast<const uint32_t*>(&m);
+      };
+      mma(w, size_of(up.x, dn.x), 0u, size_of(up.y, dn.y), 0u, big[0], big[1]);
+      mma(w, size_of(up.z, dn.z), 0u, size_of(up.w, dn.w), 0u, big[2], big[3]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)

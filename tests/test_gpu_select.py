@@ -188,3 +188,21 @@ def test_binding_refuses_what_it_would_misread(q2):
     bare = q2.PagedKV(cache.k, cache.k, c.dtable, 8)
     with pytest.raises(q2.Q2Error):
         bare.select(**ok)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("large", [1.0, 64.0, 1024.0, 16384.0])
+def test_keys_below_the_normal_numbers(q2, D, large):
+    """Bounds of a few steps of fp16's smallest, under queries of which one column is larger than the others: the tensor cores
+    align such numbers as if they were 2^-14, so what they drop is far above 2^-23 of the products.  All scores here are
+    multiples of 2^-30 below 2^-9, exact in fp32; equal ones go to the lower block."""
+    c = Case([64 * 2000, 64 * 333], 2, 4, D, 64, 9)
+    rng = np.random.default_rng(10)
+    c.bounds[:] = np.sort(rng.integers(-16, 17, size=c.bounds.shape), axis=3) * 2.0 ** -24
+    c.bounds[..., 5::32] = 2.0 ** -24                   # (the error's bound takes columns 32 apart together)
+    c.q[:] = np.rint(rng.normal(size=c.q.shape) * 64) / 64
+    c.q[..., 5] = large
+    for n in (1, 50, 300):
+        c.check(q2, n, 0, 0)
+    c.q[:], c.bounds[:] = c.q * 2.0 ** -20, c.bounds * 2.0 ** 10            # the queries are, and the keys hardly
+    c.check(q2, 50, 0, 0)
