@@ -102,6 +102,7 @@ struct Shape {
 template <int D, int H, bool SP>
 __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend(const __grid_constant__ AttendArgs a) {
   using S = Shape<D, H>;
+  static_assert(ctas_of<D>() <= most_ctas(D) && H <= most_heads(D), "the workspace has room for all parts");
   constexpr int RH = H / 8;                         // rows g, g + 8 of a lane that are heads
   constexpr int STAGES = S::STAGES, CPR = D / 8, RPI = 32 / CPR, NT = D / 8;
   extern __shared__ __align__(128) unsigned char q2_att_smem[];

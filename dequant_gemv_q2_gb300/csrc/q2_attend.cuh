@@ -326,15 +326,19 @@ __device__ __forceinline__ int first_token(const UnitArgs& a, const Walk& w, int
 
 // ---------------------------------------------------------------- host side
 
-// The most CTAs per SM that any of the kernels has.
-constexpr int most_ctas(int D) { return D == 256 ? 2 : 4; }
+// The most CTAs per SM, and query heads of a unit, that any of the kernels has.
+constexpr int most_ctas(int D) { return D == 64 ? 3 : 2; }
+constexpr int most_heads(int D) { return D == 256 ? 8 : kMostHeads; }
+
+// Parts of a call at most, two to a CTA, times their heads.
+inline size_t part_rows(int D, int sms) { return (size_t)2 * most_ctas(D) * sms * most_heads(D); }
 
 // The workspace: the parts' sums, in a region that fits every head_dim and both
 // kinds of cache (so the counters behind it have one place for all calls), then
 // counters.
 inline size_t part_bytes(int sms) {
   size_t n = 0;
-  for (int D : {64, 128, 256}) n = std::max(n, (size_t)2 * most_ctas(D) * sms * kMostHeads * (D * 4 + 8));
+  for (int D : {64, 128, 256}) n = std::max(n, part_rows(D, sms) * (D * 4 + 8));
   return (n + 255) / 256 * 256;
 }
 
@@ -404,7 +408,7 @@ struct UnitCall {
     a.ldo = ldo;
     a.part = static_cast<float*>(ws);
     a.count = reinterpret_cast<unsigned int*>(static_cast<char*>(ws) + parts);
-    a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * most_ctas(c.D) * dev_info().sms * kMostHeads * c.D);
+    a.ml = reinterpret_cast<float2*>(a.part + part_rows(c.D, dev_info().sms) * c.D);
     a.sel = sel;
     a.nsel = nsel;
     a.batch = batch;

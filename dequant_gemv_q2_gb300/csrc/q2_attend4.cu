@@ -170,6 +170,7 @@ __device__ __forceinline__ void mma_from(bool zero, float (&c)[4], uint32_t a0, 
 template <int D, int G, int H, bool FOLD, bool SP>
 __global__ void __launch_bounds__(kThreads, ctas_of<D>()) k_attend4(const __grid_constant__ Attend4Args a) {
   using S = Shape<D, G, H>;
+  static_assert(ctas_of<D>() <= most_ctas(D) && H <= most_heads(D), "the workspace has room for all parts");
   constexpr int NH = H / 8, STAGES = S::STAGES, NB = D / 32;   // NB: 16-byte pieces of a row, 32 columns each
   constexpr int TW = S::TW, NTL = TW / kTile, UNIT = kWarps * TW;
   constexpr int RPI = 32 / NB, BPG = NB / G;                   // rows of a copy instruction; pieces of a group

@@ -43,3 +43,31 @@ def test_products(q2):
         assert pk.ws is own and torch.equal(pk.gemv(x), want)       # the one before stays
     pk.set_workspace(torch.zeros(need // 8, dtype=torch.int64, device="cuda"))
     assert torch.equal(pk.gemv(x), want)
+
+
+def test_attention_needs_no_more_than_its_parts(q2):
+    """Two parts to a CTA, of as many rows of D numbers, a maximum and a denominator as a unit has heads (two CTAs per SM of 16
+    heads of 128 are the most), then a counter per (sequence, key-value head): a workspace of this size serves every call."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    parts = 2 * 2 * sms * 16 * (128 * 4 + 8)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    table = torch.arange(1024, dtype=torch.int32, device="cuda").view(2, 512)
+    lens = torch.tensor([32768, 9001], dtype=torch.int32, device="cuda")
+    for D, heads in ((64, 2), (64, 32), (128, 2), (128, 32), (256, 2), (256, 32)):
+        need = -(-parts // 256) * 256 + 2 * 2 * -(-(heads // 2) // (16 if D < 256 else 8)) * 4
+        ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws[:need] = 0
+        rows = lambda *shape: torch.randn(shape, device="cuda", generator=g).half()
+        q = rows(2, heads, D)
+        k, v = rows(1024, 64, 2, D), rows(1024, 64, 2, D)
+        full = q2.PagedKV(k, v, table, heads)
+        c4 = q2.PagedKV4.empty(1024, 64, 2, D, 64, table, heads)
+        c4.ks[..., 0], c4.vs[..., 0] = 0.1, 0.1
+        c4.k.random_(0, 256, generator=g)
+        c4.v.random_(0, 256, generator=g)
+        want = full.attend(q, lens), c4.attend(q, lens)
+        full = q2.PagedKV(k, v, table, heads, workspace=ws[:need])
+        c4 = q2.PagedKV4(c4.k, c4.ks, c4.v, c4.vs, table, heads, workspace=ws[:need])
+        assert torch.equal(full.attend(q, lens), want[0]) and torch.equal(c4.attend(q, lens), want[1])
+        assert (ws[need:] == 0xA5).all() and (ws[need - 16:need] == 0).all()
+    assert q2.device_errors() == 0
