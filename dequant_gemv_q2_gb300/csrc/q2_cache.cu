@@ -93,11 +93,13 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 // x c + y s to the last bit (but where the exact sum is within 2^-20 of a step
 // of the middle of two): the products' and the sum's rounding errors (Knuth,
-// "The Art of Computer Programming" 2, 4.2.2, theorem B) added at the end.
+// "The Art of Computer Programming" 2, 4.2.2, theorem B) added at the end.  In
+// explicitly rounded operations: of plain ones the compiler may fuse a product
+// into the sum behind it, whose error is then another.
 __device__ __forceinline__ float turn_exact(float x, float c, float y, float s) {
-  const float p = x * c, q = y * s, pe = fmaf(x, c, -p), qe = fmaf(y, s, -q);
-  const float t = p + q, z = t - p, e = (p - (t - z)) + (q - z);
-  const float r = t + (e + (pe + qe));
+  const float p = __fmul_rn(x, c), q = __fmul_rn(y, s), pe = fmaf(x, c, -p), qe = fmaf(y, s, -q);
+  const float t = __fadd_rn(p, q), z = __fsub_rn(t, p), e = __fadd_rn(__fsub_rn(p, __fsub_rn(t, z)), __fsub_rn(q, z));
+  const float r = __fadd_rn(t, __fadd_rn(e, __fadd_rn(pe, qe)));
   return fabsf(t) <= 3.4028235e38f ? r : t;         // (an infinite t has no error term)
 }
 

@@ -80,7 +80,9 @@ struct SelectShared {
   uint32_t list[T];
 };
 
-// (h, e) + (h2, e2), h and e the sum's fp32 value and what it lacks
+// (h, e) + (h2, e2), h and e the sum's fp32 value and what it lacks.  (Plain
+// operations: h2 may be a product that the compiler fuses into a sum, but only one of
+// fp16 numbers, which is exact.)
 __device__ __forceinline__ void join(float& h, float& e, float h2, float e2) {
   const float t = h + h2, z = t - h;
   e = (e + e2) + ((h - (t - z)) + (h2 - z));
