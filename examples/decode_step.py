@@ -98,17 +98,20 @@ class Decoder:
         self.last.copy_(delta)
 
     def capture(self):
-        """The step as a graph (lengths go on from where they are)."""
-        lens = self.lens.clone()
+        """The step as a graph.  Lengths, caches and the residual stream stay as they are: a step that makes what is made
+        once runs before with sequences of no tokens, which stores nothing."""
+        state = [(t, t.clone()) for t in (self.lens, self.h, self.last)]
+        self.lens.fill_(-1)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            self.step()                      # makes what is made once
+            self.step()
         torch.cuda.current_stream().wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             self.step()
-        self.lens.copy_(lens)
+        for t, before in state:
+            t.copy_(before)
         return graph
 
 

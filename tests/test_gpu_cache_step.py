@@ -149,3 +149,39 @@ def test_all_blocks_are_all_of_the_cache(ex):
     for bits in (16, 4):
         rel = (_steps(ex, False, bits=bits, blocks=7) - _steps(ex, False, bits=bits)).abs().max()
         assert rel < 0.05, rel
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_capturing_leaves_the_state_alone(ex, bits):
+    """Captured behind partly filled blocks with a live residual stream: nothing of the caches (their bounds among it), the
+    lengths and the stream changes, and what comes behind is what eager steps alone give."""
+    def start():
+        d = ex.Decoder(**CFG, bits=bits, blocks=2, page=32)
+        past = torch.tensor([250, 0, 70], dtype=torch.int32, device="cuda")
+        starts = torch.tensor([0, 250, 250, 320], dtype=torch.int32, device="cuda")
+        g = torch.Generator(device="cuda").manual_seed(2)
+        for cache in d.caches:
+            k, v = (torch.randn(320, CFG["kv_heads"], CFG["dim"], device="cuda", generator=g).half() for _ in range(2))
+            cache.append(k, v, past, starts=starts, rope=d.rope)
+        d.lens.copy_(past)
+        hidden = [torch.randn(3, CFG["hidden"], device="cuda", generator=g).half() for _ in range(6)]
+        return d, hidden
+
+    def state(d):
+        names = ("k", "v", "bounds") if bits == 16 else ("k", "ks", "v", "vs", "bounds")
+        return [d.lens.clone(), d.h.clone(), d.last.clone()] + [getattr(c, n).clone() for c in d.caches for n in names]
+
+    def run(d, hidden, captured):
+        step, seen = d.step, []
+        for i, h in enumerate(hidden):
+            if captured and i == 3:
+                before = state(d)
+                step = d.capture().replay
+                assert all(torch.equal(a, b) for a, b in zip(before, state(d)))
+            d.h.copy_(h)
+            step()
+            seen.append(d.last.clone())
+        return seen + state(d)
+
+    assert all(torch.equal(a, b) for a, b in zip(run(*start(), True), run(*start(), False)))
+    assert ex.q2.device_errors() == 0
