@@ -121,12 +121,12 @@ def main():
         p.add_argument("--" + name, type=int, default=value)
     p.add_argument("--cache-bits", type=int, default=16, choices=(16, 4))
     p.add_argument("--blocks", type=int, help="blocks of 64 tokens that a key-value head attends (all)")
-    p.add_argument("--past", type=int, default=256, help="tokens that sequences have already, at most")
+    p.add_argument("--past", type=int, default=256, help="sequences have fewer tokens than this already (0: none)")
     a = p.parse_args()
     q2.load(build_if_missing=True)
     d = Decoder(a.layers, a.hidden, a.q_heads, a.kv_heads, a.dim, a.ffn, a.batch, room=a.steps + a.past + 44, bits=a.cache_bits, blocks=a.blocks)
     # sequences that have 0, 37, 74, .. tokens already: prompts of random keys and values
-    past = torch.arange(a.batch, dtype=torch.int32, device="cuda") * 37 % a.past
+    past = torch.arange(a.batch, dtype=torch.int32, device="cuda") * 37 % max(a.past, 1)
     starts = torch.nn.functional.pad(past.cumsum(0), (1, 0)).to(torch.int32)
     rows = lambda: torch.randn(int(starts[-1]), a.kv_heads, a.dim, device="cuda").half()
     for cache in d.caches:

@@ -185,3 +185,13 @@ def test_capturing_leaves_the_state_alone(ex, bits):
 
     assert all(torch.equal(a, b) for a, b in zip(run(*start(), True), run(*start(), False)))
     assert ex.q2.device_errors() == 0
+
+
+@pytest.mark.parametrize("past", [0, 1, 100])
+@pytest.mark.parametrize("more", [[], ["--cache-bits", "4", "--blocks", "2"]])
+def test_the_example_from_the_command_line(ex, monkeypatch, capsys, past, more):
+    sizes = dict(layers=1, hidden=512, q_heads=8, kv_heads=2, dim=64, ffn=768, batch=3, steps=2, past=past)
+    args = [a for n, v in sizes.items() for a in ("--" + n.replace("_", "-"), str(v))]
+    monkeypatch.setattr("sys.argv", ["decode_step.py"] + args + more)
+    ex.main()
+    assert f"lengths {[37 * b % max(past, 1) + 2 for b in range(3)]}" in capsys.readouterr().out
