@@ -885,5 +885,5 @@ class PagedKV4(_Cache):
         new = lambda tail, dtype: torch.zeros((pages, kv_heads, page_size) + tail, dtype=dtype, device=table.device).transpose(1, 2)  # noqa: E731
         k, v = (new((dim // 2,), torch.uint8) for _ in range(2))
         ks, vs = (new((dim // group, 2), torch.float16) for _ in range(2))
-        kept = torch.zeros((pages, -(-page_size // BLOCK), kv_heads, 2, dim), dtype=torch.float16, device=table.device)
-        return cls(k, ks, v, vs, table, q_heads, bounds=kept if bounds else None)
+        kept = torch.zeros((pages, -(-page_size // BLOCK), kv_heads, 2, dim), dtype=torch.float16, device=table.device) if bounds else None
+        return cls(k, ks, v, vs, table, q_heads, bounds=kept)

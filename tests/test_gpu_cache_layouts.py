@@ -248,3 +248,18 @@ def test_one_block_far_above_the_rest(q2, D, q_group, lens):
     c.q[:, :, :3] *= 1000                               # and some columns of the queries far above the others
     c.check(q2, 40, 0, 1)
     assert q2.device_errors() == 0
+
+
+def test_a_cache_without_bounds_keeps_no_room_for_them(q2):
+    pages, page, H, D = 512, 16, 8, 128
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    least = 2 * pages * page * H * (D // 2 + 4 * D // 64)
+    for bounds in (False, True):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        c = q2.PagedKV4.empty(pages, page, H, D, 64, table, 16, bounds=bounds)
+        kept = c.bounds.numel() * 2 if bounds else 0
+        room = least + c.ws.numel() + kept
+        assert room <= torch.cuda.max_memory_allocated() - before < room + (1 << 20) and (c.bounds is None) == (not bounds)
+        del c
