@@ -481,8 +481,11 @@ typedef struct {
  *   - A length below 0 or above max_pages * page_size, one that is neither 0
  *     nor at least the sequence's rows, or one above rope->positions: nothing of
  *     the sequence is stored, its rows of q_out become NaN, and Q2_ERR_LENGTH is
- *     set; the same bit for starts that do not ascend within 0..ntok (nothing
- *     is written then).  A page outside 0..npages-1: its tokens are not stored,
+ *     set.  The same bit where starts[b] and starts[b + 1] do not ascend within
+ *     0..ntok: nothing of that sequence is written.  The other sequences are
+ *     stored all the same, their bounds kept up and their queries turned; rows
+ *     of q_out that two of them claim (where starts descend between them) are
+ *     undefined.  A page outside 0..npages-1: its tokens are not stored,
  *     Q2_ERR_PAGE.
  *   - Pointers 16-byte aligned, leading dimensions multiples of 8, strides as the
  *     cache's structure says (Q2_EALIGN); batch <= Q2_ATT_MAX_BATCH, q_heads <=
@@ -501,7 +504,8 @@ int q2_append4(const q2_kv4* kv, void* bounds, const void* q, long long ldq, voi
  * whole sequences.  k, v: device fp16, head h of row r at + r * ldk (ldv) + h *
  * head_dim; either may be NULL.  4 bits: fp16(m + s c), the sum rounded to fp32
  * before.  A token whose page does not exist, and rows of a sequence whose
- * length is wrong, are NaN. */
+ * length is wrong, are NaN.  Where starts descend, the rows of the others may be
+ * left as they are. */
 int q2_read(const q2_kv* kv, void* k, long long ldk, void* v, long long ldv, const int* starts, const int* lens,
             int batch, int ntok, q2_stream stream);
 int q2_read4(const q2_kv4* kv, void* k, long long ldk, void* v, long long ldv, const int* starts, const int* lens,

@@ -420,3 +420,20 @@ def test_a_prompt_among_sequences_of_few_tokens(q2, bits, group, bounds):
         c.check_q(c.run(q2))
         c.check_pools()
     assert q2.device_errors() == 0
+
+
+@pytest.mark.parametrize("bits,group", FORMS[:2])
+def test_sequences_beside_one_with_wrong_starts_are_stored(q2, bits, group):
+    """Starts that descend behind sequence 1: nothing of it is stored, all of the others is, and the rows that one sequence
+    alone claims are turned (sequence 0 has rows 0..8, 2 has 8..10, 3 has 11)."""
+    c = Case([20, 30, 40, 10], [4, 4, 3, 1], bits=bits, group=group, bounds=True, seed=15)
+    c.dstarts[1:3] = torch.tensor([9, 8], dtype=torch.int32, device="cuda")
+    c.counts, c.starts = [9, 0, 3, 1], np.array([0, 9, 8, 11, 12])
+    out = c.run(q2).cpu().numpy()
+    assert q2.device_errors() == q2.ERR_LENGTH
+    c.check_pools()
+    for b, rows in ((0, range(0, 8)), (2, range(9, 11)), (3, range(11, 12))):
+        y, mag = c.turned(b, c.q)
+        for r in rows:
+            i = r - c.starts[b]
+            assert (np.abs(out[r] - y[i]) <= 2.0 ** -11 * np.abs(y[i]) + 2.0 ** -25 + 3 * 2.0 ** -24 * mag[i]).all()
