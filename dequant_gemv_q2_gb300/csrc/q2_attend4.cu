@@ -122,8 +122,8 @@ __device__ __forceinline__ void load_pairs(const unsigned char* at, uint32_t (&r
 
 // How far, in powers of two, a score may rise above the maximum before all is
 // scaled anew: p is at most 2^kSlack.  (With 0 a third of the steps of 2048 tokens
-// scaled: 45.0 us for 64 sequences, 43.4 with 4.  Of 20 bits that the smallest p
-// have between 2^-29 and 2^-15 of the largest, four are lost.)
+// scaled: 45.0 us for 64 sequences, 43.4 with 4.  p s is held to 2^-20 of itself or,
+// half of fp16's smallest number, 2^-35 of the largest; without the slack 2^-39.)
 constexpr uint32_t kSlack = 4;
 
 // 2^x to 2 units in the last place; what is below the normal numbers is zero

@@ -513,7 +513,11 @@ int q2_read4(const q2_kv4* kv, void* k, long long ldk, void* v, long long ldv, c
 
 /* Attention of one new token per sequence over a cache in 4 bits: q2_attend on
  * what the cache stands for, of tokens that q2_append4 has stored (the last one
- * among them).  fp16 in and out, fp32 sums; no value is rounded on the way.
+ * among them).  fp16 in and out, fp32 sums; no value is expanded or rounded.
+ *   - Beside the sums' roundings: products with keys' codes are cut off, so a
+ *     head's q . k is off by up to 2^-8 s max|q| for each 32 columns, s their step
+ *     and max|q| the head's largest column; a probability times a value's step is
+ *     off by up to 2^-20 of itself or 2^-35 of the largest such product.
  *   - q, out, lens, scale, their checks and the errors are as for q2_attend, and
  *     so is the workspace (q2_attend_workspace_bytes), which calls on both kinds
  *     of cache may share if they are ordered on one stream.

@@ -175,6 +175,17 @@ def test_large_batch(q2):
     c.check(c.run(c.cache(q2)))
 
 
+@pytest.mark.parametrize("D,group,q_group", [(128, 64, 4), (128, 32, 5), (64, 64, 12), (256, 32, 8)])
+@pytest.mark.parametrize("large", [16.0, 100.0, 4000.0])
+def test_queries_with_a_large_column(q2, D, group, q_group, large):
+    """A score's error goes by the head's largest column, not by the terms: the bound of above holds, and the outputs are
+    where an fp32 sum's would be, since a column that large decides the score."""
+    c = Case([700, 64, 9], 2, q_group, D, group, 16, 30 + q_group)
+    c.q[..., 5] *= np.float16(large)
+    c.dwide[:, : c.q[0].size] = torch.from_numpy(c.q.reshape(3, -1)).cuda()
+    c.check(c.run(c.cache(q2)))
+
+
 @pytest.mark.parametrize("shift", [0.0, 100.0])
 def test_peaked_probabilities_and_offsets_far_from_zero(q2, shift):
     c = Case([600, 90], 2, 4, 128, 32, 16, 6, peak=3.0, shift=shift)
