@@ -437,3 +437,16 @@ def test_sequences_beside_one_with_wrong_starts_are_stored(q2, bits, group):
         for r in rows:
             i = r - c.starts[b]
             assert (np.abs(out[r] - y[i]) <= 2.0 ** -11 * np.abs(y[i]) + 2.0 ** -25 + 3 * 2.0 ** -24 * mag[i]).all()
+
+
+@pytest.mark.parametrize("bits,group", FORMS)
+@pytest.mark.parametrize("starts", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_queries_beside_padding_are_turned(q2, bits, group, starts, interleaved):
+    c = Case([5, 0, 70, 0, 64], [1] * 5, bits=bits, group=group, seed=16, starts=starts, interleaved=interleaved)
+    out = c.run(q2).cpu().numpy()
+    for b in (0, 2, 4):
+        y, mag = c.turned(b, c.q)
+        assert (np.abs(out[b] - y[0]) <= 2.0 ** -11 * np.abs(y[0]) + 2.0 ** -25 + 3 * 2.0 ** -24 * mag[0]).all()
+    assert (out[[1, 3]] == 7).all()
+    c.check_pools(skip=(1, 3))

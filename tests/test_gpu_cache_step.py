@@ -195,3 +195,52 @@ def test_the_example_from_the_command_line(ex, monkeypatch, capsys, past, more):
     monkeypatch.setattr("sys.argv", ["decode_step.py"] + args + more)
     ex.main()
     assert f"lengths {[37 * b % max(past, 1) + 2 for b in range(3)]}" in capsys.readouterr().out
+
+
+class _Checked:
+    """A cache whose selections and outputs are compared with those of what it holds, call for call."""
+
+    def __init__(self, cache, bits):
+        self.cache, self.bits, self.calls = cache, bits, 0
+
+    def append(self, *args, **kw):
+        return self.cache.append(*args, **kw)
+
+    def select(self, q, lens, blocks):
+        self.sel = self.cache.select(q, lens, blocks)
+        c = self.cache
+        s = Selection.__new__(Selection)
+        s.lens, s.H, s.G, s.D, s.page = lens.tolist(), c.kv_heads, c.q_heads // c.kv_heads, c.dim, c.k.shape[1]
+        s.table, s.q, s.bounds = c.table.cpu().numpy(), q.cpu().numpy(), c.bounds.cpu().numpy()
+        assert np.array_equal(self.sel.cpu().numpy(), s.expect(blocks, 0, 1))
+        return self.sel
+
+    def attend(self, q, lens, out, blocks):
+        assert blocks is self.sel
+        c = self.cache
+        c.attend(q, lens, out=out, blocks=blocks)
+        a = Attention.__new__(Attention)
+        a.lens, a.H, a.G, a.D, a.group, a.page = lens.tolist(), c.kv_heads, c.q_heads // c.kv_heads, c.dim, 64, c.k.shape[1]
+        a.bits, a.table, a.q, a.scale = self.bits, c.table.cpu().numpy(), q.cpu().numpy(), c.dim ** -0.5
+        a.pool = {n: getattr(c, n).cpu().numpy() for n in (("k", "v") if self.bits == 16 else ("k", "ks", "v", "vs"))}
+        a.check(out, blocks.cpu().numpy())
+        assert (out != 0).any(-1).all()
+        self.calls += 1
+
+
+@pytest.mark.parametrize("bits,page", [(16, 16), (4, 64), (4, 16)])
+def test_the_example_attends_the_blocks_that_promise_the_most(ex, bits, page):
+    """Every layer's selection and attention of eager steps against f64 over the blocks that the bounds name."""
+    d = ex.Decoder(**CFG, bits=bits, blocks=2, page=page)
+    past = torch.tensor([250, 0, 70], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 250, 250, 320], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for cache in d.caches:
+        k, v = (torch.randn(320, CFG["kv_heads"], CFG["dim"], device="cuda", generator=g).half() for _ in range(2))
+        cache.append(k, v, past, starts=starts, rope=d.rope)
+    d.lens.copy_(past)
+    d.caches = [_Checked(c, bits) for c in d.caches]
+    for _ in range(4):
+        d.h.copy_(torch.randn(3, CFG["hidden"], device="cuda", generator=g).half())
+        d.step()
+    assert [c.calls for c in d.caches] == [4, 4] and ex.q2.device_errors() == 0
