@@ -441,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ 
               ((((long long)page * a.sub + (begin - pi * a.pg.page) / Q2_BLOCK) * a.kv_heads + h0 + h) * 2 + w) * D + pc * 8);
           if (p0 > begin) x = w ? hmax8(x, *to) : hmin8(x, *to);              // the block goes on
           *to = x;
+        } else if (s.ok && i == 0) {                // (may be another page than the tokens')
+          atomicOr(&q2_cache_error, Q2_ERR_PAGE);
         }
       }
     }

@@ -485,8 +485,8 @@ typedef struct {
  *     0..ntok: nothing of that sequence is written.  The other sequences are
  *     stored all the same, their bounds kept up and their queries turned; rows
  *     of q_out that two of them claim (where starts descend between them) are
- *     undefined.  A page outside 0..npages-1: its tokens are not stored,
- *     Q2_ERR_PAGE.
+ *     undefined.  A page outside 0..npages-1: its tokens are not stored, nor the
+ *     bounds that lie there, Q2_ERR_PAGE.
  *   - Pointers 16-byte aligned, leading dimensions multiples of 8, strides as the
  *     cache's structure says (Q2_EALIGN); batch <= Q2_ATT_MAX_BATCH, q_heads <=
  *     65536 (Q2_ESHAPE).  ntok == 0 or batch == 0 does nothing.  One launch, launched

@@ -450,3 +450,20 @@ def test_queries_beside_padding_are_turned(q2, bits, group, starts, interleaved)
         assert (np.abs(out[b] - y[0]) <= 2.0 ** -11 * np.abs(y[0]) + 2.0 ** -25 + 3 * 2.0 ** -24 * mag[0]).all()
     assert (out[[1, 3]] == 7).all()
     c.check_pools(skip=(1, 3))
+
+
+@pytest.mark.parametrize("bits,group", FORMS[:2])
+@pytest.mark.parametrize("starts", [False, True])
+def test_bounds_without_a_page_are_an_error(q2, bits, group, starts):
+    """The tokens' own page is there, that of their block's first token is not: the tokens are stored, the bounds cannot be."""
+    c = Case([40, 90], [1, 1], bits=bits, group=group, page=16, bounds=True, seed=17, starts=starts)
+    c.dtable[0, 0] = -1
+    kept = c.bounds.copy()
+    c.check_q(c.run(q2))
+    assert q2.device_errors() == q2.ERR_PAGE
+    want, all_kept = c.expect()
+    at = c.table[1, 4], 0                                                      # block 1 of sequence 1 has its bounds
+    kept[at] = all_kept[at]
+    assert np.array_equal(c.dbounds.cpu().numpy(), kept)
+    c.bounds = None
+    c.check_pools()
