@@ -38,8 +38,8 @@
 // query heads to a key-value head (eight of 256 columns) are taken 16 (eight)
 // at a time, each reading the tokens again.
 //
-// 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 318 us
-// on the device, 6.8 TB/s, the rate of a copy; one of 131072: 89 us, 6.0; 16
+// 64 sequences of 8192 tokens, 32 query and 8 key-value heads of 128: 318 to 327 us
+// by the machine, 6.6 to 6.8 TB/s, the rate of a copy; one of 131072: 90 us, 5.9; 16
 // of 1 to 4096 with 40 query heads 30 us, 4.5 (each CTA's start, its ends of
 // sequences and the joins are 9 of them); one of 777 tokens 7.0 us: the
 // lengths, the first pages' numbers, the first rows and the join behind one

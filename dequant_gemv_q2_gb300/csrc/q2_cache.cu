@@ -26,8 +26,10 @@
 //   - four prompts, 16384 tokens in all, fp16, with bounds: 78.6 us, 5.2 TB/s of
 //     the 6.8 of a copy.  2.7 instructions per cycle: the exact products of the
 //     keys, the bounds; three CTAs of 80 registers per SM.
-//   - 16384 tokens into 4 bits: 104 us, 2.4 TB/s: instructions, the exact products
-//     and some 6 per code.  Out again 41 us, 4.6 TB/s.
+//   - the same into 4 bits in groups of 64: 104 us, 3.5 TB/s (100 without bounds):
+//     instructions, the exact products and some 6 per code.  Out again 37.5 us, 2.3
+//     TB/s: every thread finds sequence, length and page of its 16 bytes anew.  16384
+//     tokens out of fp16 30 us, 4.4 TB/s.
 //
 // The bounds and the codes decide by comparison what later calls read, so keys
 // are turned to the last bit of fp32: a key next to the border of two codes
